@@ -440,6 +440,124 @@ dspark_status dspark_copy_target_rows(const float* T_src, float* T, const int32_
                                       int gamma, int V, void* workspace, size_t workspace_bytes,
                                       cudaStream_t stream);
 
+/*
+ * Rows of logits and of tables.  The calls below train the draft head and report on the
+ * tokens a step answers with.  Their matrices are fp32, bf16 or fp16 (dspark_dtype), row-major
+ * with a leading dimension `ld` in elements (>= the row's length; any value, rows need not
+ * start on a 16-byte border) and aligned to their element.  Sums, softmax statistics and
+ * gradients are formed in fp32 and rounded once, to nearest even, where they are stored in
+ * 16 bits (fp16 results beyond its range become infinite).  A row number of 0 is accepted and
+ * launches nothing (dspark_embed_grad: zeroes the table's gradient).  N < 2^21,
+ * 1 <= V <= 2^30, K <= 128.  The workspace is any of this library's (256 bytes suffice: the
+ * status word), except where a call names its own size.  Results do not depend on the order
+ * in which CTAs run.
+ */
+typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1, DSPARK_F16 = 2 } dspark_dtype;
+
+/*
+ * Log probabilities of given tokens, with entropy, rank and top alternatives.  billytse.dev
+ * DSpark page, section 1: the target's distribution of a position is the softmax of its
+ * logits row; the rows of T and the out_tokens of a verification (-1 past its answer) are
+ * such rows and tokens.  With m = max_v z_v, s = sum_v exp(z_v - m), y = tokens[n]:
+ *   logprob    z_y - m - log s            entropy   log s - sum_v exp(z_v - m)(z_v - m) / s
+ *   rank       1 + #{v : z_v > z_y or (z_v = z_y and v < y)}
+ *   row_max    m                          row_sumexp   s
+ *   top_ids, top_logprobs [N, K]   the K largest logits, descending, ties to the smallest v
+ * A logit of -inf has probability 0.  A row of -1 in `tokens` is not read: logprob, entropy,
+ * rank, row_sumexp 0, row_max and top_logprobs -inf, top_ids -1; any other token outside
+ * [0, V) does the same and records DSPARK_ERR_DEVICE_CHECK.  A row with no logit above -inf has
+ * logprob and top_logprobs -inf, entropy 0; a row with NaN or +inf has NaN for all of them,
+ * rank 0 and top_ids -1.  K > V leaves -1 and -inf in the places beyond V.
+ *
+ *   logits [N, V] (ld), tokens [N] int32, or NULL: every row is used, logprob and rank are
+ *   not written and must be NULL; entropy, row_max, row_sumexp may be NULL; top_ids and
+ *   top_logprobs are NULL iff K = 0.
+ */
+dspark_status dspark_token_logprobs(const void* logits, int dtype, int64_t ld, const int32_t* tokens,
+                                    int N, int V, int K, float* logprob, float* entropy,
+                                    int32_t* rank, float* row_max, float* row_sumexp,
+                                    int32_t* top_ids, float* top_logprobs, void* workspace,
+                                    size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Gradient of logprob and entropy with respect to the logits:
+ *   d_logits[n, v] = d_logprob[n] ([v = y] - p_v) - d_entropy[n] p_v (log p_v + entropy[n])
+ * with p from row_max, row_sumexp (and entropy, not NULL when d_entropy is not) as
+ * dspark_token_logprobs wrote them.  d_logprob or d_entropy may be NULL (zero).  Rows without a
+ * token, and rows with no logit above -inf, get zeroes.  d_logits has the logits' dtype, its own
+ * leading dimension, and may be the logits themselves (same pointer, same ld).
+ */
+dspark_status dspark_token_logprobs_grad(const void* logits, int dtype, int64_t ld,
+                                         const int32_t* tokens, int N, int V, const float* row_max,
+                                         const float* row_sumexp, const float* entropy,
+                                         const float* d_logprob, const float* d_entropy,
+                                         void* d_logits, int64_t ld_d, void* workspace,
+                                         size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Distillation of the draft head's logits from a teacher's top logits.  weigao.cc DSpark-vs-MTP
+ * page, "loss" (cross entropy, total variation, position weights) and xhh.club DSpark page (the
+ * acceptance rule: a drafted token is accepted with probability sum_v min(p_v, q_v)).  With
+ * q = softmax(z / temperature) over the row and p = softmax(t / temperature) over the row's
+ * entries (teacher_ids >= 0; other entries are absent),
+ *   loss[n]   = w_n (c_kl sum_k p_k (log p_k - log q_k) + c_tv sum_k max(0, p_k - q_k)
+ *                    + c_ce (-log q_label))
+ *   accept[n] = sum_k min(p_k, q_k)      (the confidence head's label)
+ * with q_k = q at teacher_ids[n, k].  teacher_logits may be logits or log probabilities
+ * (only differences count), -inf for an entry of probability 0.  Ids of a row are meant to be
+ * distinct; equal ones count as the formulas say.  A row of weight 0 is not read: loss,
+ * accept 0.  A row without entries has accept 0 and only the label's term; a label of -1 has
+ * no term.  Ids and labels outside [-1, V) count as -1 and record DSPARK_ERR_DEVICE_CHECK.
+ *
+ *   logits [N, V] (ld), teacher_ids [N, K] int32 and teacher_logits [N, K] fp32 (NULL iff
+ *   K = 0), labels [N] int32 or NULL (none), weights [N] fp32 or NULL (all 1),
+ *   temperature > 0, coefficients >= 0, all finite  ->  loss [N] fp32, accept [N] fp32
+ *
+ * dspark_distill_loss_grad also writes the gradient of sum_n d_loss[n] loss[n] (d_loss NULL:
+ * all 1) with respect to the logits, reading them once:
+ *   d_logits[n, v] = d_loss[n] w_n / temperature (A q_v - sum_{k : id_k = v} a_k),
+ *   a_k = c_kl p_k + c_tv q_k [q_k < p_k], a = c_ce at the label, A the sum of all a.
+ * d_logits has the logits' dtype and its own leading dimension, and may be the logits
+ * themselves (same pointer, same ld).  Rows of weight 0 get zeroes.
+ */
+dspark_status dspark_distill_loss(const void* logits, int dtype, int64_t ld,
+                                  const int32_t* teacher_ids, const float* teacher_logits,
+                                  const int32_t* labels, const float* weights, int N, int V, int K,
+                                  float temperature, float c_kl, float c_tv, float c_ce, float* loss,
+                                  float* accept, void* workspace, size_t workspace_bytes,
+                                  cudaStream_t stream);
+dspark_status dspark_distill_loss_grad(const void* logits, int dtype, int64_t ld,
+                                       const int32_t* teacher_ids, const float* teacher_logits,
+                                       const int32_t* labels, const float* weights,
+                                       const float* d_loss, int N, int V, int K, float temperature,
+                                       float c_kl, float c_tv, float c_ce, float* loss, float* accept,
+                                       void* d_logits, int64_t ld_d, void* workspace,
+                                       size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Embedding lookup with scaling, and its gradient.  billytse.dev DSpark page, section 3.3: W1
+ * is the previous token's small embedding.
+ *   dspark_embed:       out[n, :] = scale W[ids[n], :]
+ *   dspark_embed_grad:  dW[v, :] = scale sum_{n : ids[n] = v} d_out[n, :]   (accumulate = 0)
+ *                       dW[v, :] += the same, rows without a position untouched (accumulate = 1)
+ * The sums run over the positions sorted by id, in an order that depends on the ids alone.  An
+ * id of -1 (padding) gives a zero row and adds to nothing; other ids outside [0, V) do the
+ * same and record DSPARK_ERR_DEVICE_CHECK.
+ *
+ *   W [V, D] (ld, dtype) -> out [N, D] (ld_out, out_dtype: dtype or DSPARK_F32)
+ *   d_out [N, D] (ld, dtype) -> dW [V, D] (ld_w, w_dtype: dtype or DSPARK_F32)
+ *   ids [N] int32, scale finite, 1 <= D <= 65536.  dspark_embed_grad's workspace is of
+ *   dspark_embed_grad_workspace_bytes(N, V, D) bytes (0 on bad shapes).
+ */
+dspark_status dspark_embed(const void* W, int dtype, int64_t ld, const int32_t* ids, int N, int V,
+                           int D, float scale, void* out, int out_dtype, int64_t ld_out,
+                           void* workspace, size_t workspace_bytes, cudaStream_t stream);
+size_t dspark_embed_grad_workspace_bytes(int N, int V, int D);
+dspark_status dspark_embed_grad(const void* d_out, int dtype, int64_t ld, const int32_t* ids, int N,
+                                int V, int D, float scale, int accumulate, void* dW, int w_dtype,
+                                int64_t ld_w, void* workspace, size_t workspace_bytes,
+                                cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

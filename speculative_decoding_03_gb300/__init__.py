@@ -5,7 +5,8 @@ speculative step -- ``dspark_draft``, ``dspark_confidence``, ``dspark_schedule``
 ``dspark_verify`` -- plus ``dspark_draft_confidence_schedule`` (the first three in one
 launch), ``dspark_markov_bias``, the packed-W2 variants of the draft and the verification,
 greedy drafting with its verification, the asynchronous two-step capacity scheduler,
-fixed-threshold truncation and the RNN head; every step of the computation runs in its
+fixed-threshold truncation and the RNN head, and what trains the draft head and reports on
+its tokens (the ``rows`` module); every step of the computation runs in its
 CUDA kernels.  This module only marshals arguments: it passes device pointers of
 torch tensors and the current CUDA stream through ctypes, and allocates outputs and the
 workspace with torch.  There is no CPU fallback: without the built library and a CUDA
@@ -26,6 +27,7 @@ STATUS = {0: "DSPARK_OK", 1: "DSPARK_ERR_INVALID_ARG", 2: "DSPARK_ERR_UNSUPPORTE
 
 # (name, restype, argtypes) of every exported symbol, in header order
 _P, _I, _U64, _F, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint64, ctypes.c_float, ctypes.c_size_t
+_I64 = ctypes.c_int64
 SIGNATURES = [
     ("dspark_status_string", ctypes.c_char_p, [_I]),
     ("dspark_workspace_bytes", _SZ, [_I, _I, _I, _I, _I]),
@@ -59,6 +61,16 @@ SIGNATURES = [
                                               _U64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     ("dspark_testing_set_wait_limit", None, [ctypes.c_longlong, _I]),
     ("dspark_copy_target_rows", _I, [_P, _P, _P, _I, _I, _I, _P, _SZ, _P]),
+    ("dspark_token_logprobs", _I, [_P, _I, _I64, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    ("dspark_token_logprobs_grad", _I, [_P, _I, _I64, _P, _I, _I, _P, _P, _P, _P, _P, _P, _I64, _P, _SZ,
+                                        _P]),
+    ("dspark_distill_loss", _I, [_P, _I, _I64, _P, _P, _P, _P, _I, _I, _I, _F, _F, _F, _F, _P, _P, _P,
+                                 _SZ, _P]),
+    ("dspark_distill_loss_grad", _I, [_P, _I, _I64, _P, _P, _P, _P, _P, _I, _I, _I, _F, _F, _F, _F, _P,
+                                      _P, _P, _I64, _P, _SZ, _P]),
+    ("dspark_embed", _I, [_P, _I, _I64, _P, _I, _I, _I, _F, _P, _I, _I64, _P, _SZ, _P]),
+    ("dspark_embed_grad_workspace_bytes", _SZ, [_I, _I, _I]),
+    ("dspark_embed_grad", _I, [_P, _I, _I64, _P, _I, _I, _I, _F, _I, _P, _I, _I64, _P, _SZ, _P]),
 ]
 
 _lib = None
@@ -123,8 +135,20 @@ class Workspace:
     """Caller-owned scratch for the calls (zero-filled, 256-byte aligned torch buffer)."""
 
     def __init__(self, B: int, gamma: int, V: int, r: int, H: int = 0, device="cuda"):
+        self._allocate(workspace_bytes(B, gamma, V, r, H), device)
+
+    @classmethod
+    def of_bytes(cls, nbytes: int, device="cuda") -> "Workspace":
+        """A workspace of ``nbytes`` (256 hold the status word alone)."""
+        if nbytes < 256:
+            raise ValueError(f"a workspace has at least 256 bytes, not {nbytes}")
+        ws = cls.__new__(cls)
+        ws._allocate(int(nbytes), device)
+        return ws
+
+    def _allocate(self, nbytes: int, device):
         torch = _torch()
-        self.nbytes = workspace_bytes(B, gamma, V, r, H)
+        self.nbytes = nbytes
         self.buf = torch.zeros(self.nbytes + 256, dtype=torch.uint8, device=device)
         off = (-self.buf.data_ptr()) % 256
         self.ptr = self.buf.data_ptr() + off
@@ -776,3 +800,7 @@ def rnn_to_device(W_rnn, b_rnn, dev: Dict, device="cuda") -> Dict:
     dev["W_rnn"] = as_bf16_tensor(W_rnn, device)
     dev["b_rnn"] = torch.from_numpy(np.ascontiguousarray(b_rnn, dtype=np.float32)).to(device)
     return dev
+
+
+from .rows import (distill_loss, distill_loss_grad, embed, embed_grad,  # noqa: E402
+                   embed_grad_workspace_bytes, token_logprobs, token_logprobs_grad)

@@ -24,6 +24,49 @@ dspark_status check_ws(void* ws, size_t bytes, const Plan& p) {
   return DSPARK_OK;
 }
 
+// ---- rows of logits and of tables ----
+int elem_bytes(int dtype) { return dtype == DSPARK_F32 ? 4 : 2; }
+bool known_dtype(int dtype) { return dtype == DSPARK_F32 || dtype == DSPARK_BF16 || dtype == DSPARK_F16; }
+bool finite(float x) { return x - x == 0.f; }
+
+// N rows of `len` elements `ld` apart; the pointer may be null where there are no rows
+dspark_status check_rows(const void* p, int dtype, int64_t ld, int N, int len) {
+  if (!known_dtype(dtype) || N < 0 || len < 1 || ld < len) return DSPARK_ERR_INVALID_ARG;
+  if (N > 0 && !aligned(p, elem_bytes(dtype))) return DSPARK_ERR_INVALID_ARG;
+  if (N >= (1 << 21) || len > (1 << 30) || ld > (1LL << 40)) return DSPARK_ERR_UNSUPPORTED;
+  return DSPARK_OK;
+}
+bool aligned_or_null(const void* p, uintptr_t a) { return !p || aligned(p, a); }
+
+dspark_status distill(const void* logits, int dtype, int64_t ld, const int32_t* teacher_ids,
+                      const float* teacher_logits, const int32_t* labels, const float* weights,
+                      const float* d_loss, int N, int V, int K, float temperature, float c_kl,
+                      float c_tv, float c_ce, float* loss, float* accept, bool grad, void* d_logits,
+                      int64_t ld_d, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  dspark_status st = check_rows(logits, dtype, ld, N, V);
+  if (st == DSPARK_OK && grad) st = check_rows(d_logits, dtype, ld_d, N, V);
+  if (st != DSPARK_OK) return st;
+  if (K < 0) return DSPARK_ERR_INVALID_ARG;
+  if (K > kMaxTop) return DSPARK_ERR_UNSUPPORTED;
+  // in place is the same rows; other overlaps are the caller's to avoid
+  if (grad && d_logits == logits && ld_d != ld && N > 1) return DSPARK_ERR_INVALID_ARG;
+  if (!(temperature > 0.f) || !finite(temperature) || !finite(1.f / temperature) || !(c_kl >= 0.f) ||
+      !(c_tv >= 0.f) || !(c_ce >= 0.f) || !finite(c_kl) || !finite(c_tv) || !finite(c_ce))
+    return DSPARK_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256) || workspace_bytes < 256) return DSPARK_ERR_INVALID_ARG;
+  if (!aligned_or_null(labels, 4) || !aligned_or_null(weights, 4) || !aligned_or_null(d_loss, 4))
+    return DSPARK_ERR_INVALID_ARG;
+  if ((K == 0) != !teacher_ids || (K == 0) != !teacher_logits || !aligned_or_null(teacher_ids, 4) ||
+      !aligned_or_null(teacher_logits, 4))
+    return DSPARK_ERR_INVALID_ARG;
+  if (N == 0) return DSPARK_OK;
+  if (!aligned(loss, 4) || !aligned(accept, 4)) return DSPARK_ERR_INVALID_ARG;
+  return launch_distill(logits, dtype, ld, teacher_ids, teacher_logits, labels, weights, d_loss, N, V, K,
+                        1.f / temperature, c_kl, c_tv, c_ce, loss, accept, grad ? d_logits : nullptr,
+                        ld_d, ws_at<int>(workspace, 0), stream) == cudaSuccess
+             ? DSPARK_OK : DSPARK_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -418,6 +461,111 @@ dspark_status dspark_copy_target_rows(const float* T_src, float* T, const int32_
       cudaSuccess)
     return DSPARK_ERR_CUDA;
   return DSPARK_OK;
+}
+
+dspark_status dspark_token_logprobs(const void* logits, int dtype, int64_t ld, const int32_t* tokens,
+                                    int N, int V, int K, float* logprob, float* entropy,
+                                    int32_t* rank, float* row_max, float* row_sumexp,
+                                    int32_t* top_ids, float* top_logprobs, void* workspace,
+                                    size_t workspace_bytes, cudaStream_t stream) {
+  dspark_status st = check_rows(logits, dtype, ld, N, V);
+  if (st != DSPARK_OK) return st;
+  if (K < 0) return DSPARK_ERR_INVALID_ARG;
+  if (K > kMaxTop) return DSPARK_ERR_UNSUPPORTED;
+  if (!aligned(workspace, 256) || workspace_bytes < 256) return DSPARK_ERR_INVALID_ARG;
+  if (!aligned_or_null(entropy, 4) || !aligned_or_null(row_max, 4) || !aligned_or_null(row_sumexp, 4) ||
+      !aligned_or_null(tokens, 4) || !aligned_or_null(logprob, 4) || !aligned_or_null(rank, 4) ||
+      !aligned_or_null(top_ids, 4) || !aligned_or_null(top_logprobs, 4))
+    return DSPARK_ERR_INVALID_ARG;
+  if (N == 0) return DSPARK_OK;
+  if (!tokens != !logprob || !tokens != !rank || (K == 0) != !top_ids || (K == 0) != !top_logprobs)
+    return DSPARK_ERR_INVALID_ARG;
+  return launch_token_logprobs(logits, dtype, ld, tokens, N, V, K, logprob, entropy, rank, row_max,
+                               row_sumexp, top_ids, top_logprobs, ws_at<int>(workspace, 0),
+                               stream) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+}
+
+dspark_status dspark_token_logprobs_grad(const void* logits, int dtype, int64_t ld,
+                                         const int32_t* tokens, int N, int V, const float* row_max,
+                                         const float* row_sumexp, const float* entropy,
+                                         const float* d_logprob, const float* d_entropy,
+                                         void* d_logits, int64_t ld_d, void* workspace,
+                                         size_t workspace_bytes, cudaStream_t stream) {
+  dspark_status st = check_rows(logits, dtype, ld, N, V);
+  if (st == DSPARK_OK) st = check_rows(d_logits, dtype, ld_d, N, V);
+  if (st != DSPARK_OK) return st;
+  if (d_logits == logits && ld_d != ld && N > 1) return DSPARK_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256) || workspace_bytes < 256) return DSPARK_ERR_INVALID_ARG;
+  if (!aligned_or_null(entropy, 4) || !aligned_or_null(d_logprob, 4) || !aligned_or_null(d_entropy, 4) ||
+      (d_entropy && !entropy))
+    return DSPARK_ERR_INVALID_ARG;
+  if (N == 0) return DSPARK_OK;
+  if (!aligned(tokens, 4) || !aligned(row_max, 4) || !aligned(row_sumexp, 4)) return DSPARK_ERR_INVALID_ARG;
+  return launch_token_logprobs_grad(logits, dtype, ld, tokens, N, V, row_max, row_sumexp, entropy,
+                                    d_logprob, d_entropy, d_logits, ld_d, ws_at<int>(workspace, 0),
+                                    stream) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+}
+
+dspark_status dspark_distill_loss(const void* logits, int dtype, int64_t ld,
+                                  const int32_t* teacher_ids, const float* teacher_logits,
+                                  const int32_t* labels, const float* weights, int N, int V, int K,
+                                  float temperature, float c_kl, float c_tv, float c_ce, float* loss,
+                                  float* accept, void* workspace, size_t workspace_bytes,
+                                  cudaStream_t stream) {
+  return distill(logits, dtype, ld, teacher_ids, teacher_logits, labels, weights, nullptr, N, V, K,
+                 temperature, c_kl, c_tv, c_ce, loss, accept, false, nullptr, 0, workspace,
+                 workspace_bytes, stream);
+}
+
+dspark_status dspark_distill_loss_grad(const void* logits, int dtype, int64_t ld,
+                                       const int32_t* teacher_ids, const float* teacher_logits,
+                                       const int32_t* labels, const float* weights,
+                                       const float* d_loss, int N, int V, int K, float temperature,
+                                       float c_kl, float c_tv, float c_ce, float* loss, float* accept,
+                                       void* d_logits, int64_t ld_d, void* workspace,
+                                       size_t workspace_bytes, cudaStream_t stream) {
+  return distill(logits, dtype, ld, teacher_ids, teacher_logits, labels, weights, d_loss, N, V, K,
+                 temperature, c_kl, c_tv, c_ce, loss, accept, true, d_logits, ld_d, workspace,
+                 workspace_bytes, stream);
+}
+
+dspark_status dspark_embed(const void* W, int dtype, int64_t ld, const int32_t* ids, int N, int V,
+                           int D, float scale, void* out, int out_dtype, int64_t ld_out,
+                           void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (V < 1) return DSPARK_ERR_INVALID_ARG;
+  dspark_status st = check_rows(W, dtype, ld, 1, D);
+  if (st == DSPARK_OK) st = check_rows(out, out_dtype, ld_out, N, D);
+  if (st != DSPARK_OK) return st;
+  if (D > 65536 || V > (1 << 30)) return DSPARK_ERR_UNSUPPORTED;
+  if (out_dtype != dtype && out_dtype != DSPARK_F32) return DSPARK_ERR_INVALID_ARG;
+  if (!finite(scale) || !aligned(workspace, 256) || workspace_bytes < 256) return DSPARK_ERR_INVALID_ARG;
+  if (N == 0) return DSPARK_OK;
+  if (!aligned(ids, 4)) return DSPARK_ERR_INVALID_ARG;
+  return launch_embed(W, dtype, ld, ids, N, V, D, scale, out, out_dtype, ld_out,
+                      ws_at<int>(workspace, 0), stream) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+}
+
+size_t dspark_embed_grad_workspace_bytes(int N, int V, int D) {
+  if (N < 0 || N >= (1 << 21) || V < 1 || V > (1 << 30) || D < 1 || D > 65536) return 0;
+  return embed_grad_bytes(N, V, D);
+}
+
+dspark_status dspark_embed_grad(const void* d_out, int dtype, int64_t ld, const int32_t* ids, int N,
+                                int V, int D, float scale, int accumulate, void* dW, int w_dtype,
+                                int64_t ld_w, void* workspace, size_t workspace_bytes,
+                                cudaStream_t stream) {
+  if (V < 1) return DSPARK_ERR_INVALID_ARG;
+  dspark_status st = check_rows(d_out, dtype, ld, N, D);
+  if (st == DSPARK_OK) st = check_rows(dW, w_dtype, ld_w, 1, D);
+  if (st != DSPARK_OK) return st;
+  if (D > 65536 || V > (1 << 30)) return DSPARK_ERR_UNSUPPORTED;
+  if (w_dtype != dtype && w_dtype != DSPARK_F32) return DSPARK_ERR_INVALID_ARG;
+  if (!finite(scale) || !aligned(workspace, 256) || workspace_bytes < embed_grad_bytes(N, V, D))
+    return DSPARK_ERR_INVALID_ARG;
+  if (N > 0 && !aligned(ids, 4)) return DSPARK_ERR_INVALID_ARG;
+  return launch_embed_grad(d_out, dtype, ld, ids, N, V, D, scale, accumulate != 0, dW, w_dtype, ld_w,
+                           ws_at<int>(workspace, 0), workspace, stream) == cudaSuccess
+             ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
 }  // extern "C"

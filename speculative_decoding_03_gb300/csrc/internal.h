@@ -143,6 +143,27 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// The same for `ctas` CTAs in clusters of C (1, 2, 4 or 8) consecutive ones.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_rows_cluster(void (*kernel)(KArgs...), long long ctas, int C, int threads,
+                                       size_t smem, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = C;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---- tensor maps ----
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -270,6 +291,32 @@ cudaError_t launch_schedule_threshold(const float* a, int R, int gamma, float th
 // T[b, j] for j <= ell[b] from T_src (memory the device reads, host memory included) into T
 cudaError_t launch_copy_target_rows(const float* T_src, float* T, const int32_t* ell, int B,
                                     int gamma, int V, int* err, cudaStream_t stream);
+
+// ---- rows of logits and of tables in fp32, bf16 or fp16 (dspark_dtype) ----
+constexpr int kMaxTop = 128;             // alternatives of a row, entries of a teacher's row
+// see logprobs.cu; leading dimensions in elements
+cudaError_t launch_token_logprobs(const void* z, int dtype, long long ld, const int32_t* tokens,
+                                  int N, int V, int K, float* logprob, float* entropy, int32_t* rank,
+                                  float* row_max, float* row_sumexp, int32_t* top_ids,
+                                  float* top_logprobs, int* err, cudaStream_t stream);
+cudaError_t launch_token_logprobs_grad(const void* z, int dtype, long long ld, const int32_t* tokens,
+                                       int N, int V, const float* row_max, const float* row_sumexp,
+                                       const float* entropy, const float* d_logprob,
+                                       const float* d_entropy, void* dz, long long ld_dz, int* err,
+                                       cudaStream_t stream);
+// see distill.cu; dz null: the loss alone
+cudaError_t launch_distill(const void* z, int dtype, long long ld, const int32_t* ids, const float* t,
+                           const int32_t* labels, const float* weights, const float* d_loss, int N,
+                           int V, int K, float inv_tau, float c_kl, float c_tv, float c_ce, float* loss,
+                           float* accept, void* dz, long long ld_dz, int* err, cudaStream_t stream);
+// see embed.cu; ws holds embed_grad_bytes(N, V, D)
+size_t embed_grad_bytes(int N, int V, int D);
+cudaError_t launch_embed(const void* W, int dtype, long long ld, const int32_t* ids, int N, int V, int D,
+                         float scale, void* out, int out_dtype, long long ld_out, int* err,
+                         cudaStream_t stream);
+cudaError_t launch_embed_grad(const void* d_out, int dtype, long long ld, const int32_t* ids, int N, int V,
+                              int D, float scale, int accumulate, void* dW, int w_dtype, long long ld_w,
+                              int* err, void* ws, cudaStream_t stream);
 
 // E_all (null for the Markov head): the RNN head's output rows [B][gamma][r] of the draft
 cudaError_t launch_verify(const Plan& p, const float* T, const float* U, const uint16_t* W1,
