@@ -124,7 +124,8 @@ __global__ void __launch_bounds__(kDsThreads, 4) distill_kernel(DsParams a, int 
   // can write the gradient over the row
   constexpr int kPer = kMaxTop / 32;
   int id[kPer], y = -1;
-  float tt[kPer], zk[kPer], zy = 0.f;
+  float tt[kPer], pk[kPer], zk[kPer], zy = 0.f;
+  bool any = false;
   if (warp == 0) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -144,6 +145,24 @@ __global__ void __launch_bounds__(kDsThreads, 4) distill_kernel(DsParams a, int 
         y = -1;
       }
       if (y >= 0) zy = elem_to_float(row[y]);
+    }
+    // the teacher's softmax, while the row arrives: tt becomes log p
+    float tm = -INFINITY, ps = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) tm = fmaxf(tm, tt[i]);
+    tm = warp_max(tm);
+    any = tm > -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      pk[i] = id[i] >= 0 && any ? expf(tt[i] - tm) : 0.f;
+      ps += pk[i];
+    }
+    ps = warp_sum(ps);
+    const float log_ps = logf(ps);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      pk[i] = any ? pk[i] / ps : 0.f;
+      tt[i] = tt[i] - tm - log_ps;
     }
   }
 
@@ -199,12 +218,11 @@ __global__ void __launch_bounds__(kDsThreads, 4) distill_kernel(DsParams a, int 
   float M = m, S;
   if (C > 1) {
     cluster_sync();                          // also: every CTA has read its teacher entries
-    for (int o = 0; o < C; ++o) M = fmaxf(M, cluster_ld_f4(cluster_map(&sh.stat, o)).x);
-    S = 0.f;
-    for (int o = 0; o < C; ++o) {
-      const float4 p = cluster_ld_f4(cluster_map(&sh.stat, o));
-      if (p.y != 0.f) S += p.y * ex2_approx((p.x - M) * (a.inv_tau * kLog2e));
-    }
+    // lane o reads CTA o's sums
+    const float4 p = lane < C ? cluster_ld_f4(cluster_map(&sh.stat, lane))
+                              : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    M = warp_max(p.x);
+    S = warp_sum(p.y != 0.f ? p.y * ex2_approx((p.x - M) * (a.inv_tau * kLog2e)) : 0.f);
   } else {
     S = sh.stat.y;
   }
@@ -212,19 +230,6 @@ __global__ void __launch_bounds__(kDsThreads, 4) distill_kernel(DsParams a, int 
   // ---- loss, acceptance and the entries' coefficients
   if (warp == 0) {
     const float logs = logf(S);
-    float tm = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) tm = fmaxf(tm, tt[i]);
-    tm = warp_max(tm);
-    const bool any = tm > -INFINITY;
-    float e[kPer], ps = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      e[i] = id[i] >= 0 && any ? expf(tt[i] - tm) : 0.f;
-      ps += e[i];
-    }
-    ps = warp_sum(ps);
-    const float log_ps = logf(ps);
     float kl = 0.f, tv = 0.f, acc = 0.f, sum_a = 0.f;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -233,8 +238,8 @@ __global__ void __launch_bounds__(kDsThreads, 4) distill_kernel(DsParams a, int 
         const float lq = (zk[i] - M) * a.inv_tau - logs;
         q = expf(lq);
         if (any) {
-          const float p = e[i] / ps;
-          if (p != 0.f) kl += p * ((tt[i] - tm - log_ps) - lq);
+          const float p = pk[i];
+          if (p != 0.f) kl += p * (tt[i] - lq);
           tv += fmaxf(p - q, 0.f);
           acc += fminf(p, q);
           // products with a zero coefficient are left out: 0 * inf

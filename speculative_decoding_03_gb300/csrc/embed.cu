@@ -12,8 +12,8 @@
 // that crosses tiles leaves partial sums that are joined in tile order, first within a CTA
 // (8 tiles, shared memory), then by a last kernel (workspace).  Up to 8192 positions are
 // sorted by counting (every item against every key, 1 launch), more by a radix sort of 9
-// bits a pass.  The table's other rows are zeroed by CTAs of the sorting launches that have
-// nothing to sort: the zeroes are the bulk of the bytes, and the sort hides behind them.
+// bits a pass.  The table's zeroes are the bulk of the bytes: CTAs of every launch
+// write a share of them, beside the sort and the sums.
 #include "internal.h"
 #include "rows.cuh"
 
@@ -125,52 +125,102 @@ __device__ __forceinline__ int key_of(const EgParams& a, int n) {
   return a.V;
 }
 
-// zeroes CTA `part` of `parts`'s share of dW
-__device__ __forceinline__ void fill_zero(const EgParams& a, long long part, long long parts) {
-  const long long bytes = (long long)a.D * a.elem_w;
-  char* base = static_cast<char*>(a.dW);
+// The table's zeroes are dealt over every launch of the call (`fill` CTAs of each), so that
+// they hide the sort and the sums: before the sums all rows of a CTA's share, with the sums
+// and after them only the rows that no position has.
+struct Fill {
+  int first;                 // the launch's first filling CTA in its grid
+  int from, all;             // its share is part (blockIdx - first) + from of `all`
+};
+__device__ __forceinline__ void share_of(const EgParams& a, const Fill& f, int& v0, int& v1) {
+  const long long part = f.from + ((int)blockIdx.x - f.first);
+  v0 = (int)((long long)a.V * part / f.all);
+  v1 = (int)((long long)a.V * (part + 1) / f.all);
+}
+// `bytes` zeroes from p on, by `threads` threads
+__device__ __forceinline__ void zero_bytes(char* p, long long bytes, int t, int threads) {
   const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-  if (a.ld_w == a.D) {                      // one run of bytes
-    const long long total = bytes * a.V;
-    const long long head = min(total, (long long)((16u - (reinterpret_cast<uintptr_t>(base) & 15u)) & 15u));
-    uint4* p = reinterpret_cast<uint4*>(base + head);
-    const long long n4 = (total - head) / 16;
-    const long long i0 = n4 * part / parts, i1 = n4 * (part + 1) / parts;
-    long long i = i0 + threadIdx.x;
-    for (; i + 3 * kEmThreads < i1; i += 4 * kEmThreads) {
-      p[i] = z;
-      p[i + kEmThreads] = z;
-      p[i + 2 * kEmThreads] = z;
-      p[i + 3 * kEmThreads] = z;
-    }
-    for (; i < i1; i += kEmThreads) p[i] = z;
-    if (part == 0) {
-      const long long tail = total - head - n4 * 16;
-      if ((long long)threadIdx.x < head) base[threadIdx.x] = 0;
-      if ((long long)threadIdx.x < tail) base[total - tail + threadIdx.x] = 0;
-    }
-    return;
+  const int head = (int)min(bytes, (long long)((16u - (reinterpret_cast<uintptr_t>(p) & 15u)) & 15u));
+  uint4* q = reinterpret_cast<uint4*>(p + head);
+  const long long n4 = (bytes - head) / 16;
+  long long i = t;
+  for (; i + 3 * threads < n4; i += 4 * threads) {
+    __stcs(q + i, z);
+    __stcs(q + i + threads, z);
+    __stcs(q + i + 2 * threads, z);
+    __stcs(q + i + 3 * threads, z);
   }
-  const long long v0 = (long long)a.V * part / parts, v1 = (long long)a.V * (part + 1) / parts;
-  for (long long v = v0 + (threadIdx.x >> 5); v < v1; v += kEmWarps) {
-    char* row = base + v * a.ld_w * a.elem_w;
-    const long long head = min(bytes, (long long)((16u - (reinterpret_cast<uintptr_t>(row) & 15u)) & 15u));
-    const long long n4 = (bytes - head) / 16, tail = bytes - head - n4 * 16;
-    const int lane = threadIdx.x & 31;
-    for (long long i = lane; i < n4; i += 32) reinterpret_cast<uint4*>(row + head)[i] = z;
-    if (lane < head) row[lane] = 0;
-    if (lane < tail) row[bytes - tail + lane] = 0;
+  for (; i < n4; i += threads) __stcs(q + i, z);
+  const int tail = (int)(bytes - head - n4 * 16);
+  if (t < head) p[t] = 0;
+  if (t < tail) p[bytes - tail + t] = 0;
+}
+__device__ __forceinline__ void fill_rows(const EgParams& a, const Fill& f) {
+  int v0, v1;
+  share_of(a, f, v0, v1);
+  const long long row = (long long)a.D * a.elem_w, step = a.ld_w * a.elem_w;
+  char* base = static_cast<char*>(a.dW) + v0 * step;
+  if (step == row) {
+    zero_bytes(base, row * (v1 - v0), threadIdx.x, kEmThreads);
+  } else {
+    for (int v = threadIdx.x >> 5; v < v1 - v0; v += kEmWarps)
+      zero_bytes(base + v * step, row, threadIdx.x & 31, 32);
+  }
+}
+// The same without the rows of the sorted keys: `block` threads mark them in shared memory,
+// kFillRows rows at a time.
+constexpr int kFillRows = 2048;
+__device__ __forceinline__ void fill_other_rows(const EgParams& a, const Fill& f, const int* skey,
+                                                uint32_t* marks, int block) {
+  __shared__ int found_s;
+  int v0, v1;
+  share_of(a, f, v0, v1);
+  const long long row = (long long)a.D * a.elem_w, step = a.ld_w * a.elem_w;
+  char* base = static_cast<char*>(a.dW);
+  // the first sorted position of a key >= v0: `block` probes at a time
+  int lo = 0, hi = a.N;
+  while (hi > lo) {
+    const int width = (hi - lo + block - 1) / block;
+    const int at = lo + (int)threadIdx.x * width;
+    __syncthreads();
+    if (threadIdx.x == 0) found_s = 0;
+    __syncthreads();
+    const unsigned below = __ballot_sync(0xffffffffu, at < hi && skey[at] < v0);
+    if ((threadIdx.x & 31) == 0 && below) atomicAdd(&found_s, __popc(below));
+    __syncthreads();
+    const int n = found_s;                  // probes 0 .. n - 1 are below v0
+    const int end = hi;
+    hi = min(end, lo + n * width);
+    lo = n == 0 ? lo : lo + (n - 1) * width + 1;
+    if (n == 0) hi = lo;
+  }
+  for (int r0 = v0; r0 < v1; r0 += kFillRows) {
+    const int r1 = min(v1, r0 + kFillRows);
+    __syncthreads();
+    for (int i = threadIdx.x; i < kFillRows / 32; i += block) marks[i] = 0u;
+    __syncthreads();
+    // this part's keys, `block` at a time
+    for (;;) {
+      const int i = lo + threadIdx.x;
+      const int k = i < a.N ? skey[i] : a.V;
+      if (k < r1) atomicOr(&marks[(k - r0) >> 5], 1u << ((k - r0) & 31));
+      const int n = __syncthreads_count(k < r1);
+      lo += n;
+      if (n < block) break;
+    }
+    for (int v = r0 + (threadIdx.x >> 5); v < r1; v += block / 32)
+      if (!(marks[(v - r0) >> 5] >> ((v - r0) & 31) & 1u)) zero_bytes(base + v * step, row, threadIdx.x & 31, 32);
   }
 }
 
 // every item's place among all keys: the keys below it, and the equal ones before it
-__global__ void __launch_bounds__(kEmThreads) eg_rank_kernel(EgParams a, int sort_ctas, int fill_ctas) {
+__global__ void __launch_bounds__(kEmThreads) eg_rank_kernel(EgParams a, Fill f) {
   extern __shared__ int4 keys4[];
   int* keys = reinterpret_cast<int*>(keys4);
   pdl_wait();
   pdl_launch_dependents();
-  if ((int)blockIdx.x >= sort_ctas) {
-    fill_zero(a, blockIdx.x - sort_ctas, fill_ctas);
+  if ((int)blockIdx.x >= f.first) {
+    fill_rows(a, f);
     return;
   }
   const int n4 = (a.N + 3) / 4;
@@ -200,13 +250,12 @@ __global__ void __launch_bounds__(kEmThreads) eg_rank_kernel(EgParams a, int sor
 }
 
 // radix pass: digit counts of every tile
-__global__ void __launch_bounds__(kEmThreads) eg_count_kernel(EgParams a, int pass, int sort_ctas,
-                                                              int fill_from, int fill_ctas, int fill_all) {
+__global__ void __launch_bounds__(kEmThreads) eg_count_kernel(EgParams a, int pass, Fill f) {
   __shared__ int hist[kRadix];
   pdl_wait();
   pdl_launch_dependents();
-  if ((int)blockIdx.x >= sort_ctas) {
-    if (fill_ctas) fill_zero(a, fill_from + (blockIdx.x - sort_ctas), fill_all);
+  if ((int)blockIdx.x >= f.first) {
+    fill_rows(a, f);
     return;
   }
   for (int i = threadIdx.x; i < kRadix; i += kEmThreads) hist[i] = 0;
@@ -226,15 +275,14 @@ __global__ void __launch_bounds__(kEmThreads) eg_count_kernel(EgParams a, int pa
 }
 
 // radix pass: every key to its place, equal digits in their order
-__global__ void __launch_bounds__(kEmThreads) eg_scatter_kernel(EgParams a, int pass, int sort_ctas,
-                                                                int fill_from, int fill_ctas, int fill_all) {
+__global__ void __launch_bounds__(kEmThreads) eg_scatter_kernel(EgParams a, int pass, Fill f) {
   __shared__ int wh[kEmWarps][kRadix];
   __shared__ int base_s[kRadix];
   __shared__ int warp_s[kEmWarps];
   pdl_wait();
   pdl_launch_dependents();
-  if ((int)blockIdx.x >= sort_ctas) {
-    if (fill_ctas) fill_zero(a, fill_from + (blockIdx.x - sort_ctas), fill_all);
+  if ((int)blockIdx.x >= f.first) {
+    fill_rows(a, f);
     return;
   }
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -246,7 +294,7 @@ __global__ void __launch_bounds__(kEmThreads) eg_scatter_kernel(EgParams a, int 
   int before[2] = {0, 0}, all[2] = {0, 0};
   const int tile = blockIdx.x;
 #pragma unroll 8
-  for (int t = 0; t < sort_ctas; ++t) {
+  for (int t = 0; t < f.first; ++t) {
     const int2 n = *reinterpret_cast<const int2*>(a.counts + (size_t)t * kRadix + 2 * tid);
     all[0] += n.x;
     all[1] += n.y;
@@ -351,7 +399,7 @@ __device__ __forceinline__ void put_part(const EgParams& a, int tile, int slot, 
 // Sums of the sorted positions: CTA = 8 consecutive tiles of P positions (a warp each) x one
 // column block.
 template <typename T, typename O, bool Vec>
-__global__ void __launch_bounds__(kEmThreads) eg_sum_kernel(EgParams a, int buf) {
+__global__ void __launch_bounds__(kEmThreads) eg_sum_kernel(EgParams a, int buf, Fill f) {
   constexpr int N = Chunk<T>::N;
   constexpr int kAhead = 8;                 // rows in flight
   __shared__ float part_s[kEmWarps][2][N][32];
@@ -361,6 +409,10 @@ __global__ void __launch_bounds__(kEmThreads) eg_sum_kernel(EgParams a, int buf)
   pdl_launch_dependents();
   const int* skey = a.key[buf];
   const int* spos = a.pos[buf];
+  if ((int)blockIdx.x >= f.first) {
+    fill_other_rows(a, f, skey, reinterpret_cast<uint32_t*>(part_s), kEmThreads);
+    return;
+  }
   const int P = a.P, V = a.V;
   const int cta0 = cta * kEmWarps * P;
   const int i0 = min(a.N, cta0 + warp * P), i1 = min(a.N, i0 + P), cnt = i1 - i0;
@@ -460,13 +512,17 @@ __global__ void __launch_bounds__(kEmThreads) eg_sum_kernel(EgParams a, int buf)
 // Runs across CTA tiles: CTA (t, cb) sums the run that begins in t and goes on.  Four warps
 // take consecutive parts of its tiles, joined in order.
 template <typename O, int N, bool Vec>
-__global__ void __launch_bounds__(128) eg_join_kernel(EgParams a, int buf) {
+__global__ void __launch_bounds__(128) eg_join_kernel(EgParams a, int buf, Fill f) {
   __shared__ float part_s[4][N][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x / a.cols, cb = blockIdx.x - t * a.cols;
   pdl_wait();
   pdl_launch_dependents();
   const int* skey = a.key[buf];
+  if ((int)blockIdx.x >= f.first) {
+    fill_other_rows(a, f, skey, reinterpret_cast<uint32_t*>(part_s), 128);
+    return;
+  }
   const int span = kEmWarps * a.P;
   const int i0 = t * span, i1 = i0 + span;
   if (i1 >= a.N) return;
@@ -551,12 +607,17 @@ cudaError_t launch_em(const EmParams& p, cudaStream_t stream) {
 }
 
 template <typename T, typename O, bool Vec>
-cudaError_t launch_eg_sums(EgParams p, int buf, cudaStream_t stream) {
+cudaError_t launch_eg_sums(EgParams p, int buf, int fill, int from, int all, cudaStream_t stream) {
   p.cols = cdiv(p.D, 32 * Chunk<T>::N);
-  const dim3 grid((unsigned)(p.tiles * p.cols));
-  cudaError_t e = launch_pdl(eg_sum_kernel<T, O, Vec>, grid, dim3(kEmThreads), 0, stream, p, buf);
-  if (e == cudaSuccess && p.tiles > 1)
-    e = launch_pdl(eg_join_kernel<O, Chunk<T>::N, Vec>, grid, dim3(128), 0, stream, p, buf);
+  const int ctas = p.tiles * p.cols;
+  Fill f = {ctas, from, all};
+  cudaError_t e = launch_pdl(eg_sum_kernel<T, O, Vec>, dim3((unsigned)(ctas + fill)), dim3(kEmThreads), 0,
+                             stream, p, buf, f);
+  if (e == cudaSuccess && p.tiles > 1) {
+    f.from += fill;
+    e = launch_pdl(eg_join_kernel<O, Chunk<T>::N, Vec>, dim3((unsigned)(ctas + fill)), dim3(128), 0, stream,
+                   p, buf, f);
+  }
   return e;
 }
 
@@ -572,30 +633,36 @@ cudaError_t launch_eg(EgParams p, void* ws, cudaStream_t stream) {
   p.P = plan.P;
   p.tiles = plan.tiles;
   p.elem_w = sizeof(O);
-  int buf = 0;
+  int buf = 0, done = 0;
   cudaError_t e = cudaSuccess;
-  const int fill = p.accumulate ? 0 : 4 * 152;
+  // filling CTAs of each launch: four an SM, but no more than there are 16 KB to write
+  const int launches = (plan.radix_tiles ? 2 * plan.passes : 1) + (p.N > 0) + (plan.tiles > 1);
+  const long long most = (long long)p.V * p.D * p.elem_w / (16384LL * launches) + 1;
+  const int fill = p.accumulate ? 0 : (int)(most < 4 * 152 ? most : 4 * 152);
+  const int all = launches * fill;
   if (plan.radix_tiles == 0) {
-    const int sort_ctas = cdiv(p.N, kRankItems);
-    if (sort_ctas + fill > 0)
-      e = launch_pdl(eg_rank_kernel, dim3(sort_ctas + fill), dim3(kEmThreads), align_up((size_t)p.N * 4, 16),
-                     stream, p, sort_ctas, fill);
+    const int ctas = cdiv(p.N, kRankItems);
+    if (ctas + fill > 0)
+      e = launch_pdl(eg_rank_kernel, dim3(ctas + fill), dim3(kEmThreads), align_up((size_t)p.N * 4, 16), stream,
+                     p, Fill{ctas, 0, all});
     if (p.N == 0) return e;
+    done = 1;
   } else {
-    const int launches = 2 * plan.passes;
     for (int i = 0; i < plan.passes && e == cudaSuccess; ++i) {
-      e = launch_pdl(eg_count_kernel, dim3(plan.radix_tiles + fill), dim3(kEmThreads), 0, stream, p, i,
-                     plan.radix_tiles, 2 * i * fill, fill, launches * fill);
+      const dim3 grid(plan.radix_tiles + fill);
+      e = launch_pdl(eg_count_kernel, grid, dim3(kEmThreads), 0, stream, p, i,
+                     Fill{plan.radix_tiles, done++ * fill, all});
       if (e == cudaSuccess)
-        e = launch_pdl(eg_scatter_kernel, dim3(plan.radix_tiles + fill), dim3(kEmThreads), 0, stream, p, i,
-                       plan.radix_tiles, (2 * i + 1) * fill, fill, launches * fill);
+        e = launch_pdl(eg_scatter_kernel, grid, dim3(kEmThreads), 0, stream, p, i,
+                       Fill{plan.radix_tiles, done++ * fill, all});
     }
     buf = (plan.passes - 1) & 1;
   }
   if (e != cudaSuccess) return e;
   const bool vec = rows_aligned(p.d_out, p.ld, sizeof(T)) && rows_aligned(p.dW, p.ld_w, sizeof(O)) &&
                    p.D % Chunk<T>::N == 0;
-  return vec ? launch_eg_sums<T, O, true>(p, buf, stream) : launch_eg_sums<T, O, false>(p, buf, stream);
+  return vec ? launch_eg_sums<T, O, true>(p, buf, fill, done * fill, all, stream)
+             : launch_eg_sums<T, O, false>(p, buf, fill, done * fill, all, stream);
 }
 
 }  // namespace

@@ -25,6 +25,7 @@ namespace {
 constexpr int kLpThreads = 256;
 constexpr int kLpBatch = 4;                 // 16-byte chunks a thread loads at once
 constexpr int kLpCap = 1024;                // candidate keys of a CTA
+constexpr int kLpList = 512;                // slots listed to be read again
 constexpr int kLpTop = kMaxTop;             // most alternatives
 constexpr int kLpMaxSlots = 64;             // batch maxima kept per thread
 
@@ -62,7 +63,8 @@ struct LpShared {
   float gmax[kLpThreads];
   float4 part[kLpThreads / 32];
   float4 stat;                                        // m, s, t, (int) elements before y
-  int n_best, n_cand, before, merged[kLpTop];
+  int n_best, n_cand, n_list, before, merged[kLpTop];
+  int list[kLpList];
   float thr;
 };
 
@@ -173,6 +175,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(LpParams 
   if (lane == 0) sh.part[warp].x = m;
   if (tid == 0) {
     sh.n_cand = 0;
+    sh.n_list = 0;
     sh.before = 0;
     sh.n_best = 0;
     sh.thr = -INFINITY;
@@ -224,21 +227,38 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(LpParams 
   };
   if (K > 0 || a.tokens) {
     if (tid < loose_n) consider(elem_to_float(row[loose]), loose);
-    for (int u = 0; u < used; ++u) {
-      if (slot_max[u * kLpThreads + tid] < reach) continue;
-      const int from = c0 + tid + u * a.per_slot * span;
-      const int to = min(c1, from + a.per_slot * span);
-      for (int i = from; i < to; i += kLpThreads) {
-        float z[N];
-        unpack_chunk<T>(__ldg(body + i), z);
-        float bm = z[0];
+    auto look = [&](int i) {
+      float z[N];
+      unpack_chunk<T>(__ldg(body + i), z);
+      float bm = z[0];
 #pragma unroll
-        for (int e = 1; e < N; ++e) bm = fmaxf(bm, z[e]);
-        if (bm >= reach) {
-          const int v = rc.head + i * N;
+      for (int e = 1; e < N; ++e) bm = fmaxf(bm, z[e]);
+      if (bm >= reach) {
+        const int v = rc.head + i * N;
 #pragma unroll
-          for (int e = 0; e < N; ++e) consider(z[e], v + e);
-        }
+        for (int e = 0; e < N; ++e) consider(z[e], v + e);
+      }
+    };
+    // the slots that reach it, listed, then their chunks dealt over all threads
+    for (int u = 0; u < used; ++u)
+      if (slot_max[u * kLpThreads + tid] >= reach) {
+        const int at = atomicAdd(&sh.n_list, 1);
+        if (at < kLpList) sh.list[at] = u * kLpThreads + tid;
+      }
+    __syncthreads();
+    const int per = a.per_slot * kLpBatch;
+    if (sh.n_list <= kLpList) {
+      const int tasks = sh.n_list * per;
+      for (int k = tid; k < tasks; k += kLpThreads) {
+        const int e = sh.list[k / per], g = k % per;
+        const int i = c0 + (e & (kLpThreads - 1)) + ((e / kLpThreads) * per + g) * kLpThreads;
+        if (i < c1) look(i);
+      }
+    } else {
+      for (int u = 0; u < used; ++u) {
+        if (slot_max[u * kLpThreads + tid] < reach) continue;
+        const int from = c0 + tid + u * per * kLpThreads, to = min(c1, from + per * kLpThreads);
+        for (int i = from; i < to; i += kLpThreads) look(i);
       }
     }
   }
@@ -278,6 +298,10 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(LpParams 
       if (tid == 0) sh.n_best = got;
     }
   }
+  if (C > 1 && K > 0) {
+    __syncthreads();
+    for (int j = sh.n_best + tid; j < K; j += kLpThreads) sh.best[j] = 0ull;
+  }
   if (tid == 0) {
     float S = 0.f, Tm = 0.f;
     for (int w = 0; w < kLpThreads / 32; ++w) {
@@ -293,18 +317,14 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(LpParams 
   int total_before = 0;
   if (C > 1) {
     cluster_sync();
-    for (int o = 0; o < C; ++o) M = fmaxf(M, cluster_ld_f4(cluster_map(&sh.stat, o)).x);
-    S = 0.f;
-    Tm = 0.f;
-    for (int o = 0; o < C; ++o) {
-      const float4 p = cluster_ld_f4(cluster_map(&sh.stat, o));
-      total_before += __float_as_int(p.w);
-      if (p.y != 0.f) {
-        const float d = p.x - M, f = ex2_approx(d * kLog2e);
-        S += p.y * f;
-        if (f > 0.f) Tm += f * (p.z + d * p.y);
-      }
-    }
+    // lane o reads CTA o's statistics
+    const float4 p = lane < C ? cluster_ld_f4(cluster_map(&sh.stat, lane))
+                              : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    M = warp_max(p.x);
+    const float d = p.x - M, f = p.y != 0.f ? ex2_approx(d * kLog2e) : 0.f;
+    S = warp_sum(p.y != 0.f ? p.y * f : 0.f);
+    Tm = warp_sum(f > 0.f ? f * (p.z + d * p.y) : 0.f);
+    total_before = __reduce_add_sync(0xffffffffu, lane < C ? __float_as_int(p.w) : 0);
   } else {
     S = sh.stat.y;
     Tm = sh.stat.z;
@@ -332,14 +352,14 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(LpParams 
     int total = sh.n_best;
     if (C > 1) {
       // every list to this CTA's shared memory (0 beyond a list's end)
-      total = 0;
-      for (int o = 0; o < C; ++o) {
-        int got;
-        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(got) : "r"(cluster_map(&sh.n_best, o)) : "memory");
-        total += got;
-        const uint32_t from = cluster_map(&sh.best[0], o);
-        for (int j = tid; j < K; j += kLpThreads)
-          sh.all[o * kLpTop + j] = j < got ? cluster_ld_u64(from + 8u * j) : 0ull;
+      int got = 0;
+      if (lane < C)
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(got) : "r"(cluster_map(&sh.n_best, lane)) : "memory");
+      total = __reduce_add_sync(0xffffffffu, got);
+      for (int p = tid; p < C * K; p += kLpThreads) {
+        const int o = p / K, j = p - o * K;
+        // (best is 0 from a list's end on)
+        sh.all[o * kLpTop + j] = cluster_ld_u64(cluster_map(&sh.best[0], o) + 8u * j);
       }
       for (int j = tid; j < K; j += kLpThreads) sh.merged[j] = 0;
       __syncthreads();
@@ -476,7 +496,7 @@ __global__ void __launch_bounds__(kLgThreads) token_logprobs_grad_kernel(LgParam
 // SM), but no segment below 2048 chunks (32 KB), under which a CTA's fixed work shows
 int row_ctas(long long rows, long long chunks) {
   int C = 1;
-  while (C < 8 && (rows * C < 16LL * kTargetCtas) && chunks / (2 * C) >= 2048) C *= 2;
+  while (C < 8 && (rows * C < 4LL * kTargetCtas) && chunks / (2 * C) >= 2048) C *= 2;
   // few rows: the latency of a segment counts, down to one batch per thread
   while (C < 8 && rows * C < 152 && chunks / (2 * C) >= kLpThreads) C *= 2;
   return C;
