@@ -13,10 +13,15 @@
 //   dz_v = g w / tau (A q_v - sum_{k : id_k = v} a_k).
 //
 // Bound by one read and one write of the row.  A cluster of CTAs holds a whole row in
-// shared memory (bulk copies, a few pieces deep so that the sums start on the first), so
-// the gradient needs no second read: sums, one exchange through distributed shared memory,
-// gradient from the same shared memory.  Several CTAs an SM overlap one row's reads with
-// another's writes.  Rows beyond a cluster's shared memory read their rest again.
+// shared memory, so the gradient needs no second read of it: sums, one exchange of the
+// warps' sums between the cluster's CTAs, gradient from the same shared memory.  Clusters
+// are persistent, and nothing in a row waits for a whole CTA: a producer warp refills each
+// 16 KB piece of the row's part with the next row's bytes as soon as the eight consumer
+// warps have left it, a teacher warp prepares the next row's entries (ids, softmax, the
+// student's logits at them), and a warp sends its sums to every CTA of the cluster with
+// stores that complete on that CTA's barrier.  An element that the teacher names is written
+// a second time by the warp that wrote it first.  Rows beyond a cluster's shared memory read
+// their rest again.
 #include "internal.h"
 #include "rows.cuh"
 #include "sm100_ptx.cuh"
@@ -26,11 +31,15 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kDsThreads = 256;
-constexpr int kDsPiece = 16 * 1024;                 // bytes of a bulk copy
-constexpr int kDsMaxPieces = 13;
-constexpr int kDsMost = kDsMaxPieces * kDsPiece;    // resident bytes of a CTA (208 KB)
-constexpr int kDsTarget = 72 * 1024;                // three CTAs an SM
+constexpr int kDsWarps = 8;                         // consumer warps
+constexpr int kDsThreads = kDsWarps * 32;           // consumer threads
+constexpr int kDsBlock = kDsThreads + 64;           // and the producer's and the teacher's warp
+constexpr int kDsPiece = 8 * 1024;                  // bytes of a bulk copy
+constexpr int kPieceChunks = kDsPiece / 16;
+constexpr int kRing = 13;                           // pieces of a CTA: 104 KB, two CTAs an SM
+constexpr int kDsTarget = 80 * 1024;                // most of them one row's, the rest the next's
+constexpr int kSumsLane = 8 * kDsWarps / 32;        // warps' sums a lane reads
+constexpr int kPer = kMaxTop / 32;                  // entries of a lane
 
 struct DsParams {
   const void* z;
@@ -40,8 +49,8 @@ struct DsParams {
   const int32_t* labels;     // [N] or null
   const float* weights;      // [N] or null
   const float* d_loss;       // [N] or null
-  int V, K;
-  int resident;              // 16-byte chunks of a CTA kept in shared memory
+  int N, V, K;
+  int resident;              // 16-byte chunks of a row's part kept in shared memory
   float inv_tau, c_kl, c_tv, c_ce;
   float* loss;
   float* accept;
@@ -50,15 +59,17 @@ struct DsParams {
   int* err;
 };
 
+struct Teacher {
+  int id[kMaxTop];           // -1: no entry, or none with weight
+  float p[kMaxTop], log_p[kMaxTop], z[kMaxTop];
+  float sum_p, zy;
+  int y, any, twice, y_named;   // twice: an id occurs more than once; y_named: y among the ids
+};
+
 struct DsShared {
-  float4 part[kDsThreads / 32];
-  float4 stat;
-  int id[kMaxTop + 4];
-  float a[kMaxTop + 4];
-  float q[kMaxTop + 4];
-  float scale;               // A g w / (tau s)
-  float sum_a, gw;
-  uint64_t bar[kDsMaxPieces];
+  float2 sums[2][8 * kDsWarps];          // (max, sum) of every consumer warp of the cluster
+  Teacher teacher[2];
+  uint64_t full[kRing], empty[kRing], sums_full[2], teacher_full[2], teacher_free[2];
 };
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -68,297 +79,463 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       "l"(src), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
 }
+// two fp32 into CTA `rank`'s copy of *dst, counted as 8 bytes by its copy of *bar
+__device__ __forceinline__ void send_f2(float2* dst, uint64_t* bar, uint32_t rank, float x, float y) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
+                   cluster_map(dst, rank)),
+               "f"(x), "f"(y), "r"(cluster_map(bar, rank))
+               : "memory");
+}
+// a wait on data that other CTAs of the cluster send
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity) {
+  const long long t0 = sm_cycles();
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(10000000u)
+        : "memory");
+    if (ok) return true;
+    if (sm_cycles() - t0 > kWaitCycles) return false;
+  }
+}
+
+template <typename T>
+struct RowPart {             // a CTA's part of a row
+  const T* row;
+  const uint4* body;
+  RowChunks rc;
+  int c0, c1, held;
+};
+template <typename T>
+__device__ __forceinline__ RowPart<T> row_part(const DsParams& a, int n, int c, int C) {
+  RowPart<T> r;
+  r.row = static_cast<const T*>(a.z) + (long long)n * a.ld;
+  r.rc = row_chunks(r.row, a.V);
+  r.body = reinterpret_cast<const uint4*>(r.row + r.rc.head);
+  r.c0 = (int)((long long)r.rc.chunks * c / C);
+  r.c1 = (int)((long long)r.rc.chunks * (c + 1) / C);
+  r.held = min(r.c1 - r.c0, a.resident);
+  return r;
+}
+
+// The teacher's entries of row n and its label into `te`, by one warp.
+template <typename T>
+__device__ __forceinline__ void read_teacher(const DsParams& a, int n, const T* row, Teacher& te) {
+  const int lane = threadIdx.x & 31, K = a.K, V = a.V;
+  int id[kPer];
+  float t[kPer], p[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int k = lane + 32 * i;
+    id[i] = k < K ? a.ids[(size_t)n * K + k] : -1;
+    t[i] = k < K ? a.t[(size_t)n * K + k] * a.inv_tau : -INFINITY;
+  }
+  int y = a.labels ? a.labels[n] : -1;
+  if (y < -1 || y >= V) {
+    if (lane == 0) set_device_error(a.err, DSPARK_ERR_DEVICE_CHECK);
+    y = -1;
+  }
+  float tm = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (id[i] < -1 || id[i] >= V) {
+      set_device_error(a.err, DSPARK_ERR_DEVICE_CHECK);
+      id[i] = -1;
+    }
+    if (id[i] < 0) t[i] = -INFINITY;
+    tm = fmaxf(tm, t[i]);
+  }
+  const float zy = y >= 0 ? elem_to_float(row[y]) : 0.f;
+  float z[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) z[i] = id[i] >= 0 ? elem_to_float(row[id[i]]) : 0.f;
+  tm = warp_max(tm);
+  const bool any = tm > -INFINITY;
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (!any) id[i] = -1;                    // entries without weight are like any element
+    p[i] = id[i] >= 0 ? expf(t[i] - tm) : 0.f;
+    sum += p[i];
+  }
+  sum = warp_sum(sum);
+  const float log_sum = logf(sum);
+  float sum_p = 0.f;
+  bool y_named = false;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int k = lane + 32 * i;
+    if (id[i] >= 0) p[i] /= sum;
+    sum_p += p[i];
+    y_named |= id[i] >= 0 && id[i] == y;
+    if (k < K) {
+      te.id[k] = id[i];
+      te.p[k] = p[i];
+      te.log_p[k] = t[i] - tm - log_sum;
+      te.z[k] = z[i];
+    }
+  }
+  sum_p = warp_sum(sum_p);
+  __syncwarp();
+  bool twice = false;
+  for (int j = 0; j < K; ++j) {
+    const int o = te.id[j];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) twice |= o >= 0 && id[i] == o && lane + 32 * i != j;
+  }
+  twice = __any_sync(0xffffffffu, twice);
+  y_named = __any_sync(0xffffffffu, y_named);
+  if (lane == 0) {
+    te.sum_p = sum_p;
+    te.zy = zy;
+    te.y = y;
+    te.any = any;
+    te.twice = twice;
+    te.y_named = y_named;
+  }
+  __syncwarp();
+}
 
 template <typename T, bool Grad>
-__global__ void __launch_bounds__(kDsThreads, 4) distill_kernel(DsParams a, int C) {
+__global__ void __launch_bounds__(kDsBlock, 2) distill_kernel(DsParams a, int C) {
   constexpr int N = Chunk<T>::N;
   extern __shared__ __align__(128) uint4 rows_s[];
   __shared__ DsShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int n = (int)(blockIdx.x / C);
-  const int c = (int)(blockIdx.x - (unsigned)n * C);
+  const int c = (int)(blockIdx.x % C), first = (int)(blockIdx.x / C), step = (int)(gridDim.x / C);
   const int V = a.V, K = a.K;
-  const T* row = static_cast<const T*>(a.z) + (long long)n * a.ld;
-  T* out = Grad ? static_cast<T*>(a.dz) + (long long)n * a.ld_dz : nullptr;
+  const int pieces = (a.resident + kPieceChunks - 1) / kPieceChunks;
+  if (tid == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], kDsWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.sums_full[i], 1);
+      mbar_init(&sh.teacher_full[i], 1);
+      mbar_init(&sh.teacher_free[i], kDsWarps);
+    }
+    fence_mbar_init();
+  }
+  if (C > 1) cluster_sync();
+  else __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
+  bool late = false;                         // a bounded wait ran out: give up
 
-  auto zero_out = [&] {
-    if constexpr (Grad) {
-      const RowChunks oc = row_chunks(out, V);
-      uint4* o4 = reinterpret_cast<uint4*>(out + oc.head);
-      const int e0 = (int)((long long)oc.chunks * c / C), e1 = (int)((long long)oc.chunks * (c + 1) / C);
-      for (int i = e0 + tid; i < e1; i += kDsThreads) __stcs(o4 + i, make_uint4(0u, 0u, 0u, 0u));
-      if (c == 0 && tid < oc.head + oc.tail)
-        out[tid < oc.head ? tid : V - oc.tail + (tid - oc.head)] = elem_from_float<T>(0.f);
-    }
-  };
-  const float w = a.weights ? a.weights[n] : 1.f;
-  if (w == 0.f) {                            // a masked row: nothing of it is read
-    zero_out();
-    if (c == 0 && tid == 0) {
-      a.loss[n] = 0.f;
-      a.accept[n] = 0.f;
-    }
-    return;
-  }
-
-  const RowChunks rc = row_chunks(row, V);
-  const uint4* body = reinterpret_cast<const uint4*>(row + rc.head);
-  const int c0 = (int)((long long)rc.chunks * c / C), c1 = (int)((long long)rc.chunks * (c + 1) / C);
-  const int held = min(c1 - c0, a.resident);
-  constexpr int kPieceChunks = kDsPiece / 16;
-  const int pieces = (held + kPieceChunks - 1) / kPieceChunks;
-  if (tid == 0) {
-    for (int i = 0; i < pieces; ++i) mbar_init(&sh.bar[i], 1);
-    fence_mbar_init();
-    for (int i = 0; i < pieces; ++i) {
-      const int k = min(kPieceChunks, held - i * kPieceChunks);
-      mbar_arrive_expect_tx(&sh.bar[i], (uint32_t)k * 16u);
-      bulk_load(rows_s + i * kPieceChunks, body + c0 + i * kPieceChunks, (uint32_t)k * 16u, &sh.bar[i]);
-    }
-  }
-  __syncthreads();
-
-  // ---- the teacher's entries (warp 0, up to 4 a lane) and the label, read before any CTA
-  // can write the gradient over the row
-  constexpr int kPer = kMaxTop / 32;
-  int id[kPer], y = -1;
-  float tt[kPer], pk[kPer], zk[kPer], zy = 0.f;
-  bool any = false;
-  if (warp == 0) {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int k = lane + 32 * i;
-      id[i] = k < K ? a.ids[(size_t)n * K + k] : -1;
-      if (id[i] < -1 || id[i] >= V) {
-        set_device_error(a.err, DSPARK_ERR_DEVICE_CHECK);
-        id[i] = -1;
-      }
-      tt[i] = id[i] >= 0 ? a.t[(size_t)n * K + k] * a.inv_tau : -INFINITY;
-      zk[i] = id[i] >= 0 ? elem_to_float(row[id[i]]) : 0.f;
-    }
-    if (a.labels) {
-      y = a.labels[n];
-      if (y < -1 || y >= V) {
-        if (lane == 0) set_device_error(a.err, DSPARK_ERR_DEVICE_CHECK);
-        y = -1;
-      }
-      if (y >= 0) zy = elem_to_float(row[y]);
-    }
-    // the teacher's softmax, while the row arrives: tt becomes log p
-    float tm = -INFINITY, ps = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) tm = fmaxf(tm, tt[i]);
-    tm = warp_max(tm);
-    any = tm > -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      pk[i] = id[i] >= 0 && any ? expf(tt[i] - tm) : 0.f;
-      ps += pk[i];
-    }
-    ps = warp_sum(ps);
-    const float log_ps = logf(ps);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      pk[i] = any ? pk[i] / ps : 0.f;
-      tt[i] = tt[i] - tm - log_ps;
-    }
-  }
-
-  // ---- sums
-  RunningSoftmax<false> rs;
-  rs.init(a.inv_tau);
-  float tmax = -INFINITY;
-  const int loose_n = c == 0 ? rc.head + rc.tail : 0;
-  const int loose = tid < rc.head ? tid : V - rc.tail + (tid - rc.head);
-  float zl = 0.f;
-  if (tid < loose_n) {
-    zl = elem_to_float(row[loose]);
-    rs.add_one(zl);
-    tmax = fmaxf(tmax, zl);
-  }
-  auto take = [&](const uint4& q) {
-    float z[N];
-    unpack_chunk<T>(q, z);
-    float bm = z[0];
-#pragma unroll
-    for (int i = 1; i < N; ++i) bm = fmaxf(bm, z[i]);
-    tmax = fmaxf(tmax, bm);
-    rs.template add<N>(z, bm);
-  };
-  bool late = false;
-  for (int i = 0; i < pieces; ++i) {
-    if (!late && !mbar_wait(&sh.bar[i], 0)) late = true;
-    const int end = min(held, (i + 1) * kPieceChunks);
-    for (int j = i * kPieceChunks + tid; j < end; j += kDsThreads) take(rows_s[j]);
-  }
-  for (int j = c0 + held + tid; j < c1; j += kDsThreads) take(body[j]);
-  float m = warp_max(tmax);
-  if (lane == 0) sh.part[warp].x = m;
-  __syncthreads();
-  m = sh.part[0].x;
-#pragma unroll
-  for (int i = 1; i < kDsThreads / 32; ++i) m = fmaxf(m, sh.part[i].x);
-  float s, unused;
-  rs.finish(m, s, unused);
-  if (late) {                                // a copy that never arrived: the row becomes NaN
-    set_device_error(a.err, DSPARK_ERR_TIMEOUT);
-    s = __int_as_float(0x7FC00000);
-  }
-  s = warp_sum(s);
-  if (lane == 0) sh.part[warp].y = s;
-  __syncthreads();
-  if (tid == 0) {
-    float S = 0.f;
-    for (int i = 0; i < kDsThreads / 32; ++i) S += sh.part[i].y;
-    sh.stat = make_float4(m, S, 0.f, 0.f);
-  }
-  __syncthreads();
-  float M = m, S;
-  if (C > 1) {
-    cluster_sync();                          // also: every CTA has read its teacher entries
-    // lane o reads CTA o's sums
-    const float4 p = lane < C ? cluster_ld_f4(cluster_map(&sh.stat, lane))
-                              : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-    M = warp_max(p.x);
-    S = warp_sum(p.y != 0.f ? p.y * ex2_approx((p.x - M) * (a.inv_tau * kLog2e)) : 0.f);
-  } else {
-    S = sh.stat.y;
-  }
-
-  // ---- loss, acceptance and the entries' coefficients
-  if (warp == 0) {
-    const float logs = logf(S);
-    float kl = 0.f, tv = 0.f, acc = 0.f, sum_a = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      float ak = 0.f, q = 0.f;
-      if (id[i] >= 0) {
-        const float lq = (zk[i] - M) * a.inv_tau - logs;
-        q = expf(lq);
-        if (any) {
-          const float p = pk[i];
-          if (p != 0.f) kl += p * (tt[i] - lq);
-          tv += fmaxf(p - q, 0.f);
-          acc += fminf(p, q);
-          // products with a zero coefficient are left out: 0 * inf
-          if (a.c_kl != 0.f) ak = a.c_kl * p;
-          if (q < p) ak += a.c_tv * q;
+  if (warp == kDsWarps) {
+    // ---- producer: a row's part piece by piece, each as soon as its last reader is gone
+    if (lane == 0) {
+      int sent = 0;                          // pieces so far; slot sent % kRing
+      for (int n = first; n < a.N && !late; n += step) {
+        if (a.weights && a.weights[n] == 0.f) continue;
+        const RowPart<T> r = row_part<T>(a, n, c, C);
+        for (int i = 0; i < pieces; ++i, ++sent) {
+          const int slot = sent % kRing, use = sent / kRing;
+          if (use > 0 && !mbar_wait(&sh.empty[slot], (use - 1) & 1)) { late = true; break; }
+          const int k = max(0, min(kPieceChunks, r.held - i * kPieceChunks));
+          mbar_arrive_expect_tx(&sh.full[slot], (uint32_t)k * 16u);
+          if (k > 0)
+            bulk_load(rows_s + slot * kPieceChunks, r.body + r.c0 + i * kPieceChunks, (uint32_t)k * 16u,
+                      &sh.full[slot]);
         }
       }
-      sum_a += ak;
-      const int k = lane + 32 * i;
-      if (k < K) {
-        sh.id[k] = any ? id[i] : -1;         // entries without weight are like any element
-        sh.a[k] = ak;
-        sh.q[k] = q;
-      }
+      // copies in flight end before the CTA does (at once, unless the consumers gave up)
+      for (int j = max(0, sent - kRing); j < sent; ++j) mbar_wait(&sh.full[j % kRing], (j / kRing) & 1);
     }
-    kl = warp_sum(kl);
-    tv = warp_sum(tv);
-    acc = warp_sum(acc);
-    sum_a = warp_sum(sum_a);
-    if (lane == 0) {
-      const float lqy = (zy - M) * a.inv_tau - logs;
-      const float ay = y >= 0 ? a.c_ce : 0.f;
-      sh.id[K] = y;
-      sh.a[K] = ay;
-      sh.q[K] = y >= 0 ? expf(lqy) : 0.f;
-      const bool on = any || y >= 0;
+  } else if (warp == kDsWarps + 1) {
+    // ---- teacher: the entries of the next rows
+    int it = 0;
+    for (int n = first; n < a.N && !late; n += step) {
+      if (a.weights && a.weights[n] == 0.f) continue;
+      const int b = it & 1;
+      if (it >= 2 && !mbar_wait(&sh.teacher_free[b], ((it >> 1) - 1) & 1)) { late = true; break; }
+      read_teacher(a, n, static_cast<const T*>(a.z) + (long long)n * a.ld, sh.teacher[b]);
+      if (lane == 0) mbar_arrive(&sh.teacher_full[b]);
+      ++it;
+    }
+  } else {
+    int it = 0;
+    int slot0 = 0;                           // the row's first piece
+    uint32_t phase0 = 0;
+    float w_next = first < a.N && a.weights ? a.weights[first] : 1.f;
+    for (int n = first; n < a.N; n += step) {
+      const float w = w_next;
+      if (n + step < a.N && a.weights) w_next = a.weights[n + step];
+      T* out = Grad ? static_cast<T*>(a.dz) + (long long)n * a.ld_dz : nullptr;
+      auto zero_out = [&] {
+        if constexpr (Grad) {
+          const RowChunks oc = row_chunks(out, V);
+          uint4* o4 = reinterpret_cast<uint4*>(out + oc.head);
+          const int e0 = (int)((long long)oc.chunks * c / C), e1 = (int)((long long)oc.chunks * (c + 1) / C);
+          for (int i = e0 + tid; i < e1; i += kDsThreads) __stcs(o4 + i, make_uint4(0u, 0u, 0u, 0u));
+          if (c == 0 && tid < oc.head + oc.tail)
+            out[tid < oc.head ? tid : V - oc.tail + (tid - oc.head)] = elem_from_float<T>(0.f);
+        }
+      };
+      if (w == 0.f) {                        // a masked row: nothing of it is read
+        zero_out();
+        if (c == 0 && tid == 0) {
+          a.loss[n] = 0.f;
+          a.accept[n] = 0.f;
+        }
+        continue;
+      }
+      const int b = it & 1;
+      const uint32_t buf_phase = (it >> 1) & 1;
+      if (tid == 0) mbar_arrive_expect_tx(&sh.sums_full[b], (uint32_t)(C * kDsWarps * 8));
+      const RowPart<T> r = row_part<T>(a, n, c, C);
       const float g = a.d_loss ? a.d_loss[n] : 1.f;
-      sum_a += ay;
-      sh.sum_a = sum_a;
-      sh.gw = g * w * a.inv_tau;
-      sh.scale = on && sum_a * sh.gw != 0.f ? sum_a * sh.gw / S : 0.f;
-      if (c == 0) {
-        float l = 0.f;
-        if (any && a.c_kl != 0.f) l += a.c_kl * kl;
-        if (any && a.c_tv != 0.f) l += a.c_tv * tv;
-        if (y >= 0 && a.c_ce != 0.f) l -= a.c_ce * lqy;
-        a.loss[n] = on ? l * w : 0.f;
-        a.accept[n] = any ? acc : 0.f;
+
+      // ---- sums
+      RunningSoftmax<false> rs;
+      rs.init(a.inv_tau);
+      float tmax = -INFINITY;
+      const int loose_n = c == 0 ? r.rc.head + r.rc.tail : 0;
+      const int loose = tid < r.rc.head ? tid : V - r.rc.tail + (tid - r.rc.head);
+      float zl = 0.f;
+      if (tid < loose_n) {
+        zl = elem_to_float(r.row[loose]);
+        rs.add_one(zl);
+        tmax = fmaxf(tmax, zl);
       }
-    }
-  }
-  if constexpr (Grad) {
-    __syncthreads();
-    const float scale = sh.scale;
-    // the entries' own elements: sum over equal ids in entry order (the same in every
-    // thread that holds one of them, so that two writes of an element agree)
-    int fix_at = -1;
-    float fix = 0.f;
-    if (tid <= K) {
-      const int v = sh.id[tid];
-      if (v >= 0) {
-        float av = 0.f;
-        for (int j = 0; j <= K; ++j)
-          if (sh.id[j] == v) av += sh.a[j];
-        fix_at = v;
-        fix = sh.gw * (sh.sum_a * sh.q[tid] - av);
-      }
-    }
-    if (scale == 0.f) {
-      zero_out();
-    } else {
-      const F2 nM = f2(-M, -M), kk = f2(a.inv_tau * kLog2e, a.inv_tau * kLog2e), sc = f2(scale, scale);
-      auto grad = [&](const uint4& q) {
+      constexpr int G = 2;                   // chunks at once
+      auto take = [&](const uint4 (&q)[G]) {
+        float z[G * N];
+#pragma unroll
+        for (int u = 0; u < G; ++u) {
+          float x[N];
+          unpack_chunk<T>(q[u], x);
+#pragma unroll
+          for (int e = 0; e < N; ++e) z[u * N + e] = x[e];
+        }
+        float bm = fmaxf(z[0], z[1]);
+#pragma unroll
+        for (int e = 2; e < G * N; ++e) bm = fmaxf(bm, z[e]);
+        tmax = fmaxf(tmax, bm);
+        rs.template add<G * N>(z, bm);
+      };
+      auto take_one = [&](const uint4& q) {
         float z[N];
         unpack_chunk<T>(q, z);
+        float bm = z[0];
 #pragma unroll
-        for (int i = 0; i < N; i += 2) {
-          float x, yv;
-          f2_get(f2_mul(f2_add(f2(z[i], z[i + 1]), nM), kk), x, yv);
-          f2_get(f2_mul(f2(ex2_approx(x), ex2_approx(yv)), sc), z[i], z[i + 1]);
-        }
-        return pack_chunk<T>(z);
+        for (int e = 1; e < N; ++e) bm = fmaxf(bm, z[e]);
+        tmax = fmaxf(tmax, bm);
+        rs.template add<N>(z, bm);
       };
-      const bool same = ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
-      if (same) {
-        uint4* o4 = reinterpret_cast<uint4*>(out + rc.head);
-        for (int j = tid; j < held; j += kDsThreads) __stcs(o4 + c0 + j, grad(rows_s[j]));
-        for (int j = c0 + held + tid; j < c1; j += kDsThreads) __stcs(o4 + j, grad(body[j]));
-      } else {                               // output rows off the input rows' 16-byte grid
-        T* o = out + rc.head;
-        for (int j = c0 + tid; j < c1; j += kDsThreads) {
-          const uint4 g = grad(j < c0 + held ? rows_s[j - c0] : body[j]);
-          const T* ge = reinterpret_cast<const T*>(&g);
+      int slot = slot0;
+      uint32_t phase = phase0;
+      auto next_piece = [&] {
+        if (++slot == kRing) {
+          slot = 0;
+          phase ^= 1;
+        }
+      };
+      for (int i = 0; i < pieces; ++i, next_piece()) {
+        if (!late && !mbar_wait(&sh.full[slot], phase)) late = true;
+        const int end = min(kPieceChunks, r.held - i * kPieceChunks);
+        const uint4* piece = rows_s + slot * kPieceChunks;
+        int j = tid;
+        for (; j + (G - 1) * kDsThreads < end; j += G * kDsThreads) {
+          uint4 q[G];
 #pragma unroll
-          for (int e = 0; e < N; ++e) o[(long long)j * N + e] = ge[e];
+          for (int u = 0; u < G; ++u) q[u] = piece[j + u * kDsThreads];
+          take(q);
+        }
+        for (; j < end; j += kDsThreads) take_one(piece[j]);
+        if constexpr (!Grad) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.empty[slot]);
         }
       }
-      if (tid < loose_n)
-        out[loose] = elem_from_float<T>(ex2_approx((zl - M) * (a.inv_tau * kLog2e)) * scale);
-    }
-    if (scale != 0.f) {
-      __syncthreads();                       // the entries' elements after the row's
-      const bool loose_at = fix_at >= 0 && (fix_at < rc.head || fix_at >= V - rc.tail);
-      const int at = fix_at >= 0 && !loose_at ? (fix_at - rc.head) / N : -1;
-      // an element of another CTA's part is that CTA's to write
-      if (fix_at >= 0 && (loose_at ? c == 0 : at >= c0 && at < c1)) out[fix_at] = elem_from_float<T>(fix);
+      for (int j = r.c0 + r.held + tid; j < r.c1; j += kDsThreads) take_one(r.body[j]);
+      const float wm = warp_max(tmax);
+      float s, unused;
+      rs.finish(wm, s, unused);
+      s = warp_sum(s);
+      // the teacher's entries are read (from the row, too) before any CTA can write it
+      Teacher& te = sh.teacher[b];
+      if (!late && !mbar_wait(&sh.teacher_full[b], buf_phase)) late = true;
+      if (lane < C) send_f2(&sh.sums[b][c * kDsWarps + warp], &sh.sums_full[b], lane, wm, s);
+      if (!late && !wait_cluster(&sh.sums_full[b], buf_phase)) late = true;
+      late = __any_sync(0xffffffffu, late);
+      if (late) break;
+      float2 part[kSumsLane];
+      float M = -INFINITY, S = 0.f;
+#pragma unroll
+      for (int i = 0; i < kSumsLane; ++i) {
+        part[i] = lane + 32 * i < C * kDsWarps ? sh.sums[b][lane + 32 * i] : make_float2(-INFINITY, 0.f);
+        M = fmaxf(M, part[i].x);
+      }
+      M = warp_max(M);
+      const float kl2 = a.inv_tau * kLog2e;
+#pragma unroll
+      for (int i = 0; i < kSumsLane; ++i)
+        if (part[i].y != 0.f) S += part[i].y * ex2_approx((part[i].x - M) * kl2);
+      S = warp_sum(S);
+      const float logs = logf(S);
+      auto log_q = [&](float z) { return (z - M) * a.inv_tau - logs; };
+      // a_k of an entry; products with a zero coefficient are left out (0 * inf)
+      auto coef = [&](float p, float q) {
+        float x = a.c_kl != 0.f ? a.c_kl * p : 0.f;
+        if (q < p) x += a.c_tv * q;
+        return x;
+      };
+      const int y = te.y;
+      const bool any = te.any, on = any || y >= 0;
+      const float ay = y >= 0 ? a.c_ce : 0.f;
+
+      if constexpr (Grad) {
+        float sum_a = (any && a.c_kl != 0.f ? a.c_kl * te.sum_p : 0.f) + ay;
+        if (a.c_tv != 0.f && any) {
+          float tv = 0.f;
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            const int k = lane + 32 * i;
+            if (k < K && te.id[k] >= 0) {
+              const float q = expf(log_q(te.z[k]));
+              if (q < te.p[k]) tv += q;
+            }
+          }
+          sum_a += a.c_tv * warp_sum(tv);
+        }
+        const float gw = g * w * a.inv_tau;
+        const float scale = on && sum_a * gw != 0.f ? sum_a * gw / S : 0.f;
+        if (scale == 0.f) {
+          zero_out();
+          __syncwarp();
+          slot = slot0;
+          for (int i = 0; i < pieces; ++i, next_piece())
+            if (lane == 0) mbar_arrive(&sh.empty[slot]);
+        } else {
+          const F2 nM = f2(-M, -M), kk = f2(kl2, kl2), sc = f2(scale, scale);
+          auto grad = [&](const uint4& q) {
+            float z[N];
+            unpack_chunk<T>(q, z);
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+              float x, yv;
+              f2_get(f2_mul(f2_add(f2(z[i], z[i + 1]), nM), kk), x, yv);
+              f2_get(f2_mul(f2(ex2_approx(x), ex2_approx(yv)), sc), z[i], z[i + 1]);
+            }
+            return pack_chunk<T>(z);
+          };
+          const bool same = ((reinterpret_cast<uintptr_t>(r.row) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
+          T* o = out + r.rc.head;
+          auto put = [&](int j, const uint4& q) {
+            const uint4 v = grad(q);
+            if (same) {
+              __stcs(reinterpret_cast<uint4*>(o) + j, v);
+            } else {                         // output rows off the input rows' 16-byte grid
+              const T* ve = reinterpret_cast<const T*>(&v);
+#pragma unroll
+              for (int e = 0; e < N; ++e) o[(long long)j * N + e] = ve[e];
+            }
+          };
+          slot = slot0;
+          for (int i = 0; i < pieces; ++i, next_piece()) {
+            const int end = min(kPieceChunks, r.held - i * kPieceChunks);
+            const uint4* piece = rows_s + slot * kPieceChunks;
+#pragma unroll
+            for (int u = 0; u < kPieceChunks / kDsThreads; ++u) {
+              const int j = u * kDsThreads + tid;
+              if (j < end) put(r.c0 + i * kPieceChunks + j, piece[j]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.empty[slot]);
+          }
+          for (int j = r.c0 + r.held + tid; j < r.c1; j += kDsThreads) put(j, r.body[j]);
+          if (tid < loose_n) out[loose] = elem_from_float<T>(ex2_approx((zl - M) * kl2) * scale);
+          // the teacher's elements and the label's, after the row's, by the warp that holds
+          // them: dz = g w / tau (A q - sum of a over the entries with this id)
+          __syncwarp();
+          auto mine = [&](int v) {
+            if (v < r.rc.head || v >= V - r.rc.tail) return c == 0 && warp == 0;
+            const int at = (v - r.rc.head) / N;
+            return at >= r.c0 && at < r.c1 && (((at - r.c0) & (kDsThreads - 1)) >> 5) == warp;
+          };
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            const int k = lane + 32 * i;
+            const int v = k < K ? te.id[k] : -1;
+            if (v < 0 || !mine(v)) continue;
+            const float q = expf(log_q(te.z[k]));
+            float av = v == y ? ay : 0.f;
+            if (te.twice) {                  // in entry order, so that equal ids write the same
+              for (int j = 0; j < K; ++j)
+                if (te.id[j] == v) av += coef(te.p[j], q);
+            } else {
+              av += coef(te.p[k], q);
+            }
+            out[v] = elem_from_float<T>(gw * (sum_a * q - av));
+          }
+          if (lane == 0 && y >= 0 && !te.y_named && mine(y))
+            out[y] = elem_from_float<T>(gw * (sum_a * expf(log_q(te.zy)) - ay));
+        }
+      }
+      // ---- loss and acceptance, by the last warp of one CTA
+      if (warp == kDsWarps - 1 && it % C == c) {
+        float kl = 0.f, tv = 0.f, acc = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int k = lane + 32 * i;
+          if (k < K && te.id[k] >= 0) {
+            const float lq = log_q(te.z[k]), q = expf(lq), p = te.p[k];
+            if (p != 0.f) kl += p * (te.log_p[k] - lq);
+            tv += fmaxf(p - q, 0.f);
+            acc += fminf(p, q);
+          }
+        }
+        kl = warp_sum(kl);
+        tv = warp_sum(tv);
+        acc = warp_sum(acc);
+        if (lane == 0) {
+          float l = 0.f;
+          if (any && a.c_kl != 0.f) l += a.c_kl * kl;
+          if (any && a.c_tv != 0.f) l += a.c_tv * tv;
+          if (y >= 0 && a.c_ce != 0.f) l -= a.c_ce * log_q(te.zy);
+          a.loss[n] = on ? l * w : 0.f;
+          a.accept[n] = any ? acc : 0.f;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.teacher_free[b]);
+      slot0 += pieces;
+      if (slot0 >= kRing) {
+        slot0 -= kRing;
+        phase0 ^= 1;
+      }
+      ++it;
     }
   }
-  if (C > 1) cluster_sync();                 // no CTA leaves while another reads its sums
+  if (late) set_device_error(a.err, DSPARK_ERR_TIMEOUT);
+  __syncwarp();
+  if (C > 1) cluster_sync();                 // no CTA leaves while another may still send to it
 }
 
 template <typename T, bool Grad>
-cudaError_t launch(DsParams p, int N, cudaStream_t stream) {
+cudaError_t launch(DsParams p, cudaStream_t stream) {
   const int chunks = p.V / Chunk<T>::N;
   int C = 1;
-  // the row's part of a CTA small enough for three CTAs an SM; more CTAs a row while there
-  // are fewer than two an SM, as long as each has 8 KB
+  // the row's part of a CTA small enough that some of the ring is left for the next row's;
+  // more CTAs a row while there are fewer than two an SM, as long as each has 8 KB
   while (C < 8 && (long long)cdiv(chunks, C) * 16 > kDsTarget) C *= 2;
-  while (C < 8 && (long long)N * C < 304 && chunks / (2 * C) >= 512) C *= 2;
+  while (C < 8 && (long long)p.N * C < 304 && chunks / (2 * C) >= 512) C *= 2;
   const int part = cdiv(chunks, C) + 1;
-  p.resident = part * 16LL <= kDsMost ? part : kDsMost / 16;
-  const size_t smem = (size_t)p.resident * 16;
-  static std::atomic<int> cache[kMaxCachedDevices];
-  const int ok = per_device_grid(cache, [] {
-    return cudaFuncSetAttribute(distill_kernel<T, Grad>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kDsMost) == cudaSuccess ? 1 : -1;
-  });
-  if (ok <= 0) return cudaErrorInvalidConfiguration;
-  return launch_rows_cluster(distill_kernel<T, Grad>, (long long)N * C, C, kDsThreads, smem, stream, p, C);
+  p.resident = part < kRing * kPieceChunks ? part : kRing * kPieceChunks;
+  const size_t smem = (size_t)kRing * kDsPiece;
+  // clusters that the device holds at once: more would wait for these to end
+  static std::atomic<int> cache[4][kMaxCachedDevices];
+  const int most = device_clusters(cache[C == 1 ? 0 : C == 2 ? 1 : C == 4 ? 2 : 3], distill_kernel<T, Grad>, C,
+                                   kDsBlock, smem);
+  if (most <= 0) return cudaErrorInvalidConfiguration;
+  const long long clusters = p.N < most ? p.N : most;
+  return launch_rows_cluster(distill_kernel<T, Grad>, clusters * C, C, kDsBlock, smem, stream, p, C);
 }
 
 }  // namespace
@@ -369,13 +546,13 @@ cudaError_t launch_distill(const void* z, int dtype, long long ld, const int32_t
                            float* accept, void* dz, long long ld_dz, int* err, cudaStream_t stream) {
   DsParams p = {};
   p.z = z; p.ld = ld; p.ids = ids; p.t = t; p.labels = labels; p.weights = weights; p.d_loss = d_loss;
-  p.V = V; p.K = K; p.inv_tau = inv_tau; p.c_kl = c_kl; p.c_tv = c_tv; p.c_ce = c_ce;
+  p.N = N; p.V = V; p.K = K; p.inv_tau = inv_tau; p.c_kl = c_kl; p.c_tv = c_tv; p.c_ce = c_ce;
   p.loss = loss; p.accept = accept; p.dz = dz; p.ld_dz = ld_dz; p.err = err;
   switch (dtype) {
-    case DSPARK_F32: return dz ? launch<float, true>(p, N, stream) : launch<float, false>(p, N, stream);
+    case DSPARK_F32: return dz ? launch<float, true>(p, stream) : launch<float, false>(p, stream);
     case DSPARK_BF16:
-      return dz ? launch<__nv_bfloat16, true>(p, N, stream) : launch<__nv_bfloat16, false>(p, N, stream);
-    default: return dz ? launch<__half, true>(p, N, stream) : launch<__half, false>(p, N, stream);
+      return dz ? launch<__nv_bfloat16, true>(p, stream) : launch<__nv_bfloat16, false>(p, stream);
+    default: return dz ? launch<__half, true>(p, stream) : launch<__half, false>(p, stream);
   }
 }
 

@@ -120,6 +120,34 @@ inline int per_device_grid(std::atomic<int> (&cache)[kMaxCachedDevices], F&& set
   return sms * per;
 }
 
+// Clusters of C CTAs of a kernel that the current device holds at once (0: failure), with
+// the kernel's shared-memory attribute set; cached per device.
+template <typename... KArgs>
+inline int device_clusters(std::atomic<int> (&cache)[kMaxCachedDevices], void (*kernel)(KArgs...), int C,
+                           int threads, size_t smem) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxCachedDevices) return 0;
+  const int v = cache[dev].load(std::memory_order_acquire);
+  if (v != 0) return v;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)C);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) return 0;
+  cache[dev].store(n, std::memory_order_release);
+  return n;
+}
+
 template <typename T>
 inline T* ws_at(void* ws, size_t off) {
   return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
