@@ -34,10 +34,11 @@ using namespace sm100;
 constexpr int kDsWarps = 8;                         // consumer warps
 constexpr int kDsThreads = kDsWarps * 32;           // consumer threads
 constexpr int kDsBlock = kDsThreads + 64;           // and the producer's and the teacher's warp
-constexpr int kDsPiece = 8 * 1024;                  // bytes of a bulk copy
+constexpr int kDsPiece = 16 * 1024;                 // bytes of a bulk copy
 constexpr int kPieceChunks = kDsPiece / 16;
-constexpr int kRing = 13;                           // pieces of a CTA: 104 KB, two CTAs an SM
+constexpr int kRing = 6;                            // pieces of a CTA: 96 KB, two CTAs an SM
 constexpr int kDsTarget = 80 * 1024;                // most of them one row's, the rest the next's
+constexpr int kShare = kPieceChunks / kDsThreads;   // chunks of a piece for a consumer thread
 constexpr int kSumsLane = 8 * kDsWarps / 32;        // warps' sums a lane reads
 constexpr int kPer = kMaxTop / 32;                  // entries of a lane
 
@@ -62,12 +63,14 @@ struct DsParams {
 struct Teacher {
   int id[kMaxTop];           // -1: no entry, or none with weight
   float p[kMaxTop], log_p[kMaxTop], z[kMaxTop];
+  int own[kMaxTop];          // entries of this CTA's part of the row
   float sum_p, zy;
-  int y, any, twice, y_named;   // twice: an id occurs more than once; y_named: y among the ids
+  int y, any, n_own, twice, y_own;   // twice: an id of theirs occurs more than once;
+                                     // y_own: y is in this part and not among the ids
 };
 
 struct DsShared {
-  float2 sums[2][8 * kDsWarps];          // (max, sum) of every consumer warp of the cluster
+  float2 sums[2][8 * kDsWarps];          // (reference, sum) of every consumer warp of the cluster
   Teacher teacher[2];
   uint64_t full[kRing], empty[kRing], sums_full[2], teacher_full[2], teacher_free[2];
 };
@@ -111,21 +114,23 @@ struct RowPart {             // a CTA's part of a row
   int c0, c1, held;
 };
 template <typename T>
-__device__ __forceinline__ RowPart<T> row_part(const DsParams& a, int n, int c, int C) {
+__device__ __forceinline__ RowPart<T> row_part(const DsParams& a, int n, int c, int log_C) {
   RowPart<T> r;
   r.row = static_cast<const T*>(a.z) + (long long)n * a.ld;
   r.rc = row_chunks(r.row, a.V);
   r.body = reinterpret_cast<const uint4*>(r.row + r.rc.head);
-  r.c0 = (int)((long long)r.rc.chunks * c / C);
-  r.c1 = (int)((long long)r.rc.chunks * (c + 1) / C);
+  r.c0 = (int)((long long)r.rc.chunks * c >> log_C);
+  r.c1 = (int)((long long)r.rc.chunks * (c + 1) >> log_C);
   r.held = min(r.c1 - r.c0, a.resident);
   return r;
 }
 
 // The teacher's entries of row n and its label into `te`, by one warp.
 template <typename T>
-__device__ __forceinline__ void read_teacher(const DsParams& a, int n, const T* row, Teacher& te) {
+__device__ __forceinline__ void read_teacher(const DsParams& a, int n, const RowPart<T>& r, bool first_part,
+                                             Teacher& te) {
   const int lane = threadIdx.x & 31, K = a.K, V = a.V;
+  const T* row = r.row;
   int id[kPer];
   float t[kPer], p[kPer];
 #pragma unroll
@@ -164,11 +169,18 @@ __device__ __forceinline__ void read_teacher(const DsParams& a, int n, const T* 
   }
   sum = warp_sum(sum);
   const float log_sum = logf(sum);
+  auto owned = [&](int v) {
+    if (v < r.rc.head || v >= V - r.rc.tail) return v >= 0 && first_part;
+    const int at = (v - r.rc.head) / Chunk<T>::N;
+    return at >= r.c0 && at < r.c1;
+  };
   float sum_p = 0.f;
   bool y_named = false;
+  int n_own = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int k = lane + 32 * i;
+    if (32 * i >= K) break;
     if (id[i] >= 0) p[i] /= sum;
     sum_p += p[i];
     y_named |= id[i] >= 0 && id[i] == y;
@@ -178,35 +190,45 @@ __device__ __forceinline__ void read_teacher(const DsParams& a, int n, const T* 
       te.log_p[k] = t[i] - tm - log_sum;
       te.z[k] = z[i];
     }
+    const bool mine = owned(id[i]);
+    const unsigned all = __ballot_sync(0xffffffffu, mine);
+    if (mine) te.own[n_own + __popc(all & ((1u << lane) - 1u))] = k;
+    n_own += __popc(all);
   }
   sum_p = warp_sum(sum_p);
+  y_named = __any_sync(0xffffffffu, y_named);
   __syncwarp();
   bool twice = false;
-  for (int j = 0; j < K; ++j) {
-    const int o = te.id[j];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) twice |= o >= 0 && id[i] == o && lane + 32 * i != j;
+  if (n_own <= 32) {
+    const int v = lane < n_own ? te.id[te.own[lane]] : -1 - lane;
+    twice = __popc(__match_any_sync(0xffffffffu, v)) > 1;
+  } else {
+    for (int j = 0; j < n_own; ++j) {
+      const int o = te.id[te.own[j]];
+      for (int i = lane; i < j; i += 32) twice |= te.id[te.own[i]] == o;
+    }
   }
   twice = __any_sync(0xffffffffu, twice);
-  y_named = __any_sync(0xffffffffu, y_named);
   if (lane == 0) {
     te.sum_p = sum_p;
     te.zy = zy;
     te.y = y;
     te.any = any;
+    te.n_own = n_own;
     te.twice = twice;
-    te.y_named = y_named;
+    te.y_own = !y_named && owned(y);
   }
   __syncwarp();
 }
 
 template <typename T, bool Grad>
-__global__ void __launch_bounds__(kDsBlock, 2) distill_kernel(DsParams a, int C) {
+__global__ void __launch_bounds__(kDsBlock, 2) distill_kernel(DsParams a, int log_C) {
   constexpr int N = Chunk<T>::N;
   extern __shared__ __align__(128) uint4 rows_s[];
   __shared__ DsShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int c = (int)(blockIdx.x % C), first = (int)(blockIdx.x / C), step = (int)(gridDim.x / C);
+  const int C = 1 << log_C;                  // CTAs of a row
+  const int c = (int)(blockIdx.x & (C - 1)), first = (int)(blockIdx.x >> log_C), step = (int)(gridDim.x >> log_C);
   const int V = a.V, K = a.K;
   const int pieces = (a.resident + kPieceChunks - 1) / kPieceChunks;
   if (tid == 0) {
@@ -233,7 +255,7 @@ __global__ void __launch_bounds__(kDsBlock, 2) distill_kernel(DsParams a, int C)
       int sent = 0;                          // pieces so far; slot sent % kRing
       for (int n = first; n < a.N && !late; n += step) {
         if (a.weights && a.weights[n] == 0.f) continue;
-        const RowPart<T> r = row_part<T>(a, n, c, C);
+        const RowPart<T> r = row_part<T>(a, n, c, log_C);
         for (int i = 0; i < pieces; ++i, ++sent) {
           const int slot = sent % kRing, use = sent / kRing;
           if (use > 0 && !mbar_wait(&sh.empty[slot], (use - 1) & 1)) { late = true; break; }
@@ -254,7 +276,7 @@ __global__ void __launch_bounds__(kDsBlock, 2) distill_kernel(DsParams a, int C)
       if (a.weights && a.weights[n] == 0.f) continue;
       const int b = it & 1;
       if (it >= 2 && !mbar_wait(&sh.teacher_free[b], ((it >> 1) - 1) & 1)) { late = true; break; }
-      read_teacher(a, n, static_cast<const T*>(a.z) + (long long)n * a.ld, sh.teacher[b]);
+      read_teacher<T>(a, n, row_part<T>(a, n, c, log_C), c == 0, sh.teacher[b]);
       if (lane == 0) mbar_arrive(&sh.teacher_full[b]);
       ++it;
     }
@@ -271,7 +293,8 @@ __global__ void __launch_bounds__(kDsBlock, 2) distill_kernel(DsParams a, int C)
         if constexpr (Grad) {
           const RowChunks oc = row_chunks(out, V);
           uint4* o4 = reinterpret_cast<uint4*>(out + oc.head);
-          const int e0 = (int)((long long)oc.chunks * c / C), e1 = (int)((long long)oc.chunks * (c + 1) / C);
+          const int e0 = (int)((long long)oc.chunks * c >> log_C);
+          const int e1 = (int)((long long)oc.chunks * (c + 1) >> log_C);
           for (int i = e0 + tid; i < e1; i += kDsThreads) __stcs(o4 + i, make_uint4(0u, 0u, 0u, 0u));
           if (c == 0 && tid < oc.head + oc.tail)
             out[tid < oc.head ? tid : V - oc.tail + (tid - oc.head)] = elem_from_float<T>(0.f);
@@ -288,23 +311,22 @@ __global__ void __launch_bounds__(kDsBlock, 2) distill_kernel(DsParams a, int C)
       const int b = it & 1;
       const uint32_t buf_phase = (it >> 1) & 1;
       if (tid == 0) mbar_arrive_expect_tx(&sh.sums_full[b], (uint32_t)(C * kDsWarps * 8));
-      const RowPart<T> r = row_part<T>(a, n, c, C);
+      const RowPart<T> r = row_part<T>(a, n, c, log_C);
       const float g = a.d_loss ? a.d_loss[n] : 1.f;
 
       // ---- sums
-      RunningSoftmax<false> rs;
+      RunningSum rs;
       rs.init(a.inv_tau);
-      float tmax = -INFINITY;
       const int loose_n = c == 0 ? r.rc.head + r.rc.tail : 0;
       const int loose = tid < r.rc.head ? tid : V - r.rc.tail + (tid - r.rc.head);
       float zl = 0.f;
       if (tid < loose_n) {
         zl = elem_to_float(r.row[loose]);
         rs.add_one(zl);
-        tmax = fmaxf(tmax, zl);
       }
-      constexpr int G = 2;                   // chunks at once
-      auto take = [&](const uint4 (&q)[G]) {
+      // G chunks at once
+      auto take = [&](const auto& q) {
+        constexpr int G = sizeof(q) / sizeof(q[0]);
         float z[G * N];
 #pragma unroll
         for (int u = 0; u < G; ++u) {
@@ -313,20 +335,11 @@ __global__ void __launch_bounds__(kDsBlock, 2) distill_kernel(DsParams a, int C)
 #pragma unroll
           for (int e = 0; e < N; ++e) z[u * N + e] = x[e];
         }
-        float bm = fmaxf(z[0], z[1]);
-#pragma unroll
-        for (int e = 2; e < G * N; ++e) bm = fmaxf(bm, z[e]);
-        tmax = fmaxf(tmax, bm);
-        rs.template add<G * N>(z, bm);
+        rs.add(z);
       };
       auto take_one = [&](const uint4& q) {
-        float z[N];
-        unpack_chunk<T>(q, z);
-        float bm = z[0];
-#pragma unroll
-        for (int e = 1; e < N; ++e) bm = fmaxf(bm, z[e]);
-        tmax = fmaxf(tmax, bm);
-        rs.template add<N>(z, bm);
+        const uint4 one[1] = {q};
+        take(one);
       };
       int slot = slot0;
       uint32_t phase = phase0;
@@ -338,26 +351,24 @@ __global__ void __launch_bounds__(kDsBlock, 2) distill_kernel(DsParams a, int C)
       };
       for (int i = 0; i < pieces; ++i, next_piece()) {
         if (!late && !mbar_wait(&sh.full[slot], phase)) late = true;
-        const int end = min(kPieceChunks, r.held - i * kPieceChunks);
-        const uint4* piece = rows_s + slot * kPieceChunks;
-        int j = tid;
-        for (; j + (G - 1) * kDsThreads < end; j += G * kDsThreads) {
-          uint4 q[G];
+        const uint4* piece = rows_s + slot * kPieceChunks + tid;
+        const int left = r.held - i * kPieceChunks;
+        if (left >= kPieceChunks) {
+          uint4 q[kShare];
 #pragma unroll
-          for (int u = 0; u < G; ++u) q[u] = piece[j + u * kDsThreads];
+          for (int u = 0; u < kShare; ++u) q[u] = piece[u * kDsThreads];
           take(q);
+        } else {
+          for (int j = 0; j + tid < left; j += kDsThreads) take_one(piece[j]);
         }
-        for (; j < end; j += kDsThreads) take_one(piece[j]);
         if constexpr (!Grad) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.empty[slot]);
         }
       }
       for (int j = r.c0 + r.held + tid; j < r.c1; j += kDsThreads) take_one(r.body[j]);
-      const float wm = warp_max(tmax);
-      float s, unused;
-      rs.finish(wm, s, unused);
-      s = warp_sum(s);
+      const float wm = warp_max(rs.reference());
+      const float s = warp_sum(rs.at(wm));
       // the teacher's entries are read (from the row, too) before any CTA can write it
       Teacher& te = sh.teacher[b];
       if (!late && !mbar_wait(&sh.teacher_full[b], buf_phase)) late = true;
@@ -439,12 +450,16 @@ __global__ void __launch_bounds__(kDsBlock, 2) distill_kernel(DsParams a, int C)
           };
           slot = slot0;
           for (int i = 0; i < pieces; ++i, next_piece()) {
-            const int end = min(kPieceChunks, r.held - i * kPieceChunks);
-            const uint4* piece = rows_s + slot * kPieceChunks;
+            const uint4* piece = rows_s + slot * kPieceChunks + tid;
+            const int left = r.held - i * kPieceChunks, at = r.c0 + i * kPieceChunks + tid;
+            if (left >= kPieceChunks) {
+              uint4 q[kShare];
 #pragma unroll
-            for (int u = 0; u < kPieceChunks / kDsThreads; ++u) {
-              const int j = u * kDsThreads + tid;
-              if (j < end) put(r.c0 + i * kPieceChunks + j, piece[j]);
+              for (int u = 0; u < kShare; ++u) q[u] = piece[u * kDsThreads];
+#pragma unroll
+              for (int u = 0; u < kShare; ++u) put(at + u * kDsThreads, q[u]);
+            } else {
+              for (int j = 0; j + tid < left; j += kDsThreads) put(at + j, piece[j]);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.empty[slot]);
@@ -454,16 +469,14 @@ __global__ void __launch_bounds__(kDsBlock, 2) distill_kernel(DsParams a, int C)
           // the teacher's elements and the label's, after the row's, by the warp that holds
           // them: dz = g w / tau (A q - sum of a over the entries with this id)
           __syncwarp();
-          auto mine = [&](int v) {
-            if (v < r.rc.head || v >= V - r.rc.tail) return c == 0 && warp == 0;
-            const int at = (v - r.rc.head) / N;
-            return at >= r.c0 && at < r.c1 && (((at - r.c0) & (kDsThreads - 1)) >> 5) == warp;
+          // (an element outside the chunks is warp 0's)
+          auto holder = [&](int v) {
+            const int at = (v - r.rc.head) / N - r.c0;
+            return v < r.rc.head || v >= V - r.rc.tail ? 0 : (at & (kDsThreads - 1)) >> 5;
           };
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const int k = lane + 32 * i;
-            const int v = k < K ? te.id[k] : -1;
-            if (v < 0 || !mine(v)) continue;
+          for (int i = lane; i < te.n_own; i += 32) {
+            const int k = te.own[i], v = te.id[k];
+            if (holder(v) != warp) continue;
             const float q = expf(log_q(te.z[k]));
             float av = v == y ? ay : 0.f;
             if (te.twice) {                  // in entry order, so that equal ids write the same
@@ -474,12 +487,12 @@ __global__ void __launch_bounds__(kDsBlock, 2) distill_kernel(DsParams a, int C)
             }
             out[v] = elem_from_float<T>(gw * (sum_a * q - av));
           }
-          if (lane == 0 && y >= 0 && !te.y_named && mine(y))
+          if (lane == 0 && te.y_own && holder(y) == warp)
             out[y] = elem_from_float<T>(gw * (sum_a * expf(log_q(te.zy)) - ay));
         }
       }
       // ---- loss and acceptance, by the last warp of one CTA
-      if (warp == kDsWarps - 1 && it % C == c) {
+      if (warp == kDsWarps - 1 && (it & (C - 1)) == c) {
         float kl = 0.f, tv = 0.f, acc = 0.f;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
@@ -521,21 +534,21 @@ __global__ void __launch_bounds__(kDsBlock, 2) distill_kernel(DsParams a, int C)
 template <typename T, bool Grad>
 cudaError_t launch(DsParams p, cudaStream_t stream) {
   const int chunks = p.V / Chunk<T>::N;
-  int C = 1;
+  int C = 1, log_C = 0;
   // the row's part of a CTA small enough that some of the ring is left for the next row's;
   // more CTAs a row while there are fewer than two an SM, as long as each has 8 KB
-  while (C < 8 && (long long)cdiv(chunks, C) * 16 > kDsTarget) C *= 2;
-  while (C < 8 && (long long)p.N * C < 304 && chunks / (2 * C) >= 512) C *= 2;
+  while (C < 8 && (long long)cdiv(chunks, C) * 16 > kDsTarget) C *= 2, ++log_C;
+  while (C < 8 && (long long)p.N * C < 304 && chunks / (2 * C) >= 512) C *= 2, ++log_C;
   const int part = cdiv(chunks, C) + 1;
   p.resident = part < kRing * kPieceChunks ? part : kRing * kPieceChunks;
   const size_t smem = (size_t)kRing * kDsPiece;
   // clusters that the device holds at once: more would wait for these to end
   static std::atomic<int> cache[4][kMaxCachedDevices];
-  const int most = device_clusters(cache[C == 1 ? 0 : C == 2 ? 1 : C == 4 ? 2 : 3], distill_kernel<T, Grad>, C,
+  const int most = device_clusters(cache[log_C], distill_kernel<T, Grad>, C,
                                    kDsBlock, smem);
   if (most <= 0) return cudaErrorInvalidConfiguration;
   const long long clusters = p.N < most ? p.N : most;
-  return launch_rows_cluster(distill_kernel<T, Grad>, clusters * C, C, kDsBlock, smem, stream, p, C);
+  return launch_rows_cluster(distill_kernel<T, Grad>, clusters * C, C, kDsBlock, smem, stream, p, log_C);
 }
 
 }  // namespace

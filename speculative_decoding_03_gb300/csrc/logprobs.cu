@@ -116,8 +116,8 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(LpParams 
   const float zy = a.tokens ? elem_to_float(row[y]) : INFINITY;
 
   // ---- one pass: sums, this thread's maximum and its batch maxima
-  RunningSoftmax<true> rs;
-  rs.init(1.f);
+  RunningSoftmax rs;
+  rs.init();
   float tmax = -INFINITY;
   // CTA 0 takes the elements outside the 16-byte chunks, one to a thread
   const int loose_n = c == 0 ? rc.head + rc.tail : 0;
@@ -139,9 +139,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(LpParams 
     for (int g = 0; g < kLpBatch; ++g) {
       float z[N];
       unpack_chunk<T>(q[g], z);
-      float bm = z[0];
-#pragma unroll
-      for (int i = 1; i < N; ++i) bm = fmaxf(bm, z[i]);
+      const float bm = max_of(z);
       smax = fmaxf(smax, bm);
       rs.template add<N>(z, bm);
     }
@@ -156,9 +154,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(LpParams 
   for (; at < c1; at += kLpThreads) {
     float z[N];
     unpack_chunk<T>(__ldg(body + at), z);
-    float bm = z[0];
-#pragma unroll
-    for (int i = 1; i < N; ++i) bm = fmaxf(bm, z[i]);
+    const float bm = max_of(z);
     smax = fmaxf(smax, bm);
     rs.template add<N>(z, bm);
     in_slot = 1;
@@ -230,9 +226,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(LpParams 
     auto look = [&](int i) {
       float z[N];
       unpack_chunk<T>(__ldg(body + i), z);
-      float bm = z[0];
-#pragma unroll
-      for (int e = 1; e < N; ++e) bm = fmaxf(bm, z[e]);
+      const float bm = max_of(z);
       if (bm >= reach) {
         const int v = rc.head + i * N;
 #pragma unroll

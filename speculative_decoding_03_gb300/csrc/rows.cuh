@@ -163,10 +163,23 @@ __device__ __forceinline__ unsigned long long cluster_ld_u64(uint32_t addr) {
   return v;
 }
 
+// the largest of the warp's values that are not NaN
 __device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+// the largest of n elements that are not NaN
+template <int n>
+__device__ __forceinline__ float max_of(const float (&z)[n]) {
+  float m[n];
 #pragma unroll
-  for (int m = 16; m >= 1; m >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, m));
-  return x;
+  for (int i = 0; i < n; ++i) m[i] = z[i];
+#pragma unroll
+  for (int w = 1; w < n; w *= 2)
+#pragma unroll
+    for (int i = 0; i + w < n; i += 2 * w) m[i] = fmaxf(m[i], m[i + w]);
+  return m[0];
 }
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
@@ -175,63 +188,58 @@ __device__ __forceinline__ float warp_sum(float x) {
 }
 
 // ------------------------------------------------------------- running softmax statistics
-// s = sum exp(k (z - R)) and, with Moment, t = sum exp(k (z - R)) k (z - R) over the
-// elements seen, against a reference R that a batch raises to its own maximum only when it
-// exceeds R by more than kMargin / k: sums stay below V e^8, and the rescale is rare.  k is
-// the inverse temperature.  Elements of -inf contribute nothing; NaN and +inf make s NaN.
+// s = sum exp(z - R) and t = sum exp(z - R) (z - R) over the elements seen, against a
+// reference R that a batch raises to its own maximum only when it exceeds R by more than
+// kMargin: sums stay below V e^8, and the rescale is rare.  Elements of -inf contribute
+// nothing; NaN and +inf make s NaN.
 constexpr float kMargin = 8.f;
 
-template <bool Moment>
 struct RunningSoftmax {
-  float R, k;
+  float R;
   F2 s, t;
-  __device__ __forceinline__ void init(float inv_temperature) {
+  __device__ __forceinline__ void init() {
     R = -FLT_MAX;
-    k = inv_temperature;
     s = f2(0.f, 0.f);
     t = f2(0.f, 0.f);
   }
   // n (even) elements; bm: their maximum (NaN ignored)
   template <int n>
   __device__ __forceinline__ void add(const float (&z)[n], float bm) {
-    if ((bm - R) * k > kMargin) {            // also the first batch: R = -FLT_MAX
-      const float d = (R - bm) * k;          // <= 0, may be -inf (then s = t = 0)
+    if (bm - R > kMargin) {                  // also the first batch: R = -FLT_MAX
+      const float d = R - bm;                // < 0, may be -inf (then s = t = 0)
       const float f = ex2_approx(d * kLog2e);
-      float a, b;
+      float a, b, u, v;
       f2_get(s, a, b);
-      if constexpr (Moment) {
-        float u, v;
-        f2_get(t, u, v);
-        t = f > 0.f ? f2(f * (u + d * a), f * (v + d * b)) : f2(0.f, 0.f);
-      }
+      f2_get(t, u, v);
+      t = f > 0.f ? f2(f * (u + d * a), f * (v + d * b)) : f2(0.f, 0.f);
       s = f2(f * a, f * b);
       R = bm;
     }
-    const F2 nR = f2(-R, -R), kk = f2(k * kLog2e, k * kLog2e);
+    const F2 nR = f2(-R, -R), kk = f2(kLog2e, kLog2e);
     F2 tb = f2(0.f, 0.f);
+    F2 sb[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
     for (int i = 0; i < n; i += 2) {
       const F2 d = f2_add(f2(z[i], z[i + 1]), nR);
       float x, y;
       f2_get(f2_mul(d, kk), x, y);
       const F2 e = f2(ex2_approx(x), ex2_approx(y));
-      s = f2_add(s, e);
-      if constexpr (Moment) tb = f2_fma(e, d, tb);
+      sb[i / 2 & 1] = f2_add(sb[i / 2 & 1], e);
+      tb = f2_fma(e, d, tb);
     }
-    if constexpr (Moment) {
-      float u, v;
-      f2_get(tb, u, v);
-      if (!(fabsf(u + v) <= FLT_MAX)) {      // an element of -inf: 0 * -inf
-        u = 0.f;
+    s = f2_add(s, f2_add(sb[0], sb[1]));
+    float u, v;
+    f2_get(tb, u, v);
+    if (!(fabsf(u + v) <= FLT_MAX)) {        // an element of -inf: 0 * -inf
+      u = 0.f;
 #pragma unroll
-        for (int i = 0; i < n; ++i) {
-          const float d = z[i] - R;
-          if (d > -FLT_MAX) u = fmaf(ex2_approx(d * k * kLog2e), d, u);
-        }
-        tb = f2(u, 0.f);
+      for (int i = 0; i < n; ++i) {
+        const float d = z[i] - R;
+        if (d > -FLT_MAX) u = fmaf(ex2_approx(d * kLog2e), d, u);
       }
-      t = f2_fma(tb, f2(k, k), t);
+      tb = f2(u, 0.f);
     }
+    t = f2_add(t, tb);
   }
   __device__ __forceinline__ void add_one(float z) {
     const float two[2] = {z, -INFINITY};
@@ -239,19 +247,73 @@ struct RunningSoftmax {
   }
   // the sums moved to the reference m >= R (m finite unless nothing was seen)
   __device__ __forceinline__ void finish(float m, float& so, float& to) const {
-    float a, b;
+    float a, b, u, v;
     f2_get(s, a, b);
+    f2_get(t, u, v);
     so = a + b;
     to = 0.f;
     if (so == 0.f) return;
-    const float d = (R - m) * k;
+    const float d = R - m;
     const float f = ex2_approx(d * kLog2e);
-    if constexpr (Moment) {
-      float u, v;
-      f2_get(t, u, v);
-      to = f > 0.f ? f * ((u + v) + d * so) : 0.f;
-    }
+    to = f > 0.f ? f * ((u + v) + d * so) : 0.f;
     so *= f;
+  }
+};
+
+// s = sum exp(k (z - R)) alone, without a maximum per element: R is raised (to a batch's
+// maximum, which only then is looked for) when the sum leaves [2^-20, 2^30], which the first
+// batch with an element above -inf does and after it only elements more than 20 / k above R.
+struct RunningSum {
+  float R, k;
+  F2 s;
+  __device__ __forceinline__ void init(float inv_temperature) {
+    R = -FLT_MAX;
+    k = inv_temperature;
+    s = f2(0.f, 0.f);
+  }
+  template <int n>
+  __device__ __forceinline__ F2 batch(const float (&z)[n]) const {
+    const F2 nR = f2(-R, -R), kk = f2(k * kLog2e, k * kLog2e);
+    F2 sb[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll
+    for (int i = 0; i < n; i += 2) {
+      float x, y;
+      f2_get(f2_mul(f2_add(f2(z[i], z[i + 1]), nR), kk), x, y);
+      sb[i / 2 & 1] = f2_add(sb[i / 2 & 1], f2(ex2_approx(x), ex2_approx(y)));
+    }
+    return f2_add(sb[0], sb[1]);
+  }
+  template <int n>
+  __device__ __forceinline__ void add(const float (&z)[n]) {
+    F2 t = f2_add(s, batch<n>(z));
+    float a, b;
+    f2_get(t, a, b);
+    if (!(a + b >= 0x1p-20f && a + b <= 0x1p30f)) {
+      const float bm = max_of(z);
+      float u, v;
+      f2_get(s, u, v);
+      if (bm > R || (u + v == 0.f && bm > -INFINITY)) {
+        const float f = u + v == 0.f ? 0.f : ex2_approx((R - bm) * k * kLog2e);
+        s = f2(f * u, f * v);
+        R = bm;
+      }
+      t = f2_add(s, batch<n>(z));
+    }
+    s = t;
+  }
+  __device__ __forceinline__ void add_one(float z) {
+    const float two[2] = {z, -INFINITY};
+    add<2>(two);
+  }
+  // the reference of what was seen (-inf: nothing above -inf), and the sum moved to m >= it
+  __device__ __forceinline__ float reference() const { return sum() == 0.f ? -INFINITY : R; }
+  __device__ __forceinline__ float sum() const {
+    float a, b;
+    f2_get(s, a, b);
+    return a + b;
+  }
+  __device__ __forceinline__ float at(float m) const {
+    return sum() == 0.f ? 0.f : sum() * ex2_approx((R - m) * k * kLog2e);
   }
 };
 
