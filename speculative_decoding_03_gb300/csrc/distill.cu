@@ -75,56 +75,6 @@ struct DsShared {
   uint64_t full[kRing], empty[kRing], sums_full[2], teacher_full[2], teacher_free[2];
 };
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
-}
-// two fp32 into CTA `rank`'s copy of *dst, counted as 8 bytes by its copy of *bar
-__device__ __forceinline__ void send_f2(float2* dst, uint64_t* bar, uint32_t rank, float x, float y) {
-  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
-                   cluster_map(dst, rank)),
-               "f"(x), "f"(y), "r"(cluster_map(bar, rank))
-               : "memory");
-}
-// a wait on data that other CTAs of the cluster send
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity) {
-  const long long t0 = sm_cycles();
-  for (;;) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(10000000u)
-        : "memory");
-    if (ok) return true;
-    if (sm_cycles() - t0 > kWaitCycles) return false;
-  }
-}
-
-template <typename T>
-struct RowPart {             // a CTA's part of a row
-  const T* row;
-  const uint4* body;
-  RowChunks rc;
-  int c0, c1, held;
-};
-template <typename T>
-__device__ __forceinline__ RowPart<T> row_part(const DsParams& a, int n, int c, int log_C) {
-  RowPart<T> r;
-  r.row = static_cast<const T*>(a.z) + (long long)n * a.ld;
-  r.rc = row_chunks(r.row, a.V);
-  r.body = reinterpret_cast<const uint4*>(r.row + r.rc.head);
-  r.c0 = (int)((long long)r.rc.chunks * c >> log_C);
-  r.c1 = (int)((long long)r.rc.chunks * (c + 1) >> log_C);
-  r.held = min(r.c1 - r.c0, a.resident);
-  return r;
-}
-
 // The teacher's entries of row n and its label into `te`, by one warp.
 template <typename T>
 __device__ __forceinline__ void read_teacher(const DsParams& a, int n, const RowPart<T>& r, bool first_part,
@@ -255,7 +205,7 @@ __global__ void __launch_bounds__(kDsBlock, 2) distill_kernel(DsParams a, int lo
       int sent = 0;                          // pieces so far; slot sent % kRing
       for (int n = first; n < a.N && !late; n += step) {
         if (a.weights && a.weights[n] == 0.f) continue;
-        const RowPart<T> r = row_part<T>(a, n, c, log_C);
+        const RowPart<T> r = row_part<T>(a.z, a.ld, n, a.V, c, log_C, a.resident);
         for (int i = 0; i < pieces; ++i, ++sent) {
           const int slot = sent % kRing, use = sent / kRing;
           if (use > 0 && !mbar_wait(&sh.empty[slot], (use - 1) & 1)) { late = true; break; }
@@ -276,7 +226,7 @@ __global__ void __launch_bounds__(kDsBlock, 2) distill_kernel(DsParams a, int lo
       if (a.weights && a.weights[n] == 0.f) continue;
       const int b = it & 1;
       if (it >= 2 && !mbar_wait(&sh.teacher_free[b], ((it >> 1) - 1) & 1)) { late = true; break; }
-      read_teacher<T>(a, n, row_part<T>(a, n, c, log_C), c == 0, sh.teacher[b]);
+      read_teacher<T>(a, n, row_part<T>(a.z, a.ld, n, a.V, c, log_C, a.resident), c == 0, sh.teacher[b]);
       if (lane == 0) mbar_arrive(&sh.teacher_full[b]);
       ++it;
     }
@@ -311,7 +261,7 @@ __global__ void __launch_bounds__(kDsBlock, 2) distill_kernel(DsParams a, int lo
       const int b = it & 1;
       const uint32_t buf_phase = (it >> 1) & 1;
       if (tid == 0) mbar_arrive_expect_tx(&sh.sums_full[b], (uint32_t)(C * kDsWarps * 8));
-      const RowPart<T> r = row_part<T>(a, n, c, log_C);
+      const RowPart<T> r = row_part<T>(a.z, a.ld, n, a.V, c, log_C, a.resident);
       const float g = a.d_loss ? a.d_loss[n] : 1.f;
 
       // ---- sums

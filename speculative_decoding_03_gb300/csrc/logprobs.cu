@@ -7,33 +7,42 @@
 //   rank    = 1 + #{v : z_v > z_y, or z_v = z_y and v < y},
 // and the K largest logits (ties to the smallest v) with their log probabilities.
 //
-// Bound by the one read of the row from HBM.  A row is cut into the CTAs of a cluster
-// (1, 2, 4 or 8): a thread keeps its softmax sums and the maximum of everything it read in
-// registers, and the maximum of each batch it read in shared memory; nothing is selected
-// while streaming.  The K-th largest of the group maxima of 2 K or more groups of threads
-// is a lower bound of the K-th largest logit that only slightly more than K elements reach
-// (-G log(1 - K / G) of them for G groups of random data: 89 at K = 64, G = 128); the few
-// batches whose maximum reaches it (or the token's logit, for the rank) are read again
-// from L2.  Those candidates are ranked by counting, and the CTAs merge their K best
-// through distributed shared memory.
+// Bound by the one read of the row from HBM.  A row is cut into the CTAs of a cluster (1, 2,
+// 4 or 8).  Clusters are persistent, so that a row's end costs no memory time: a producer
+// warp streams the parts of row after row through a ring of 16 KB pieces, eight consumer
+// warps keep only sums, a maximum a thread and the maximum of every 64 bytes, and four
+// closing warps do what a row still needs while the consumers are in the next one.
+//
+// The K best without a selection in the stream: the K-th largest of G >= 2 K maxima of groups
+// of threads is a lower bound of the row's K-th largest logit that only slightly more than K
+// elements reach (-G log(1 - K / G) of them for random data: 89 at K = 64, G = 128).  The few
+// 64-byte slots whose maximum reaches it are read again, and one CTA of the cluster (in turn)
+// ranks, by counting, the elements that the others send to it.  The rank is counted in the
+// stream: a sampled token may have hundreds of elements before it.
 #include "internal.h"
 #include "rows.cuh"
 
 namespace dspark {
 namespace {
 
-constexpr int kLpThreads = 256;
-constexpr int kLpBatch = 4;                 // 16-byte chunks a thread loads at once
-constexpr int kLpCap = 1024;                // candidate keys of a CTA
+using namespace sm100;
+
+constexpr int kLpWarps = 8, kLpThreads = kLpWarps * 32;   // consumers
+constexpr int kLpClose = 128;               // closing threads (4 warps)
+constexpr int kLpBlock = kLpThreads + 32 + kLpClose;
+constexpr int kLpPieceChunks = 1024;        // 16 KB: 4 chunks (64 bytes) of each consumer
+constexpr int kLpRing = 4;                  // pieces in flight, two CTAs an SM
+constexpr int kLpSlots = 12;                // maxima of a consumer thread kept for a row
+constexpr int kLpCap = 768;                 // candidate keys of a CTA
 constexpr int kLpList = 512;                // slots listed to be read again
 constexpr int kLpTop = kMaxTop;             // most alternatives
-constexpr int kLpMaxSlots = 64;             // batch maxima kept per thread
+constexpr int kLpMaxima = 256;              // most groups
 
 struct LpParams {
   const void* z;
   long long ld;
   const int32_t* tokens;     // may be null: every row is used, no logprob and no rank
-  int V, K, slots, per_slot; // per_slot batches share a slot of batch maxima
+  int N, V, K, log_per;      // 2^log_per pieces share a consumer thread's maximum
   float* logprob;
   float* entropy;
   int32_t* rank;
@@ -44,6 +53,17 @@ struct LpParams {
   int* err;
 };
 
+// 1 if a > b (a >= b), else 0
+__device__ __forceinline__ float one_if_gt(float a, float b) {
+  float r;
+  asm("set.gt.f32.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float one_if_ge(float a, float b) {
+  float r;
+  asm("set.ge.f32.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 // larger value first, then the smaller index; never 0 for an element that is not NaN
 __device__ __forceinline__ unsigned long long top_key(float z, int idx) {
   return argmax_key(z + 0.f, idx);          // -0 orders as +0
@@ -56,332 +76,567 @@ __device__ __forceinline__ int key_index(unsigned long long key) {
   return (int)(0xFFFFFFFFu - (uint32_t)key);
 }
 
+// A maximum as a whole number of the same order (-0 just below +0).
+__device__ __forceinline__ uint32_t group_key(float m) {
+  const uint32_t u = __float_as_uint(m);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float group_value(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? key & 0x7FFFFFFFu : ~key);
+}
+// A number that at least K of the n (at most 256) keys reach: the K-th largest less 1023 at
+// most (2^-13 of its value), found by halving the keys' range.  By a whole warp.
+__device__ __forceinline__ uint32_t kth_bound(const uint32_t* keys, int n, int K) {
+  const int lane = threadIdx.x & 31;
+  uint32_t k[8], lo = 0xFFFFFFFFu, hi = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    k[i] = lane + 32 * i < n ? keys[lane + 32 * i] : 0u;      // 0: below every value
+    if (lane + 32 * i < n) lo = min(lo, k[i]);
+    hi = max(hi, k[i]);
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);   // all n reach it, and n >= K
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  while (hi - lo > 1023u) {
+    const uint32_t mid = lo + (hi - lo) / 2 + 1;
+    int reach = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) reach += k[i] >= mid;
+    if (__reduce_add_sync(0xffffffffu, reach) >= K) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
 struct LpShared {
   unsigned long long cand[kLpCap];
-  unsigned long long best[kLpTop];                    // this CTA's K best, descending
-  unsigned long long all[8 * kLpTop];                 // every CTA's, for the merge
-  float gmax[kLpThreads];
-  float4 part[kLpThreads / 32];
-  float4 stat;                                        // m, s, t, (int) elements before y
-  int n_best, n_cand, n_list, before, merged[kLpTop];
+  unsigned long long best[kLpTop];                    // this CTA's K best, then 0
+  unsigned long long all[8 * kLpTop];                 // every CTA's, where they are merged
+  float2 counts[8];                                   // and their number (as bits)
+  uint32_t gmax[2][kLpMaxima];                        // this CTA's group maxima, as keys
+  uint32_t gall[2][kLpMaxima];                        // the cluster's
+  float4 part[2][kLpWarps];                           // a consumer warp's m, s, t, elements before y
+  float2 ms[2][8 * kLpWarps];                         // the cluster's: m, s
+  float2 tb[2][8 * kLpWarps];                         // t, elements before y (as bits)
   int list[kLpList];
-  float thr;
+  int n_cand, n_list;
+  uint64_t full[kLpRing], empty[kLpRing];
+  uint64_t stats_full[2], stats_free[2];              // consumers to closing warps and back
+  uint64_t sums_full[2], merge_full;                  // messages of the cluster's CTAs
 };
 
-// best[0 .. K) = the K largest of cand[0 .. n), descending; returns min(n, K).  All threads.
-__device__ __forceinline__ int select_top(LpShared& sh, int n, int K) {
-  for (int i = threadIdx.x; i < n; i += kLpThreads) {
-    const unsigned long long key = sh.cand[i];
-    int r = 0;
-    for (int j = 0; j < n; ++j) r += sh.cand[j] > key;
-    if (r < K) sh.best[r] = key;
+// The rows of a cluster, in order, for a whole warp: every step-th row that has a token, so
+// that rows without one leave no cluster idle.  (Each warp reads all the tokens for that;
+// above kLpDeal rows the rows are dealt by number instead, and those without a token skipped.)
+constexpr int kLpDeal = 1 << 16;
+struct RowsOf {
+  const int32_t* tokens;
+  int N, V, step, want, n, seen;
+  unsigned window;                           // rows with a token among n .. n + 31
+  bool deal;
+  __device__ __forceinline__ unsigned look(int at) const {
+    const int i = at + (threadIdx.x & 31);
+    const int y = i < N ? tokens[i] : -1;
+    return __ballot_sync(0xffffffffu, y >= 0 && y < V);
   }
-  __syncthreads();
+  __device__ __forceinline__ RowsOf(const int32_t* t, int N_, int V_, int first, int step_)
+      : tokens(t), N(N_), V(V_), step(step_), want(first), n(0), seen(0), deal(t && N_ <= kLpDeal) {
+    window = deal ? look(0) : 0u;
+  }
+  // the next row, or -1
+  __device__ __forceinline__ int next() {
+    if (!deal) {
+      while (want < N) {
+        const int r = want;
+        want += step;
+        if (!tokens || (tokens[r] >= 0 && tokens[r] < V)) return r;
+      }
+      return -1;
+    }
+    while (n < N && seen + __popc(window) <= want) {
+      seen += __popc(window);
+      n += 32;
+      window = n < N ? look(n) : 0u;
+    }
+    if (n >= N) return -1;
+    unsigned left = window;
+    for (int k = want - seen; k > 0; --k) left &= left - 1;
+    want += step;
+    return n + __ffs(left) - 1;
+  }
+};
+
+__device__ __forceinline__ void close_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kLpClose) : "memory");
+}
+// the barrier, and whether any closing thread has `p`
+__device__ __forceinline__ bool close_any(bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, 1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)p), "n"(kLpClose)
+      : "memory");
+  return r != 0;
+}
+
+// best[0 .. K) = the K largest of cand[0 .. n), descending, then 0; returns min(n, K).  All
+// closing threads; up to 64 keys by two threads a key, each against half of them.
+__device__ __forceinline__ int select_top(LpShared& sh, int x, int n, int K) {
+  if (n <= kLpClose / 2) {
+    const int i = x >> 1;
+    const unsigned long long key = i < n ? sh.cand[i] : 0ull;
+    int r = 0;
+#pragma unroll 4
+    for (int j = x & 1; j < n; j += 2) r += sh.cand[j] > key;
+    r += __shfl_xor_sync(0xffffffffu, r, 1);
+    if (i < n && r < K && (x & 1) == 0) sh.best[r] = key;
+  } else {
+    for (int i = x; i < n; i += kLpClose) {
+      const unsigned long long key = sh.cand[i];
+      int r = 0;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) r += sh.cand[j] > key;
+      if (r < K) sh.best[r] = key;
+    }
+  }
+  for (int i = n + x; i < K; i += kLpClose) sh.best[i] = 0ull;
+  close_sync();
   return n < K ? n : K;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(LpParams a, int C) {
+__global__ void __launch_bounds__(kLpBlock, 2) token_logprobs_kernel(LpParams a, int log_C) {
   constexpr int N = Chunk<T>::N;
+  extern __shared__ __align__(128) uint4 ring_s[];    // [kLpRing][1024], then the slot maxima
   __shared__ LpShared sh;
-  extern __shared__ float slot_max[];       // [slots][kLpThreads]
+  float* const slots_s = reinterpret_cast<float*>(ring_s + kLpRing * kLpPieceChunks);   // [2][kLpSlots][256]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int n = (int)(blockIdx.x / C);
-  const int c = (int)(blockIdx.x - (unsigned)n * C);
+  const int C = 1 << log_C;                  // CTAs of a row
+  const int c = (int)(blockIdx.x & (C - 1)), first = (int)(blockIdx.x >> log_C), step = (int)(gridDim.x >> log_C);
   const int V = a.V, K = a.K;
+  // groups of the cluster (at least one a warp) and of this CTA
+  int log_G = log_C + 3;
+  while ((1 << log_G) < 2 * K && (1 << log_G) < kLpMaxima) ++log_G;
+  const int G = 1 << log_G, log_own = log_G - log_C, own = 1 << log_own;
+  if (tid == 0) {
+    for (int i = 0; i < kLpRing; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], kLpWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.stats_full[i], kLpWarps);
+      mbar_init(&sh.stats_free[i], 1);
+      mbar_init(&sh.sums_full[i], 1);
+    }
+    mbar_init(&sh.merge_full, 1);
+    fence_mbar_init();
+  }
+  if (C > 1) cluster_sync();
+  else __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
-  const int y = a.tokens ? a.tokens[n] : -1;
-  if (a.tokens && (y < 0 || y >= V)) {      // the same in every CTA of the cluster
-    if (c == 0) {
-      if (tid == 0) {
-        if (y != -1) set_device_error(a.err, DSPARK_ERR_DEVICE_CHECK);
-        a.logprob[n] = 0.f;
-        a.rank[n] = 0;
-        if (a.entropy) a.entropy[n] = 0.f;
-        if (a.row_max) a.row_max[n] = -INFINITY;
-        if (a.row_sumexp) a.row_sumexp[n] = 0.f;
-      }
-      for (int j = tid; j < K; j += kLpThreads) {
-        a.top_ids[(size_t)n * K + j] = -1;
-        a.top_logprobs[(size_t)n * K + j] = -INFINITY;
-      }
-    }
-    return;
-  }
-  const T* row = static_cast<const T*>(a.z) + (long long)n * a.ld;
-  const RowChunks rc = row_chunks(row, V);
-  const uint4* body = reinterpret_cast<const uint4*>(row + rc.head);
-  const int c0 = (int)((long long)rc.chunks * c / C), c1 = (int)((long long)rc.chunks * (c + 1) / C);
-  const float zy = a.tokens ? elem_to_float(row[y]) : INFINITY;
+  auto part_of = [&](int n) { return row_part<T>(a.z, a.ld, n, V, c, log_C, 0x7FFFFFFF); };
+  bool late = false;                         // a bounded wait ran out: give up
 
-  // ---- one pass: sums, this thread's maximum and its batch maxima
-  RunningSoftmax rs;
-  rs.init();
-  float tmax = -INFINITY;
-  // CTA 0 takes the elements outside the 16-byte chunks, one to a thread
-  const int loose_n = c == 0 ? rc.head + rc.tail : 0;
-  const int loose = tid < rc.head ? tid : V - rc.tail + (tid - rc.head);
-  if (tid < loose_n) {
-    const float z = elem_to_float(row[loose]);
-    rs.add_one(z);
-    tmax = fmaxf(tmax, z);
-  }
-  const int span = kLpThreads * kLpBatch;
-  int at = c0 + tid, in_slot = 0;
-  float* slot = slot_max + tid;
-  float smax = -INFINITY;
-  for (; at + (kLpBatch - 1) * kLpThreads < c1; at += span) {
-    uint4 q[kLpBatch];
+  if (warp < kLpWarps) {
+    // ---- consumers
+    int it = 0, slot = 0;
+    uint32_t phase = 0;
+    RowsOf rows(a.tokens, a.N, V, first, step);
+    int n_next = rows.next();
+    while (n_next >= 0 && !late) {
+      const int n = n_next;
+      n_next = rows.next();
+      const int y = a.tokens ? a.tokens[n] : 0;
+      const int b = it & 1;
+      const RowPart<T> r = part_of(n);
+      const int loose_n = c == 0 ? r.rc.head + r.rc.tail : 0;   // elements outside the chunks
+      const float zl = tid < loose_n
+                           ? elem_to_float(r.row[tid < r.rc.head ? tid : V - r.rc.tail + (tid - r.rc.head)])
+                           : -INFINITY;
+      if (it >= 2 && !mbar_wait(&sh.stats_free[b], ((it >> 1) - 1) & 1)) late = true;
+      RunningSoftmax rs;
+      rs.init();
+      float tmax = -INFINITY, smax = -INFINITY;
+      // elements before y: those above its logit, and equal ones of lower index
+      const float zy = a.tokens ? elem_to_float(r.row[y]) : INFINITY;
+      F2 before = f2(0.f, 0.f);
+      float* out = slots_s + b * kLpSlots * kLpThreads + tid;
+      for (int i = 0; i < r.held; i += kLpPieceChunks) {
+        if (!late && !mbar_wait(&sh.full[slot], phase)) late = true;
+        // a thread's 4 chunks lie together; each group of 8 lanes reads other banks
+        const uint4* piece = ring_s + slot * kLpPieceChunks + 4 * tid;
+        const int turn = (tid >> 1) & 3, left = r.held - i - 4 * tid;
+        // (the 64 bytes that hold y itself are counted element by element)
+        const int v0 = r.rc.head + (r.c0 + i + 4 * tid) * N;
+        const bool ahead = v0 + 4 * N <= y;  // all of them before y: equal ones count
+        auto take = [&](const auto& q) {
+          constexpr int M = sizeof(q) / sizeof(q[0]);
+          float z[M * N];
 #pragma unroll
-    for (int g = 0; g < kLpBatch; ++g) q[g] = __ldg(body + at + g * kLpThreads);
+          for (int g = 0; g < M; ++g) {
+            float x[N];
+            unpack_chunk<T>(q[g], x);
 #pragma unroll
-    for (int g = 0; g < kLpBatch; ++g) {
-      float z[N];
-      unpack_chunk<T>(q[g], z);
-      const float bm = max_of(z);
-      smax = fmaxf(smax, bm);
-      rs.template add<N>(z, bm);
-    }
-    if (++in_slot == a.per_slot) {
-      *slot = smax;
-      slot += kLpThreads;
-      tmax = fmaxf(tmax, smax);
-      smax = -INFINITY;
-      in_slot = 0;
-    }
-  }
-  for (; at < c1; at += kLpThreads) {
-    float z[N];
-    unpack_chunk<T>(__ldg(body + at), z);
-    const float bm = max_of(z);
-    smax = fmaxf(smax, bm);
-    rs.template add<N>(z, bm);
-    in_slot = 1;
-  }
-  if (in_slot) {
-    *slot = smax;
-    slot += kLpThreads;
-    tmax = fmaxf(tmax, smax);
-  }
-  const int used = (int)((slot - slot_max) / kLpThreads);
-
-  // ---- the CTA's statistics
-  float m = warp_max(tmax);
-  if (lane == 0) sh.part[warp].x = m;
-  if (tid == 0) {
-    sh.n_cand = 0;
-    sh.n_list = 0;
-    sh.before = 0;
-    sh.n_best = 0;
-    sh.thr = -INFINITY;
-  }
-  __syncthreads();
-  m = sh.part[0].x;
-#pragma unroll
-  for (int w = 1; w < kLpThreads / 32; ++w) m = fmaxf(m, sh.part[w].x);
-  __syncthreads();
-  float s, t;
-  rs.finish(m, s, t);
-  s = warp_sum(s);
-  t = warp_sum(t);
-  if (lane == 0) sh.part[warp] = make_float4(0.f, s, t, 0.f);
-  // ---- a lower bound of the CTA's K-th largest element
-  int G = 32;
-  while (G < 2 * K && G < kLpThreads) G <<= 1;
-  if (K > 0) {
-    sh.gmax[tid] = tmax;
-    __syncthreads();
-    float g = -INFINITY;
-    if (tid < G)
-      for (int j = tid; j < kLpThreads; j += G) g = fmaxf(g, sh.gmax[j]);
-    __syncthreads();
-    if (tid < G) sh.gmax[tid] = g;
-    __syncthreads();
-    if (tid < G) {
-      int r = 0;
-      for (int j = 0; j < G; j += 4) {
-        const float4 o = *reinterpret_cast<const float4*>(&sh.gmax[j]);
-        r += (o.x > g || (o.x == g && j < tid)) + (o.y > g || (o.y == g && j + 1 < tid)) +
-             (o.z > g || (o.z == g && j + 2 < tid)) + (o.w > g || (o.w == g && j + 3 < tid));
-      }
-      if (r == K - 1) sh.thr = g;
-    }
-  }
-  __syncthreads();
-  const float thr = K > 0 ? sh.thr : INFINITY;
-
-  // ---- candidates for the K best and the elements before y: the batches that reach either
-  const float reach = fminf(thr, zy);
-  int before = 0;
-  auto consider = [&](float z, int v) {
-    if (z > zy || (z == zy && v < y)) ++before;
-    if (K > 0 && z >= thr) {
-      const int at = atomicAdd(&sh.n_cand, 1);
-      if (at < kLpCap) sh.cand[at] = top_key(z, v);
-    }
-  };
-  if (K > 0 || a.tokens) {
-    if (tid < loose_n) consider(elem_to_float(row[loose]), loose);
-    auto look = [&](int i) {
-      float z[N];
-      unpack_chunk<T>(__ldg(body + i), z);
-      const float bm = max_of(z);
-      if (bm >= reach) {
-        const int v = rc.head + i * N;
-#pragma unroll
-        for (int e = 0; e < N; ++e) consider(z[e], v + e);
-      }
-    };
-    // the slots that reach it, listed, then their chunks dealt over all threads
-    for (int u = 0; u < used; ++u)
-      if (slot_max[u * kLpThreads + tid] >= reach) {
-        const int at = atomicAdd(&sh.n_list, 1);
-        if (at < kLpList) sh.list[at] = u * kLpThreads + tid;
-      }
-    __syncthreads();
-    const int per = a.per_slot * kLpBatch;
-    if (sh.n_list <= kLpList) {
-      const int tasks = sh.n_list * per;
-      for (int k = tid; k < tasks; k += kLpThreads) {
-        const int e = sh.list[k / per], g = k % per;
-        const int i = c0 + (e & (kLpThreads - 1)) + ((e / kLpThreads) * per + g) * kLpThreads;
-        if (i < c1) look(i);
-      }
-    } else {
-      for (int u = 0; u < used; ++u) {
-        if (slot_max[u * kLpThreads + tid] < reach) continue;
-        const int from = c0 + tid + u * per * kLpThreads, to = min(c1, from + per * kLpThreads);
-        for (int i = from; i < to; i += kLpThreads) look(i);
-      }
-    }
-  }
-  before = __reduce_add_sync(0xffffffffu, before);
-  if (lane == 0 && before) atomicAdd(&sh.before, before);
-  __syncthreads();
-  if (K > 0) {
-    int n_cand = sh.n_cand;
-    if (n_cand > kLpCap) {
-      // more elements at or above the bound than keys fit (equal logits, or all the large
-      // ones in few threads' hands): the same selection tile by tile, keeping the K best
-      int kept = 0;
-      auto sweep = [&](int from, int to) {
-        for (int base = from; base < to; base += kLpCap / 2) {
-          __syncthreads();
-          if (tid == 0) sh.n_cand = kept;
-          for (int j = tid; j < kept; j += kLpThreads) sh.cand[j] = sh.best[j];
-          const unsigned long long floor_key = kept == K ? sh.best[K - 1] : 0ull;
-          __syncthreads();
-          for (int v = base + tid; v < min(to, base + kLpCap / 2); v += kLpThreads) {
-            const float z = elem_to_float(row[v]);
-            const unsigned long long key = top_key(z, v);
-            if (z == z && key > floor_key) sh.cand[atomicAdd(&sh.n_cand, 1)] = key;
+            for (int e = 0; e < N; ++e) z[g * N + e] = x[e];
           }
-          __syncthreads();
-          if (sh.n_cand > kept) kept = select_top(sh, sh.n_cand, K);
+          const float bm = max_of(z);
+          smax = fmaxf(smax, bm);
+          rs.add(z, bm);
+          if (a.tokens) {
+            if (ahead) {
+#pragma unroll
+              for (int e = 0; e < M * N; e += 2)
+                before = f2_add(before, f2(one_if_ge(z[e], zy), one_if_ge(z[e + 1], zy)));
+            } else {
+#pragma unroll
+              for (int e = 0; e < M * N; e += 2)
+                before = f2_add(before, f2(one_if_gt(z[e], zy), one_if_gt(z[e + 1], zy)));
+            }
+          }
+        };
+        constexpr int M = 16 / N;            // chunks of 16 elements
+        if (left >= 4) {
+#pragma unroll
+          for (int g = 0; g < 4; g += M) {
+            uint4 q[M];
+#pragma unroll
+            for (int u = 0; u < M; ++u) q[u] = piece[(g + u + turn) & 3];
+            take(q);
+          }
+        } else {
+          for (int g = 0; g < left; ++g) {
+            const uint4 q[1] = {piece[g]};
+            take(q);
+          }
         }
-      };
-      if (c == 0) sweep(0, rc.head);
-      sweep(rc.head + c0 * N, rc.head + c1 * N);
-      if (c == 0) sweep(V - rc.tail, V);
-      n_cand = -1;
-      if (tid == 0) sh.n_best = kept;
+        if (a.tokens && v0 <= y && y < v0 + 4 * N) {
+          // the 64 bytes that hold y, or end before it: equal elements before it
+          const T* z = reinterpret_cast<const T*>(piece);
+          for (int e = 0; e < min(y - v0, left * N); ++e) before = f2_add(before, f2(elem_to_float(z[e]) == zy ? 1.f : 0.f, 0.f));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.empty[slot]);
+        if (++slot == kLpRing) {
+          slot = 0;
+          phase ^= 1;
+        }
+        const int done = i / kLpPieceChunks + 1;
+        if ((done & ((1 << a.log_per) - 1)) == 0 || i + kLpPieceChunks >= r.held) {
+          *out = smax;
+          out += kLpThreads;
+          tmax = fmaxf(tmax, smax);
+          smax = -INFINITY;
+        }
+      }
+      if (tid < loose_n) {
+        rs.add_one(zl);
+        tmax = fmaxf(tmax, zl);
+        const int v = tid < r.rc.head ? tid : V - r.rc.tail + (tid - r.rc.head);
+        if (zl > zy || (zl == zy && v < y)) before = f2_add(before, f2(1.f, 0.f));
+      }
+      const float m = warp_max(tmax);
+      float s, t;
+      rs.finish(m, s, t);
+      s = warp_sum(s);
+      t = warp_sum(t);
+      float n0, n1;
+      f2_get(before, n0, n1);                // whole numbers below 2^24: V / 512 at most
+      const int n_before = __reduce_add_sync(0xffffffffu, (int)n0 + (int)n1);
+      if (lane == 0) sh.part[b][warp] = make_float4(m, s, t, __int_as_float(n_before));
+      float g = tmax;
+      for (int o = 16; o >= own / kLpWarps; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+      if (lane < own / kLpWarps) {
+        sh.gmax[b][warp * (own / kLpWarps) + lane] = group_key(g);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.stats_full[b]);
+      late = __any_sync(0xffffffffu, late);
+      ++it;
     }
-    if (n_cand >= 0) {
-      const int got = select_top(sh, n_cand, K);
-      if (tid == 0) sh.n_best = got;
+  } else if (warp == kLpWarps) {
+    // ---- producer
+    int sent = 0;
+    RowsOf rows(a.tokens, a.N, V, first, step);
+    for (int n; !late && (n = rows.next()) >= 0;) {
+      if (lane == 0) {
+        const RowPart<T> r = part_of(n);
+        for (int i = 0; i < r.held; i += kLpPieceChunks, ++sent) {
+          const int slot = sent % kLpRing, use = sent / kLpRing;
+          if (use > 0 && !mbar_wait(&sh.empty[slot], (use - 1) & 1)) { late = true; break; }
+          const int k = min(kLpPieceChunks, r.held - i);
+          mbar_arrive_expect_tx(&sh.full[slot], (uint32_t)k * 16u);
+          bulk_load(ring_s + slot * kLpPieceChunks, r.body + r.c0 + i, (uint32_t)k * 16u, &sh.full[slot]);
+        }
+      }
+      late = __any_sync(0xffffffffu, late);
     }
-  }
-  if (C > 1 && K > 0) {
-    __syncthreads();
-    for (int j = sh.n_best + tid; j < K; j += kLpThreads) sh.best[j] = 0ull;
-  }
-  if (tid == 0) {
-    float S = 0.f, Tm = 0.f;
-    for (int w = 0; w < kLpThreads / 32; ++w) {
-      S += sh.part[w].y;
-      Tm += sh.part[w].z;
+    if (lane == 0) {
+      // copies in flight end before the CTA does (at once, unless the consumers gave up)
+      for (int j = max(0, sent - kLpRing); j < sent; ++j) mbar_wait(&sh.full[j % kLpRing], (j / kLpRing) & 1);
     }
-    sh.stat = make_float4(m, S, Tm, __int_as_float(sh.before));
-  }
-  __syncthreads();
-
-  // ---- the cluster's statistics and its K best
-  float M = m, S, Tm;
-  int total_before = 0;
-  if (C > 1) {
-    cluster_sync();
-    // lane o reads CTA o's statistics
-    const float4 p = lane < C ? cluster_ld_f4(cluster_map(&sh.stat, lane))
-                              : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-    M = warp_max(p.x);
-    const float d = p.x - M, f = p.y != 0.f ? ex2_approx(d * kLog2e) : 0.f;
-    S = warp_sum(p.y != 0.f ? p.y * f : 0.f);
-    Tm = warp_sum(f > 0.f ? f * (p.z + d * p.y) : 0.f);
-    total_before = __reduce_add_sync(0xffffffffu, lane < C ? __float_as_int(p.w) : 0);
   } else {
-    S = sh.stat.y;
-    Tm = sh.stat.z;
-    total_before = __float_as_int(sh.stat.w);
-  }
-  const bool bad = !(S <= FLT_MAX);         // NaN or +inf among the logits
-  const float logs = logf(S);
-  if (c == 0 && tid == 0) {
+    // ---- closing warps
+    const int x = tid - kLpThreads - 32;     // 0 .. 127
     const float nan = __int_as_float(0x7FC00000);
-    if (a.tokens) {
-      a.logprob[n] = bad ? nan : S > 0.f ? zy - M - logs : -INFINITY;
-      a.rank[n] = bad ? 0 : total_before + 1;
-    }
-    if (a.entropy) a.entropy[n] = bad ? nan : S > 0.f ? logs - Tm / S : 0.f;
-    if (a.row_max) a.row_max[n] = M;
-    if (a.row_sumexp) a.row_sumexp[n] = bad ? nan : S;
-  }
-  if (K > 0) {
-    auto put = [&](int r, unsigned long long key) {
-      const size_t o = (size_t)n * K + r;
-      const float nan = __int_as_float(0x7FC00000);
-      a.top_ids[o] = bad ? -1 : key_index(key);
-      a.top_logprobs[o] = bad ? nan : S > 0.f ? key_value(key) - M - logs : -INFINITY;
-    };
-    int total = sh.n_best;
-    if (C > 1) {
-      // every list to this CTA's shared memory (0 beyond a list's end)
-      int got = 0;
-      if (lane < C)
-        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(got) : "r"(cluster_map(&sh.n_best, lane)) : "memory");
-      total = __reduce_add_sync(0xffffffffu, got);
-      for (int p = tid; p < C * K; p += kLpThreads) {
-        const int o = p / K, j = p - o * K;
-        // (best is 0 from a list's end on)
-        sh.all[o * kLpTop + j] = cluster_ld_u64(cluster_map(&sh.best[0], o) + 8u * j);
+    // The row that this CTA has yet to merge: the other CTAs' lists are awaited only when the
+    // next row's messages are sent, so that no CTA waits for a merge.
+    struct {
+      int n;
+      uint32_t phase;
+      float M, S, Tm, zy;
+      int before;
+    } pend = {-1, 0u, 0.f, 0.f, 0.f, 0.f, 0};
+    auto merge = [&] {
+      const int n = pend.n;
+      pend.n = -1;
+      if (!wait_cluster(&sh.merge_full, pend.phase)) late = true;
+      const bool bad = !(pend.S <= FLT_MAX); // NaN or +inf among the logits
+      const float logs = logf(pend.S);
+      // keys of the lists up to this lane's
+      int upto = lane < C ? __float_as_int(sh.counts[lane].x) : 0;
+      for (int o = 1; o < 8; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
       }
-      for (int j = tid; j < K; j += kLpThreads) sh.merged[j] = 0;
-      __syncthreads();
-      const int mine = sh.n_best;
-      for (int p = tid; p < mine * C; p += kLpThreads) {
-        const int j = p / C, o = p - j * C;
-        const unsigned long long key = sh.best[j];
-        int lo = 0, hi = K;                 // keys of list o above this one
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if (sh.all[o * kLpTop + mid] > key) lo = mid + 1;
-          else hi = mid;
+      const int total = __shfl_sync(0xffffffffu, upto, 7);
+      if (x == 0) {
+        if (a.tokens) {
+          a.logprob[n] = bad ? nan : pend.S > 0.f ? pend.zy - pend.M - logs : -INFINITY;
+          a.rank[n] = bad ? 0 : pend.before + 1;
         }
-        if (lo) atomicAdd(&sh.merged[j], lo);
+        if (a.entropy) a.entropy[n] = bad ? nan : pend.S > 0.f ? logs - pend.Tm / pend.S : 0.f;
+        if (a.row_max) a.row_max[n] = pend.M;
+        if (a.row_sumexp) a.row_sumexp[n] = bad ? nan : pend.S;
       }
-      __syncthreads();
-      for (int j = tid; j < mine; j += kLpThreads)
-        if (sh.merged[j] < K) put(sh.merged[j], sh.best[j]);
-    } else {
-      for (int j = tid; j < total; j += kLpThreads) put(j, sh.best[j]);
+      auto put = [&](int at, int id, float lp) {
+        const size_t o = (size_t)n * K + at;
+        a.top_ids[o] = bad ? -1 : id;
+        a.top_logprobs[o] = bad ? nan : lp;
+      };
+      // a thread a key: its place is the number of keys above it
+      for (int base = 0; base < total; base += kLpClose) {
+        const int p = base + x;
+        int list = 0, start = 0;
+        for (int o = 0; o < C; ++o) {
+          const int end = __shfl_sync(0xffffffffu, upto, o);
+          if (p >= end) {
+            list = o + 1;
+            start = end;
+          }
+        }
+        const unsigned long long key = p < total ? sh.all[list * K + p - start] : ~0ull;
+        int at = 0, from = 0;
+        for (int o = 0; o < C; ++o) {
+          const int end = __shfl_sync(0xffffffffu, upto, o);
+          const unsigned long long* other = sh.all + o * K;
+#pragma unroll 4
+          for (int j = 0; j < end - from; ++j) at += other[j] > key;
+          from = end;
+        }
+        if (p < total && at < K) put(at, key_index(key), pend.S > 0.f ? key_value(key) - pend.M - logs : -INFINITY);
+      }
+      for (int j = total + x; j < K; j += kLpClose) put(j, -1, -INFINITY);
+      late = close_any(late);                // also: all[] is free for the next row merged here
+    };
+    // the rows without a token
+    if (a.tokens && c == 0)
+      for (int n = first; n < a.N; n += step) {
+        const int y = a.tokens[n];
+        if (y >= 0 && y < V) continue;
+        if (x == 0) {
+          if (y != -1) set_device_error(a.err, DSPARK_ERR_DEVICE_CHECK);
+          a.logprob[n] = 0.f;
+          a.rank[n] = 0;
+          if (a.entropy) a.entropy[n] = 0.f;
+          if (a.row_max) a.row_max[n] = -INFINITY;
+          if (a.row_sumexp) a.row_sumexp[n] = 0.f;
+        }
+        for (int j = x; j < K; j += kLpClose) {
+          a.top_ids[(size_t)n * K + j] = -1;
+          a.top_logprobs[(size_t)n * K + j] = -INFINITY;
+        }
+      }
+    int it = 0;
+    RowsOf rows(a.tokens, a.N, V, first, step);
+    for (int n; (n = rows.next()) >= 0;) {
+      const int y = a.tokens ? a.tokens[n] : 0;
+      const int b = it & 1;
+      const uint32_t buf_phase = (it >> 1) & 1;
+      const int merger = it & (C - 1);       // the CTA that merges this row
+      if (x == 0) {
+        mbar_arrive_expect_tx(&sh.sums_full[b], (uint32_t)(C * kLpWarps * 16 + (K > 0 ? G * 4 : 0)));
+        sh.n_cand = 0;
+        sh.n_list = 0;
+      }
+      const RowPart<T> r = part_of(n);
+      const float zy = a.tokens ? elem_to_float(r.row[y]) : INFINITY;
+      const int loose_n = c == 0 ? r.rc.head + r.rc.tail : 0;
+      const int loose = x < r.rc.head ? x : V - r.rc.tail + (x - r.rc.head);
+      const float zl = x < loose_n ? elem_to_float(r.row[loose]) : -INFINITY;
+
+      // ---- the row's statistics: every CTA's warps' parts to every CTA
+      if (!mbar_wait(&sh.stats_full[b], buf_phase)) late = true;
+      if (x < C * kLpWarps) {                // 64 at most
+        const int o = x / kLpWarps, w = x % kLpWarps;
+        const float4 p = sh.part[b][w];
+        send_f2(&sh.ms[b][c * kLpWarps + w], &sh.sums_full[b], o, p.x, p.y);
+        send_f2(&sh.tb[b][c * kLpWarps + w], &sh.sums_full[b], o, p.z, p.w);
+      }
+      if (K > 0)
+        for (int k = x; k < G; k += kLpClose) {
+          const int o = k >> log_own, j = k & (own - 1);
+          send_f(reinterpret_cast<float*>(&sh.gall[b][c * own + j]), &sh.sums_full[b], o,
+                 __uint_as_float(sh.gmax[b][j]));
+        }
+      if (pend.n >= 0) merge();
+      if (c == merger && x == 0) mbar_arrive_expect_tx(&sh.merge_full, (uint32_t)(C * (8 + 8 * K)));
+      if (!late && !wait_cluster(&sh.sums_full[b], buf_phase)) late = true;
+      late = close_any(late);
+      if (late) break;
+      float M = -INFINITY, S = 0.f, Tm = 0.f;
+      int before = 0;
+      {
+        float2 p[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int w = lane + 32 * i;
+          p[i] = w < C * kLpWarps ? sh.ms[b][w] : make_float2(-INFINITY, 0.f);
+          M = fmaxf(M, p[i].x);
+        }
+        M = warp_max(M);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int w = lane + 32 * i;
+          const float2 tb = w < C * kLpWarps ? sh.tb[b][w] : make_float2(0.f, 0.f);
+          before += __float_as_int(tb.y);
+          if (p[i].y != 0.f) {
+            const float d = p[i].x - M, f = ex2_approx(d * kLog2e);
+            S += p[i].y * f;
+            if (f > 0.f) Tm += f * (tb.x + d * p[i].y);
+          }
+        }
+        S = warp_sum(S);
+        Tm = warp_sum(Tm);
+        before = __reduce_add_sync(0xffffffffu, before);
+      }
+
+      // ---- a lower bound of the row's K-th largest element, from the maxima of its groups
+      const float thr = K > 0 ? group_value(kth_bound(sh.gall[b], G, K)) : INFINITY;
+
+      // ---- candidates for the K best: the slots that reach the bound
+      int got = 0;
+      if (K > 0) {
+        auto consider = [&](float z, int v) {
+          if (z >= thr) {
+            const int to = atomicAdd(&sh.n_cand, 1);
+            if (to < kLpCap) sh.cand[to] = top_key(z, v);
+          }
+        };
+        if (x < loose_n) consider(zl, loose);
+        const int pieces = (r.held + kLpPieceChunks - 1) / kLpPieceChunks;
+        const int used = (pieces + (1 << a.log_per) - 1) >> a.log_per;
+        const float4* maxima = reinterpret_cast<const float4*>(slots_s + b * kLpSlots * kLpThreads);
+        float4 m4[kLpSlots * kLpThreads / 4 / kLpClose];
+#pragma unroll
+        for (int i = 0; i < kLpSlots * kLpThreads / 4 / kLpClose; ++i) {
+          const int e = x + i * kLpClose;
+          m4[i] = e < used * (kLpThreads / 4) ? maxima[e] : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        }
+#pragma unroll
+        for (int i = 0; i < kLpSlots * kLpThreads / 4 / kLpClose; ++i) {
+          const int e = x + i * kLpClose;
+          const int hits = (m4[i].x >= thr) + 2 * (m4[i].y >= thr) + 4 * (m4[i].z >= thr) + 8 * (m4[i].w >= thr);
+          if (hits && e < used * (kLpThreads / 4)) {
+            int to = atomicAdd(&sh.n_list, __popc(hits));
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              if (hits >> u & 1) {
+                if (to < kLpList) sh.list[to] = 4 * e + u;
+                ++to;
+              }
+          }
+        }
+        close_sync();
+        auto look = [&](int entry, int g) {  // chunk g of an entry's slot
+          const int j = (((entry / kLpThreads) << a.log_per) + (g >> 2)) * kLpPieceChunks +
+                        4 * (entry & (kLpThreads - 1)) + (g & 3);
+          if (j >= r.held) return;
+          float z[N];
+          unpack_chunk<T>(__ldg(r.body + r.c0 + j), z);
+          if (max_of(z) >= thr) {
+            const int v = r.rc.head + (r.c0 + j) * N;
+#pragma unroll
+            for (int e = 0; e < N; ++e) consider(z[e], v + e);
+          }
+        };
+        const int log_per = a.log_per + 2, n_list = sh.n_list;
+        if (n_list <= kLpList) {
+          for (int k = x; k < n_list << log_per; k += kLpClose) look(sh.list[k >> log_per], k & ((1 << log_per) - 1));
+        } else {
+          for (int e = x; e < used * kLpThreads; e += kLpClose)
+            if (reinterpret_cast<const float*>(maxima)[e] >= thr)
+              for (int g = 0; g < 1 << log_per; ++g) look(e, g);
+        }
+        close_sync();
+        if (x == 0) mbar_arrive(&sh.stats_free[b]);
+        const int n_cand = sh.n_cand;
+        if (n_cand <= K) {                   // (the merge ranks them)
+          got = n_cand;
+          for (int j = x; j < K; j += kLpClose) sh.best[j] = j < n_cand ? sh.cand[j] : 0ull;
+          close_sync();
+        } else if (n_cand <= kLpCap) {
+          got = select_top(sh, x, n_cand, K);
+        } else {
+          // more elements at or above the bound than keys fit (equal logits, or all the large
+          // ones in few threads' hands): the same selection tile by tile, keeping the K best
+          auto sweep = [&](int from, int to) {
+            for (int base = from; base < to; base += kLpCap / 2) {
+              close_sync();
+              if (x == 0) sh.n_cand = got;
+              for (int j = x; j < got; j += kLpClose) sh.cand[j] = sh.best[j];
+              const unsigned long long floor_key = got == K ? sh.best[K - 1] : 0ull;
+              close_sync();
+              for (int v = base + x; v < min(to, base + kLpCap / 2); v += kLpClose) {
+                const float z = elem_to_float(r.row[v]);
+                const unsigned long long key = top_key(z, v);
+                if (z == z && key > floor_key) sh.cand[atomicAdd(&sh.n_cand, 1)] = key;
+              }
+              close_sync();
+              if (sh.n_cand > got) got = select_top(sh, x, sh.n_cand, K);
+            }
+          };
+          if (c == 0) sweep(0, r.rc.head);
+          sweep(r.rc.head + r.c0 * N, r.rc.head + r.c1 * N);
+          if (c == 0) sweep(V - r.rc.tail, V);
+          if (got == 0) select_top(sh, x, 0, K);
+        }
+        for (int j = x; j < K; j += kLpClose) send_u64(&sh.all[c * K + j], &sh.merge_full, merger, sh.best[j]);
+      } else if (x == 0) {
+        mbar_arrive(&sh.stats_free[b]);
+      }
+      if (x == 0) send_f2(&sh.counts[c], &sh.merge_full, merger, __int_as_float(got), 0.f);
+
+      if (c == merger) {
+        pend.n = n;
+        pend.phase = (it >> log_C) & 1;
+        pend.M = M;
+        pend.S = S;
+        pend.Tm = Tm;
+        pend.zy = zy;
+        pend.before = before;
+      }
+      ++it;
     }
-    if (c == 0)
-      for (int j = total + tid; j < K; j += kLpThreads) {
-        a.top_ids[(size_t)n * K + j] = -1;
-        a.top_logprobs[(size_t)n * K + j] = bad ? __int_as_float(0x7FC00000) : -INFINITY;
-      }
+    if (pend.n >= 0 && !late) merge();
   }
-  if (C > 1) cluster_sync();                // no CTA leaves while another reads its lists
+  if (late) set_device_error(a.err, DSPARK_ERR_TIMEOUT);
+  __syncwarp();
+  if (C > 1) cluster_sync();                 // no CTA leaves while another may still send to it
 }
 
 // ------------------------------------------------------------------------------ gradient
@@ -486,31 +741,33 @@ __global__ void __launch_bounds__(kLgThreads) token_logprobs_grad_kernel(LgParam
   }
 }
 
-// CTAs a row is cut into: enough work items to fill the GPU several times over (4 CTAs an
-// SM), but no segment below 2048 chunks (32 KB), under which a CTA's fixed work shows
-int row_ctas(long long rows, long long chunks) {
-  int C = 1;
-  while (C < 8 && (rows * C < 4LL * kTargetCtas) && chunks / (2 * C) >= 2048) C *= 2;
-  // few rows: the latency of a segment counts, down to one batch per thread
-  while (C < 8 && rows * C < 152 && chunks / (2 * C) >= kLpThreads) C *= 2;
-  return C;
-}
-
 template <typename T>
-cudaError_t launch_lp(LpParams p, int N, cudaStream_t stream) {
+cudaError_t launch_lp(LpParams p, cudaStream_t stream) {
   const int chunks = p.V / Chunk<T>::N;
-  const int C = row_ctas(N, chunks);
-  const int batches = cdiv(cdiv(chunks + 1, C), kLpThreads * kLpBatch) + 1;
-  p.per_slot = cdiv(batches, kLpMaxSlots);
-  p.slots = cdiv(batches, p.per_slot) + 1;
-  const size_t smem = (size_t)p.slots * kLpThreads * sizeof(float);
-  static std::atomic<int> cache[kMaxCachedDevices];
-  const int ok = per_device_grid(cache, [] {
-    return cudaFuncSetAttribute(token_logprobs_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (kLpMaxSlots + 2) * kLpThreads * (int)sizeof(float)) == cudaSuccess ? 1 : -1;
-  });
-  if (ok <= 0) return cudaErrorInvalidConfiguration;
-  return launch_rows_cluster(token_logprobs_kernel<T>, (long long)N * C, C, kLpThreads, smem, stream, p, C);
+  const size_t smem = (size_t)kLpRing * kLpPieceChunks * 16 + 2 * kLpSlots * kLpThreads * sizeof(float);
+  static std::atomic<int> cache[4][kMaxCachedDevices];
+  // CTAs a row is cut into: the fewest estimated cycles, a CTA streaming 12 bytes a cycle and
+  // closing a row in 12000 (measured with both CTAs of an SM at work), beside the next row's
+  // stream.  1536 rows of 129280 in fp32: 1, 2, 4, 8 CTAs took 159, 151, 189, 312 us
+  int log_C = 0, clusters = 0;
+  long long best = 0;
+  for (int i = 3; i >= 0; --i) {
+    if (i > 0 && (chunks >> i) < kLpPieceChunks) continue;
+    const int most = device_clusters(cache[i], token_logprobs_kernel<T>, 1 << i, kLpBlock, smem);
+    if (most <= 0) return cudaErrorInvalidConfiguration;
+    const long long stream_c = (long long)(chunks >> i) * 16 / 12, close_c = 12000;
+    const long long rounds = cdiv(p.N, most);
+    const long long cost = stream_c + (rounds - 1) * (stream_c > close_c ? stream_c : close_c) + close_c;
+    if (clusters == 0 || cost < best) {
+      best = cost;
+      log_C = i;
+      clusters = p.N < most ? p.N : most;
+    }
+  }
+  const int pieces = cdiv((chunks >> log_C) + 1, kLpPieceChunks);
+  while (pieces > kLpSlots << p.log_per) ++p.log_per;
+  return launch_rows_cluster(token_logprobs_kernel<T>, (long long)clusters << log_C, 1 << log_C, kLpBlock, smem, stream,
+                             p, log_C);
 }
 
 template <typename T>
@@ -532,13 +789,13 @@ cudaError_t launch_token_logprobs(const void* z, int dtype, long long ld, const 
                                   float* row_max, float* row_sumexp, int32_t* top_ids,
                                   float* top_logprobs, int* err, cudaStream_t stream) {
   LpParams p = {};
-  p.z = z; p.ld = ld; p.tokens = tokens; p.V = V; p.K = K;
+  p.z = z; p.ld = ld; p.tokens = tokens; p.N = N; p.V = V; p.K = K;
   p.logprob = logprob; p.entropy = entropy; p.rank = rank; p.row_max = row_max;
   p.row_sumexp = row_sumexp; p.top_ids = top_ids; p.top_logprobs = top_logprobs; p.err = err;
   switch (dtype) {
-    case DSPARK_F32: return launch_lp<float>(p, N, stream);
-    case DSPARK_BF16: return launch_lp<__nv_bfloat16>(p, N, stream);
-    default: return launch_lp<__half>(p, N, stream);
+    case DSPARK_F32: return launch_lp<float>(p, stream);
+    case DSPARK_BF16: return launch_lp<__nv_bfloat16>(p, stream);
+    default: return launch_lp<__half>(p, stream);
   }
 }
 

@@ -10,6 +10,7 @@
 #include <stdint.h>
 
 #include "common.cuh"
+#include "sm100_ptx.cuh"
 
 namespace dspark {
 
@@ -142,6 +143,13 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
+// the same in two halves
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
 __device__ __forceinline__ uint32_t cluster_map(const void* smem, uint32_t rank) {
   uint32_t a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
@@ -155,6 +163,11 @@ __device__ __forceinline__ float4 cluster_ld_f4(uint32_t addr) {
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
                : "r"(addr)
                : "memory");
+  return v;
+}
+__device__ __forceinline__ float cluster_ld_f(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
 __device__ __forceinline__ unsigned long long cluster_ld_u64(uint32_t addr) {
@@ -185,6 +198,71 @@ __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int m = 16; m >= 1; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
   return x;
+}
+
+// ---------------------------------------------------------------- copies and messages
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          sm100::smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(sm100::smem_u32(bar))
+      : "memory");
+}
+// stores into CTA `rank`'s copy of *dst, counted in bytes by its copy of *bar
+__device__ __forceinline__ void send_f2(float2* dst, uint64_t* bar, uint32_t rank, float x, float y) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
+                   cluster_map(dst, rank)),
+               "f"(x), "f"(y), "r"(cluster_map(bar, rank))
+               : "memory");
+}
+__device__ __forceinline__ void send_f(float* dst, uint64_t* bar, uint32_t rank, float x) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
+                   cluster_map(dst, rank)),
+               "r"(__float_as_uint(x)), "r"(cluster_map(bar, rank))
+               : "memory");
+}
+__device__ __forceinline__ void send_u64(unsigned long long* dst, uint64_t* bar, uint32_t rank,
+                                         unsigned long long x) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(
+                   cluster_map(dst, rank)),
+               "l"(x), "r"(cluster_map(bar, rank))
+               : "memory");
+}
+// a wait on data that other CTAs of the cluster send
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity) {
+  const long long t0 = sm100::sm_cycles();
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(sm100::smem_u32(bar)), "r"(parity), "r"(10000000u)
+        : "memory");
+    if (ok) return true;
+    if (sm100::sm_cycles() - t0 > sm100::kWaitCycles) return false;
+  }
+}
+
+template <typename T>
+struct RowPart {             // a CTA's part [c0, c1) of a row's chunks, `held` of them kept
+  const T* row;
+  const uint4* body;
+  RowChunks rc;
+  int c0, c1, held;
+};
+template <typename T>
+__device__ __forceinline__ RowPart<T> row_part(const void* z, long long ld, int n, int V, int c, int log_C,
+                                               int most) {
+  RowPart<T> r;
+  r.row = static_cast<const T*>(z) + (long long)n * ld;
+  r.rc = row_chunks(r.row, V);
+  r.body = reinterpret_cast<const uint4*>(r.row + r.rc.head);
+  r.c0 = (int)((long long)r.rc.chunks * c >> log_C);
+  r.c1 = (int)((long long)r.rc.chunks * (c + 1) >> log_C);
+  r.held = min(r.c1 - r.c0, most);
+  return r;
 }
 
 // ------------------------------------------------------------- running softmax statistics
