@@ -10,10 +10,11 @@
 // sorted by (id, position), and tiles of consecutive sorted positions are summed in fp32,
 // whatever the token frequencies.  A run of one id inside a tile is written at once; a run
 // that crosses tiles leaves partial sums that are joined in tile order, first within a CTA
-// (8 tiles, shared memory), then by a last kernel (workspace).  Up to 8192 positions are
-// sorted by counting (every item against every key, 1 launch), more by a radix sort of 9
-// bits a pass.  The table's zeroes are the bulk of the bytes: CTAs of every launch
-// write a share of them, beside the sort and the sums.
+// (8 tiles, shared memory), then by a last kernel (workspace).  The sort is a stable
+// radix sort of 9 bits a pass, by one cluster of CTAs up to 131072 positions (1 launch), by the
+// grid above (2 launches a pass); up to 2048 positions need none (eg_range_kernel).  The
+// table's zeroes, the bulk of the bytes, are written in the sort's launch by the CTAs that do
+// not sort, so that the sort hides behind them.
 #include "internal.h"
 #include "rows.cuh"
 
@@ -22,8 +23,7 @@ namespace {
 
 constexpr int kEmThreads = 256;
 constexpr int kEmWarps = kEmThreads / 32;
-constexpr int kRankMost = 8192;             // positions sorted by counting
-constexpr int kRankItems = 32;              // items of a counting CTA, 8 threads each
+constexpr int kSortMost = 131072;           // positions sorted by one cluster
 constexpr int kRadixBits = 9, kRadix = 1 << kRadixBits;
 constexpr int kRadixTile = 2048;            // keys of a radix CTA
 constexpr int kRadixRounds = kRadixTile / kEmThreads;
@@ -125,18 +125,6 @@ __device__ __forceinline__ int key_of(const EgParams& a, int n) {
   return a.V;
 }
 
-// The table's zeroes are dealt over every launch of the call (`fill` CTAs of each), so that
-// they hide the sort and the sums: before the sums all rows of a CTA's share, with the sums
-// and after them only the rows that no position has.
-struct Fill {
-  int first;                 // the launch's first filling CTA in its grid
-  int from, all;             // its share is part (blockIdx - first) + from of `all`
-};
-__device__ __forceinline__ void share_of(const EgParams& a, const Fill& f, int& v0, int& v1) {
-  const long long part = f.from + ((int)blockIdx.x - f.first);
-  v0 = (int)((long long)a.V * part / f.all);
-  v1 = (int)((long long)a.V * (part + 1) / f.all);
-}
 // `bytes` zeroes from p on, by `threads` threads
 __device__ __forceinline__ void zero_bytes(char* p, long long bytes, int t, int threads) {
   const uint4 z = make_uint4(0u, 0u, 0u, 0u);
@@ -155,9 +143,9 @@ __device__ __forceinline__ void zero_bytes(char* p, long long bytes, int t, int 
   if (t < head) p[t] = 0;
   if (t < tail) p[bytes - tail + t] = 0;
 }
-__device__ __forceinline__ void fill_rows(const EgParams& a, const Fill& f) {
-  int v0, v1;
-  share_of(a, f, v0, v1);
+// Filling CTA `part` of `parts` zeroes its share of the table's rows.
+__device__ __forceinline__ void fill_rows(const EgParams& a, int part, int parts) {
+  const int v0 = (int)((long long)a.V * part / parts), v1 = (int)((long long)a.V * (part + 1) / parts);
   const long long row = (long long)a.D * a.elem_w, step = a.ld_w * a.elem_w;
   char* base = static_cast<char*>(a.dW) + v0 * step;
   if (step == row) {
@@ -167,134 +155,156 @@ __device__ __forceinline__ void fill_rows(const EgParams& a, const Fill& f) {
       zero_bytes(base + v * step, row, threadIdx.x & 31, 32);
   }
 }
-// The same without the rows of the sorted keys: `block` threads mark them in shared memory,
-// kFillRows rows at a time.
-constexpr int kFillRows = 2048;
-__device__ __forceinline__ void fill_other_rows(const EgParams& a, const Fill& f, const int* skey,
-                                                uint32_t* marks, int block) {
-  __shared__ int found_s;
-  int v0, v1;
-  share_of(a, f, v0, v1);
-  const long long row = (long long)a.D * a.elem_w, step = a.ld_w * a.elem_w;
-  char* base = static_cast<char*>(a.dW);
-  // the first sorted position of a key >= v0: `block` probes at a time
-  int lo = 0, hi = a.N;
-  while (hi > lo) {
-    const int width = (hi - lo + block - 1) / block;
-    const int at = lo + (int)threadIdx.x * width;
-    __syncthreads();
-    if (threadIdx.x == 0) found_s = 0;
-    __syncthreads();
-    const unsigned below = __ballot_sync(0xffffffffu, at < hi && skey[at] < v0);
-    if ((threadIdx.x & 31) == 0 && below) atomicAdd(&found_s, __popc(below));
-    __syncthreads();
-    const int n = found_s;                  // probes 0 .. n - 1 are below v0
-    const int end = hi;
-    hi = min(end, lo + n * width);
-    lo = n == 0 ? lo : lo + (n - 1) * width + 1;
-    if (n == 0) hi = lo;
-  }
-  for (int r0 = v0; r0 < v1; r0 += kFillRows) {
-    const int r1 = min(v1, r0 + kFillRows);
-    __syncthreads();
-    for (int i = threadIdx.x; i < kFillRows / 32; i += block) marks[i] = 0u;
-    __syncthreads();
-    // this part's keys, `block` at a time
-    for (;;) {
-      const int i = lo + threadIdx.x;
-      const int k = i < a.N ? skey[i] : a.V;
-      if (k < r1) atomicOr(&marks[(k - r0) >> 5], 1u << ((k - r0) & 31));
-      const int n = __syncthreads_count(k < r1);
-      lo += n;
-      if (n < block) break;
-    }
-    for (int v = r0 + (threadIdx.x >> 5); v < r1; v += block / 32)
-      if (!(marks[(v - r0) >> 5] >> ((v - r0) & 31) & 1u)) zero_bytes(base + v * step, row, threadIdx.x & 31, 32);
-  }
-}
 
-// every item's place among all keys: the keys below it, and the equal ones before it
-__global__ void __launch_bounds__(kEmThreads) eg_rank_kernel(EgParams a, Fill f) {
-  extern __shared__ int4 keys4[];
-  int* keys = reinterpret_cast<int*>(keys4);
-  pdl_wait();
-  pdl_launch_dependents();
-  if ((int)blockIdx.x >= f.first) {
-    fill_rows(a, f);
-    return;
-  }
-  const int n4 = (a.N + 3) / 4;
-  for (int i = threadIdx.x; i < 4 * n4; i += kEmThreads) keys[i] = i < a.N ? key_of(a, i) : 0x7FFFFFFF;
-  __syncthreads();
-  const int item = blockIdx.x * kRankItems + (threadIdx.x >> 3), sub = threadIdx.x & 7;
-  const int k = item < a.N ? keys[item] : 0;
-  int r = 0;
-  const int own = item >> 2;
-  for (int j = sub; j < n4; j += 8) {
-    const int4 o = keys4[j];
-    if (j == own) {
-      const int m = 4 * j;
-      r += (o.x < k || (o.x == k && m < item)) + (o.y < k || (o.y == k && m + 1 < item)) +
-           (o.z < k || (o.z == k && m + 2 < item)) + (o.w < k || (o.w == k && m + 3 < item));
-    } else {
-      const int below = j < own ? k : k - 1;
-      r += (o.x <= below) + (o.y <= below) + (o.z <= below) + (o.w <= below);
-    }
-  }
-#pragma unroll
-  for (int m = 4; m >= 1; m >>= 1) r += __shfl_xor_sync(0xffffffffu, r, m);
-  if (sub == 0 && item < a.N) {
-    a.key[0][r] = k;
-    a.pos[0][r] = item;
-  }
-}
+struct RadixShared {
+  int warp[kEmWarps][kRadix];   // a warp's keys of each digit, then its places
+  int base[kRadix];             // places of the next tile's keys of each digit
+  int hist[kRadix];
+  int sum[kEmWarps];
+};
 
-// radix pass: digit counts of every tile
-__global__ void __launch_bounds__(kEmThreads) eg_count_kernel(EgParams a, int pass, Fill f) {
-  __shared__ int hist[kRadix];
-  pdl_wait();
-  pdl_launch_dependents();
-  if ((int)blockIdx.x >= f.first) {
-    fill_rows(a, f);
-    return;
-  }
-  for (int i = threadIdx.x; i < kRadix; i += kEmThreads) hist[i] = 0;
-  __syncthreads();
-  const int* in = a.key[(pass & 1) ^ 1];
-  const int base = blockIdx.x * kRadixTile, shift = pass * kRadixBits;
-#pragma unroll
-  for (int i = 0; i < kRadixRounds; ++i) {
-    const int n = base + i * kEmThreads + threadIdx.x;
-    if (n < a.N) {
-      const int k = pass == 0 ? key_of(a, n) : in[n];
-      atomicAdd(&hist[(k >> shift) & (kRadix - 1)], 1);
-    }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < kRadix; i += kEmThreads) a.counts[(size_t)blockIdx.x * kRadix + i] = hist[i];
-}
-
-// radix pass: every key to its place, equal digits in their order
-__global__ void __launch_bounds__(kEmThreads) eg_scatter_kernel(EgParams a, int pass, Fill f) {
-  __shared__ int wh[kEmWarps][kRadix];
-  __shared__ int base_s[kRadix];
-  __shared__ int warp_s[kEmWarps];
-  pdl_wait();
-  pdl_launch_dependents();
-  if ((int)blockIdx.x >= f.first) {
-    fill_rows(a, f);
-    return;
-  }
+// The keys [from, from + kRadixTile) below `end` to their places, equal digits in their order;
+// rs.base moves on.  All threads; rs.base is ready.
+__device__ __forceinline__ void scatter_tile(const EgParams& a, int pass, int from, int end, RadixShared& rs) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int shift = pass * kRadixBits;
   const int* in_k = a.key[(pass & 1) ^ 1];
   const int* in_p = a.pos[(pass & 1) ^ 1];
-  for (int i = tid; i < kEmWarps * kRadix; i += kEmThreads) (&wh[0][0])[i] = 0;
-  // bins 2 tid and 2 tid + 1: keys of this digit in the tiles before, and in all
+  __syncthreads();                          // rs.warp is free
+  for (int i = tid; i < kEmWarps * kRadix; i += kEmThreads) (&rs.warp[0][0])[i] = 0;
+  int k[kRadixRounds], p[kRadixRounds], r[kRadixRounds];
+#pragma unroll
+  for (int i = 0; i < kRadixRounds; ++i) {
+    const int n = from + warp * (kRadixTile / kEmWarps) + 32 * i + lane;
+    const bool on = n < end;
+    k[i] = !on ? 0 : pass == 0 ? key_of(a, n) : in_k[n];
+    p[i] = !on ? -1 : pass == 0 ? n : in_p[n];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kRadixRounds; ++i) {
+    const int d = p[i] >= 0 ? (k[i] >> shift) & (kRadix - 1) : kRadix;    // kRadix: no key
+    const unsigned same = __match_any_sync(0xffffffffu, d);
+    const int had = p[i] >= 0 ? rs.warp[warp][d] : 0;
+    __syncwarp();
+    if (p[i] >= 0 && lane == __ffs(same) - 1) rs.warp[warp][d] = had + __popc(same);
+    __syncwarp();
+    r[i] = had + __popc(same & ((1u << lane) - 1u));
+  }
+  __syncthreads();
+  for (int b = tid; b < kRadix; b += kEmThreads) {
+    int sum = rs.base[b];
+#pragma unroll
+    for (int w = 0; w < kEmWarps; ++w) {
+      const int x = rs.warp[w][b];
+      rs.warp[w][b] = sum;
+      sum += x;
+    }
+    rs.base[b] = sum;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kRadixRounds; ++i)
+    if (p[i] >= 0) {
+      const int to = rs.warp[warp][(k[i] >> shift) & (kRadix - 1)] + r[i];
+      a.key[pass & 1][to] = k[i];
+      a.pos[pass & 1][to] = p[i];
+    }
+}
+
+// rs.base of a part whose digits 2 tid and 2 tid + 1 have `before` keys in earlier parts and
+// `all` in all parts.  All threads.
+__device__ __forceinline__ void radix_base(const int (&before)[2], const int (&all)[2], RadixShared& rs) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int pair = all[0] + all[1];
+  int scan = pair;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, scan, m);
+    if (lane >= m) scan += o;
+  }
+  if (lane == 31) rs.sum[warp] = scan;
+  __syncthreads();
+  int first = scan - pair;
+  for (int w = 0; w < warp; ++w) first += rs.sum[w];
+  rs.base[2 * tid] = first + before[0];
+  rs.base[2 * tid + 1] = first + all[0] + before[1];
+}
+
+// digit counts of the keys [from, end), by all threads
+__device__ __forceinline__ void radix_hist(const EgParams& a, int pass, int from, int end, RadixShared& rs) {
+  const int tid = threadIdx.x;
+  const int* in = a.key[(pass & 1) ^ 1];
+  __syncthreads();
+  for (int i = tid; i < kRadix; i += kEmThreads) rs.hist[i] = 0;
+  __syncthreads();
+  for (int n = from + tid; n < from + (end - from + 31) / 32 * 32; n += kEmThreads) {
+    // (whole warps: lanes of one digit add once)
+    const int k = n >= end ? -1 : pass == 0 ? key_of(a, n) : in[n];
+    const int d = k < 0 ? kRadix : (k >> (pass * kRadixBits)) & (kRadix - 1);
+    const unsigned same = __match_any_sync(0xffffffffu, d);
+    if (k >= 0 && (tid & 31) == __ffs(same) - 1) atomicAdd(&rs.hist[d], __popc(same));
+  }
+  __syncthreads();
+}
+
+// The whole sort by one cluster of 8 CTAs, each with an eighth of the keys; the grid's other
+// clusters write the table's zeroes meanwhile.
+__global__ void __launch_bounds__(kEmThreads) eg_sort_kernel(EgParams a, int passes) {
+  __shared__ RadixShared rs;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (blockIdx.x >= 8) {
+    fill_rows(a, blockIdx.x - 8, gridDim.x - 8);
+    return;
+  }
+  const int c = blockIdx.x, tid = threadIdx.x;
+  const int from = (int)((long long)a.N * c / 8), end = (int)((long long)a.N * (c + 1) / 8);
+  for (int pass = 0; pass < passes; ++pass) {
+    radix_hist(a, pass, from, end, rs);
+    cluster_sync();
+    int before[2] = {0, 0}, all[2] = {0, 0};
+#pragma unroll
+    for (int o = 0; o < 8; ++o) {
+      const unsigned long long two = cluster_ld_u64(cluster_map(&rs.hist[2 * tid], o));
+      const int n0 = (int)(uint32_t)two, n1 = (int)(two >> 32);
+      all[0] += n0;
+      all[1] += n1;
+      if (o < c) {
+        before[0] += n0;
+        before[1] += n1;
+      }
+    }
+    radix_base(before, all, rs);
+    for (int t = from; t < end; t += kRadixTile) scatter_tile(a, pass, t, end, rs);
+    cluster_sync();                         // the keys are in place, and the counts are read
+  }
+}
+
+// radix pass over many keys: digit counts of every tile; in the first pass the grid's CTAs
+// beyond the tiles write the table's zeroes
+__global__ void __launch_bounds__(kEmThreads) eg_count_kernel(EgParams a, int pass, int tiles) {
+  __shared__ RadixShared rs;
+  pdl_wait();
+  pdl_launch_dependents();
+  if ((int)blockIdx.x >= tiles) {
+    fill_rows(a, blockIdx.x - tiles, gridDim.x - tiles);
+    return;
+  }
+  const int from = blockIdx.x * kRadixTile;
+  radix_hist(a, pass, from, min(a.N, from + kRadixTile), rs);
+  for (int i = threadIdx.x; i < kRadix; i += kEmThreads) a.counts[(size_t)blockIdx.x * kRadix + i] = rs.hist[i];
+}
+
+// radix pass: every key to its place
+__global__ void __launch_bounds__(kEmThreads) eg_scatter_kernel(EgParams a, int pass) {
+  __shared__ RadixShared rs;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, tile = blockIdx.x, tiles = gridDim.x;
   int before[2] = {0, 0}, all[2] = {0, 0};
-  const int tile = blockIdx.x;
 #pragma unroll 8
-  for (int t = 0; t < f.first; ++t) {
+  for (int t = 0; t < tiles; ++t) {
     const int2 n = *reinterpret_cast<const int2*>(a.counts + (size_t)t * kRadix + 2 * tid);
     all[0] += n.x;
     all[1] += n.y;
@@ -303,57 +313,8 @@ __global__ void __launch_bounds__(kEmThreads) eg_scatter_kernel(EgParams a, int 
       before[1] += n.y;
     }
   }
-  const int pair = all[0] + all[1];
-  int scan = pair;
-#pragma unroll
-  for (int m = 1; m < 32; m <<= 1) {
-    const int o = __shfl_up_sync(0xffffffffu, scan, m);
-    if (lane >= m) scan += o;
-  }
-  if (lane == 31) warp_s[warp] = scan;
-  __syncthreads();                          // also: wh is zero
-  int first = scan - pair;
-  for (int w = 0; w < warp; ++w) first += warp_s[w];
-  base_s[2 * tid] = first + before[0];
-  base_s[2 * tid + 1] = first + all[0] + before[1];
-  // this warp's keys, in order, 32 at a time
-  int k[kRadixRounds], p[kRadixRounds], r[kRadixRounds];
-  const int from = tile * kRadixTile + warp * (kRadixTile / kEmWarps);
-#pragma unroll
-  for (int i = 0; i < kRadixRounds; ++i) {
-    const int n = from + 32 * i + lane;
-    const bool on = n < a.N;
-    k[i] = !on ? 0 : pass == 0 ? key_of(a, n) : in_k[n];
-    p[i] = !on ? -1 : pass == 0 ? n : in_p[n];
-  }
-#pragma unroll
-  for (int i = 0; i < kRadixRounds; ++i) {
-    const int d = p[i] >= 0 ? (k[i] >> shift) & (kRadix - 1) : kRadix;    // kRadix: no key
-    const unsigned same = __match_any_sync(0xffffffffu, d);
-    const int had = p[i] >= 0 ? wh[warp][d] : 0;
-    __syncwarp();
-    if (p[i] >= 0 && lane == __ffs(same) - 1) wh[warp][d] = had + __popc(same);
-    __syncwarp();
-    r[i] = had + __popc(same & ((1u << lane) - 1u));
-  }
-  __syncthreads();
-  for (int b = tid; b < kRadix; b += kEmThreads) {
-    int sum = base_s[b];
-#pragma unroll
-    for (int w = 0; w < kEmWarps; ++w) {
-      const int x = wh[w][b];
-      wh[w][b] = sum;
-      sum += x;
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kRadixRounds; ++i)
-    if (p[i] >= 0) {
-      const int to = wh[warp][(k[i] >> shift) & (kRadix - 1)] + r[i];
-      a.key[pass & 1][to] = k[i];
-      a.pos[pass & 1][to] = p[i];
-    }
+  radix_base(before, all, rs);
+  scatter_tile(a, pass, tile * kRadixTile, a.N, rs);
 }
 
 // A lane's N columns of column block cb: vector columns lie together, scalar ones 32 apart.
@@ -399,7 +360,7 @@ __device__ __forceinline__ void put_part(const EgParams& a, int tile, int slot, 
 // Sums of the sorted positions: CTA = 8 consecutive tiles of P positions (a warp each) x one
 // column block.
 template <typename T, typename O, bool Vec>
-__global__ void __launch_bounds__(kEmThreads) eg_sum_kernel(EgParams a, int buf, Fill f) {
+__global__ void __launch_bounds__(kEmThreads) eg_sum_kernel(EgParams a, int buf) {
   constexpr int N = Chunk<T>::N;
   constexpr int kAhead = 8;                 // rows in flight
   __shared__ float part_s[kEmWarps][2][N][32];
@@ -409,10 +370,6 @@ __global__ void __launch_bounds__(kEmThreads) eg_sum_kernel(EgParams a, int buf,
   pdl_launch_dependents();
   const int* skey = a.key[buf];
   const int* spos = a.pos[buf];
-  if ((int)blockIdx.x >= f.first) {
-    fill_other_rows(a, f, skey, reinterpret_cast<uint32_t*>(part_s), kEmThreads);
-    return;
-  }
   const int P = a.P, V = a.V;
   const int cta0 = cta * kEmWarps * P;
   const int i0 = min(a.N, cta0 + warp * P), i1 = min(a.N, i0 + P), cnt = i1 - i0;
@@ -512,17 +469,13 @@ __global__ void __launch_bounds__(kEmThreads) eg_sum_kernel(EgParams a, int buf,
 // Runs across CTA tiles: CTA (t, cb) sums the run that begins in t and goes on.  Four warps
 // take consecutive parts of its tiles, joined in order.
 template <typename O, int N, bool Vec>
-__global__ void __launch_bounds__(128) eg_join_kernel(EgParams a, int buf, Fill f) {
+__global__ void __launch_bounds__(128) eg_join_kernel(EgParams a, int buf) {
   __shared__ float part_s[4][N][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x / a.cols, cb = blockIdx.x - t * a.cols;
   pdl_wait();
   pdl_launch_dependents();
   const int* skey = a.key[buf];
-  if ((int)blockIdx.x >= f.first) {
-    fill_other_rows(a, f, skey, reinterpret_cast<uint32_t*>(part_s), 128);
-    return;
-  }
   const int span = kEmWarps * a.P;
   const int i0 = t * span, i1 = i0 + span;
   if (i1 >= a.N) return;
@@ -565,6 +518,176 @@ __global__ void __launch_bounds__(128) eg_join_kernel(EgParams a, int buf, Fill 
   }
 }
 
+// Few positions: a CTA owns the table rows [range kRangeRows ..) of one column block (of all of
+// them where rows are not 16-byte aligned).  It finds the positions of its rows among all ids,
+// orders them by (id, position) with a counting sort in shared memory, zeroes the rows that
+// have none and sums the others: one launch, and nothing waits for anything.  A run of
+// kLongRun positions or more is summed by the CTA's eight warps, joined in order.
+constexpr int kRangeMost = 2048;            // positions
+constexpr int kRangeRows = 2048;            // rows of a CTA, at most
+constexpr int kLongRun = 64;
+template <typename T, typename O, bool Vec>
+__global__ void __launch_bounds__(kEmThreads) eg_range_kernel(EgParams a, int rows, int col_ctas) {
+  constexpr int N = Chunk<T>::N;
+  constexpr int kAhead = 8;
+  __shared__ int count_s[kRangeRows];       // positions of a row
+  __shared__ int start_s[kRangeRows];       // its first place in pos_s, then the place after its last
+  __shared__ int row_s[kRangeMost];         // of every position: its row here, or -1
+  __shared__ int pos_s[kRangeMost];
+  __shared__ int hit_s[kRangeMost];         // rows with positions: short runs first, long ones last
+  __shared__ int n_short_s, n_long_s, next_s;
+  __shared__ float part_s[kEmWarps][N][32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int range = blockIdx.x / col_ctas, cb0 = blockIdx.x - range * col_ctas;
+  const int cb1 = Vec ? cb0 + 1 : a.cols;
+  const int v0 = range * rows, n_rows = min(a.V - v0, rows);
+  pdl_wait();
+  pdl_launch_dependents();
+  for (int i = tid; i < n_rows; i += kEmThreads) count_s[i] = 0;
+  if (tid == 0) n_short_s = n_long_s = next_s = 0;
+  __syncthreads();
+  for (int n = tid; n < a.N; n += kEmThreads) {
+    const int id = a.ids[n], v = id - v0;
+    const bool in = v >= 0 && v < n_rows;
+    if (in) atomicAdd(&count_s[v], 1);
+    row_s[n] = in ? v : -1;
+    if (blockIdx.x == 0 && (id < -1 || id >= a.V)) set_device_error(a.err, DSPARK_ERR_DEVICE_CHECK);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    // ---- where each row's positions begin (consecutive rows to a lane), and the rows that
+    // have any
+    const int each = (n_rows + 31) / 32, r0 = min(n_rows, lane * each), r1 = min(n_rows, r0 + each);
+    int sum = 0;
+    for (int v = r0; v < r1; ++v) sum += count_s[v];
+    int scan = sum;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, scan, m);
+      if (lane >= m) scan += o;
+    }
+    int at = scan - sum;
+    for (int v = r0; v < r1; ++v) {
+      const int c = count_s[v];
+      start_s[v] = at;
+      at += c;
+      if (c >= kLongRun) hit_s[kRangeMost - 1 - atomicAdd(&n_long_s, 1)] = v;
+      else if (c > 0) hit_s[atomicAdd(&n_short_s, 1)] = v;
+    }
+    __syncwarp();
+    // ---- places in position order: 32 positions at a time, equal ids by lane
+    for (int n0 = 0; n0 < a.N; n0 += 32) {
+      const int n = n0 + lane, v = n < a.N ? row_s[n] : -1;
+      const bool in = v >= 0;
+      if (!__any_sync(0xffffffffu, in)) continue;
+      const unsigned same = __match_any_sync(0xffffffffu, in ? v : -1);
+      if (in) pos_s[start_s[v] + __popc(same & ((1u << lane) - 1u))] = n;
+      __syncwarp();
+      if (in && lane == __ffs(same) - 1) start_s[v] += __popc(same);
+      __syncwarp();
+    }
+    // the places are ready: this warp begins the sums while the others fill
+    asm volatile("bar.arrive 1, %0;" ::"n"(kEmThreads) : "memory");
+  } else {
+    if (!a.accumulate) {
+      // ---- the rows without a position
+      constexpr int kFillers = kEmWarps - 1;
+      const long long step = a.ld_w * a.elem_w;
+      char* base = static_cast<char*>(a.dW) + v0 * step;
+      if (Vec) {
+        constexpr int kUnits = N * (int)sizeof(O) / 16;     // 16-byte stores of a lane
+        const int d = column<N, Vec>(cb0, lane, 0);
+        // rows of fewer than 32 lanes' columns: several at once
+        const int lanes = min(32, (a.D - cb0 * 32 * N) / N);
+        int log_each = 0;
+        while (lanes <= 16 >> log_each) ++log_each;
+        const int each = 1 << log_each, width = 32 >> log_each;
+        const int mine = lane & (width - 1);
+        char* at = base + (long long)(d - (lane - mine) * N) * sizeof(O);
+#pragma unroll 4
+        for (int v = (warp - 1) * each + (lane >> (5 - log_each)); v < n_rows; v += kFillers * each)
+          if (mine < lanes && count_s[v] == 0) {
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u)
+              __stcs(reinterpret_cast<uint4*>(at + v * step) + u, make_uint4(0u, 0u, 0u, 0u));
+          }
+      } else {
+        for (int v = warp - 1; v < n_rows; v += kFillers)
+          if (count_s[v] == 0) zero_bytes(base + v * step, (long long)a.D * a.elem_w, lane, 32);
+      }
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(kEmThreads) : "memory");
+  }
+  // ---- sums; start_s is now the place after a row's last
+  const T* in = static_cast<const T*>(a.d_out);
+  auto sum_run = [&](int from, int to, int cb, float (&acc)[N]) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) acc[e] = 0.f;
+    for (int j0 = from; j0 < to; j0 += kAhead) {
+      uint4 q[kAhead];
+      float sc[Vec ? 1 : kAhead][N];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const bool on = j0 + u < to;
+        const T* row = in + (long long)pos_s[on ? j0 + u : from] * a.ld;
+        if constexpr (Vec) {
+          const int d = column<N, Vec>(cb, lane, 0);
+          q[u] = on && d < a.D ? __ldcs(reinterpret_cast<const uint4*>(row + d)) : make_uint4(0u, 0u, 0u, 0u);
+        } else {
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            const int d = column<N, Vec>(cb, lane, e);
+            sc[u][e] = on && d < a.D ? elem_to_float(row[d]) : 0.f;
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (j0 + u >= to) break;
+        if constexpr (Vec) {
+          float x[N];
+          unpack_chunk<T>(q[u], x);
+#pragma unroll
+          for (int e = 0; e < N; ++e) acc[e] += x[e];
+        } else {
+#pragma unroll
+          for (int e = 0; e < N; ++e) acc[e] += sc[u][e];
+        }
+      }
+    }
+  };
+  float acc[N];
+  // short runs, a warp each, as warps come free
+  for (;;) {
+    int h = 0;
+    if (lane == 0) h = atomicAdd(&next_s, 1);
+    h = __shfl_sync(0xffffffffu, h, 0);
+    if (h >= n_short_s) break;
+    const int v = hit_s[h];
+    for (int cb = cb0; cb < cb1; ++cb) {
+      sum_run(start_s[v] - count_s[v], start_s[v], cb, acc);
+      add_to_row<O, N, Vec>(a, v0 + v, cb, lane, acc);
+    }
+  }
+  __syncthreads();
+  for (int h = 0; h < n_long_s; ++h) {
+    const int v = hit_s[kRangeMost - 1 - h], n = count_s[v], from = start_s[v] - n;
+    for (int cb = cb0; cb < cb1; ++cb) {
+      sum_run(from + n * warp / kEmWarps, from + n * (warp + 1) / kEmWarps, cb, acc);
+#pragma unroll
+      for (int e = 0; e < N; ++e) part_s[warp][e][lane] = acc[e];
+      __syncthreads();
+      if (warp == 0) {
+        for (int w = 1; w < kEmWarps; ++w)
+#pragma unroll
+          for (int e = 0; e < N; ++e) acc[e] += part_s[w][e][lane];
+        add_to_row<O, N, Vec>(a, v0 + v, cb, lane, acc);
+      }
+      __syncthreads();
+    }
+  }
+}
+
 struct EgPlan {
   int P, tiles, radix_tiles, passes;
   size_t off_key[2], off_pos[2], off_counts, off_part, total;
@@ -576,13 +699,12 @@ EgPlan eg_plan(int N, int V, int D) {
   const long long cols = cdiv(D, 128);
   p.P = (long long)cdiv(N, 32 * kEmWarps) * cols >= 304 ? 32 : 8;
   p.tiles = cdiv(N, kEmWarps * p.P);
-  p.radix_tiles = N > kRankMost ? cdiv(N, kRadixTile) : 0;
+  p.radix_tiles = N > kSortMost ? cdiv(N, kRadixTile) : 0;
   int bits = 1;
   while (bits < 31 && (V >> bits) != 0) ++bits;         // keys 0 .. V
   p.passes = cdiv(bits, kRadixBits);
   size_t o = 256;
   for (int i = 0; i < 2; ++i) {
-    if (i == 1 && p.radix_tiles == 0) { p.off_key[1] = p.off_key[0]; p.off_pos[1] = p.off_pos[0]; break; }
     p.off_key[i] = o; o = align_up(o + (size_t)N * 4, 256);
     p.off_pos[i] = o; o = align_up(o + (size_t)N * 4, 256);
   }
@@ -607,22 +729,37 @@ cudaError_t launch_em(const EmParams& p, cudaStream_t stream) {
 }
 
 template <typename T, typename O, bool Vec>
-cudaError_t launch_eg_sums(EgParams p, int buf, int fill, int from, int all, cudaStream_t stream) {
+cudaError_t launch_eg_sums(EgParams p, int buf, cudaStream_t stream) {
   p.cols = cdiv(p.D, 32 * Chunk<T>::N);
   const int ctas = p.tiles * p.cols;
-  Fill f = {ctas, from, all};
-  cudaError_t e = launch_pdl(eg_sum_kernel<T, O, Vec>, dim3((unsigned)(ctas + fill)), dim3(kEmThreads), 0,
-                             stream, p, buf, f);
-  if (e == cudaSuccess && p.tiles > 1) {
-    f.from += fill;
-    e = launch_pdl(eg_join_kernel<O, Chunk<T>::N, Vec>, dim3((unsigned)(ctas + fill)), dim3(128), 0, stream,
-                   p, buf, f);
-  }
+  cudaError_t e = launch_pdl(eg_sum_kernel<T, O, Vec>, dim3((unsigned)ctas), dim3(kEmThreads), 0, stream, p, buf);
+  if (e == cudaSuccess && p.tiles > 1)
+    e = launch_pdl(eg_join_kernel<O, Chunk<T>::N, Vec>, dim3((unsigned)ctas), dim3(128), 0, stream, p, buf);
   return e;
+}
+
+template <typename T, typename O, bool Vec>
+cudaError_t launch_eg_range(EgParams p, cudaStream_t stream) {
+  p.cols = cdiv(p.D, 32 * Chunk<T>::N);
+  const int col_ctas = Vec ? p.cols : 1;
+  // two CTAs an SM (1280 positions of 129280 x 256 in fp32: 26.8 us; four 29.3), or as many as
+  // keep a CTA's rows within shared memory
+  int ranges = cdiv(2 * 152, col_ctas);
+  if (ranges < cdiv(p.V, kRangeRows)) ranges = cdiv(p.V, kRangeRows);
+  if (ranges > p.V) ranges = p.V;
+  const int rows = cdiv(p.V, ranges);
+  return launch_pdl(eg_range_kernel<T, O, Vec>, dim3((unsigned)(cdiv(p.V, rows) * col_ctas)),
+                    dim3(kEmThreads), 0, stream, p, rows, col_ctas);
 }
 
 template <typename T, typename O>
 cudaError_t launch_eg(EgParams p, void* ws, cudaStream_t stream) {
+  p.elem_w = sizeof(O);
+  const bool vec = rows_aligned(p.d_out, p.ld, sizeof(T)) && rows_aligned(p.dW, p.ld_w, sizeof(O)) &&
+                   p.D % Chunk<T>::N == 0;
+  if (p.N == 0 && p.accumulate) return cudaSuccess;
+  if (p.N <= kRangeMost)
+    return vec ? launch_eg_range<T, O, true>(p, stream) : launch_eg_range<T, O, false>(p, stream);
   const EgPlan plan = eg_plan(p.N, p.V, p.D);
   for (int i = 0; i < 2; ++i) {
     p.key[i] = ws_at<int>(ws, plan.off_key[i]);
@@ -632,37 +769,23 @@ cudaError_t launch_eg(EgParams p, void* ws, cudaStream_t stream) {
   p.part = ws_at<float>(ws, plan.off_part);
   p.P = plan.P;
   p.tiles = plan.tiles;
-  p.elem_w = sizeof(O);
-  int buf = 0, done = 0;
+  const int buf = (plan.passes - 1) & 1;
   cudaError_t e = cudaSuccess;
-  // filling CTAs of each launch: four an SM, but no more than there are 16 KB to write
-  const int launches = (plan.radix_tiles ? 2 * plan.passes : 1) + (p.N > 0) + (plan.tiles > 1);
-  const long long most = (long long)p.V * p.D * p.elem_w / (16384LL * launches) + 1;
-  const int fill = p.accumulate ? 0 : (int)(most < 4 * 152 ? most : 4 * 152);
-  const int all = launches * fill;
+  // zeroing CTAs: four an SM, but no more than there are 16 KB to write
+  const long long most = (long long)p.V * p.D * p.elem_w / 16384 + 1;
+  const int fill = p.accumulate ? 0 : (int)(most < 4 * 152 ? align_up((size_t)most, 8) : 4 * 152);
   if (plan.radix_tiles == 0) {
-    const int ctas = cdiv(p.N, kRankItems);
-    if (ctas + fill > 0)
-      e = launch_pdl(eg_rank_kernel, dim3(ctas + fill), dim3(kEmThreads), align_up((size_t)p.N * 4, 16), stream,
-                     p, Fill{ctas, 0, all});
-    if (p.N == 0) return e;
-    done = 1;
+    e = launch_rows_cluster(eg_sort_kernel, 8 + fill, 8, kEmThreads, 0, stream, p, plan.passes);
   } else {
     for (int i = 0; i < plan.passes && e == cudaSuccess; ++i) {
-      const dim3 grid(plan.radix_tiles + fill);
-      e = launch_pdl(eg_count_kernel, grid, dim3(kEmThreads), 0, stream, p, i,
-                     Fill{plan.radix_tiles, done++ * fill, all});
+      e = launch_pdl(eg_count_kernel, dim3(plan.radix_tiles + (i == 0 ? fill : 0)), dim3(kEmThreads), 0, stream, p,
+                     i, plan.radix_tiles);
       if (e == cudaSuccess)
-        e = launch_pdl(eg_scatter_kernel, grid, dim3(kEmThreads), 0, stream, p, i,
-                       Fill{plan.radix_tiles, done++ * fill, all});
+        e = launch_pdl(eg_scatter_kernel, dim3(plan.radix_tiles), dim3(kEmThreads), 0, stream, p, i);
     }
-    buf = (plan.passes - 1) & 1;
   }
   if (e != cudaSuccess) return e;
-  const bool vec = rows_aligned(p.d_out, p.ld, sizeof(T)) && rows_aligned(p.dW, p.ld_w, sizeof(O)) &&
-                   p.D % Chunk<T>::N == 0;
-  return vec ? launch_eg_sums<T, O, true>(p, buf, fill, done * fill, all, stream)
-             : launch_eg_sums<T, O, false>(p, buf, fill, done * fill, all, stream);
+  return vec ? launch_eg_sums<T, O, true>(p, buf, stream) : launch_eg_sums<T, O, false>(p, buf, stream);
 }
 
 }  // namespace

@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import contextlib
 import functools
+import math
 from typing import Dict, Optional
 
 from . import DSparkError, Workspace, lib, STATUS  # noqa: F401
@@ -36,8 +37,11 @@ def _rows(t, name: str):
         raise ValueError(f"{name}: dtype {t.dtype} is not float32, bfloat16 or float16")
     if t.dim() < 1 or not t.is_cuda:
         raise ValueError(f"{name}: a CUDA tensor of at least one dimension is needed")
-    shape, stride = t.shape, t.stride()
+    shape = t.shape
     length = shape[-1]
+    if t.is_contiguous():
+        return code, t.numel() // length if length else math.prod(shape[:-1]), length, length
+    stride = t.stride()
     if length > 1 and stride[-1] != 1:
         raise ValueError(f"{name}: its last dimension is not contiguous (strides {tuple(stride)})")
     n, ld = 1, length
@@ -58,7 +62,7 @@ def _vector(t, name: str, n: int, dtype, like, k: Optional[int] = None):
     if t is None:
         return None
     if t.dtype is not dtype or t.numel() != (n if k is None else n * k) or not t.is_contiguous() \
-            or t.device != like.device:
+            or t.get_device() != like.get_device():
         want = f"{n}" if k is None else f"{n} x {k}"
         raise ValueError(f"{name}: {want} contiguous {dtype} on {like.device} are needed, not "
                          f"{tuple(t.shape)} {t.dtype} on {t.device}")
@@ -75,11 +79,15 @@ def _device(like, ws: Workspace, *others):
             raise ValueError(f"tensors on {like.device} and {t.device}")
 
 
-def _on(stream):
+_NOTHING = contextlib.nullcontext()
+
+
+def _on(stream, like):
     """(stream handle, context in which outputs are allocated for it)."""
     torch, _ = _types()
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream, contextlib.nullcontext()
+        # (the handle alone: a Stream object takes 3 us to make)
+        return torch._C._cuda_getCurrentRawStream(like.device.index), _NOTHING
     return stream.cuda_stream, torch.cuda.stream(stream)
 
 
@@ -101,7 +109,7 @@ def token_logprobs(logits, tokens, top: int, ws: Workspace, out: Optional[Dict] 
     torch, _ = _types()
     code, n, V, ld = _rows(logits, "logits")
     _device(logits, ws)
-    handle, allocate = _on(stream)
+    handle, allocate = _on(stream, logits)
     tok = _vector(tokens, "tokens", n, torch.int32, logits)
     f32, i32 = torch.float32, torch.int32
     if out is None:
@@ -132,7 +140,7 @@ def token_logprobs_grad(logits, tokens, row_max, row_sumexp, entropy, d_logprob,
     torch, _ = _types()
     code, n, V, ld = _rows(logits, "logits")
     _device(logits, ws)
-    handle, allocate = _on(stream)
+    handle, allocate = _on(stream, logits)
     out, ld_d = _like_logits(out, logits, code, n, V, allocate)
     f32 = torch.float32
     v = lambda t, name, dtype=f32: _vector(t, name, n, dtype, logits)  # noqa: E731
@@ -160,7 +168,7 @@ def _distill(grad: bool, logits, teacher_ids, teacher_logits, ws, labels, weight
     torch, _ = _types()
     code, n, V, ld = _rows(logits, "logits")
     _device(logits, ws)
-    handle, allocate = _on(stream)
+    handle, allocate = _on(stream, logits)
     f32, i32 = torch.float32, torch.int32
     K = 0 if teacher_ids is None else teacher_ids.shape[-1]
     lead, d = tuple(logits.shape[:-1]), logits.device
@@ -215,7 +223,7 @@ def embed(W, ids, ws: Workspace, scale: float = 1.0, out=None, dtype=None, strea
         raise ValueError(f"W: a table [V, D] is needed, not {tuple(W.shape)}")
     code, V, D, ld = _rows(W, "W")
     _device(W, ws)
-    handle, allocate = _on(stream)
+    handle, allocate = _on(stream, W)
     n = ids.numel()
     if out is None:
         with allocate:
@@ -245,7 +253,7 @@ def embed_grad(d_out, ids, V: int, ws: Workspace, scale: float = 1.0, out=None, 
     torch, _ = _types()
     code, n, D, ld = _rows(d_out, "d_out")
     _device(d_out, ws)
-    handle, allocate = _on(stream)
+    handle, allocate = _on(stream, d_out)
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out, the table to add to")
