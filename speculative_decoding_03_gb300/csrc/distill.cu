@@ -366,7 +366,8 @@ __global__ void __launch_bounds__(kDsBlock, 2) distill_kernel(DsParams a, int lo
           sum_a += a.c_tv * warp_sum(tv);
         }
         const float gw = g * w * a.inv_tau;
-        const float scale = on && sum_a * gw != 0.f ? sum_a * gw / S : 0.f;
+        // (a row with NaN or +inf shows it, whatever its coefficients)
+        const float scale = on && (sum_a * gw != 0.f || !(S <= FLT_MAX)) ? sum_a * gw / S : 0.f;
         if (scale == 0.f) {
           zero_out();
           __syncwarp();
@@ -450,8 +451,9 @@ __global__ void __launch_bounds__(kDsBlock, 2) distill_kernel(DsParams a, int lo
           if (k < K && te.id[k] >= 0) {
             const float lq = log_q(te.z[k]), q = expf(lq), p = te.p[k];
             if (p != 0.f) kl += p * (te.log_p[k] - lq);
-            tv += fmaxf(p - q, 0.f);
-            acc += fminf(p, q);
+            const float d = p - q;
+            tv += d > 0.f ? d : 0.f * d;     // (a NaN stays one)
+            acc += (d > 0.f ? q : p) + 0.f * d;
           }
         }
         kl = warp_sum(kl);

@@ -435,6 +435,25 @@ def test_distill_labels_alone_and_no_gradient_of_masked_values(ws):
     assert ds.distill_loss(z, None, None, ws, labels, w, kl=0.0, ce=1.0)["loss"][0].isnan()
 
 
+@pytest.mark.parametrize("terms", [dict(), dict(kl=0.0, tv=1.0), dict(kl=0.0, tv=0.5, ce=0.5)], ids=["kl", "tv", "tv+ce"])
+def test_distill_shows_nan_and_inf(terms, ws):
+    """A NaN or +inf in a live row, or a NaN from the teacher, reaches loss, acceptance and
+    gradient; other rows are untouched."""
+    n, V, K = 4, 1000, 8
+    z = logits(n, V, torch.float32, 45)
+    ids, t = teacher(n, V, K, 46)
+    ids[ids < 0] = 999
+    labels = torch.full((n,), 5, dtype=torch.int32, device="cuda")
+    clean = ds.distill_loss_grad(z, ids, t, ws, labels, **terms)
+    z[1, 77], z[2, 78] = math.nan, math.inf
+    t[3, 2] = math.nan
+    got = ds.distill_loss_grad(z, ids, t, ws, labels, **terms)
+    for key in got:
+        assert torch.equal(got[key][0], clean[key][0])
+        assert got[key][1:3].isnan().all()
+    assert got["loss"][3].isnan() and got["accept"][3].isnan()
+
+
 def test_distill_against_differences(ws):
     n, V, K, h = 4, 300, 10, 1e-2
     z = logits(n, V, torch.float32, 40)
