@@ -171,6 +171,210 @@ __device__ __forceinline__ void read_teacher(const DsParams& a, int n, const Row
   __syncwarp();
 }
 
+// What follows a row's sums: q = exp((z - M) / tau) / S.
+struct RowEnd {
+  const DsParams& a;
+  const Teacher& te;
+  int n;
+  float w, M, S, logs, kl2;
+  float sum_a, gw, scale;    // A; g w / tau; A g w / (tau S), 0 for a row of zeroes
+  __device__ __forceinline__ RowEnd(const DsParams& a_, const Teacher& te_, int n_, float w_, float M_, float S_)
+      : a(a_), te(te_), n(n_), w(w_), M(M_), S(S_), logs(logf(S_)), kl2(a_.inv_tau * kLog2e) {}
+  __device__ __forceinline__ float log_q(float z) const { return (z - M) * a.inv_tau - logs; }
+  // a_k of an entry; products with a zero coefficient are left out (0 * inf)
+  __device__ __forceinline__ float coef(float p, float q) const {
+    float x = a.c_kl != 0.f ? a.c_kl * p : 0.f;
+    if (q < p) x += a.c_tv * q;
+    return x;
+  }
+  __device__ __forceinline__ float ay() const { return te.y >= 0 ? a.c_ce : 0.f; }
+  __device__ __forceinline__ bool on() const { return te.any || te.y >= 0; }
+  // the gradient's factors, by a whole warp
+  __device__ __forceinline__ void factors(float g) {
+    const int lane = threadIdx.x & 31;
+    sum_a = (te.any && a.c_kl != 0.f ? a.c_kl * te.sum_p : 0.f) + ay();
+    if (a.c_tv != 0.f && te.any) {
+      float tv = 0.f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int k = lane + 32 * i;
+        if (k < a.K && te.id[k] >= 0) {
+          const float q = expf(log_q(te.z[k]));
+          if (q < te.p[k]) tv += q;
+        }
+      }
+      sum_a += a.c_tv * warp_sum(tv);
+    }
+    gw = g * w * a.inv_tau;
+    // (a row with NaN or +inf shows it, whatever its coefficients)
+    scale = on() && (sum_a * gw != 0.f || !(S <= FLT_MAX)) ? sum_a * gw / S : 0.f;
+  }
+  // the gradient of a chunk, without the entries' own terms
+  template <typename T>
+  __device__ __forceinline__ uint4 grad(const uint4& q) const {
+    constexpr int N = Chunk<T>::N;
+    const F2 nM = f2(-M, -M), kk = f2(kl2, kl2), sc = f2(scale, scale);
+    float z[N];
+    unpack_chunk<T>(q, z);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      float x, y;
+      f2_get(f2_mul(f2_add(f2(z[i], z[i + 1]), nM), kk), x, y);
+      f2_get(f2_mul(f2(ex2_approx(x), ex2_approx(y)), sc), z[i], z[i + 1]);
+    }
+    return pack_chunk<T>(z);
+  }
+  __device__ __forceinline__ float grad_one(float z) const { return ex2_approx((z - M) * kl2) * scale; }
+  // The entries' own elements and the label's, A q - sum of a over the entries with this id,
+  // for those that `mine` gives to this warp; after the row's chunks.
+  template <typename T, typename Mine>
+  __device__ __forceinline__ void write_entries(T* out, Mine&& mine) const {
+    const int lane = threadIdx.x & 31;
+    for (int i = lane; i < te.n_own; i += 32) {
+      const int k = te.own[i], v = te.id[k];
+      if (!mine(v)) continue;
+      const float q = expf(log_q(te.z[k]));
+      float av = v == te.y ? ay() : 0.f;
+      if (te.twice) {                        // in entry order, so that equal ids write the same
+        for (int j = 0; j < a.K; ++j)
+          if (te.id[j] == v) av += coef(te.p[j], q);
+      } else {
+        av += coef(te.p[k], q);
+      }
+      out[v] = elem_from_float<T>(gw * (sum_a * q - av));
+    }
+    if (lane == 0 && te.y_own && mine(te.y))
+      out[te.y] = elem_from_float<T>(gw * (sum_a * expf(log_q(te.zy)) - ay()));
+  }
+  // loss and acceptance, by a whole warp
+  __device__ __forceinline__ void write_loss() const {
+    const int lane = threadIdx.x & 31;
+    float kl = 0.f, tv = 0.f, acc = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int k = lane + 32 * i;
+      if (k < a.K && te.id[k] >= 0) {
+        const float lq = log_q(te.z[k]), q = expf(lq), p = te.p[k];
+        if (p != 0.f) kl += p * (te.log_p[k] - lq);
+        const float d = p - q;
+        tv += d > 0.f ? d : 0.f * d;         // (a NaN stays one)
+        acc += (d > 0.f ? q : p) + 0.f * d;
+      }
+    }
+    kl = warp_sum(kl);
+    tv = warp_sum(tv);
+    acc = warp_sum(acc);
+    if (lane == 0) {
+      float l = 0.f;
+      if (te.any && a.c_kl != 0.f) l += a.c_kl * kl;
+      if (te.any && a.c_tv != 0.f) l += a.c_tv * tv;
+      if (te.y >= 0 && a.c_ce != 0.f) l -= a.c_ce * log_q(te.zy);
+      a.loss[n] = on() ? l * w : 0.f;
+      a.accept[n] = te.any ? acc : 0.f;
+    }
+  }
+};
+
+// zeroes of part c of 2^log_C of an output row, by `threads` threads
+template <typename T>
+__device__ __forceinline__ void zero_row(T* out, int V, int c, int log_C, int t, int threads) {
+  const RowChunks oc = row_chunks(out, V);
+  uint4* o4 = reinterpret_cast<uint4*>(out + oc.head);
+  const int e0 = (int)((long long)oc.chunks * c >> log_C), e1 = (int)((long long)oc.chunks * (c + 1) >> log_C);
+  for (int i = e0 + t; i < e1; i += threads) __stcs(o4 + i, make_uint4(0u, 0u, 0u, 0u));
+  if (c == 0 && t < oc.head + oc.tail)
+    out[t < oc.head ? t : V - oc.tail + (t - oc.head)] = elem_from_float<T>(0.f);
+}
+
+// Short rows: a CTA of four warps a row, the sums and the gradient from two reads (the second
+// finds the row in L1 or L2).  Many small CTAs an SM hide a row's steps behind other rows.
+constexpr int kShortThreads = 128;
+constexpr int kShortChunks = 2048;          // 32 KB
+template <typename T, bool Grad>
+__global__ void __launch_bounds__(kShortThreads, 8) distill_short_kernel(DsParams a) {
+  constexpr int N = Chunk<T>::N;
+  __shared__ Teacher te;
+  __shared__ float2 sums_s[kShortThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n = blockIdx.x, V = a.V;
+  pdl_wait();
+  pdl_launch_dependents();
+  T* out = Grad ? static_cast<T*>(a.dz) + (long long)n * a.ld_dz : nullptr;
+  const float w = a.weights ? a.weights[n] : 1.f;
+  if (w == 0.f) {                            // a masked row: nothing of it is read
+    if constexpr (Grad) zero_row(out, V, 0, 0, tid, kShortThreads);
+    if (tid == 0) {
+      a.loss[n] = 0.f;
+      a.accept[n] = 0.f;
+    }
+    return;
+  }
+  const RowPart<T> r = row_part<T>(a.z, a.ld, n, V, 0, 0, 0x7FFFFFFF);
+  if (warp == 0) read_teacher<T>(a, n, r, true, te);
+  RunningSum rs;
+  rs.init(a.inv_tau);
+  const int loose_n = r.rc.head + r.rc.tail;
+  const int loose = tid < r.rc.head ? tid : V - r.rc.tail + (tid - r.rc.head);
+  const float zl = tid < loose_n ? elem_to_float(r.row[loose]) : -INFINITY;
+  constexpr int G = 16 / N;                  // chunks of 16 elements
+  int j = tid;
+  for (; j + (G - 1) * kShortThreads < r.held; j += G * kShortThreads) {
+    uint4 q[G];
+#pragma unroll
+    for (int u = 0; u < G; ++u) q[u] = r.body[j + u * kShortThreads];
+    float z[16];
+#pragma unroll
+    for (int u = 0; u < G; ++u) {
+      float x[N];
+      unpack_chunk<T>(q[u], x);
+#pragma unroll
+      for (int e = 0; e < N; ++e) z[u * N + e] = x[e];
+    }
+    rs.add(z);
+  }
+  for (; j < r.held; j += kShortThreads) {
+    float z[N];
+    unpack_chunk<T>(r.body[j], z);
+    rs.add(z);
+  }
+  if (tid < loose_n) rs.add_one(zl);
+  const float wm = warp_max(rs.reference());
+  const float ws = warp_sum(rs.at(wm));
+  if (lane == 0) sums_s[warp] = make_float2(wm, ws);
+  __syncthreads();                           // also: the teacher's entries are read
+  float M = -INFINITY, S = 0.f;
+#pragma unroll
+  for (int i = 0; i < kShortThreads / 32; ++i) M = fmaxf(M, sums_s[i].x);
+#pragma unroll
+  for (int i = 0; i < kShortThreads / 32; ++i)
+    if (sums_s[i].y != 0.f) S += sums_s[i].y * ex2_approx((sums_s[i].x - M) * (a.inv_tau * kLog2e));
+  RowEnd end(a, te, n, w, M, S);
+  if constexpr (Grad) {
+    end.factors(a.d_loss ? a.d_loss[n] : 1.f);
+    if (end.scale == 0.f) {
+      zero_row(out, V, 0, 0, tid, kShortThreads);
+    } else {
+      const bool same = ((reinterpret_cast<uintptr_t>(r.row) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
+      T* o = out + r.rc.head;
+#pragma unroll 4
+      for (int i = tid; i < r.held; i += kShortThreads) {
+        const uint4 v = end.grad<T>(r.body[i]);
+        if (same) {
+          __stcs(reinterpret_cast<uint4*>(o) + i, v);
+        } else {                             // output rows off the input rows' 16-byte grid
+          const T* ve = reinterpret_cast<const T*>(&v);
+#pragma unroll
+          for (int e = 0; e < N; ++e) o[(long long)i * N + e] = ve[e];
+        }
+      }
+      if (tid < loose_n) out[loose] = elem_from_float<T>(end.grad_one(zl));
+      __syncthreads();                       // the entries' elements after the row's
+      if (warp == 0) end.write_entries(out, [](int) { return true; });
+    }
+  }
+  if (warp == kShortThreads / 32 - 1) end.write_loss();
+}
+
 template <typename T, bool Grad>
 __global__ void __launch_bounds__(kDsBlock, 2) distill_kernel(DsParams a, int log_C) {
   constexpr int N = Chunk<T>::N;
@@ -179,7 +383,7 @@ __global__ void __launch_bounds__(kDsBlock, 2) distill_kernel(DsParams a, int lo
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = 1 << log_C;                  // CTAs of a row
   const int c = (int)(blockIdx.x & (C - 1)), first = (int)(blockIdx.x >> log_C), step = (int)(gridDim.x >> log_C);
-  const int V = a.V, K = a.K;
+  const int V = a.V;
   const int pieces = (a.resident + kPieceChunks - 1) / kPieceChunks;
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
@@ -240,15 +444,7 @@ __global__ void __launch_bounds__(kDsBlock, 2) distill_kernel(DsParams a, int lo
       if (n + step < a.N && a.weights) w_next = a.weights[n + step];
       T* out = Grad ? static_cast<T*>(a.dz) + (long long)n * a.ld_dz : nullptr;
       auto zero_out = [&] {
-        if constexpr (Grad) {
-          const RowChunks oc = row_chunks(out, V);
-          uint4* o4 = reinterpret_cast<uint4*>(out + oc.head);
-          const int e0 = (int)((long long)oc.chunks * c >> log_C);
-          const int e1 = (int)((long long)oc.chunks * (c + 1) >> log_C);
-          for (int i = e0 + tid; i < e1; i += kDsThreads) __stcs(o4 + i, make_uint4(0u, 0u, 0u, 0u));
-          if (c == 0 && tid < oc.head + oc.tail)
-            out[tid < oc.head ? tid : V - oc.tail + (tid - oc.head)] = elem_from_float<T>(0.f);
-        }
+        if constexpr (Grad) zero_row(out, V, c, log_C, tid, kDsThreads);
       };
       if (w == 0.f) {                        // a masked row: nothing of it is read
         zero_out();
@@ -339,58 +535,21 @@ __global__ void __launch_bounds__(kDsBlock, 2) distill_kernel(DsParams a, int lo
       for (int i = 0; i < kSumsLane; ++i)
         if (part[i].y != 0.f) S += part[i].y * ex2_approx((part[i].x - M) * kl2);
       S = warp_sum(S);
-      const float logs = logf(S);
-      auto log_q = [&](float z) { return (z - M) * a.inv_tau - logs; };
-      // a_k of an entry; products with a zero coefficient are left out (0 * inf)
-      auto coef = [&](float p, float q) {
-        float x = a.c_kl != 0.f ? a.c_kl * p : 0.f;
-        if (q < p) x += a.c_tv * q;
-        return x;
-      };
-      const int y = te.y;
-      const bool any = te.any, on = any || y >= 0;
-      const float ay = y >= 0 ? a.c_ce : 0.f;
+      RowEnd end(a, te, n, w, M, S);
 
       if constexpr (Grad) {
-        float sum_a = (any && a.c_kl != 0.f ? a.c_kl * te.sum_p : 0.f) + ay;
-        if (a.c_tv != 0.f && any) {
-          float tv = 0.f;
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const int k = lane + 32 * i;
-            if (k < K && te.id[k] >= 0) {
-              const float q = expf(log_q(te.z[k]));
-              if (q < te.p[k]) tv += q;
-            }
-          }
-          sum_a += a.c_tv * warp_sum(tv);
-        }
-        const float gw = g * w * a.inv_tau;
-        // (a row with NaN or +inf shows it, whatever its coefficients)
-        const float scale = on && (sum_a * gw != 0.f || !(S <= FLT_MAX)) ? sum_a * gw / S : 0.f;
-        if (scale == 0.f) {
+        end.factors(g);
+        if (end.scale == 0.f) {
           zero_out();
           __syncwarp();
           slot = slot0;
           for (int i = 0; i < pieces; ++i, next_piece())
             if (lane == 0) mbar_arrive(&sh.empty[slot]);
         } else {
-          const F2 nM = f2(-M, -M), kk = f2(kl2, kl2), sc = f2(scale, scale);
-          auto grad = [&](const uint4& q) {
-            float z[N];
-            unpack_chunk<T>(q, z);
-#pragma unroll
-            for (int i = 0; i < N; i += 2) {
-              float x, yv;
-              f2_get(f2_mul(f2_add(f2(z[i], z[i + 1]), nM), kk), x, yv);
-              f2_get(f2_mul(f2(ex2_approx(x), ex2_approx(yv)), sc), z[i], z[i + 1]);
-            }
-            return pack_chunk<T>(z);
-          };
           const bool same = ((reinterpret_cast<uintptr_t>(r.row) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
           T* o = out + r.rc.head;
           auto put = [&](int j, const uint4& q) {
-            const uint4 v = grad(q);
+            const uint4 v = end.grad<T>(q);
             if (same) {
               __stcs(reinterpret_cast<uint4*>(o) + j, v);
             } else {                         // output rows off the input rows' 16-byte grid
@@ -416,58 +575,17 @@ __global__ void __launch_bounds__(kDsBlock, 2) distill_kernel(DsParams a, int lo
             if (lane == 0) mbar_arrive(&sh.empty[slot]);
           }
           for (int j = r.c0 + r.held + tid; j < r.c1; j += kDsThreads) put(j, r.body[j]);
-          if (tid < loose_n) out[loose] = elem_from_float<T>(ex2_approx((zl - M) * kl2) * scale);
-          // the teacher's elements and the label's, after the row's, by the warp that holds
-          // them: dz = g w / tau (A q - sum of a over the entries with this id)
+          if (tid < loose_n) out[loose] = elem_from_float<T>(end.grad_one(zl));
+          // the entries' elements after the row's, by the warp that wrote them first (those
+          // outside the chunks: warp 0)
           __syncwarp();
-          // (an element outside the chunks is warp 0's)
-          auto holder = [&](int v) {
+          end.write_entries(out, [&](int v) {
             const int at = (v - r.rc.head) / N - r.c0;
-            return v < r.rc.head || v >= V - r.rc.tail ? 0 : (at & (kDsThreads - 1)) >> 5;
-          };
-          for (int i = lane; i < te.n_own; i += 32) {
-            const int k = te.own[i], v = te.id[k];
-            if (holder(v) != warp) continue;
-            const float q = expf(log_q(te.z[k]));
-            float av = v == y ? ay : 0.f;
-            if (te.twice) {                  // in entry order, so that equal ids write the same
-              for (int j = 0; j < K; ++j)
-                if (te.id[j] == v) av += coef(te.p[j], q);
-            } else {
-              av += coef(te.p[k], q);
-            }
-            out[v] = elem_from_float<T>(gw * (sum_a * q - av));
-          }
-          if (lane == 0 && te.y_own && holder(y) == warp)
-            out[y] = elem_from_float<T>(gw * (sum_a * expf(log_q(te.zy)) - ay));
+            return (v < r.rc.head || v >= V - r.rc.tail ? 0 : (at & (kDsThreads - 1)) >> 5) == warp;
+          });
         }
       }
-      // ---- loss and acceptance, by the last warp of one CTA
-      if (warp == kDsWarps - 1 && (it & (C - 1)) == c) {
-        float kl = 0.f, tv = 0.f, acc = 0.f;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int k = lane + 32 * i;
-          if (k < K && te.id[k] >= 0) {
-            const float lq = log_q(te.z[k]), q = expf(lq), p = te.p[k];
-            if (p != 0.f) kl += p * (te.log_p[k] - lq);
-            const float d = p - q;
-            tv += d > 0.f ? d : 0.f * d;     // (a NaN stays one)
-            acc += (d > 0.f ? q : p) + 0.f * d;
-          }
-        }
-        kl = warp_sum(kl);
-        tv = warp_sum(tv);
-        acc = warp_sum(acc);
-        if (lane == 0) {
-          float l = 0.f;
-          if (any && a.c_kl != 0.f) l += a.c_kl * kl;
-          if (any && a.c_tv != 0.f) l += a.c_tv * tv;
-          if (y >= 0 && a.c_ce != 0.f) l -= a.c_ce * log_q(te.zy);
-          a.loss[n] = on ? l * w : 0.f;
-          a.accept[n] = any ? acc : 0.f;
-        }
-      }
+      if (warp == kDsWarps - 1 && (it & (C - 1)) == c) end.write_loss();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.teacher_free[b]);
       slot0 += pieces;
@@ -486,6 +604,8 @@ __global__ void __launch_bounds__(kDsBlock, 2) distill_kernel(DsParams a, int lo
 template <typename T, bool Grad>
 cudaError_t launch(DsParams p, cudaStream_t stream) {
   const int chunks = p.V / Chunk<T>::N;
+  if (chunks <= kShortChunks)
+    return launch_pdl(distill_short_kernel<T, Grad>, dim3((unsigned)p.N), dim3(kShortThreads), 0, stream, p);
   int C = 1, log_C = 0;
   // the row's part of a CTA small enough that some of the ring is left for the next row's;
   // more CTAs a row while there are fewer than two an SM, as long as each has 8 KB

@@ -37,6 +37,9 @@ constexpr int kLpCap = 768;                 // candidate keys of a CTA
 constexpr int kLpList = 512;                // slots listed to be read again
 constexpr int kLpTop = kMaxTop;             // most alternatives
 constexpr int kLpMaxima = 256;              // most groups
+constexpr int kLpShortSlots = 8;
+// a short row: 32 KB
+constexpr int kLpShortChunks = 2048;
 
 struct LpParams {
   const void* z;
@@ -183,9 +186,38 @@ __device__ __forceinline__ bool close_any(bool p) {
   return r != 0;
 }
 
+// the outputs of a row without a token, by kLpClose threads
+__device__ __forceinline__ void no_token(const LpParams& a, int n, int y, int x) {
+  if (x == 0) {
+    if (y != -1) set_device_error(a.err, DSPARK_ERR_DEVICE_CHECK);
+    a.logprob[n] = 0.f;
+    a.rank[n] = 0;
+    if (a.entropy) a.entropy[n] = 0.f;
+    if (a.row_max) a.row_max[n] = -INFINITY;
+    if (a.row_sumexp) a.row_sumexp[n] = 0.f;
+  }
+  for (int j = x; j < a.K; j += kLpClose) {
+    a.top_ids[(size_t)n * a.K + j] = -1;
+    a.top_logprobs[(size_t)n * a.K + j] = -INFINITY;
+  }
+}
+// a row's single numbers, by one thread
+__device__ __forceinline__ void write_row(const LpParams& a, int n, bool bad, float M, float S, float Tm,
+                                          float logs, float zy, int before) {
+  const float nan = __int_as_float(0x7FC00000);
+  if (a.tokens) {
+    a.logprob[n] = bad ? nan : S > 0.f ? zy - M - logs : -INFINITY;
+    a.rank[n] = bad ? 0 : before + 1;
+  }
+  if (a.entropy) a.entropy[n] = bad ? nan : S > 0.f ? logs - Tm / S : 0.f;
+  if (a.row_max) a.row_max[n] = M;
+  if (a.row_sumexp) a.row_sumexp[n] = bad ? nan : S;
+}
+
 // best[0 .. K) = the K largest of cand[0 .. n), descending, then 0; returns min(n, K).  All
 // closing threads; up to 64 keys by two threads a key, each against half of them.
-__device__ __forceinline__ int select_top(LpShared& sh, int x, int n, int K) {
+template <typename Shared>
+__device__ __forceinline__ int select_top(Shared& sh, int x, int n, int K) {
   if (n <= kLpClose / 2) {
     const int i = x >> 1;
     const unsigned long long key = i < n ? sh.cand[i] : 0ull;
@@ -206,6 +238,168 @@ __device__ __forceinline__ int select_top(LpShared& sh, int x, int n, int K) {
   for (int i = n + x; i < K; i += kLpClose) sh.best[i] = 0ull;
   close_sync();
   return n < K ? n : K;
+}
+
+// The same where more elements reach the bound than keys fit (equal logits, or all the large
+// ones in few threads' hands): the selection goes tile by tile over the elements [from, to) and
+// keeps the K best in sh.best, `got` of them so far.
+template <typename Shared, typename T>
+__device__ __noinline__ void sweep(Shared& sh, int x, const T* row, int from, int to, int K, int& got) {
+  constexpr int kTile = (kLpCap - kLpTop) / kLpClose * kLpClose;
+  for (int base = from; base < to; base += kTile) {
+    close_sync();
+    if (x == 0) sh.n_cand = got;
+    for (int j = x; j < got; j += kLpClose) sh.cand[j] = sh.best[j];
+    const unsigned long long floor_key = got == K ? sh.best[K - 1] : 0ull;
+    close_sync();
+    for (int v = base + x; v < min(to, base + kTile); v += kLpClose) {
+      const float z = elem_to_float(row[v]);
+      const unsigned long long key = top_key(z, v);
+      if (z == z && key > floor_key) sh.cand[atomicAdd(&sh.n_cand, 1)] = key;
+    }
+    close_sync();
+    if (sh.n_cand > got) got = select_top(sh, x, sh.n_cand, K);
+  }
+}
+
+// Short rows: a CTA of 128 threads a row, with the same bound, re-read and ranking; many CTAs
+// an SM hide a row's steps behind other rows.
+struct LpShortShared {
+  unsigned long long cand[kLpCap];
+  unsigned long long best[kLpTop];
+  uint32_t gmax[kLpMaxima];
+  float4 part[kLpClose / 32];
+  float slots[kLpShortSlots][kLpClose];
+  int n_cand;
+};
+template <typename T>
+__global__ void __launch_bounds__(kLpClose, 8) token_logprobs_short_kernel(LpParams a) {
+  constexpr int N = Chunk<T>::N, G = 16 / N, kThreads = kLpClose, kWarps = kThreads / 32;
+  __shared__ LpShortShared sh;
+  const int x = threadIdx.x, lane = x & 31, warp = x >> 5;
+  const int n = blockIdx.x, V = a.V, K = a.K;
+  pdl_wait();
+  pdl_launch_dependents();
+  const float nan = __int_as_float(0x7FC00000);
+  const int y = a.tokens ? a.tokens[n] : 0;
+  if (y < 0 || y >= V) {
+    no_token(a, n, y, x);
+    return;
+  }
+  if (x == 0) sh.n_cand = 0;
+  const RowPart<T> r = row_part<T>(a.z, a.ld, n, V, 0, 0, 0x7FFFFFFF);
+  const float zy = a.tokens ? elem_to_float(r.row[y]) : INFINITY;
+  const int loose_n = r.rc.head + r.rc.tail;
+  const int loose = x < r.rc.head ? x : V - r.rc.tail + (x - r.rc.head);
+  const float zl = x < loose_n ? elem_to_float(r.row[loose]) : -INFINITY;
+  RunningSoftmax rs;
+  rs.init();
+  float tmax[2] = {-INFINITY, -INFINITY};    // of even slots and odd ones
+  int before = 0, used = 0;
+  // (16 elements a slot: G chunks, kThreads apart)
+  for (int i = x; i < r.held; i += G * kThreads, ++used) {
+    float z[16];
+#pragma unroll
+    for (int u = 0; u < G; ++u) {
+      const int j = i + u * kThreads;
+      float e[N];
+      if (j < r.held) {
+        unpack_chunk<T>(__ldg(r.body + j), e);
+        const int v = r.rc.head + j * N;
+        if (a.tokens) {
+#pragma unroll
+          for (int k = 0; k < N; ++k) before += e[k] > zy || (e[k] == zy && v + k < y);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k) e[k] = -INFINITY;
+      }
+#pragma unroll
+      for (int k = 0; k < N; ++k) z[u * N + k] = e[k];
+    }
+    const float bm = max_of(z);
+    rs.add(z, bm);
+    sh.slots[used][x] = bm;
+    const float even = tmax[0];              // (the two change places with every slot)
+    tmax[0] = tmax[1];
+    tmax[1] = fmaxf(even, bm);
+  }
+  if (x < loose_n) {
+    rs.add_one(zl);
+    tmax[0] = fmaxf(tmax[0], zl);
+    before += zl > zy || (zl == zy && loose < y);
+  }
+  {
+    const float m = warp_max(fmaxf(tmax[0], tmax[1]));
+    float s, t;
+    rs.finish(m, s, t);
+    s = warp_sum(s);
+    t = warp_sum(t);
+    before = __reduce_add_sync(0xffffffffu, before);
+    if (lane == 0) sh.part[warp] = make_float4(m, s, t, __int_as_float(before));
+  }
+  int groups = 32;
+  while (groups < 2 * K && groups < kLpMaxima) groups <<= 1;
+  if (groups == kLpMaxima) {
+    sh.gmax[x] = group_key(tmax[0]);
+    sh.gmax[kThreads + x] = group_key(tmax[1]);
+  } else {
+    float g = fmaxf(tmax[0], tmax[1]);
+    for (int o = 16; o >= groups / kWarps; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+    if (lane < groups / kWarps) sh.gmax[warp * (groups / kWarps) + lane] = group_key(g);
+  }
+  __syncthreads();
+  float M = -INFINITY, S = 0.f, Tm = 0.f;
+  before = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) M = fmaxf(M, sh.part[i].x);
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    const float4 p = sh.part[i];
+    before += __float_as_int(p.w);
+    if (p.y != 0.f) {
+      const float d = p.x - M, f = ex2_approx(d * kLog2e);
+      S += p.y * f;
+      if (f > 0.f) Tm += f * (p.z + d * p.y);
+    }
+  }
+  const bool bad = !(S <= FLT_MAX);          // NaN or +inf among the logits
+  const float logs = logf(S);
+  if (x == 0) write_row(a, n, bad, M, S, Tm, logs, zy, before);
+  if (K == 0) return;
+  const float thr = group_value(kth_bound(sh.gmax, groups, K));
+  auto consider = [&](float z, int v) {
+    if (z >= thr) {
+      const int to = atomicAdd(&sh.n_cand, 1);
+      if (to < kLpCap) sh.cand[to] = top_key(z, v);
+    }
+  };
+  if (x < loose_n) consider(zl, loose);
+  for (int u = 0; u < used; ++u) {
+    if (sh.slots[u][x] < thr) continue;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int j = x + (u * G + g) * kThreads;
+      if (j >= r.held) break;
+      float z[N];
+      unpack_chunk<T>(__ldg(r.body + j), z);
+#pragma unroll
+      for (int e = 0; e < N; ++e) consider(z[e], r.rc.head + j * N + e);
+    }
+  }
+  __syncthreads();
+  int got = 0;
+  if (sh.n_cand <= kLpCap) {
+    got = select_top(sh, x, sh.n_cand, K);
+  } else {
+    sweep(sh, x, r.row, 0, V, K, got);
+  }
+  for (int j = x; j < K; j += kThreads) {
+    const unsigned long long key = j < got ? sh.best[j] : 0ull;
+    const size_t o = (size_t)n * K + j;
+    a.top_ids[o] = bad || j >= got ? -1 : key_index(key);
+    a.top_logprobs[o] = bad ? nan : j < got && S > 0.f ? key_value(key) - M - logs : -INFINITY;
+  }
 }
 
 template <typename T>
@@ -404,15 +598,7 @@ __global__ void __launch_bounds__(kLpBlock, 2) token_logprobs_kernel(LpParams a,
         if (lane >= o) upto += v;
       }
       const int total = __shfl_sync(0xffffffffu, upto, 7);
-      if (x == 0) {
-        if (a.tokens) {
-          a.logprob[n] = bad ? nan : pend.S > 0.f ? pend.zy - pend.M - logs : -INFINITY;
-          a.rank[n] = bad ? 0 : pend.before + 1;
-        }
-        if (a.entropy) a.entropy[n] = bad ? nan : pend.S > 0.f ? logs - pend.Tm / pend.S : 0.f;
-        if (a.row_max) a.row_max[n] = pend.M;
-        if (a.row_sumexp) a.row_sumexp[n] = bad ? nan : pend.S;
-      }
+      if (x == 0) write_row(a, n, bad, pend.M, pend.S, pend.Tm, logs, pend.zy, pend.before);
       auto put = [&](int at, int id, float lp) {
         const size_t o = (size_t)n * K + at;
         a.top_ids[o] = bad ? -1 : id;
@@ -448,18 +634,7 @@ __global__ void __launch_bounds__(kLpBlock, 2) token_logprobs_kernel(LpParams a,
       for (int n = first; n < a.N; n += step) {
         const int y = a.tokens[n];
         if (y >= 0 && y < V) continue;
-        if (x == 0) {
-          if (y != -1) set_device_error(a.err, DSPARK_ERR_DEVICE_CHECK);
-          a.logprob[n] = 0.f;
-          a.rank[n] = 0;
-          if (a.entropy) a.entropy[n] = 0.f;
-          if (a.row_max) a.row_max[n] = -INFINITY;
-          if (a.row_sumexp) a.row_sumexp[n] = 0.f;
-        }
-        for (int j = x; j < K; j += kLpClose) {
-          a.top_ids[(size_t)n * K + j] = -1;
-          a.top_logprobs[(size_t)n * K + j] = -INFINITY;
-        }
+        no_token(a, n, y, x);
       }
     int it = 0;
     RowsOf rows(a.tokens, a.N, V, first, step);
@@ -592,27 +767,9 @@ __global__ void __launch_bounds__(kLpBlock, 2) token_logprobs_kernel(LpParams a,
         } else if (n_cand <= kLpCap) {
           got = select_top(sh, x, n_cand, K);
         } else {
-          // more elements at or above the bound than keys fit (equal logits, or all the large
-          // ones in few threads' hands): the same selection tile by tile, keeping the K best
-          auto sweep = [&](int from, int to) {
-            for (int base = from; base < to; base += kLpCap / 2) {
-              close_sync();
-              if (x == 0) sh.n_cand = got;
-              for (int j = x; j < got; j += kLpClose) sh.cand[j] = sh.best[j];
-              const unsigned long long floor_key = got == K ? sh.best[K - 1] : 0ull;
-              close_sync();
-              for (int v = base + x; v < min(to, base + kLpCap / 2); v += kLpClose) {
-                const float z = elem_to_float(r.row[v]);
-                const unsigned long long key = top_key(z, v);
-                if (z == z && key > floor_key) sh.cand[atomicAdd(&sh.n_cand, 1)] = key;
-              }
-              close_sync();
-              if (sh.n_cand > got) got = select_top(sh, x, sh.n_cand, K);
-            }
-          };
-          if (c == 0) sweep(0, r.rc.head);
-          sweep(r.rc.head + r.c0 * N, r.rc.head + r.c1 * N);
-          if (c == 0) sweep(V - r.rc.tail, V);
+          if (c == 0) sweep(sh, x, r.row, 0, r.rc.head, K, got);
+          sweep(sh, x, r.row, r.rc.head + r.c0 * N, r.rc.head + r.c1 * N, K, got);
+          if (c == 0) sweep(sh, x, r.row, V - r.rc.tail, V, K, got);
           if (got == 0) select_top(sh, x, 0, K);
         }
         for (int j = x; j < K; j += kLpClose) send_u64(&sh.all[c * K + j], &sh.merge_full, merger, sh.best[j]);
@@ -744,6 +901,10 @@ __global__ void __launch_bounds__(kLgThreads) token_logprobs_grad_kernel(LgParam
 template <typename T>
 cudaError_t launch_lp(LpParams p, cudaStream_t stream) {
   const int chunks = p.V / Chunk<T>::N;
+  if (chunks <= kLpShortChunks) {
+    static_assert(kLpShortChunks * Chunk<T>::N <= kLpShortSlots * kLpClose * 16, "slots of a short row");
+    return launch_pdl(token_logprobs_short_kernel<T>, dim3((unsigned)p.N), dim3(kLpClose), 0, stream, p);
+  }
   const size_t smem = (size_t)kLpRing * kLpPieceChunks * 16 + 2 * kLpSlots * kLpThreads * sizeof(float);
   static std::atomic<int> cache[4][kMaxCachedDevices];
   // CTAs a row is cut into: the fewest estimated cycles, a CTA streaming 12 bytes a cycle and

@@ -6,7 +6,7 @@ Tolerances.  A softmax sum of at most 9001 terms is formed by lanes that add at 
 each (512 lanes a CTA) and a tree of 10: under 50 roundings of 2^-24, 3e-6 relative; an
 exponential adds 2^-22, and its argument's rounding |z - m| 2^-23 <= 5e-6 for terms that
 matter (e^-40 at most beside them).  So sums agree within 1e-5 relative (SUM), logarithms of
-them within 1e-5 absolute.  An output of 16 bits is rounded once more, by half a step of its
+them within 1e-5 absolute (20011 terms: the lanes of 2 to 8 CTAs, no more each).  An output of 16 bits is rounded once more, by half a step of its
 type.  Longer rows (one case) have 8 CTAs and 125 terms a lane: the same bound."""
 import math
 
@@ -110,7 +110,8 @@ def check_logprobs(z, tokens, top, ws):
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
 @pytest.mark.parametrize("layout", ["packed", "strided", "odd"])
 @pytest.mark.parametrize("n,V,top", [(1, 1, 1), (3, 7, 2), (2, 8, 8), (5, 1000, 20), (4, 1000, 128),
-                                     (1, 9001, 5), (3, 9001, 128), (700, 515, 1), (2, 4099, 0), (2, 100, 128)])
+                                     (1, 9001, 5), (3, 9001, 128), (700, 515, 1), (2, 4099, 0), (2, 100, 128),
+                                     (3, 20011, 64)])
 def test_logprobs(dtype, layout, n, V, top, ws):
     z = logits(n, V, dtype, 1, layout)
     tokens = torch.randint(0, V, (n,), generator=gen(2), device="cuda", dtype=torch.int32)
@@ -345,7 +346,8 @@ def check_distill(z, ids, t, labels, w, g, ws, out=None, tol=1.0, **kw):
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
 @pytest.mark.parametrize("layout", ["packed", "strided", "odd"])
-@pytest.mark.parametrize("n,V,K", [(1, 1, 1), (3, 7, 3), (4, 8, 128), (16, 1000, 8), (2, 9001, 128), (5, 9001, 33)])
+@pytest.mark.parametrize("n,V,K", [(1, 1, 1), (3, 7, 3), (4, 8, 128), (16, 1000, 8), (2, 9001, 128), (5, 9001, 33),
+                                   (3, 20011, 64)])
 @pytest.mark.parametrize("terms", [dict(kl=1.0), dict(kl=0.0, tv=0.9, ce=0.1), dict(kl=0.5, tv=0.3, ce=0.2, temperature=2.0)],
                          ids=["kl", "tv+ce", "all"])
 def test_distill(dtype, layout, n, V, K, terms, ws):
@@ -363,7 +365,7 @@ def test_distill(dtype, layout, n, V, K, terms, ws):
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
 @pytest.mark.parametrize("out", ["in place", "off by one"])
-@pytest.mark.parametrize("n,V", [(3, 1000), (2, 9001), (400, 257)])
+@pytest.mark.parametrize("n,V", [(3, 1000), (2, 9001), (400, 257), (2, 20011)])
 def test_distill_output_buffers(dtype, out, n, V, ws):
     z = logits(n, V, dtype, 30)
     ids, t = teacher(n, V, 16, 31)
