@@ -518,13 +518,14 @@ __global__ void __launch_bounds__(128) eg_join_kernel(EgParams a, int buf) {
   }
 }
 
-// Few positions: a CTA owns the table rows [range kRangeRows ..) of one column block (of all of
+// Few positions of narrow rows: a CTA owns the table rows [range kRangeRows ..) of one column block (of all of
 // them where rows are not 16-byte aligned).  It finds the positions of its rows among all ids,
 // orders them by (id, position) with a counting sort in shared memory, zeroes the rows that
 // have none and sums the others: one launch, and nothing waits for anything.  A run of
 // kLongRun positions or more is summed by the CTA's eight warps, joined in order.
 constexpr int kRangeMost = 2048;            // positions
 constexpr int kRangeRows = 2048;            // rows of a CTA, at most
+constexpr int kRangeCols = 4;               // column blocks (512 bytes of d_out), at most
 constexpr int kLongRun = 64;
 template <typename T, typename O, bool Vec>
 __global__ void __launch_bounds__(kEmThreads) eg_range_kernel(EgParams a, int rows, int col_ctas) {
@@ -758,7 +759,9 @@ cudaError_t launch_eg(EgParams p, void* ws, cudaStream_t stream) {
   const bool vec = rows_aligned(p.d_out, p.ld, sizeof(T)) && rows_aligned(p.dW, p.ld_w, sizeof(O)) &&
                    p.D % Chunk<T>::N == 0;
   if (p.N == 0 && p.accumulate) return cudaSuccess;
-  if (p.N <= kRangeMost)
+  // (1280 positions of 129280 x 256 in fp32, 2 column blocks: 26 us and 32 by the sort; of
+  // 30000 x 2560, 20 blocks: 78 and 57)
+  if (p.N <= kRangeMost && cdiv(p.D, 32 * Chunk<T>::N) <= kRangeCols)
     return vec ? launch_eg_range<T, O, true>(p, stream) : launch_eg_range<T, O, false>(p, stream);
   const EgPlan plan = eg_plan(p.N, p.V, p.D);
   for (int i = 0; i < 2; ++i) {

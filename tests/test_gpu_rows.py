@@ -568,7 +568,7 @@ def check_embed_grad(d_out, ids, V, out=None, dtype=None, accumulate=False):
 @pytest.mark.parametrize("kind", ["uniform", "uneven", "same"])
 @pytest.mark.parametrize("n,V,D", [(0, 5, 8), (1, 1, 1), (9, 100, 17), (64, 10, 8), (1000, 300, 256), (8192, 50, 16),
                                    (8193, 1000, 24), (30000, 300000, 8), (20000, 513, 33), (2049, 70, 40),
-                                   (140000, 5000, 16)])
+                                   (140000, 5000, 16), (700, 50, 2560)])
 def test_embed_grad(dtype, out_dtype, kind, n, V, D):
     d_out = logits(n, D, dtype, 60)
     check_embed_grad(d_out, ids_of(kind, n, V, 61), V, dtype=out_dtype)
