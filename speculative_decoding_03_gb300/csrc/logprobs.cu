@@ -32,6 +32,9 @@ constexpr int kLpClose = 128;               // closing threads (4 warps)
 constexpr int kLpBlock = kLpThreads + 32 + kLpClose;
 constexpr int kLpPieceChunks = 1024;        // 16 KB: 4 chunks (64 bytes) of each consumer
 constexpr int kLpRing = 4;                  // pieces in flight, two CTAs an SM
+// rows announced: the producer is at most 5 rows before the consumers' (its ring holds 4
+// pieces of at least a row each), and those 2 before the closing warps
+constexpr int kLpRows = 8;
 constexpr int kLpSlots = 12;                // maxima of a consumer thread kept for a row
 constexpr int kLpCap = 768;                 // candidate keys of a CTA
 constexpr int kLpList = 512;                // slots listed to be read again
@@ -88,7 +91,7 @@ __device__ __forceinline__ float group_value(uint32_t key) {
   return __uint_as_float((key & 0x80000000u) ? key & 0x7FFFFFFFu : ~key);
 }
 // A number that at least K of the n (at most 256) keys reach: the K-th largest less 1023 at
-// most (2^-13 of its value), found by halving the keys' range.  By a whole warp.
+// most (2^-13 of its value), found by quartering the keys' range.  By a whole warp.
 __device__ __forceinline__ uint32_t kth_bound(const uint32_t* keys, int n, int K) {
   const int lane = threadIdx.x & 31;
   uint32_t k[8], lo = 0xFFFFFFFFu, hi = 0u;
@@ -101,12 +104,26 @@ __device__ __forceinline__ uint32_t kth_bound(const uint32_t* keys, int n, int K
   lo = __reduce_min_sync(0xffffffffu, lo);   // all n reach it, and n >= K
   hi = __reduce_max_sync(0xffffffffu, hi);
   while (hi - lo > 1023u) {
-    const uint32_t mid = lo + (hi - lo) / 2 + 1;
-    int reach = 0;
+    // three marks at once, their counts (256 at most) in 10 bits each
+    const uint32_t step = (hi - lo) / 4 + 1;
+    uint32_t reach = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) reach += k[i] >= mid;
-    if (__reduce_add_sync(0xffffffffu, reach) >= K) lo = mid;
-    else hi = mid - 1;
+    for (int i = 0; i < 8; ++i)
+      if (32 * i < n)
+        reach += (uint32_t)(k[i] >= lo + step) + ((uint32_t)(k[i] >= lo + 2 * step) << 10) +
+                 ((uint32_t)(k[i] >= lo + 3 * step) << 20);
+    reach = __reduce_add_sync(0xffffffffu, reach);
+    if ((int)(reach >> 20) >= K) {
+      lo += 3 * step;
+    } else if ((int)(reach >> 10 & 1023u) >= K) {
+      hi = lo + 3 * step - 1;
+      lo += 2 * step;
+    } else if ((int)(reach & 1023u) >= K) {
+      hi = lo + 2 * step - 1;
+      lo += step;
+    } else {
+      hi = lo + step - 1;
+    }
   }
   return lo;
 }
@@ -123,28 +140,34 @@ struct LpShared {
   float2 tb[2][8 * kLpWarps];                         // t, elements before y (as bits)
   int list[kLpList];
   int n_cand, n_list;
+  int row[kLpRows];                                   // the producer's rows, -1 after the last
+  uint64_t row_full[kLpRows];
   uint64_t full[kLpRing], empty[kLpRing];
   uint64_t stats_full[2], stats_free[2];              // consumers to closing warps and back
   uint64_t sums_full[2], merge_full;                  // messages of the cluster's CTAs
 };
 
 // The rows of a cluster, in order, for a whole warp: every step-th row that has a token, so
-// that rows without one leave no cluster idle.  (Each warp reads all the tokens for that;
-// above kLpDeal rows the rows are dealt by number instead, and those without a token skipped.)
+// that rows without one leave no cluster idle.  (It reads all the tokens for that; above
+// kLpDeal rows the rows are dealt by number instead, and those without a token skipped.)
 constexpr int kLpDeal = 1 << 16;
 struct RowsOf {
+  static constexpr int kWindows = 8;         // of 32 rows, read together
   const int32_t* tokens;
   int N, V, step, want, n, seen;
-  unsigned window;                           // rows with a token among n .. n + 31
+  unsigned window[kWindows];                 // rows with a token from n on
   bool deal;
-  __device__ __forceinline__ unsigned look(int at) const {
-    const int i = at + (threadIdx.x & 31);
-    const int y = i < N ? tokens[i] : -1;
-    return __ballot_sync(0xffffffffu, y >= 0 && y < V);
+  __device__ __forceinline__ void look() {
+    const int lane = threadIdx.x & 31;
+    int y[kWindows];
+#pragma unroll
+    for (int i = 0; i < kWindows; ++i) y[i] = n + 32 * i + lane < N ? tokens[n + 32 * i + lane] : -1;
+#pragma unroll
+    for (int i = 0; i < kWindows; ++i) window[i] = __ballot_sync(0xffffffffu, y[i] >= 0 && y[i] < V);
   }
   __device__ __forceinline__ RowsOf(const int32_t* t, int N_, int V_, int first, int step_)
       : tokens(t), N(N_), V(V_), step(step_), want(first), n(0), seen(0), deal(t && N_ <= kLpDeal) {
-    window = deal ? look(0) : 0u;
+    if (deal) look();
   }
   // the next row, or -1
   __device__ __forceinline__ int next() {
@@ -156,16 +179,27 @@ struct RowsOf {
       }
       return -1;
     }
-    while (n < N && seen + __popc(window) <= want) {
-      seen += __popc(window);
-      n += 32;
-      window = n < N ? look(n) : 0u;
+    for (; n < N; look()) {
+      int left = want - seen, found = -1, all = 0;
+#pragma unroll
+      for (int i = 0; i < kWindows; ++i) {
+        const int c = __popc(window[i]);
+        if (found < 0 && left < c) {
+          unsigned w = window[i];
+          for (int k = left; k > 0; --k) w &= w - 1;
+          found = n + 32 * i + __ffs(w) - 1;
+        }
+        left -= c;
+        all += c;
+      }
+      if (found >= 0) {
+        want += step;
+        return found;
+      }
+      seen += all;
+      n += 32 * kWindows;
     }
-    if (n >= N) return -1;
-    unsigned left = window;
-    for (int k = want - seen; k > 0; --k) left &= left - 1;
-    want += step;
-    return n + __ffs(left) - 1;
+    return -1;
   }
 };
 
@@ -426,6 +460,7 @@ __global__ void __launch_bounds__(kLpBlock, 2) token_logprobs_kernel(LpParams a,
       mbar_init(&sh.stats_free[i], 1);
       mbar_init(&sh.sums_full[i], 1);
     }
+    for (int i = 0; i < kLpRows; ++i) mbar_init(&sh.row_full[i], 1);
     mbar_init(&sh.merge_full, 1);
     fence_mbar_init();
   }
@@ -435,16 +470,23 @@ __global__ void __launch_bounds__(kLpBlock, 2) token_logprobs_kernel(LpParams a,
   pdl_launch_dependents();
   auto part_of = [&](int n) { return row_part<T>(a.z, a.ld, n, V, c, log_C, 0x7FFFFFFF); };
   bool late = false;                         // a bounded wait ran out: give up
+  // the cluster's it-th row, or -1; by whole warps
+  auto announced = [&](int it) {
+    const bool ok = mbar_wait(&sh.row_full[it % kLpRows], (it / kLpRows) & 1);
+    if (!__all_sync(0xffffffffu, ok)) {
+      late = true;
+      return -1;
+    }
+    return sh.row[it % kLpRows];
+  };
 
   if (warp < kLpWarps) {
     // ---- consumers
     int it = 0, slot = 0;
     uint32_t phase = 0;
-    RowsOf rows(a.tokens, a.N, V, first, step);
-    int n_next = rows.next();
-    while (n_next >= 0 && !late) {
-      const int n = n_next;
-      n_next = rows.next();
+    while (!late) {
+      const int n = announced(it);
+      if (n < 0) break;
       const int y = a.tokens ? a.tokens[n] : 0;
       const int b = it & 1;
       const RowPart<T> r = part_of(n);
@@ -556,7 +598,13 @@ __global__ void __launch_bounds__(kLpBlock, 2) token_logprobs_kernel(LpParams a,
     // ---- producer
     int sent = 0;
     RowsOf rows(a.tokens, a.N, V, first, step);
-    for (int n; !late && (n = rows.next()) >= 0;) {
+    for (int it = 0;; ++it) {
+      const int n = rows.next();
+      if (lane == 0) {
+        sh.row[it % kLpRows] = n;
+        mbar_arrive(&sh.row_full[it % kLpRows]);
+      }
+      if (n < 0) break;
       if (lane == 0) {
         const RowPart<T> r = part_of(n);
         for (int i = 0; i < r.held; i += kLpPieceChunks, ++sent) {
@@ -568,6 +616,7 @@ __global__ void __launch_bounds__(kLpBlock, 2) token_logprobs_kernel(LpParams a,
         }
       }
       late = __any_sync(0xffffffffu, late);
+      if (late) break;
     }
     if (lane == 0) {
       // copies in flight end before the CTA does (at once, unless the consumers gave up)
@@ -637,8 +686,10 @@ __global__ void __launch_bounds__(kLpBlock, 2) token_logprobs_kernel(LpParams a,
         no_token(a, n, y, x);
       }
     int it = 0;
-    RowsOf rows(a.tokens, a.N, V, first, step);
-    for (int n; (n = rows.next()) >= 0;) {
+    for (;;) {
+      const int n = announced(it);
+      late = close_any(late);
+      if (late || n < 0) break;
       const int y = a.tokens ? a.tokens[n] : 0;
       const int b = it & 1;
       const uint32_t buf_phase = (it >> 1) & 1;
