@@ -18,7 +18,13 @@
 // elements reach (-G log(1 - K / G) of them for random data: 89 at K = 64, G = 128).  The few
 // 64-byte slots whose maximum reaches it are read again, and one CTA of the cluster (in turn)
 // ranks, by counting, the elements that the others send to it.  The rank is counted in the
-// stream: a sampled token may have hundreds of elements before it.
+// stream: a sampled token may have hundreds of elements before it, and reading those again
+// cost more than the stream (224 against 189 us at the size below).
+//
+// Measured on a GB300 (copy rate 6782 GB/s): 1536 rows of 129280 in fp32, 64 alternatives,
+// 154 us = 5.15 TB/s (0.76 of the copy rate; 10.1 rounds of 152 clusters take 11, and a CTA
+// stands still about 1500 of 23000 cycles between rows); 256 rows of 151936, 128 with a token,
+// 20 alternatives, 28 us; rows of up to 64 KB by token_logprobs_short_kernel below.
 #include "internal.h"
 #include "rows.cuh"
 
@@ -40,9 +46,9 @@ constexpr int kLpCap = 768;                 // candidate keys of a CTA
 constexpr int kLpList = 512;                // slots listed to be read again
 constexpr int kLpTop = kMaxTop;             // most alternatives
 constexpr int kLpMaxima = 256;              // most groups
-constexpr int kLpShortSlots = 8;
-// a short row: 32 KB
-constexpr int kLpShortChunks = 2048;
+constexpr int kLpShortSlots = 16;
+// a short row: up to 64 KB (2000 rows of 16000 in fp32: 56 us, 80 by the ring)
+constexpr int kLpShortChunks = 4096;
 
 struct LpParams {
   const void* z;
@@ -140,6 +146,7 @@ struct LpShared {
   float2 tb[2][8 * kLpWarps];                         // t, elements before y (as bits)
   int list[kLpList];
   int n_cand, n_list;
+  float thr;
   int row[kLpRows];                                   // the producer's rows, -1 after the last
   uint64_t row_full[kLpRows];
   uint64_t full[kLpRing], empty[kLpRing];
@@ -304,7 +311,9 @@ struct LpShortShared {
   uint32_t gmax[kLpMaxima];
   float4 part[kLpClose / 32];
   float slots[kLpShortSlots][kLpClose];
-  int n_cand;
+  int list[kLpList];
+  float thr;
+  int n_cand, n_list;
 };
 template <typename T>
 __global__ void __launch_bounds__(kLpClose, 8) token_logprobs_short_kernel(LpParams a) {
@@ -320,7 +329,7 @@ __global__ void __launch_bounds__(kLpClose, 8) token_logprobs_short_kernel(LpPar
     no_token(a, n, y, x);
     return;
   }
-  if (x == 0) sh.n_cand = 0;
+  if (x == 0) sh.n_cand = sh.n_list = 0;
   const RowPart<T> r = row_part<T>(a.z, a.ld, n, V, 0, 0, 0x7FFFFFFF);
   const float zy = a.tokens ? elem_to_float(r.row[y]) : INFINITY;
   const int loose_n = r.rc.head + r.rc.tail;
@@ -401,7 +410,12 @@ __global__ void __launch_bounds__(kLpClose, 8) token_logprobs_short_kernel(LpPar
   const float logs = logf(S);
   if (x == 0) write_row(a, n, bad, M, S, Tm, logs, zy, before);
   if (K == 0) return;
-  const float thr = group_value(kth_bound(sh.gmax, groups, K));
+  if (warp == 0) {
+    const uint32_t key = kth_bound(sh.gmax, groups, K);
+    if (lane == 0) sh.thr = group_value(key);
+  }
+  __syncthreads();
+  const float thr = sh.thr;
   auto consider = [&](float z, int v) {
     if (z >= thr) {
       const int to = atomicAdd(&sh.n_cand, 1);
@@ -409,17 +423,31 @@ __global__ void __launch_bounds__(kLpClose, 8) token_logprobs_short_kernel(LpPar
     }
   };
   if (x < loose_n) consider(zl, loose);
-  for (int u = 0; u < used; ++u) {
-    if (sh.slots[u][x] < thr) continue;
+  // the slots that reach the bound, listed, then their chunks dealt over all threads
+  unsigned hits = 0u;
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const int j = x + (u * G + g) * kThreads;
-      if (j >= r.held) break;
-      float z[N];
-      unpack_chunk<T>(__ldg(r.body + j), z);
+  for (int u = 0; u < kLpShortSlots; ++u) hits |= (unsigned)(u < used && sh.slots[u][x] >= thr) << u;
+  if (hits) {
+    int to = atomicAdd(&sh.n_list, __popc(hits));
+    for (unsigned left = hits; left; left &= left - 1, ++to)
+      if (to < kLpList) sh.list[to] = (__ffs(left) - 1) * kThreads + x;
+  }
+  __syncthreads();
+  auto look = [&](int entry, int g) {        // chunk g of a slot
+    const int j = (entry & (kThreads - 1)) + (entry / kThreads * G + g) * kThreads;
+    if (j >= r.held) return;
+    float z[N];
+    unpack_chunk<T>(__ldg(r.body + j), z);
+    if (max_of(z) >= thr) {
 #pragma unroll
       for (int e = 0; e < N; ++e) consider(z[e], r.rc.head + j * N + e);
     }
+  };
+  if (sh.n_list <= kLpList) {
+    for (int k = x; k < sh.n_list * G; k += kThreads) look(sh.list[k / G], k % G);
+  } else {
+    for (; hits; hits &= hits - 1)
+      for (int g = 0; g < G; ++g) look((__ffs(hits) - 1) * kThreads + x, g);
   }
   __syncthreads();
   int got = 0;
@@ -752,7 +780,13 @@ __global__ void __launch_bounds__(kLpBlock, 2) token_logprobs_kernel(LpParams a,
       }
 
       // ---- a lower bound of the row's K-th largest element, from the maxima of its groups
-      const float thr = K > 0 ? group_value(kth_bound(sh.gall[b], G, K)) : INFINITY;
+      // (by one warp: four would take issue slots from the consumers)
+      if (K > 0 && x < 32) {
+        const uint32_t key = kth_bound(sh.gall[b], G, K);
+        if (lane == 0) sh.thr = group_value(key);
+      }
+      close_sync();
+      const float thr = K > 0 ? sh.thr : INFINITY;
 
       // ---- candidates for the K best: the slots that reach the bound
       int got = 0;
@@ -849,7 +883,9 @@ __global__ void __launch_bounds__(kLpBlock, 2) token_logprobs_kernel(LpParams a,
 
 // ------------------------------------------------------------------------------ gradient
 // dz_v = g_lp ([v = y] - p_v) - g_H p_v (log p_v + H), p_v = exp(z_v - m) / s: one read and
-// one write of the row, nothing kept between them, so a grid of independent segments.
+// one write of the row, nothing kept between them, so a grid of independent segments of 64 KB
+// (four 16-byte loads a thread in flight).  Bound by memory: 1280 rows of 129280 in bf16, 1152
+// with a token, 99 us = 6.35 TB/s (0.94 of the copy rate).
 constexpr int kLgThreads = 256;
 constexpr int kLgBatch = 4;
 
@@ -952,7 +988,8 @@ __global__ void __launch_bounds__(kLgThreads) token_logprobs_grad_kernel(LgParam
 template <typename T>
 cudaError_t launch_lp(LpParams p, cudaStream_t stream) {
   const int chunks = p.V / Chunk<T>::N;
-  if (chunks <= kLpShortChunks) {
+  // (20 rows of 16000 in fp32, 64 KB: 15 us, 13 by the ring; of 8000 no difference)
+  if (chunks <= kLpShortChunks / 2 || (chunks <= kLpShortChunks && p.N >= 304)) {
     static_assert(kLpShortChunks * Chunk<T>::N <= kLpShortSlots * kLpClose * 16, "slots of a short row");
     return launch_pdl(token_logprobs_short_kernel<T>, dim3((unsigned)p.N), dim3(kLpClose), 0, stream, p);
   }
