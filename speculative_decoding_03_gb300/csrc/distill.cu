@@ -22,6 +22,13 @@
 // stores that complete on that CTA's barrier.  An element that the teacher names is written
 // a second time by the warp that wrote it first.  Rows beyond a cluster's shared memory read
 // their rest again.
+//
+// Measured on a GB300 (copy rate 6782 GB/s): 1280 rows of 129280 in fp32, 1216 of them with a
+// weight, 206 us = 6.26 TB/s (0.92 of the copy rate); 1920 rows of 151936 in bf16, 1824 with a
+// weight, 199 us = 5.73 TB/s (0.85).  What is left is the consumers' own work: a build without
+// stores, without loads or without the exchange took as long.  8 consumer warps and 16 KB
+// pieces: 16 warps 345 against 266 us, 8 KB 213 against 206, 32 KB 232; one CTA an SM with twice
+// the ring 447 against 266.
 #include "internal.h"
 #include "rows.cuh"
 #include "sm100_ptx.cuh"
@@ -287,7 +294,8 @@ __device__ __forceinline__ void zero_row(T* out, int V, int c, int log_C, int t,
 }
 
 // Short rows: a CTA of four warps a row, the sums and the gradient from two reads (the second
-// finds the row in L1 or L2).  Many small CTAs an SM hide a row's steps behind other rows.
+// finds the row in L1 or L2).  Many small CTAs an SM hide a row's steps behind other rows:
+// 2000 rows of 4000 in fp32 18 us, 26 by the ring; of 8000 31 and 32.
 constexpr int kShortThreads = 128;
 constexpr int kShortChunks = 2048;          // 32 KB
 template <typename T, bool Grad>

@@ -4,7 +4,8 @@
 // Markov bias reads its rows by token id.  out[n] = scale W[id_n] (0 where id_n is -1), and
 // the table's gradient is dW[v] = scale sum_{n : id_n = v} d_out[n].
 //
-// The lookup is a copy bound by memory: a warp a row, 16 bytes a lane.
+// The lookup is a copy bound by memory: a warp a row (or 2 KB of it), 16 bytes a lane.  16384
+// rows of 2560 in bf16: 19.9 us for 168 MB, some of them from L2.
 //
 // The gradient sums in a fixed order, so equal inputs give equal bits: the positions are
 // sorted by (id, position), and tiles of consecutive sorted positions are summed in fp32,
@@ -15,6 +16,11 @@
 // grid above (2 launches a pass); up to 2048 positions need none (eg_range_kernel).  The
 // table's zeroes, the bulk of the bytes, are written in the sort's launch by the CTAs that do
 // not sort, so that the sort hides behind them.
+//
+// Measured on a GB300 (copy rate 6782 GB/s; a plain memset writes 7.5 TB/s): 32768 positions of
+// 151936 x 2560 in bf16, tokens by 1 / rank, 167 us for 946 MB = 5.68 TB/s (sort and zeroes 115,
+// sums 41, join 10); 1280 positions of 129280 x 256 in fp32, 26 us for 134 MB = 5.2 TB/s (a
+// memset of the table alone takes 21).
 #include "internal.h"
 #include "rows.cuh"
 
