@@ -437,7 +437,9 @@ __global__ void __launch_bounds__(kDsBlock, 2) distill_kernel(DsParams a, int lo
     for (int n = first; n < a.N && !late; n += step) {
       if (a.weights && a.weights[n] == 0.f) continue;
       const int b = it & 1;
-      if (it >= 2 && !mbar_wait(&sh.teacher_free[b], ((it >> 1) - 1) & 1)) { late = true; break; }
+      late = it >= 2 && !mbar_wait(&sh.teacher_free[b], ((it >> 1) - 1) & 1);
+      late = __any_sync(0xffffffffu, late);
+      if (late) break;
       read_teacher<T>(a, n, row_part<T>(a.z, a.ld, n, a.V, c, log_C, a.resident), c == 0, sh.teacher[b]);
       if (lane == 0) mbar_arrive(&sh.teacher_full[b]);
       ++it;

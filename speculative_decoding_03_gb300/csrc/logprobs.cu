@@ -665,7 +665,8 @@ __global__ void __launch_bounds__(kLpBlock, 2) token_logprobs_kernel(LpParams a,
     auto merge = [&] {
       const int n = pend.n;
       pend.n = -1;
-      if (!wait_cluster(&sh.merge_full, pend.phase)) late = true;
+      late = close_any(late || !wait_cluster(&sh.merge_full, pend.phase));
+      if (late) return;                      // (the lists' lengths are not there)
       const bool bad = !(pend.S <= FLT_MAX); // NaN or +inf among the logits
       const float logs = logf(pend.S);
       // keys of the lists up to this lane's

@@ -339,8 +339,9 @@ struct RunningSoftmax {
 };
 
 // s = sum exp(k (z - R)) alone, without a maximum per element: R is raised (to a batch's
-// maximum, which only then is looked for) when the sum leaves [2^-20, 2^30], which the first
-// batch with an element above -inf does and after it only elements more than 20 / k above R.
+// maximum, which only then is looked for) when the sum leaves [2^-20, 2^14], which the first
+// batch with an element above -inf does and after it only elements about 10 / k above R.  (A
+// wider range would cost logarithms of the sum digits: they are taken relative to R.)
 struct RunningSum {
   float R, k;
   F2 s;
@@ -366,7 +367,7 @@ struct RunningSum {
     F2 t = f2_add(s, batch<n>(z));
     float a, b;
     f2_get(t, a, b);
-    if (!(a + b >= 0x1p-20f && a + b <= 0x1p30f)) {
+    if (!(a + b >= 0x1p-20f && a + b <= 0x1p14f)) {
       const float bm = max_of(z);
       float u, v;
       f2_get(s, u, v);
