@@ -12,14 +12,14 @@
 // whatever the token frequencies.  A run of one id inside a tile is written at once; a run
 // that crosses tiles leaves partial sums that are joined in tile order, first within a CTA
 // (8 tiles, shared memory), then by a last kernel (workspace).  The sort is a stable
-// radix sort of 9 bits a pass, by one cluster of CTAs up to 131072 positions (1 launch), by the
-// grid above (2 launches a pass); up to 2048 positions need none (eg_range_kernel).  The
+// radix sort of 9 bits a pass, by one cluster of CTAs where the zeroes hide it or positions are
+// few (1 launch), else by the grid (2 launches a pass); up to 2048 positions need none (eg_range_kernel).  The
 // table's zeroes, the bulk of the bytes, are written in the sort's launch by the CTAs that do
 // not sort, so that the sort hides behind them.
 //
 // Measured on a GB300 (copy rate 6782 GB/s; a plain memset writes 7.5 TB/s): 32768 positions of
 // 151936 x 2560 in bf16, tokens by 1 / rank, 167 us for 946 MB = 5.68 TB/s (sort and zeroes 115,
-// sums 41, join 10); 1280 positions of 129280 x 256 in fp32, 26 us for 134 MB = 5.2 TB/s (a
+// sums 41, join under 10); 1280 positions of 129280 x 256 in fp32, 26 us for 134 MB = 5.2 TB/s (a
 // memset of the table alone takes 21).
 #include "internal.h"
 #include "rows.cuh"
@@ -29,7 +29,9 @@ namespace {
 
 constexpr int kEmThreads = 256;
 constexpr int kEmWarps = kEmThreads / 32;
-constexpr int kSortMost = 131072;           // positions sorted by one cluster
+constexpr int kSortMost = 8192;             // positions always sorted by one cluster
+// bytes of zeroes for each position that make the cluster's sort the shorter way
+constexpr long long kSortHidden = 4000;
 constexpr int kRadixBits = 9, kRadix = 1 << kRadixBits;
 constexpr int kRadixTile = 2048;            // keys of a radix CTA
 constexpr int kRadixRounds = kRadixTile / kEmThreads;
@@ -488,13 +490,14 @@ __global__ void __launch_bounds__(128) eg_join_kernel(EgParams a, int buf) {
   const int k = skey[i1];
   if (k >= a.V || skey[i1 - 1] != k) return;
   if (skey[i0] == k && i0 > 0 && skey[i0 - 1] == k) return;   // began before this tile
-  int lo = i1 + 1, hi = a.N;                // the run's end
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (skey[mid] == k) lo = mid + 1;
-    else hi = mid;
+  // tiles after t that hold it: those that begin with it, 128 looked at together
+  int n = 0;
+  for (;;) {
+    const long long at = (long long)(t + 1 + n + (int)threadIdx.x) * span;
+    const int more = __syncthreads_count(at < a.N && skey[at] == k);
+    n += more;
+    if (more < 128) break;
   }
-  const int n = (lo - 1) / span - t;        // tiles after t that hold it
   const int u0 = (int)((long long)n * warp / 4), u1 = (int)((long long)n * (warp + 1) / 4);
   float sum[N];
 #pragma unroll
@@ -783,7 +786,9 @@ cudaError_t launch_eg(EgParams p, void* ws, cudaStream_t stream) {
   // zeroing CTAs: four an SM, but no more than there are 16 KB to write
   const long long most = (long long)p.V * p.D * p.elem_w / 16384 + 1;
   const int fill = p.accumulate ? 0 : (int)(most < 4 * 152 ? align_up((size_t)most, 8) : 4 * 152);
-  if (plan.radix_tiles == 0) {
+  // by the grid where the zeroes would not hide the cluster's sort: of 151936 x 256 in bf16 (78
+  // MB) 16384, 32768, 131072 positions take 40, 60, 170 us by the cluster, 45, 54, 73 by the grid
+  if (p.N <= kSortMost || (!p.accumulate && (long long)p.V * p.D * p.elem_w >= kSortHidden * p.N)) {
     e = launch_rows_cluster(eg_sort_kernel, 8 + fill, 8, kEmThreads, 0, stream, p, plan.passes);
   } else {
     for (int i = 0; i < plan.passes && e == cudaSuccess; ++i) {
