@@ -132,6 +132,25 @@ def test_logprobs_many_rows_of_one_cta_and_long_rows(ws):
         close(got["entropy"], ref["entropy"], atol=9 * SUM)
 
 
+@pytest.mark.parametrize("n", [3000, 70000])
+def test_logprobs_few_answers_among_many_rows(n, ws):
+    """Long rows, nearly all without a token, below and above the number of rows that are dealt
+    by their tokens."""
+    V = 33000
+    z = torch.empty(n, V, dtype=torch.bfloat16, device="cuda").normal_(0, 3, generator=gen(16))
+    tokens = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    at = torch.randperm(n, generator=gen(17), device="cuda")[:40]
+    tokens[at] = torch.randint(0, V, (40,), generator=gen(18), device="cuda", dtype=torch.int32)
+    got = ds.token_logprobs(z, tokens, 7, ws)
+    ref = ref_logprobs(z[at], tokens[at], 7)
+    for key in ("top_ids", "rank"):
+        assert torch.equal(got[key][at].long(), ref[key])
+    for key in ("logprob", "top_logprobs", "row_sumexp"):
+        close(got[key][at], ref[key], atol=3 * SUM)
+    off = tokens < 0
+    assert (got["logprob"][off] == 0).all() and (got["rank"][off] == 0).all() and (got["top_ids"][off] == -1).all()
+
+
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
 @pytest.mark.parametrize("V", [1000, 9001, 40000])
 def test_logprobs_ties_and_orders(dtype, V, ws):
@@ -568,10 +587,17 @@ def check_embed_grad(d_out, ids, V, out=None, dtype=None, accumulate=False):
 @pytest.mark.parametrize("kind", ["uniform", "uneven", "same"])
 @pytest.mark.parametrize("n,V,D", [(0, 5, 8), (1, 1, 1), (9, 100, 17), (64, 10, 8), (1000, 300, 256), (8192, 50, 16),
                                    (8193, 1000, 24), (30000, 300000, 8), (20000, 513, 33), (2049, 70, 40),
-                                   (140000, 5000, 16), (700, 50, 2560)])
+                                   (140000, 5000, 16), (700, 50, 2560), (3000, 300000, 8)])
 def test_embed_grad(dtype, out_dtype, kind, n, V, D):
     d_out = logits(n, D, dtype, 60)
     check_embed_grad(d_out, ids_of(kind, n, V, 61), V, dtype=out_dtype)
+
+
+@pytest.mark.parametrize("kind", ["uniform", "uneven", "same"])
+def test_embed_grad_many_positions_of_a_large_table(kind):
+    """Zeroes enough to hide one cluster's sort of several tiles a CTA."""
+    n, V, D = 17000, 70000, 256
+    check_embed_grad(logits(n, D, torch.float32, 58), ids_of(kind, n, V, 59), V)
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
