@@ -22,9 +22,9 @@
 // cost more than the stream (224 against 189 us at the size below).
 //
 // Measured on a GB300 (copy rate 6782 GB/s): 1536 rows of 129280 in fp32, 64 alternatives,
-// 154 us = 5.15 TB/s (0.76 of the copy rate; 10.1 rounds of 152 clusters take 11, and a CTA
+// 152 us = 5.2 TB/s (0.77 of the copy rate; 10.1 rounds of 152 clusters take 11, and a CTA
 // stands still about 1500 of 23000 cycles between rows); 256 rows of 151936, 128 with a token,
-// 20 alternatives, 28 us; rows of up to 64 KB by token_logprobs_short_kernel below.
+// 20 alternatives, 24 us; rows of up to 64 KB by token_logprobs_short_kernel below.
 #include "internal.h"
 #include "rows.cuh"
 
@@ -997,15 +997,16 @@ cudaError_t launch_lp(LpParams p, cudaStream_t stream) {
   const size_t smem = (size_t)kLpRing * kLpPieceChunks * 16 + 2 * kLpSlots * kLpThreads * sizeof(float);
   static std::atomic<int> cache[4][kMaxCachedDevices];
   // CTAs a row is cut into: the fewest estimated cycles, a CTA streaming 12 bytes a cycle and
-  // closing a row in 12000 (measured with both CTAs of an SM at work), beside the next row's
-  // stream.  1536 rows of 129280 in fp32: 1, 2, 4, 8 CTAs took 159, 151, 189, 312 us
+  // closing a row in 14000 (measured with both CTAs of an SM at work), beside the next row's
+  // stream.  1536 rows of 129280 in fp32: 1, 2, 4 CTAs took 164, 152, 201 us; 256 rows
+  // of 151936, half of them with a token: 1, 2, 4, 8 took 35, 24, 28, 37; 64 rows: 29, 20, 16, 20
   int log_C = 0, clusters = 0;
   long long best = 0;
   for (int i = 3; i >= 0; --i) {
     if (i > 0 && (chunks >> i) < kLpPieceChunks) continue;
     const int most = device_clusters(cache[i], token_logprobs_kernel<T>, 1 << i, kLpBlock, smem);
     if (most <= 0) return cudaErrorInvalidConfiguration;
-    const long long stream_c = (long long)(chunks >> i) * 16 / 12, close_c = 12000;
+    const long long stream_c = (long long)(chunks >> i) * 16 / 12, close_c = 14000;
     const long long rounds = cdiv(p.N, most);
     const long long cost = stream_c + (rounds - 1) * (stream_c > close_c ? stream_c : close_c) + close_c;
     if (clusters == 0 || cost < best) {
