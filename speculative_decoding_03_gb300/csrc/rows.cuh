@@ -1,7 +1,7 @@
 // Device helpers of the kernels that stream rows of logits or of a table in 32, bf16 or
 // fp16 bits: 16-byte chunks unpacked to fp32, packed two-wide fp32 arithmetic, the chunk
-// layout of a row that may start off a 16-byte border, and thread-block-cluster barriers
-// with reads of another CTA's shared memory.
+// layout of a row that may start off a 16-byte border, thread-block-cluster barriers
+// with reads and messages between CTAs' shared memory, and running softmax sums.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -134,21 +134,9 @@ __device__ __forceinline__ RowChunks row_chunks(const T* row, int V) {
 }
 
 // ------------------------------------------------------------------------- clusters
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
 // every CTA of the cluster arrives, then waits; orders shared-memory accesses between CTAs
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
-// the same in two halves
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t cluster_map(const void* smem, uint32_t rank) {
   uint32_t a;
@@ -156,19 +144,6 @@ __device__ __forceinline__ uint32_t cluster_map(const void* smem, uint32_t rank)
                : "=r"(a)
                : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(smem))), "r"(rank));
   return a;
-}
-__device__ __forceinline__ float4 cluster_ld_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-__device__ __forceinline__ float cluster_ld_f(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
 }
 __device__ __forceinline__ unsigned long long cluster_ld_u64(uint32_t addr) {
   unsigned long long v;

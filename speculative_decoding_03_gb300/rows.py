@@ -17,7 +17,7 @@ import functools
 import math
 from typing import Dict, Optional
 
-from . import DSparkError, Workspace, lib, STATUS  # noqa: F401
+from . import DSparkError, Workspace, lib
 
 
 @functools.lru_cache(maxsize=None)
@@ -69,14 +69,11 @@ def _vector(t, name: str, n: int, dtype, like, k: Optional[int] = None):
     return t.data_ptr()
 
 
-def _device(like, ws: Workspace, *others):
+def _device(like, ws: Workspace):
     torch, _ = _types()
     if like.device.index != torch.cuda.current_device() or ws.buf.device != like.device:
         raise ValueError(f"tensors on {like.device}, workspace on {ws.buf.device}: both must be on "
                          f"the current device (cuda:{torch.cuda.current_device()})")
-    for t in others:
-        if t.device != like.device:
-            raise ValueError(f"tensors on {like.device} and {t.device}")
 
 
 _NOTHING = contextlib.nullcontext()
