@@ -1024,10 +1024,10 @@ cudaError_t launch_lp(LpParams p, cudaStream_t stream) {
 template <typename T>
 cudaError_t launch_lg(LgParams p, int N, cudaStream_t stream) {
   const int chunks = p.V / Chunk<T>::N;
-  // segments of about 4096 chunks (64 KB), or as many as give every SM eight CTAs
-  int segs = cdiv(chunks, 4096);
+  // segments of about 4096 chunks (64 KB), or as many as give every SM eight CTAs; one where a
+  // row is shorter than a chunk
+  int segs = chunks > 0 ? cdiv(chunks, 4096) : 1;
   while ((long long)segs * N < 2LL * kTargetCtas && chunks / (segs * 2) >= kLgThreads) segs *= 2;
-  if (segs < 1) segs = 1;
   p.segs = segs;
   return launch_pdl(token_logprobs_grad_kernel<T>, dim3((unsigned)((long long)segs * N)),
                     dim3(kLgThreads), 0, stream, p);

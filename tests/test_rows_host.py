@@ -1,0 +1,26 @@
+"""What the calls on rows do on the host before they launch, in a process that sees no device: a
+call that is not refused ends with the launch's error and touches none of its pointers."""
+import os
+import signal
+import subprocess
+import sys
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CUDA_ERROR = 3
+
+
+def status_of(call):
+    """Exit status of a process without devices that makes `call` (of test_rows_abi)."""
+    code = f"import sys; sys.path[:0] = [{os.path.join(ROOT, 'tests')!r}, {ROOT!r}]\n" \
+           f"import test_rows_abi as t\nsys.exit(t.{call})"
+    env = dict(os.environ, CUDA_VISIBLE_DEVICES="")
+    return subprocess.run([sys.executable, "-c", code], env=env, timeout=300).returncode
+
+
+@pytest.mark.parametrize("V,dtype", [(1, 0), (3, 0), (1, 1), (7, 2), (8, 1)])
+def test_token_logprobs_grad_of_rows_shorter_than_a_chunk(V, dtype):
+    """A row of fewer elements than 16 bytes hold has no chunk to cut into segments."""
+    status = status_of(f"logprobs_grad(V={V}, ld={V}, ld_d={V}, dtype={dtype})")
+    assert status != -signal.SIGFPE and status == CUDA_ERROR
