@@ -56,10 +56,9 @@ dspark_status distill(const void* logits, int dtype, int64_t ld, const int32_t* 
   if (!aligned(workspace, 256) || workspace_bytes < 256) return DSPARK_ERR_INVALID_ARG;
   if (!aligned_or_null(labels, 4) || !aligned_or_null(weights, 4) || !aligned_or_null(d_loss, 4))
     return DSPARK_ERR_INVALID_ARG;
-  if ((K == 0) != !teacher_ids || (K == 0) != !teacher_logits || !aligned_or_null(teacher_ids, 4) ||
-      !aligned_or_null(teacher_logits, 4))
-    return DSPARK_ERR_INVALID_ARG;
-  if (N == 0) return DSPARK_OK;
+  if (!aligned_or_null(teacher_ids, 4) || !aligned_or_null(teacher_logits, 4)) return DSPARK_ERR_INVALID_ARG;
+  if (N == 0) return DSPARK_OK;              // (pointers of empty arrays may be null)
+  if ((K == 0) != !teacher_ids || (K == 0) != !teacher_logits) return DSPARK_ERR_INVALID_ARG;
   if (!aligned(loss, 4) || !aligned(accept, 4)) return DSPARK_ERR_INVALID_ARG;
   return launch_distill(logits, dtype, ld, teacher_ids, teacher_logits, labels, weights, d_loss, N, V, K,
                         1.f / temperature, c_kl, c_tv, c_ce, loss, accept, grad ? d_logits : nullptr,
