@@ -798,7 +798,7 @@ cudaError_t launch_eg(EgParams p, void* ws, cudaStream_t stream) {
         e = launch_pdl(eg_scatter_kernel, dim3(plan.radix_tiles), dim3(kEmThreads), 0, stream, p, i);
     }
   }
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.N == 0) return e;   // (no position: the zeroes are the gradient)
   return vec ? launch_eg_sums<T, O, true>(p, buf, stream) : launch_eg_sums<T, O, false>(p, buf, stream);
 }
 
