@@ -506,8 +506,10 @@ dspark_status dspark_token_logprobs_grad(const void* logits, int dtype, int64_t 
  * with q_k = q at teacher_ids[n, k].  teacher_logits may be logits or log probabilities
  * (only differences count), -inf for an entry of probability 0.  Ids of a row are meant to be
  * distinct; equal ones count as the formulas say.  A row of weight 0 is not read: loss,
- * accept 0.  A row without entries has accept 0 and only the label's term; a label of -1 has
- * no term.  Ids and labels outside [-1, V) count as -1 and record DSPARK_ERR_DEVICE_CHECK.
+ * accept 0.  A row without entries, or with none above -inf, has accept 0 and only the label's
+ * term; a label of -1 has no term.  A NaN or +inf among the entries' teacher_logits makes accept
+ * NaN, and loss and gradient too unless c_kl = c_tv = 0.  Ids and labels outside [-1, V) count
+ * as -1 and record DSPARK_ERR_DEVICE_CHECK.
  *
  *   logits [N, V] (ld), teacher_ids [N, K] int32 and teacher_logits [N, K] fp32 (NULL iff
  *   K = 0), labels [N] int32 or NULL (none), weights [N] fp32 or NULL (all 1),

@@ -102,6 +102,7 @@ __device__ __forceinline__ void read_teacher(const DsParams& a, int n, const Row
     y = -1;
   }
   float tm = -INFINITY;
+  bool nan = false;                          // (the maximum passes over NaN)
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     if (id[i] < -1 || id[i] >= V) {
@@ -109,6 +110,7 @@ __device__ __forceinline__ void read_teacher(const DsParams& a, int n, const Row
       id[i] = -1;
     }
     if (id[i] < 0) t[i] = -INFINITY;
+    nan |= t[i] != t[i];
     tm = fmaxf(tm, t[i]);
   }
   const float zy = y >= 0 ? elem_to_float(row[y]) : 0.f;
@@ -116,7 +118,8 @@ __device__ __forceinline__ void read_teacher(const DsParams& a, int n, const Row
 #pragma unroll
   for (int i = 0; i < kPer; ++i) z[i] = id[i] >= 0 ? elem_to_float(row[id[i]]) : 0.f;
   tm = warp_max(tm);
-  const bool any = tm > -INFINITY;
+  // NaN or +inf among the entries: every p is NaN, and the row shows it
+  const bool any = tm > -INFINITY || __any_sync(0xffffffffu, nan);
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -207,7 +210,7 @@ struct RowEnd {
         const int k = lane + 32 * i;
         if (k < a.K && te.id[k] >= 0) {
           const float q = expf(log_q(te.z[k]));
-          if (q < te.p[k]) tv += q;
+          tv += q < te.p[k] ? q : 0.f * te.p[k];   // (a NaN stays one)
         }
       }
       sum_a += a.c_tv * warp_sum(tv);

@@ -1,11 +1,15 @@
 """The calls on rows of logits and of tables at the edges of what they take.  Tolerances as in
 test_gpu_rows."""
+import math
+
 import pytest
 
 pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 ds = pytest.importorskip("speculative_decoding_03_gb300")
+
+from test_gpu_rows import logits, teacher  # noqa: E402
 
 
 @pytest.fixture(autouse=True)
@@ -19,6 +23,10 @@ def ws():
     w = ds.Workspace.of_bytes(256)
     yield w
     assert w.status() == 0
+
+
+def ones(n):
+    return torch.ones(n, device="cuda")
 
 
 # ------------------------------------------------------------------------------ no rows
@@ -50,3 +58,59 @@ def test_embed_grad_of_no_positions(dtype, out_dtype, D, layout):
     ds.embed_grad(d_out, ids, V, w, out=buf[:, :D])
     assert (buf[:, :D] == 0).all() and (buf[:, D:] == 7).all()
     assert w.status() == 0
+
+
+# ----------------------------------------------------------------- teachers without a number
+
+TERMS = [dict(), dict(kl=0.0, tv=1.0), dict(kl=0.0, tv=0.5, ce=0.5), dict(kl=0.3, tv=0.3, ce=0.4)]
+
+
+@pytest.mark.parametrize("terms", TERMS, ids=["kl", "tv", "tv+ce", "all"])
+@pytest.mark.parametrize("V", [1000, 20008])           # a CTA a row; rows cut over a cluster
+@pytest.mark.parametrize("K", [1, 8, 40])
+@pytest.mark.parametrize("labelled", [False, True])
+def test_distill_shows_a_teacher_without_a_number(K, V, terms, labelled, ws):
+    """A NaN or +inf among the logits of a row's entries reaches its loss, acceptance and whole
+    gradient, whatever the other entries are; absent entries and rows of weight 0 are not read,
+    and other rows are untouched."""
+    n = 7
+    z = logits(n, V, torch.float32, 100)
+    ids, t = teacher(n, V, K, 101)
+    ids = torch.where(ids < 0, V - 1, ids)
+    if K > 1:
+        ids[4, 1] = -1
+    labels = torch.full((n,), 5 if labelled else -1, dtype=torch.int32, device="cuda")
+    w = ones(n)
+    w[5] = 0
+    clean = ds.distill_loss_grad(z, ids, t, ws, labels, w, **terms)
+    bad = t.clone()
+    bad[1] = math.nan                                  # every entry
+    bad[2] = -math.inf
+    bad[2, K - 1] = math.nan                           # beside entries of probability 0
+    bad[3, 0] = math.inf
+    if K > 1:
+        bad[4, 1] = math.nan                           # an absent entry
+    bad[5] = math.nan                                  # a row of weight 0
+    bad[6, K // 2] = math.nan                          # beside ordinary entries
+    got = ds.distill_loss_grad(z, ids, bad, ws, labels, w, **terms)
+    alone = ds.distill_loss(z, ids, bad, ws, labels, w, **terms)
+    for key in got:
+        for row in (0, 4, 5):
+            assert torch.equal(got[key][row], clean[key][row]), (key, row)
+        for row in (1, 2, 3, 6):
+            assert got[key][row].isnan().all(), (key, row)
+    for key in alone:
+        assert torch.equal(alone[key].isnan(), got[key].isnan())
+
+
+@pytest.mark.parametrize("V", [1000, 20008])
+def test_distill_of_labels_alone_beside_a_teacher_without_a_number(V, ws):
+    """With the label's term alone the teacher enters the acceptance only."""
+    z = logits(2, V, torch.float32, 102)
+    ids, t = teacher(2, V, 8, 103)
+    labels = torch.tensor([3, 4], dtype=torch.int32, device="cuda")
+    clean = ds.distill_loss_grad(z, ids, t, ws, labels, kl=0.0, ce=1.0)
+    t[1] = math.nan
+    got = ds.distill_loss_grad(z, ids, t, ws, labels, kl=0.0, ce=1.0)
+    assert torch.equal(got["loss"], clean["loss"]) and torch.equal(got["d_logits"], clean["d_logits"])
+    assert got["accept"][0] == clean["accept"][0] and got["accept"][1].isnan()
