@@ -94,7 +94,7 @@ __device__ __forceinline__ void read_teacher(const DsParams& a, int n, const Row
   for (int i = 0; i < kPer; ++i) {
     const int k = lane + 32 * i;
     id[i] = k < K ? a.ids[(size_t)n * K + k] : -1;
-    t[i] = k < K ? a.t[(size_t)n * K + k] * a.inv_tau : -INFINITY;
+    t[i] = k < K ? a.t[(size_t)n * K + k] : -INFINITY;
   }
   int y = a.labels ? a.labels[n] : -1;
   if (y < -1 || y >= V) {
@@ -124,7 +124,9 @@ __device__ __forceinline__ void read_teacher(const DsParams& a, int n, const Row
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     if (!any) id[i] = -1;                    // entries without weight are like any element
-    p[i] = id[i] >= 0 ? expf(t[i] - tm) : 0.f;
+    // over the temperature only now: t / tau itself may be beyond fp32, or lose the difference
+    t[i] = (t[i] - tm) * a.inv_tau;
+    p[i] = id[i] >= 0 ? expf(t[i]) : 0.f;
     sum += p[i];
   }
   sum = warp_sum(sum);
@@ -147,7 +149,7 @@ __device__ __forceinline__ void read_teacher(const DsParams& a, int n, const Row
     if (k < K) {
       te.id[k] = id[i];
       te.p[k] = p[i];
-      te.log_p[k] = t[i] - tm - log_sum;
+      te.log_p[k] = t[i] - log_sum;
       te.z[k] = z[i];
     }
     const bool mine = owned(id[i]);

@@ -9,7 +9,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 ds = pytest.importorskip("speculative_decoding_03_gb300")
 
-from test_gpu_rows import logits, teacher  # noqa: E402
+from test_gpu_rows import SUM, close, logits, ref_distill, teacher  # noqa: E402
 
 
 @pytest.fixture(autouse=True)
@@ -114,3 +114,36 @@ def test_distill_of_labels_alone_beside_a_teacher_without_a_number(V, ws):
     got = ds.distill_loss_grad(z, ids, t, ws, labels, kl=0.0, ce=1.0)
     assert torch.equal(got["loss"], clean["loss"]) and torch.equal(got["d_logits"], clean["d_logits"])
     assert got["accept"][0] == clean["accept"][0] and got["accept"][1].isnan()
+
+
+# ---------------------------------------------------------------------- small temperatures
+
+@pytest.mark.parametrize("V", [1000, 20008])
+@pytest.mark.parametrize("shift", [-5.0, 0.0, 5.0])
+def test_distill_at_a_temperature_near_zero(shift, V, ws):
+    """Only differences of the teacher's logits count: at 1e-38 both distributions are their
+    largest logit, whatever the logits' sign, although a logit over the temperature is
+    beyond fp32."""
+    n, K = 4, 8
+    z = logits(n, V, torch.float32, 104)
+    ids = z.topk(K, 1).indices.to(torch.int32)
+    t = -0.5 * torch.arange(K, device="cuda").repeat(n, 1) + shift
+    got = ds.distill_loss_grad(z, ids, t, ws, temperature=1e-38, kl=1.0, tv=1.0)
+    assert (got["accept"] == 1).all() and (got["loss"] == 0).all() and (got["d_logits"] == 0).all()
+
+
+@pytest.mark.parametrize("V", [1000, 20008])
+def test_distill_takes_logits_far_from_zero(V, ws):
+    """t / temperature rounded before the maximum is subtracted would be off by |t / temperature|
+    2^-24 = 2.6e-4 here, ten times the tolerance."""
+    n, K = 5, 33
+    z = logits(n, V, torch.float32, 105)
+    ids, t = teacher(n, V, K, 106)
+    t += 3000.0
+    labels = torch.full((n,), 7, dtype=torch.int32, device="cuda")
+    kw = dict(temperature=0.7, kl=0.5, tv=0.3, ce=0.2)
+    got = ds.distill_loss_grad(z, ids, t, ws, labels, ones(n), **kw)
+    ref = ref_distill(z, ids, t, labels, ones(n), ones(n), 0.7, 0.5, 0.3, 0.2)
+    close(got["loss"], ref["loss"], rtol=2 * SUM, atol=6 * SUM)
+    close(got["accept"], ref["accept"], rtol=2 * SUM, atol=2 * SUM)
+    close(got["d_logits"], ref["d_logits"], rtol=2 * SUM, atol=2 * SUM / 0.7)
