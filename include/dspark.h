@@ -513,7 +513,8 @@ dspark_status dspark_token_logprobs_grad(const void* logits, int dtype, int64_t 
  *
  *   logits [N, V] (ld), teacher_ids [N, K] int32 and teacher_logits [N, K] fp32 (NULL iff
  *   K = 0), labels [N] int32 or NULL (none), weights [N] fp32 or NULL (all 1),
- *   temperature > 0, coefficients >= 0, all finite  ->  loss [N] fp32, accept [N] fp32
+ *   temperature > 0 (and log2(e) / temperature within fp32: from 4.3e-39 on), coefficients >= 0,
+ *   all finite  ->  loss [N] fp32, accept [N] fp32
  *
  * dspark_distill_loss_grad also writes the gradient of sum_n d_loss[n] loss[n] (d_loss NULL:
  * all 1) with respect to the logits, reading them once:

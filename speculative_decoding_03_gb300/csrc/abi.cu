@@ -2,6 +2,7 @@
 // and the launch sequence of each call.  See include/dspark.h for the contract.
 #include <stdint.h>
 
+#include "common.cuh"
 #include "internal.h"
 
 using namespace dspark;
@@ -50,7 +51,8 @@ dspark_status distill(const void* logits, int dtype, int64_t ld, const int32_t* 
   if (K > kMaxTop) return DSPARK_ERR_UNSUPPORTED;
   // in place is the same rows; other overlaps are the caller's to avoid
   if (grad && d_logits == logits && ld_d != ld && N > 1) return DSPARK_ERR_INVALID_ARG;
-  if (!(temperature > 0.f) || !finite(temperature) || !finite(1.f / temperature) || !(c_kl >= 0.f) ||
+  // (the kernels' factor of a difference of logits: infinite times 0 would be NaN)
+  if (!(temperature > 0.f) || !finite(temperature) || !finite(1.f / temperature * kLog2e) || !(c_kl >= 0.f) ||
       !(c_tv >= 0.f) || !(c_ce >= 0.f) || !finite(c_kl) || !finite(c_tv) || !finite(c_ce))
     return DSPARK_ERR_INVALID_ARG;
   if (!aligned(workspace, 256) || workspace_bytes < 256) return DSPARK_ERR_INVALID_ARG;

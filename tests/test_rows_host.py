@@ -7,6 +7,8 @@ import sys
 
 import pytest
 
+from test_rows_abi import INVALID, distill
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CUDA_ERROR = 3
 
@@ -24,3 +26,12 @@ def test_token_logprobs_grad_of_rows_shorter_than_a_chunk(V, dtype):
     """A row of fewer elements than 16 bytes hold has no chunk to cut into segments."""
     status = status_of(f"logprobs_grad(V={V}, ld={V}, ld_d={V}, dtype={dtype})")
     assert status != -signal.SIGFPE and status == CUDA_ERROR
+
+
+@pytest.mark.parametrize("grad", [False, True])
+def test_distill_refuses_a_temperature_whose_scale_overflows(grad):
+    """The kernels form log2(e) / temperature, which passes fp32's largest number below 4.24e-39."""
+    for tau in (3e-39, 4.2e-39):
+        assert distill(grad, tau=tau) == INVALID
+    assert status_of(f"distill({grad}, tau=4.3e-39)") == CUDA_ERROR      # taken
+    assert status_of(f"distill({grad}, tau=3.4e38)") == CUDA_ERROR
