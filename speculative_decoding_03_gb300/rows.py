@@ -102,7 +102,9 @@ def token_logprobs(logits, tokens, top: int, ws: Workspace, out: Optional[Dict] 
     (then no ``logprob`` and no ``rank``).  Returns (or fills ``out``) a dict of tensors of
     the rows' shape: ``logprob``, ``entropy``, ``rank`` (1 for the largest logit),
     ``row_max``, ``row_sumexp``, and with ``top`` > 0 ``top_ids`` and ``top_logprobs``
-    [..., top], largest first."""
+    [..., top], largest first.  ``out`` says what is written: it holds ``logprob`` and ``rank``
+    just where tokens are given, ``top_ids`` and ``top_logprobs`` where ``top`` > 0 (with 0 they
+    stay as they are), and may lack the others."""
     torch, _ = _types()
     code, n, V, ld = _rows(logits, "logits")
     _device(logits, ws)
@@ -171,9 +173,10 @@ def _distill(grad: bool, logits, teacher_ids, teacher_logits, ws, labels, weight
     lead, d = tuple(logits.shape[:-1]), logits.device
     if out is None:
         out = {}
-        with allocate:
-            out["loss"] = torch.empty(lead, dtype=f32, device=d)
-            out["accept"] = torch.empty(lead, dtype=f32, device=d)
+    for key in ("loss", "accept"):
+        if out.get(key) is None:
+            with allocate:
+                out[key] = torch.empty(lead, dtype=f32, device=d)
     v = lambda t, name, dtype=f32, k=None: _vector(t, name, n, dtype, logits, k)  # noqa: E731
     args = [logits.data_ptr(), code, ld, v(teacher_ids, "teacher_ids", i32, K),
             v(teacher_logits, "teacher_logits", f32, K), v(labels, "labels", i32), v(weights, "weights")]
@@ -197,7 +200,8 @@ def distill_loss(logits, teacher_ids, teacher_logits, ws: Workspace, labels=None
     none), ``weights`` [...] fp32 (0: the row is not read).  Per row, with p and q the
     teacher's and the student's softmax at ``temperature``: ``loss`` = weight (kl KL(p || q) +
     tv TV(p, q) - ce log q[label]) and ``accept`` = sum min(p, q), the probability that a
-    token drafted from q is accepted.  Returns (or fills ``out``) a dict of both."""
+    token drafted from q is accepted.  Returns a dict of both, ``out`` if it is given: entries
+    that it holds are written, those that it lacks are made."""
     return _distill(False, logits, teacher_ids, teacher_logits, ws, labels, weights, None, temperature, kl,
                     tv, ce, out, stream)
 
@@ -206,8 +210,8 @@ def distill_loss_grad(logits, teacher_ids, teacher_logits, ws: Workspace, labels
                       d_loss=None, temperature: float = 1.0, kl: float = 1.0, tv: float = 0.0,
                       ce: float = 0.0, out: Optional[Dict] = None, stream=None) -> Dict:
     """``distill_loss`` and, from the same read of the logits, ``d_logits``: the gradient of
-    sum(d_loss * loss) (``d_loss`` [...] fp32, None: all 1).  ``out["d_logits"]`` may be the
-    logits themselves."""
+    sum(d_loss * loss) (``d_loss`` [...] fp32, None: all 1).  ``out={"d_logits": logits}`` writes
+    it over the logits."""
     return _distill(True, logits, teacher_ids, teacher_logits, ws, labels, weights, d_loss, temperature, kl,
                     tv, ce, out, stream)
 

@@ -147,3 +147,19 @@ def test_distill_takes_logits_far_from_zero(V, ws):
     close(got["loss"], ref["loss"], rtol=2 * SUM, atol=6 * SUM)
     close(got["accept"], ref["accept"], rtol=2 * SUM, atol=2 * SUM)
     close(got["d_logits"], ref["d_logits"], rtol=2 * SUM, atol=2 * SUM / 0.7)
+
+
+# -------------------------------------------------------------------- partly given outputs
+
+def test_distill_makes_the_outputs_that_are_not_given(ws):
+    n, V, K = 3, 1000, 8
+    z = logits(n, V, torch.float32, 107)
+    ids, t = teacher(n, V, K, 108)
+    want = ds.distill_loss_grad(z, ids, t, ws)
+    got = ds.distill_loss_grad(z, ids, t, ws, out={"d_logits": z})
+    assert got["d_logits"] is z and set(got) == {"loss", "accept", "d_logits"}
+    assert all(torch.equal(got[k], want[k]) for k in want)
+    loss = torch.empty(n, device="cuda")
+    z = logits(n, V, torch.float32, 107)
+    got = ds.distill_loss(z, ids, t, ws, out={"loss": loss})
+    assert got["loss"] is loss and torch.equal(loss, want["loss"]) and torch.equal(got["accept"], want["accept"])
