@@ -467,7 +467,8 @@ typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1, DSPARK_F16 = 2 } dspark_dtype;
  * rank, row_sumexp 0, row_max and top_logprobs -inf, top_ids -1; any other token outside
  * [0, V) does the same and records DSPARK_ERR_DEVICE_CHECK.  A row with no logit above -inf has
  * logprob and top_logprobs -inf, entropy 0; a row with NaN or +inf has NaN for all of them,
- * rank 0 and top_ids -1.  K > V leaves -1 and -inf in the places beyond V.
+ * rank 0 and top_ids -1.  K > V leaves -1 and -inf in the places beyond V.  K > 0 needs
+ * V <= 2^26 (DSPARK_ERR_UNSUPPORTED beyond).
  *
  *   logits [N, V] (ld), tokens [N] int32, or NULL: every row is used, logprob and rank are
  *   not written and must be NULL; entropy, row_max, row_sumexp may be NULL; top_ids and

@@ -472,7 +472,7 @@ dspark_status dspark_token_logprobs(const void* logits, int dtype, int64_t ld, c
   dspark_status st = check_rows(logits, dtype, ld, N, V);
   if (st != DSPARK_OK) return st;
   if (K < 0) return DSPARK_ERR_INVALID_ARG;
-  if (K > kMaxTop) return DSPARK_ERR_UNSUPPORTED;
+  if (K > kMaxTop || (K > 0 && V > kMaxTopLength)) return DSPARK_ERR_UNSUPPORTED;
   if (!aligned(workspace, 256) || workspace_bytes < 256) return DSPARK_ERR_INVALID_ARG;
   if (!aligned_or_null(entropy, 4) || !aligned_or_null(row_max, 4) || !aligned_or_null(row_sumexp, 4) ||
       !aligned_or_null(tokens, 4) || !aligned_or_null(logprob, 4) || !aligned_or_null(rank, 4) ||

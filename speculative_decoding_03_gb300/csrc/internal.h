@@ -322,6 +322,7 @@ cudaError_t launch_copy_target_rows(const float* T_src, float* T, const int32_t*
 
 // ---- rows of logits and of tables in fp32, bf16 or fp16 (dspark_dtype) ----
 constexpr int kMaxTop = 128;             // alternatives of a row, entries of a teacher's row
+constexpr int kMaxTopLength = 1 << 26;   // logits of a row with alternatives
 // see logprobs.cu; leading dimensions in elements
 cudaError_t launch_token_logprobs(const void* z, int dtype, long long ld, const int32_t* tokens,
                                   int N, int V, int K, float* logprob, float* entropy, int32_t* rank,

@@ -17,9 +17,11 @@
 // of threads is a lower bound of the row's K-th largest logit that only slightly more than K
 // elements reach (-G log(1 - K / G) of them for random data: 89 at K = 64, G = 128).  The few
 // 64-byte slots whose maximum reaches it are read again, and one CTA of the cluster (in turn)
-// ranks, by counting, the elements that the others send to it.  The rank is counted in the
-// stream: a sampled token may have hundreds of elements before it, and reading those again
-// cost more than the stream (224 against 189 us at the size below).
+// ranks, by counting, the elements that the others send to it.  (Few logits above -inf, or many in
+// ascending order, leave more candidates than fit, and sweep() below takes the row up tile by
+// tile: 1536 x 129280 in fp32 with 10 logits left take 3.9 ms, with 100 0.82, ascending 57.)  The
+// rank is counted in the stream: a sampled token may have hundreds of elements before it, and
+// reading those again cost more than the stream (224 against 189 us at the size below).
 //
 // Measured on a GB300 (copy rate 6782 GB/s): 1536 rows of 129280 in fp32, 64 alternatives,
 // 152 us = 5.2 TB/s (0.77 of the copy rate; 10.1 rounds of 152 clusters take 11, and a CTA
@@ -45,6 +47,7 @@ constexpr int kLpSlots = 12;                // maxima of a consumer thread kept 
 constexpr int kLpCap = 768;                 // candidate keys of a CTA
 constexpr int kLpList = 512;                // slots listed to be read again
 constexpr int kLpTop = kMaxTop;             // most alternatives
+constexpr int kLpSwept = kMaxTopLength / 8; // elements of a CTA's part where there are any
 constexpr int kLpMaxima = 256;              // most groups
 constexpr int kLpShortSlots = 16;
 // a short row: up to 64 KB (2000 rows of 16000 in fp32: 56 us, 80 by the ring)
@@ -283,7 +286,9 @@ __device__ __forceinline__ int select_top(Shared& sh, int x, int n, int K) {
 
 // The same where more elements reach the bound than keys fit (equal logits, or all the large
 // ones in few threads' hands): the selection goes tile by tile over the elements [from, to) and
-// keeps the K best in sh.best, `got` of them so far.
+// keeps the K best in sh.best, `got` of them so far.  A tile whose every element is better than
+// all before takes up to 112000 cycles (K = 128, both CTAs of an SM at it), and the row two rows
+// on waits for it: 2^23 elements a CTA take 1.5e9 cycles, a wait ends after 4e9.
 template <typename Shared, typename T>
 __device__ __noinline__ void sweep(Shared& sh, int x, const T* row, int from, int to, int K, int& got) {
   constexpr int kTile = (kLpCap - kLpTop) / kLpClose * kLpClose;
@@ -1004,6 +1009,7 @@ cudaError_t launch_lp(LpParams p, cudaStream_t stream) {
   long long best = 0;
   for (int i = 3; i >= 0; --i) {
     if (i > 0 && (chunks >> i) < kLpPieceChunks) continue;
+    if (i < 3 && p.K > 0 && (p.V >> i) > kLpSwept) break;
     const int most = device_clusters(cache[i], token_logprobs_kernel<T>, 1 << i, kLpBlock, smem);
     if (most <= 0) return cudaErrorInvalidConfiguration;
     const long long stream_c = (long long)(chunks >> i) * 16 / 12, close_c = 14000;

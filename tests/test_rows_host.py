@@ -7,7 +7,7 @@ import sys
 
 import pytest
 
-from test_rows_abi import INVALID, distill
+from test_rows_abi import INVALID, UNSUPPORTED, distill, logprobs
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CUDA_ERROR = 3
@@ -35,3 +35,12 @@ def test_distill_refuses_a_temperature_whose_scale_overflows(grad):
         assert distill(grad, tau=tau) == INVALID
     assert status_of(f"distill({grad}, tau=4.3e-39)") == CUDA_ERROR      # taken
     assert status_of(f"distill({grad}, tau=3.4e38)") == CUDA_ERROR
+
+
+def test_token_logprobs_bounds_the_rows_that_have_alternatives():
+    """Logits in ascending order are taken up tile by tile: beyond 2^26 of them that could outlast
+    the kernel's waits.  Without alternatives rows may be longer."""
+    assert logprobs(V=(1 << 26) + 1, ld=1 << 27) == UNSUPPORTED
+    assert logprobs(V=1 << 30, ld=1 << 30, K=1) == UNSUPPORTED
+    assert status_of("logprobs(V=1 << 26, ld=1 << 26)") == CUDA_ERROR    # taken
+    assert status_of("logprobs(V=1 << 30, ld=1 << 30, K=0, ids=None, top=None)") == CUDA_ERROR
