@@ -2,7 +2,8 @@
 
 The target's rows give the teacher's top logits (``token_logprobs``); the student's logits are
 the backbone's base logits plus the head's bias (``markov_bias``); ``distill_loss_grad`` gives
-the loss, the expected acceptance and the gradient in place of the logits; the head's two
+the loss, the acceptance expected of a target cut to those top logits (here 32 of 1024, which
+hold about 0.6 of its probability) and the gradient in place of the logits; the head's two
 matrices get theirs from two plain products and ``embed_grad``.  The loss is the DSpark pages'
 (weigao.cc DSpark-vs-MTP page, "loss": total variation 0.9, cross entropy 0.1, weights that
 fall over the block's positions).  Synthetic data: the target differs from the base logits by

@@ -503,8 +503,11 @@ dspark_status dspark_token_logprobs_grad(const void* logits, int dtype, int64_t 
  * entries (teacher_ids >= 0; other entries are absent),
  *   loss[n]   = w_n (c_kl sum_k p_k (log p_k - log q_k) + c_tv sum_k max(0, p_k - q_k)
  *                    + c_ce (-log q_label))
- *   accept[n] = sum_k min(p_k, q_k)      (the confidence head's label)
- * with q_k = q at teacher_ids[n, k].  teacher_logits may be logits or log probabilities
+ *   accept[n] = sum_k min(p_k, q_k)
+ * with q_k = q at teacher_ids[n, k].  p sums to 1 over the entries, so accept is the probability
+ * that a token drafted from q is accepted by a target cut to them; by the whole target it differs
+ * from that by at most the probability that the entries leave out, to either side (the confidence
+ * head's label, when that is small).  teacher_logits may be logits or log probabilities
  * (only differences count), -inf for an entry of probability 0.  Ids of a row are meant to be
  * distinct; equal ones count as the formulas say.  A row of weight 0 is not read: loss,
  * accept 0.  A row without entries, or with none above -inf, has accept 0 and only the label's

@@ -7,7 +7,8 @@
 // K logits t / tau, q the softmax of the student's row z / tau, and label y,
 //   loss = w (c_kl sum_k p_k (log p_k - log q_k) + c_tv sum_k max(0, p_k - q_k)
 //             + c_ce (-log q_y)),        accept = sum_k min(p_k, q_k).
-// (p sums to 1 over the K entries, so sum max(0, p - q) is the total variation distance.)
+// (p sums to 1 over the K entries, so sum max(0, p - q) is the total variation distance, and
+// accept is the acceptance by a target cut to them.)
 // Every term's gradient is A q_v - a_v with a_k = c_kl p_k + c_tv q_k [q_k < p_k] (and c_ce
 // at the label), A = sum of all a:
 //   dz_v = g w / tau (A q_v - sum_{k : id_k = v} a_k).

@@ -200,7 +200,9 @@ def distill_loss(logits, teacher_ids, teacher_logits, ws: Workspace, labels=None
     none), ``weights`` [...] fp32 (0: the row is not read).  Per row, with p and q the
     teacher's and the student's softmax at ``temperature``: ``loss`` = weight (kl KL(p || q) +
     tv TV(p, q) - ce log q[label]) and ``accept`` = sum min(p, q), the probability that a
-    token drafted from q is accepted.  Returns a dict of both, ``out`` if it is given: entries
+    token drafted from q is accepted by a target cut to the entries (p sums to 1 over them).  By
+    the whole target it differs from that by at most the probability that the entries leave out:
+    1 - exp(teacher_logits).sum(-1) for ``token_logprobs``'s at temperature 1.  Returns a dict of both, ``out`` if it is given: entries
     that it holds are written, those that it lacks are made."""
     return _distill(False, logits, teacher_ids, teacher_logits, ws, labels, weights, None, temperature, kl,
                     tv, ce, out, stream)

@@ -163,3 +163,20 @@ def test_distill_makes_the_outputs_that_are_not_given(ws):
     z = logits(n, V, torch.float32, 107)
     got = ds.distill_loss(z, ids, t, ws, out={"loss": loss})
     assert got["loss"] is loss and torch.equal(loss, want["loss"]) and torch.equal(got["accept"], want["accept"])
+
+
+# --------------------------------------------------------------------- what accept stands for
+
+@pytest.mark.parametrize("K", [4, 32, 128])
+@pytest.mark.parametrize("V,spread", [(1000, 3.0), (20008, 1.0)])
+def test_accept_is_off_by_no_more_than_the_mass_left_out(K, V, spread, ws):
+    """With a teacher's top log probabilities: accept against sum min(p, q) over the vocabulary."""
+    n = 16
+    T = logits(n, V, torch.float32, 109) * spread / 3
+    z = logits(n, V, torch.float32, 110) * spread / 3 + T
+    top = ds.token_logprobs(T, None, K, ws)
+    got = ds.distill_loss(z, top["top_ids"], top["top_logprobs"], ws)["accept"].double()
+    p, q = torch.softmax(T.double(), 1), torch.softmax(z.double(), 1)
+    left = 1 - top["top_logprobs"].double().exp().sum(1)
+    off = (got - torch.minimum(p, q).sum(1)).abs()
+    assert (off <= left + 4 * SUM).all() and (left > 0).any()
