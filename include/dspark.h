@@ -447,7 +447,7 @@ dspark_status dspark_copy_target_rows(const float* T_src, float* T, const int32_
  * start on a 16-byte border) and aligned to their element.  Sums, softmax statistics and
  * gradients are formed in fp32 and rounded once, to nearest even, where they are stored in
  * 16 bits (fp16 results beyond its range become infinite).  The exponential of a logit x below its
- * row's maximum (over the temperature) is good to (2 + x) 2^-23 of itself.  A row number of 0 is accepted and
+ * row's maximum (over the temperature) is good to about (2 + 3 x) 2^-23 of itself.  A row number of 0 is accepted and
  * launches nothing (dspark_embed_grad: zeroes the table's gradient).  N < 2^21,
  * 1 <= V <= 2^30, K <= 128.  The workspace is any of this library's (256 bytes suffice: the
  * status word), except where a call names its own size.  Results do not depend on the order
