@@ -566,6 +566,132 @@ dspark_status dspark_embed_grad(const void* d_out, int dtype, int64_t ld, const 
                                 int64_t ld_w, void* workspace, size_t workspace_bytes,
                                 cudaStream_t stream);
 
+/*
+ * The target's side of a step.  Between the schedule and the verification the target runs over
+ * the scheduled tokens (billytse.dev DSpark page, section 1: one parallel pass of the target
+ * scores the drafted block); the calls below are the parts of that pass that depend on the
+ * step: the tokens' keys and values go into a paged cache, the tokens attend to what is cached,
+ * and after a verification the accepted ones' keys and values stay.  dspark_tree_verify verifies
+ * against given probabilities (a target's after temperature, top-p or penalties) from given
+ * uniform numbers, where dspark_verify takes the softmax of logits and draws its own.
+ *
+ * Rows.  Request b's n_b tokens are consecutive rows: with starts [B + 1] int32, rows
+ * starts[b] .. starts[b + 1] - 1 (packed; counts NULL), else rows b N .. b N + counts[b] - 1
+ * (padded; counts [B] int32, or NULL: all N).  N is the most tokens of a request, `rows` the rows
+ * of every per-row array (padded: B N); rows of no token are neither read nor written.  Token 0 is the last
+ * committed one.  parents [rows] int32 makes the tokens a tree: a token's parent by its place in
+ * the request, before the token's own; -1 for token 0 (and for others whose only ancestor is the
+ * committed text).  parents NULL: a chain.  A tree has N <= 64, and so has every call but
+ * dspark_cache_append.
+ *
+ * Cache.  A slot s of request b is line s mod page_size of page pages[b, s / page_size]
+ * (pages [B, max_pages] int32); lengths [B] int32 are the slots used before the step, and token
+ * i of the step has slot lengths[b] + i.  The k and v of a layer are [pages, page_size, heads,
+ * head_dim] with the strides given (in elements, multiples of 8; head_dim's is 1) and 16-byte
+ * aligned.  page_size is a power of two from 16 to 256.  Pages of a table that hold no slot in
+ * use are not looked at.
+ *
+ * Counts outside [0, N], rows outside the batch, lengths that the table has no room for, pages
+ * outside the cache and parents that are not before their token record
+ * DSPARK_ERR_DEVICE_CHECK: the request, slot or parent counts as none.  B < 65536, B = 0 launches
+ * nothing.  The workspace is any of this library's (256 bytes suffice) unless a call names its
+ * own size.
+ */
+typedef struct {
+  void *k, *v;                /* DSPARK_BF16 or DSPARK_F16 */
+  int dtype, layers, pages, page_size, heads, head_dim;
+  int64_t layer_stride, page_stride, slot_stride, head_stride;   /* the same for k and v */
+} dspark_paged_cache;
+
+/*
+ * Appends k and v [rows, heads, head_dim] of the step's tokens to layer `layer` of the cache, and
+ * writes q_out from q [rows, q_heads, head_dim] (q NULL: none).  Each head of q (and k) is
+ * normalised where q_weight (k_weight) [head_dim] fp32 is given and rotated where inv_freq
+ * [rotated / 2] fp32 is:
+ *   x = x / sqrt(mean(x^2) + eps) * weight
+ *   (x_a, x_b) = (x_a cos - x_b sin, x_b cos + x_a sin),  angle position * inv_freq[j]
+ * of pairs j: elements j and j + rotated / 2, or 2 j and 2 j + 1 (interleaved); elements from
+ * `rotated` on stay.  position = lengths[b] + the token's depth in its tree (a chain: its place).
+ * Angles are formed in 64 bits, the rest in fp32, with one rounding where a value is stored.
+ * q_out may be q itself (same strides); arrays overlap in no other way.
+ *
+ *   strides of rows and heads in elements, multiples of 8; pointers 16-byte aligned; inv_freq and
+ *   weights 16-byte aligned; head_dim a multiple of 16 up to 256; rotated a multiple of 16 up to
+ *   head_dim; eps >= 0.
+ */
+dspark_status dspark_cache_append(const dspark_paged_cache* cache, int layer, const int32_t* starts,
+                                  const int32_t* counts, const int32_t* parents, int B, int N, int rows,
+                                  const int32_t* pages, int max_pages, const int32_t* lengths,
+                                  const void* k, int64_t k_row, int64_t k_head, const void* v,
+                                  int64_t v_row, int64_t v_head, const void* q, int64_t q_row,
+                                  int64_t q_head, int q_heads, void* q_out, int64_t q_out_row,
+                                  int64_t q_out_head, const float* inv_freq, int rotated,
+                                  int interleaved, const float* q_weight, const float* k_weight,
+                                  float eps, void* workspace, size_t workspace_bytes,
+                                  cudaStream_t stream);
+
+/*
+ * Attention of the step's tokens over the cache, to which they have been appended:
+ *   out[i, h] = sum_s p_s v[s, h / G],  p = softmax over s of scale q[i, h] . k[s, h / G]
+ * with G = q_heads / heads, s over the slots below lengths[b], token i's own and its
+ * ancestors'.  lse [rows, q_heads] fp32 (NULL: not written) is the logarithm of the sum of
+ * exp(scale q k).  Scores, softmax and sums are in fp32; the probabilities are rounded to the
+ * cache's type for their product with the values.  Keys and values that a token does not see
+ * never reach it, whatever they hold.  A token all of whose scores are -inf gets zeroes and an lse
+ * of -inf.
+ *
+ *   q, out [rows, q_heads, head_dim] of the cache's type (strides as above), q_heads a multiple of
+ *   heads; head_dim 64 or 128; scale > 0; workspace of
+ *   dspark_tree_attention_workspace_bytes (0 on bad shapes).
+ */
+size_t dspark_tree_attention_workspace_bytes(int B, int N, int q_heads, int heads, int head_dim);
+dspark_status dspark_tree_attention(const dspark_paged_cache* cache, int layer, const int32_t* starts,
+                                    const int32_t* counts, const int32_t* parents, int B, int N,
+                                    int rows, const int32_t* pages, int max_pages,
+                                    const int32_t* lengths, const void* q, int64_t q_row,
+                                    int64_t q_head, int q_heads, float scale, void* out,
+                                    int64_t out_row, int64_t out_head, float* lse, void* workspace,
+                                    size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Verification of a step's tokens, lossless for children drawn independently from q, or (q NULL)
+ * for children that the draft names without chance.  p [rows, V] is the target's distribution
+ * after each token, q [rows, V] the one from which a token's children were drawn (fp32, bf16 or
+ * fp16, entries >= 0, p's sums about 1), uniforms [rows] fp32 in [0, 1).  From token 0 on, with
+ * r = p of the current token and s = 1, its children are tried in order of their place:
+ *   child i with token x is accepted iff uniforms[i] q(x) s < r(x)     (q(x) = 1 without q)
+ *   rejected: r = max(r - s q, 0), s = sum of r;  without q: s = s - r(x), r(x) = 0
+ * An accepted child becomes the current token.  When none is left, the last token is drawn from r:
+ * the smallest v whose sum up to it exceeds uniforms[token 0] times the sum of all (r all zero:
+ * the same of p).  Tests, and the draw's sums, are in 64 bits or their like (2^-45 of the sum);
+ * r - s q is rounded once to 32 bits, and so is s after a child drawn from q.
+ *
+ *   accept_len [B]; path [B, N]: the accepted tokens' places; out_tokens [B, N]: their ids, then
+ *   the last token; n_out [B] = accept_len + 1; -1 behind them.  A request without tokens has
+ *   n_out 0.  tokens [rows] int32 (token 0's is not looked at); one outside [0, V) is never
+ *   accepted, and a row with nothing to draw from gives -1: both record
+ *   DSPARK_ERR_DEVICE_CHECK.  p's and q's leading dimensions are in elements (any alignment).
+ */
+dspark_status dspark_tree_verify(const void* p, int64_t ld_p, const void* q, int64_t ld_q, int dtype,
+                                 int V, const int32_t* tokens, const float* uniforms,
+                                 const int32_t* starts, const int32_t* counts, const int32_t* parents,
+                                 int B, int N, int rows, int32_t* accept_len, int32_t* path,
+                                 int32_t* out_tokens, int32_t* n_out, void* workspace,
+                                 size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Moves the accepted tokens' keys and values together, in every layer of the cache: slot
+ * lengths[b] + path[b, j] to slot lengths[b] + 1 + j for j < accept_len[b] (path [B, N] and
+ * accept_len [B] as dspark_tree_verify wrote them; path[b, j] > j).  Token 0's slot stays, so
+ * lengths[b] + 1 + accept_len[b] slots are then used.  Other slots keep what they hold.  Pages
+ * belong to one request each.  An accept_len outside [0, N - 1] moves nothing of its request
+ * and a path entry outside (j, N) not its token; both record DSPARK_ERR_DEVICE_CHECK.
+ */
+dspark_status dspark_cache_keep(const dspark_paged_cache* cache, int B, int N, const int32_t* pages,
+                                int max_pages, const int32_t* lengths, const int32_t* path,
+                                const int32_t* accept_len, void* workspace, size_t workspace_bytes,
+                                cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

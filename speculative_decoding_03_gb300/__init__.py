@@ -5,8 +5,9 @@ speculative step -- ``dspark_draft``, ``dspark_confidence``, ``dspark_schedule``
 ``dspark_verify`` -- plus ``dspark_draft_confidence_schedule`` (the first three in one
 launch), ``dspark_markov_bias``, the packed-W2 variants of the draft and the verification,
 greedy drafting with its verification, the asynchronous two-step capacity scheduler,
-fixed-threshold truncation and the RNN head, and what trains the draft head and reports on
-its tokens (the ``rows`` module); every step of the computation runs in its
+fixed-threshold truncation and the RNN head, what trains the draft head and reports on
+its tokens (the ``rows`` module), and the parts of the target's forward that depend on the step
+(the ``target`` module); every step of the computation runs in its
 CUDA kernels.  This module only marshals arguments: it passes device pointers of
 torch tensors and the current CUDA stream through ctypes, and allocates outputs and the
 workspace with torch.  There is no CPU fallback: without the built library and a CUDA
@@ -71,6 +72,14 @@ SIGNATURES = [
     ("dspark_embed", _I, [_P, _I, _I64, _P, _I, _I, _I, _F, _P, _I, _I64, _P, _SZ, _P]),
     ("dspark_embed_grad_workspace_bytes", _SZ, [_I, _I, _I]),
     ("dspark_embed_grad", _I, [_P, _I, _I64, _P, _I, _I, _I, _F, _I, _P, _I, _I64, _P, _SZ, _P]),
+    ("dspark_cache_append", _I, [_P, _I, _P, _P, _P, _I, _I, _I, _P, _I, _P, _P, _I64, _I64, _P, _I64, _I64,
+                                 _P, _I64, _I64, _I, _P, _I64, _I64, _P, _I, _I, _P, _P, _F, _P, _SZ, _P]),
+    ("dspark_tree_attention_workspace_bytes", _SZ, [_I, _I, _I, _I, _I]),
+    ("dspark_tree_attention", _I, [_P, _I, _P, _P, _P, _I, _I, _I, _P, _I, _P, _P, _I64, _I64, _I, _F, _P,
+                                   _I64, _I64, _P, _P, _SZ, _P]),
+    ("dspark_tree_verify", _I, [_P, _I64, _P, _I64, _I, _I, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P,
+                                _P, _SZ, _P]),
+    ("dspark_cache_keep", _I, [_P, _I, _I, _P, _I, _P, _P, _P, _P, _SZ, _P]),
 ]
 
 _lib = None
@@ -804,3 +813,5 @@ def rnn_to_device(W_rnn, b_rnn, dev: Dict, device="cuda") -> Dict:
 
 from .rows import (distill_loss, distill_loss_grad, embed, embed_grad,  # noqa: E402
                    embed_grad_workspace_bytes, token_logprobs, token_logprobs_grad)
+from .target import (PagedCache, cache_append, cache_keep, tree_attention,  # noqa: E402
+                     tree_attention_workspace_bytes, tree_verify)

@@ -39,6 +39,65 @@ dspark_status check_rows(const void* p, int dtype, int64_t ld, int N, int len) {
 }
 bool aligned_or_null(const void* p, uintptr_t a) { return !p || aligned(p, a); }
 
+// ---- the target's side of a step ----
+bool stride8(int64_t s) { return s >= 0 && s % 8 == 0 && s <= (1LL << 40); }
+
+dspark_status check_cache(const dspark_paged_cache* c, CacheStrides* cs, TargetSlots* slots) {
+  if (!c || (c->dtype != DSPARK_BF16 && c->dtype != DSPARK_F16) || c->layers < 1 || c->pages < 1 ||
+      c->heads < 1 || c->head_dim < 1 || c->page_size < 1)
+    return DSPARK_ERR_INVALID_ARG;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !stride8(c->layer_stride) || !stride8(c->page_stride) ||
+      !stride8(c->slot_stride) || !stride8(c->head_stride))
+    return DSPARK_ERR_INVALID_ARG;
+  if (c->head_dim % 16 != 0 || c->head_dim > 256 || c->heads > 1024 || c->layers > 1024) return DSPARK_ERR_UNSUPPORTED;
+  // lines that overlap (strides of 0 among them) have no place of their own
+  if ((c->heads > 1 && c->head_stride < c->head_dim) || (c->page_size > 1 && c->slot_stride < c->head_dim) ||
+      (c->pages > 1 && c->page_stride < c->head_dim) || (c->layers > 1 && c->layer_stride < c->head_dim))
+    return DSPARK_ERR_INVALID_ARG;
+  int shift = 4;
+  while (shift < 8 && (1 << shift) < c->page_size) ++shift;
+  if (1 << shift != c->page_size || c->pages > (1 << 30)) return DSPARK_ERR_UNSUPPORTED;
+  cs->page = c->page_stride;
+  cs->slot = c->slot_stride;
+  cs->head = c->head_stride;
+  cs->layer = c->layer_stride;
+  cs->heads = c->heads;
+  cs->head_dim = c->head_dim;
+  cs->layers = c->layers;
+  slots->n_pages = c->pages;
+  slots->page_shift = shift;
+  return DSPARK_OK;
+}
+
+// the requests' rows; `most`: the largest N
+dspark_status check_target_rows(const int32_t* starts, const int32_t* counts, const int32_t* parents, int B, int N,
+                                int rows, int most, TargetRows* out) {
+  if (B < 0 || N < 1 || rows < 0 || (starts && counts)) return DSPARK_ERR_INVALID_ARG;
+  if (B >= 65536 || N > (parents ? kMaxTree : most) || rows >= (1 << 30)) return DSPARK_ERR_UNSUPPORTED;
+  if (!starts && (long long)B * N > rows) return DSPARK_ERR_INVALID_ARG;
+  if (!aligned_or_null(starts, 4) || !aligned_or_null(counts, 4) || !aligned_or_null(parents, 4))
+    return DSPARK_ERR_INVALID_ARG;
+  *out = {starts, counts, parents, B, N, rows};
+  return DSPARK_OK;
+}
+
+dspark_status check_slots(const int32_t* pages, int max_pages, const int32_t* lengths, int B, TargetSlots* slots) {
+  if (max_pages < 1 || (B > 0 && (!aligned(pages, 4) || !aligned(lengths, 4)))) return DSPARK_ERR_INVALID_ARG;
+  if ((long long)max_pages << slots->page_shift > (1LL << 30)) return DSPARK_ERR_UNSUPPORTED;
+  slots->pages = pages;
+  slots->lengths = lengths;
+  slots->max_pages = max_pages;
+  return DSPARK_OK;
+}
+
+dspark_status check_heads(const void* p, int64_t row, int64_t head, int n_rows) {
+  return (n_rows == 0 || aligned(p, 16)) && stride8(row) && stride8(head) ? DSPARK_OK : DSPARK_ERR_INVALID_ARG;
+}
+
+void* layer_of(void* p, const dspark_paged_cache* c, int layer) {
+  return static_cast<uint16_t*>(p) + layer * c->layer_stride;
+}
+
 dspark_status distill(const void* logits, int dtype, int64_t ld, const int32_t* teacher_ids,
                       const float* teacher_logits, const int32_t* labels, const float* weights,
                       const float* d_loss, int N, int V, int K, float temperature, float c_kl,
@@ -567,6 +626,130 @@ dspark_status dspark_embed_grad(const void* d_out, int dtype, int64_t ld, const 
   return launch_embed_grad(d_out, dtype, ld, ids, N, V, D, scale, accumulate != 0, dW, w_dtype, ld_w,
                            ws_at<int>(workspace, 0), workspace, stream) == cudaSuccess
              ? DSPARK_OK : DSPARK_ERR_CUDA;
+}
+
+dspark_status dspark_cache_append(const dspark_paged_cache* cache, int layer, const int32_t* starts,
+                                  const int32_t* counts, const int32_t* parents, int B, int N, int rows,
+                                  const int32_t* pages, int max_pages, const int32_t* lengths,
+                                  const void* k, int64_t k_row, int64_t k_head, const void* v,
+                                  int64_t v_row, int64_t v_head, const void* q, int64_t q_row,
+                                  int64_t q_head, int q_heads, void* q_out, int64_t q_out_row,
+                                  int64_t q_out_head, const float* inv_freq, int rotated,
+                                  int interleaved, const float* q_weight, const float* k_weight,
+                                  float eps, void* workspace, size_t workspace_bytes,
+                                  cudaStream_t stream) {
+  CacheStrides cs;
+  TargetSlots slots;
+  TargetRows tr;
+  dspark_status st = check_cache(cache, &cs, &slots);
+  if (st == DSPARK_OK) st = check_target_rows(starts, counts, parents, B, N, rows, 1 << 30, &tr);
+  if (st == DSPARK_OK) st = check_slots(pages, max_pages, lengths, B, &slots);
+  if (st == DSPARK_OK) st = check_heads(k, k_row, k_head, rows);
+  if (st == DSPARK_OK) st = check_heads(v, v_row, v_head, rows);
+  if (st != DSPARK_OK) return st;
+  if (layer < 0 || layer >= cache->layers || !q != !q_out) return DSPARK_ERR_INVALID_ARG;
+  if (q) {
+    st = check_heads(q, q_row, q_head, rows);
+    if (st == DSPARK_OK) st = check_heads(q_out, q_out_row, q_out_head, rows);
+    if (st != DSPARK_OK) return st;
+    if (q_heads < 1 || (q_out == q && (q_out_row != q_row || q_out_head != q_head))) return DSPARK_ERR_INVALID_ARG;
+    if ((q_heads > 1 && q_out_head < cs.head_dim) || (rows > 1 && q_out_row < cs.head_dim)) return DSPARK_ERR_INVALID_ARG;
+    if (q_heads > 65536) return DSPARK_ERR_UNSUPPORTED;
+  } else {
+    q_heads = 0;
+    if (q_weight) return DSPARK_ERR_INVALID_ARG;
+  }
+  if (inv_freq) {
+    if (!aligned(inv_freq, 16) || rotated < 2 || rotated > cs.head_dim) return DSPARK_ERR_INVALID_ARG;
+    if (rotated % 16 != 0) return DSPARK_ERR_UNSUPPORTED;
+  }
+  if (!aligned_or_null(q_weight, 16) || !aligned_or_null(k_weight, 16) || !finite(eps) || eps < 0.f)
+    return DSPARK_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256) || workspace_bytes < 256) return DSPARK_ERR_INVALID_ARG;
+  if (B == 0 || rows == 0) return DSPARK_OK;
+  return launch_cache_append({q, q_row, q_head}, {k, k_row, k_head}, {v, v_row, v_head}, q_heads, q_out, q_out_row,
+                             q_out_head, layer_of(cache->k, cache, layer), layer_of(cache->v, cache, layer), cs,
+                             cache->dtype, tr, slots, {inv_freq, rotated, interleaved != 0}, {q_weight, k_weight, eps},
+                             ws_at<int>(workspace, 0), stream) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+}
+
+size_t dspark_tree_attention_workspace_bytes(int B, int N, int q_heads, int heads, int head_dim) {
+  if (B < 0 || B >= 65536 || N < 1 || N > kMaxTree || heads < 1 || heads > 1024 || q_heads < heads ||
+      q_heads % heads != 0 || (head_dim != 64 && head_dim != 128))
+    return 0;
+  return tree_attention_bytes(B, N, q_heads, heads, head_dim);
+}
+
+dspark_status dspark_tree_attention(const dspark_paged_cache* cache, int layer, const int32_t* starts,
+                                    const int32_t* counts, const int32_t* parents, int B, int N,
+                                    int rows, const int32_t* pages, int max_pages,
+                                    const int32_t* lengths, const void* q, int64_t q_row,
+                                    int64_t q_head, int q_heads, float scale, void* out,
+                                    int64_t out_row, int64_t out_head, float* lse, void* workspace,
+                                    size_t workspace_bytes, cudaStream_t stream) {
+  CacheStrides cs;
+  TargetSlots slots;
+  TargetRows tr;
+  dspark_status st = check_cache(cache, &cs, &slots);
+  if (st == DSPARK_OK) st = check_target_rows(starts, counts, parents, B, N, rows, kMaxTree, &tr);
+  if (st == DSPARK_OK) st = check_slots(pages, max_pages, lengths, B, &slots);
+  if (st == DSPARK_OK) st = check_heads(q, q_row, q_head, rows);
+  if (st == DSPARK_OK) st = check_heads(out, out_row, out_head, rows);
+  if (st != DSPARK_OK) return st;
+  if (layer < 0 || layer >= cache->layers || q_heads < 1 || q_heads % cs.heads != 0 || !(scale > 0.f) || !finite(scale))
+    return DSPARK_ERR_INVALID_ARG;
+  if ((q_heads > 1 && out_head < cs.head_dim) || (rows > 1 && out_row < cs.head_dim)) return DSPARK_ERR_INVALID_ARG;
+  if (!aligned_or_null(lse, 4)) return DSPARK_ERR_INVALID_ARG;
+  if (cs.head_dim != 64 && cs.head_dim != 128) return DSPARK_ERR_UNSUPPORTED;
+  // a request's (row block, head, tile) units are counted in 32 bits
+  const long long blocks = cdiv((long long)N * (q_heads / cs.heads), 128);
+  if (q_heads > 65536 || (((long long)max_pages << slots.page_shift) / 128 + 1) * blocks * cs.heads >= (1LL << 31))
+    return DSPARK_ERR_UNSUPPORTED;
+  if (!aligned(workspace, 256) || workspace_bytes < tree_attention_bytes(B, N, q_heads, cs.heads, cs.head_dim))
+    return DSPARK_ERR_INVALID_ARG;
+  if (B == 0 || rows == 0) return DSPARK_OK;
+  return launch_tree_attention({q, q_row, q_head}, q_heads, layer_of(cache->k, cache, layer),
+                               layer_of(cache->v, cache, layer), cs, cache->dtype, tr, slots, scale, out, out_row,
+                               out_head, lse, ws_at<int>(workspace, 0), workspace, stream) == cudaSuccess
+             ? DSPARK_OK : DSPARK_ERR_CUDA;
+}
+
+dspark_status dspark_tree_verify(const void* p, int64_t ld_p, const void* q, int64_t ld_q, int dtype,
+                                 int V, const int32_t* tokens, const float* uniforms,
+                                 const int32_t* starts, const int32_t* counts, const int32_t* parents,
+                                 int B, int N, int rows, int32_t* accept_len, int32_t* path,
+                                 int32_t* out_tokens, int32_t* n_out, void* workspace,
+                                 size_t workspace_bytes, cudaStream_t stream) {
+  TargetRows tr;
+  dspark_status st = check_target_rows(starts, counts, parents, B, N, rows, kMaxTree, &tr);
+  if (st == DSPARK_OK) st = check_rows(p, dtype, ld_p, rows, V);
+  if (st == DSPARK_OK && q) st = check_rows(q, dtype, ld_q, rows, V);
+  if (st != DSPARK_OK) return st;
+  if (!aligned(workspace, 256) || workspace_bytes < 256) return DSPARK_ERR_INVALID_ARG;
+  if (B == 0) return DSPARK_OK;
+  if ((rows > 0 && (!aligned(tokens, 4) || !aligned(uniforms, 4))) || !aligned(accept_len, 4) || !aligned(path, 4) ||
+      !aligned(out_tokens, 4) || !aligned(n_out, 4))
+    return DSPARK_ERR_INVALID_ARG;
+  return launch_tree_verify(p, q, dtype, ld_p, ld_q, V, tokens, uniforms, tr, accept_len, path, out_tokens, n_out,
+                            ws_at<int>(workspace, 0), stream) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+}
+
+dspark_status dspark_cache_keep(const dspark_paged_cache* cache, int B, int N, const int32_t* pages,
+                                int max_pages, const int32_t* lengths, const int32_t* path,
+                                const int32_t* accept_len, void* workspace, size_t workspace_bytes,
+                                cudaStream_t stream) {
+  CacheStrides cs;
+  TargetSlots slots;
+  dspark_status st = check_cache(cache, &cs, &slots);
+  if (st == DSPARK_OK) st = check_slots(pages, max_pages, lengths, B, &slots);
+  if (st != DSPARK_OK) return st;
+  if (B < 0 || N < 1) return DSPARK_ERR_INVALID_ARG;
+  if (B >= 65536 || N > kMaxTree) return DSPARK_ERR_UNSUPPORTED;
+  if (!aligned(workspace, 256) || workspace_bytes < 256) return DSPARK_ERR_INVALID_ARG;
+  if (B == 0) return DSPARK_OK;
+  if (!aligned(path, 4) || !aligned(accept_len, 4)) return DSPARK_ERR_INVALID_ARG;
+  return launch_cache_keep(cache->k, cache->v, cs, slots, B, N, path, accept_len, ws_at<int>(workspace, 0), stream) ==
+                 cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -347,6 +347,59 @@ cudaError_t launch_embed_grad(const void* d_out, int dtype, long long ld, const 
                               int D, float scale, int accumulate, void* dW, int w_dtype, long long ld_w,
                               int* err, void* ws, cudaStream_t stream);
 
+// ---- the target's side of a step: cached keys and values, drafted trees ----
+constexpr int kMaxTree = 64;             // tokens of a request that form a tree
+// the requests' rows: packed (starts [B + 1]) or padded to N (counts [B], null: all N)
+struct TargetRows {
+  const int32_t* starts;
+  const int32_t* counts;
+  const int32_t* parents;                // [rows], null: chains
+  int B, N, rows;
+};
+// where their tokens are cached: slot s of request b is line s % page of pages[b][s / page]
+struct TargetSlots {
+  const int32_t* pages;
+  const int32_t* lengths;
+  int max_pages, n_pages, page_shift;
+};
+// one layer's keys or values: strides in elements
+struct CacheStrides {
+  long long page, slot, head, layer;
+  int heads, head_dim, layers;
+};
+// rows of heads: strides in elements
+struct HeadRows {
+  const void* p;
+  long long row, head;
+};
+struct Rotation {
+  const float* inv_freq;                 // [rotated / 2], null: none
+  int rotated, interleaved;
+};
+struct HeadNorm {
+  const float *q_weight, *k_weight;      // null: not normalised
+  float eps;
+};
+// see cache.cu
+cudaError_t launch_cache_append(const HeadRows& q, const HeadRows& k, const HeadRows& v, int q_heads, void* q_out,
+                                long long q_out_row, long long q_out_head, void* k_cache, void* v_cache,
+                                const CacheStrides& cs, int dtype, const TargetRows& rows, const TargetSlots& slots,
+                                const Rotation& rot, const HeadNorm& norm, int* err, cudaStream_t stream);
+cudaError_t launch_cache_keep(void* k_cache, void* v_cache, const CacheStrides& cs, const TargetSlots& slots, int B,
+                              int N, const int32_t* path, const int32_t* accept_len, int* err,
+                              cudaStream_t stream);
+// see tree_attention.cu
+size_t tree_attention_bytes(int B, int N, int q_heads, int heads, int head_dim);
+cudaError_t launch_tree_attention(const HeadRows& q, int q_heads, const void* k_cache, const void* v_cache,
+                                  const CacheStrides& cs, int dtype, const TargetRows& rows,
+                                  const TargetSlots& slots, float scale, void* out, long long out_row,
+                                  long long out_head, float* lse, int* err, void* ws, cudaStream_t stream);
+// see tree_verify.cu
+cudaError_t launch_tree_verify(const void* p, const void* q, int dtype, long long ld_p, long long ld_q, int V,
+                               const int32_t* tokens, const float* uniforms, const TargetRows& rows,
+                               int32_t* accept_len, int32_t* path, int32_t* out_tokens, int32_t* n_out, int* err,
+                               cudaStream_t stream);
+
 // E_all (null for the Markov head): the RNN head's output rows [B][gamma][r] of the draft
 cudaError_t launch_verify(const Plan& p, const float* T, const float* U, const uint16_t* W1,
                           const uint16_t* W2, const uint16_t* W2p, const float* E_all,

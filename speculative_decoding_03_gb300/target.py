@@ -1,0 +1,247 @@
+"""The target's side of a step: what of its forward depends on the step itself.
+
+Between a schedule and a verification the target runs over the scheduled tokens.  Their keys and
+values go into a paged cache (``cache_append``, which also normalises and rotates queries and
+keys), the tokens, a chain or a tree, attend to it (``tree_attention``), ``tree_verify`` verifies
+them against the target's probabilities from given uniform numbers, and ``cache_keep`` moves the
+accepted ones' keys and values together.
+
+Rows of tokens are padded, [B, N, ...] with ``counts`` [B] int32 (None: all N), as the step's own
+calls have them, or packed, [rows, ...] with ``starts`` [B + 1] int32 (request b's are rows
+starts[b] .. starts[b + 1] - 1) and ``nodes``, the most tokens of a request.  ``parents`` [B, N]
+or [rows] int32 names each token's parent by its place in the request (-1 for the first); None: a
+chain.  A tree has at most 64 tokens.  ``pages`` [B, max_pages] and ``lengths`` [B] int32 say where
+a request's tokens are cached and how many were before the step.  ``stream`` is the stream the
+kernels run on (default: the current one); outputs that a call allocates belong to it, and the
+caller orders it after what produced the inputs.  A call raises ValueError for tensors of the
+wrong type, shape, layout or device, and DSparkError for what the library refuses; nothing is
+launched in either case.  What only the device sees (counts, lengths, pages, parents out of range)
+is reported by ``ws.status()``.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Dict, Optional
+
+from . import DSparkError, Workspace, lib
+from .rows import _device, _done, _on, _rows, _types, _vector
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int), ("layers", ctypes.c_int),
+                ("pages", ctypes.c_int), ("page_size", ctypes.c_int), ("heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("layer_stride", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("slot_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class PagedCache:
+    """Keys and values in pages: ``k`` and ``v`` [pages, page_size, heads, head_dim], or with a
+    leading dimension of layers, bf16 or fp16, of equal strides (any whose last is 1 and whose
+    others are multiples of 8).  The handle holds on to both tensors and writes into them."""
+
+    def __init__(self, k, v):
+        torch, codes = _types()
+        if k.dtype is not torch.bfloat16 and k.dtype is not torch.float16:
+            raise ValueError(f"k: dtype {k.dtype} is not bfloat16 or float16")
+        if k.dim() not in (4, 5) or not k.is_cuda or k.numel() == 0:
+            raise ValueError(f"k: a CUDA tensor [(layers,) pages, page_size, heads, head_dim] is needed, not "
+                             f"{tuple(k.shape)} on {k.device}")
+        if v.dtype is not k.dtype or v.shape != k.shape or v.stride() != k.stride() or v.device != k.device:
+            raise ValueError("k and v have one type, shape, device and strides")
+        shape, stride = tuple(k.shape), k.stride()
+        if stride[-1] != 1:
+            raise ValueError(f"k: its last dimension is not contiguous (strides {tuple(stride)})")
+        if len(shape) == 4:
+            shape, stride = (1,) + shape, (0,) + tuple(stride)
+        # (a dimension of one has no stride of its own)
+        stride = [0 if size == 1 else step for size, step in zip(shape, stride)]
+        self.k, self.v = k, v
+        self.layers, self.n_pages, self.page_size, self.heads, self.head_dim = shape
+        self.dtype, self.device = k.dtype, k.device
+        self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), codes[k.dtype], *shape, *stride[:4])
+        self._ptr = ctypes.addressof(self._struct)
+
+
+def _tokens(lead, starts, counts, nodes, like):
+    """(B or None, N, rows, starts, counts) of rows with the leading dimensions ``lead``."""
+    torch, _ = _types()
+    if starts is None:
+        if len(lead) != 2:
+            raise ValueError(f"rows [B, N, ...] are needed where starts is not given, not {tuple(lead)}")
+        B, N = lead
+        return B, N, B * N, None, _vector(counts, "counts", B, torch.int32, like)
+    if len(lead) != 1 or counts is not None or nodes is None:
+        raise ValueError("packed rows have one leading dimension, starts and nodes, and no counts")
+    if starts.numel() < 1:
+        raise ValueError("starts: [B + 1] entries are needed")
+    B = starts.numel() - 1
+    return B, nodes, lead[0], _vector(starts, "starts", B + 1, torch.int32, like), None
+
+
+def _slots(pages, lengths, B, like):
+    torch, _ = _types()
+    if pages.dim() != 2:
+        raise ValueError(f"pages: a table [B, max_pages] is needed, not {tuple(pages.shape)}")
+    most = pages.shape[1]
+    return (_vector(pages, "pages", B, torch.int32, like, most), most,
+            _vector(lengths, "lengths", B, torch.int32, like))
+
+
+def _heads(t, name, lead, dim, cache):
+    """(pointer, row stride, head stride, heads) of rows of heads."""
+    if t.dtype is not cache.dtype or t.device != cache.device:
+        raise ValueError(f"{name}: {cache.dtype} on {cache.device} is needed, not {t.dtype} on {t.device}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != len(lead) + 2 or shape[:-2] != lead or shape[-1] != dim:
+        raise ValueError(f"{name}: {tuple(lead)} rows of heads of {dim} are needed, not {tuple(shape)}")
+    if stride[-1] != 1:
+        raise ValueError(f"{name}: its last dimension is not contiguous (strides {tuple(stride)})")
+    if len(lead) == 1:
+        row = stride[0]
+    else:
+        row = stride[1]
+        if lead[0] > 1:
+            if lead[1] == 1:
+                row = stride[0]
+            elif stride[0] != lead[1] * row:
+                raise ValueError(f"{name}: its leading dimensions do not flatten into rows of one stride "
+                                 f"(shape {tuple(shape)}, strides {tuple(stride)})")
+    heads = shape[-2]
+    n = lead[0] if len(lead) == 1 else lead[0] * lead[1]
+    return t.data_ptr(), row if n > 1 else 0, stride[-2] if heads > 1 else 0, heads
+
+
+def cache_append(cache: PagedCache, k, v, pages, lengths, ws: Workspace, q=None, q_out=None, starts=None,
+                 counts=None, nodes: Optional[int] = None, parents=None, inv_freq=None, interleaved: bool = False,
+                 q_weight=None, k_weight=None, eps: float = 1e-6, layer: int = 0, stream=None):
+    """Appends ``k`` and ``v`` [..., heads, head_dim] of the step's tokens to the cache, and
+    returns ``q`` [..., q_heads, head_dim] normalised and rotated like the keys (in ``q_out``,
+    which may be ``q``; None without ``q``).
+
+    Token i of request b has slot lengths[b] + i.  ``q_weight`` and ``k_weight`` [head_dim] fp32:
+    each head is divided by its root mean square (``eps`` added to the mean) and multiplied by the
+    weight.  ``inv_freq`` [R / 2] fp32: the first R elements of each head are rotated by position
+    times frequency, in pairs (j, j + R / 2), or (2 j, 2 j + 1) with ``interleaved``; the position is
+    lengths[b] plus the token's depth in its tree.  A chain may be of any length (a prompt)."""
+    torch, _ = _types()
+    f32 = torch.float32
+    _device(k, ws)
+    handle, allocate = _on(stream, k)
+    D = cache.head_dim
+    lead = k.shape[:-2]
+    B, N, rows, s, c = _tokens(lead, starts, counts, nodes, k)
+    k_p, k_row, k_head, heads = _heads(k, "k", lead, D, cache)
+    v_p, v_row, v_head, v_heads = _heads(v, "v", lead, D, cache)
+    if heads != cache.heads or v_heads != heads:
+        raise ValueError(f"k and v: {cache.heads} heads are needed, not {heads} and {v_heads}")
+    q_p = q_row = q_head = q_heads = o_p = o_row = o_head = 0
+    if q is not None:
+        q_p, q_row, q_head, q_heads = _heads(q, "q", lead, D, cache)
+        if q_out is None:
+            with allocate:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        o_p, o_row, o_head, o_heads = _heads(q_out, "q_out", lead, D, cache)
+        if o_heads != q_heads:
+            raise ValueError(f"q_out: {q_heads} heads are needed, not {o_heads}")
+    elif q_out is not None:
+        raise ValueError("q_out is given without q")
+    rotated = 0 if inv_freq is None else 2 * inv_freq.numel()
+    table, most, used = _slots(pages, lengths, B, k)
+    _done("dspark_cache_append", lib().dspark_cache_append(
+        cache._ptr, layer, s, c, _vector(parents, "parents", rows, torch.int32, k), B, N, rows, table, most, used,
+        k_p, k_row, k_head, v_p, v_row, v_head, q_p or None, q_row, q_head, q_heads, o_p or None, o_row, o_head,
+        _vector(inv_freq, "inv_freq", rotated // 2, f32, k), rotated, interleaved,
+        _vector(q_weight, "q_weight", D, f32, k), _vector(k_weight, "k_weight", D, f32, k), eps,
+        ws.ptr, ws.nbytes, handle))
+    return q_out
+
+
+def tree_attention_workspace_bytes(B: int, nodes: int, q_heads: int, heads: int, head_dim: int) -> int:
+    """Bytes of the workspace that ``tree_attention`` needs for B requests of up to ``nodes`` tokens."""
+    nbytes = lib().dspark_tree_attention_workspace_bytes(B, nodes, q_heads, heads, head_dim)
+    if nbytes == 0:
+        raise ValueError(f"unsupported shapes B={B} nodes={nodes} q_heads={q_heads} heads={heads} head_dim={head_dim}")
+    return int(nbytes)
+
+
+def tree_attention(q, cache: PagedCache, pages, lengths, ws: Workspace, starts=None, counts=None,
+                   nodes: Optional[int] = None, parents=None, scale: Optional[float] = None, out=None, lse=None,
+                   layer: int = 0, stream=None):
+    """Attention of the step's tokens ``q`` [..., q_heads, head_dim] over the cache, to which their
+    keys and values have been appended: each sees the slots before the step, its ancestors and
+    itself.  ``scale`` (default head_dim ** -0.5) multiplies the scores.  Returns ``out`` like
+    ``q``; ``lse`` [..., q_heads] fp32, if given, gets the logarithms of the softmax's sums.
+    head_dim is 64 or 128, and a request has at most 64 tokens."""
+    torch, _ = _types()
+    _device(q, ws)
+    handle, allocate = _on(stream, q)
+    lead, D = q.shape[:-2], cache.head_dim
+    B, N, rows, s, c = _tokens(lead, starts, counts, nodes, q)
+    q_p, q_row, q_head, q_heads = _heads(q, "q", lead, D, cache)
+    if out is None:
+        with allocate:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    o_p, o_row, o_head, o_heads = _heads(out, "out", lead, D, cache)
+    if o_heads != q_heads:
+        raise ValueError(f"out: {q_heads} heads are needed, not {o_heads}")
+    table, most, used = _slots(pages, lengths, B, q)
+    _done("dspark_tree_attention", lib().dspark_tree_attention(
+        cache._ptr, layer, s, c, _vector(parents, "parents", rows, torch.int32, q), B, N, rows, table, most, used,
+        q_p, q_row, q_head, q_heads, D ** -0.5 if scale is None else scale, o_p, o_row, o_head,
+        _vector(lse, "lse", rows, torch.float32, q, q_heads), ws.ptr, ws.nbytes, handle))
+    return out
+
+
+def tree_verify(p, tokens, uniforms, ws: Workspace, q=None, starts=None, counts=None, nodes: Optional[int] = None,
+                parents=None, out: Optional[Dict] = None, stream=None) -> Dict:
+    """Verification of the step's tokens against the target's probabilities ``p`` [..., V] (fp32, bf16
+    or fp16; p's row of a token is the distribution after it).
+
+    ``tokens`` [...] int32 (a request's first is its last committed token), ``uniforms`` [...] fp32 in
+    [0, 1): the first token's is the last draw's, the others' decide their token.  ``q`` [..., V]: the
+    distribution from which a token's children were drawn, each independently; None: children
+    that the draft names without chance (greedy drafts, its most probable tokens).  Returns (or
+    fills ``out``) a dict of int32 tensors: ``accept_len`` [B], ``path`` [B, N] the accepted tokens'
+    places, ``out_tokens`` [B, N] their ids and the last token, ``n_out`` [B]; -1 behind them."""
+    torch, _ = _types()
+    i32 = torch.int32
+    code, n, V, ld = _rows(p, "p")
+    _device(p, ws)
+    handle, allocate = _on(stream, p)
+    B, N, rows, s, c = _tokens(p.shape[:-1], starts, counts, nodes, p)
+    ld_q, q_p = ld, None
+    if q is not None:
+        code_q, n_q, V_q, ld_q = _rows(q, "q")
+        if (code_q, n_q, V_q) != (code, n, V) or q.device != p.device:
+            raise ValueError(f"q: {n} x {V} {p.dtype} on {p.device} are needed, not {tuple(q.shape)} {q.dtype}")
+        q_p = q.data_ptr()
+    if out is None:
+        with allocate:
+            out = {"accept_len": torch.empty(B, dtype=i32, device=p.device),
+                   "path": torch.empty((B, N), dtype=i32, device=p.device),
+                   "out_tokens": torch.empty((B, N), dtype=i32, device=p.device),
+                   "n_out": torch.empty(B, dtype=i32, device=p.device)}
+    _done("dspark_tree_verify", lib().dspark_tree_verify(
+        p.data_ptr(), ld, q_p, ld_q, code, V, _vector(tokens, "tokens", rows, i32, p),
+        _vector(uniforms, "uniforms", rows, torch.float32, p), s, c, _vector(parents, "parents", rows, i32, p), B, N,
+        rows, _vector(out["accept_len"], "accept_len", B, i32, p), _vector(out["path"], "path", B, i32, p, N),
+        _vector(out["out_tokens"], "out_tokens", B, i32, p, N), _vector(out["n_out"], "n_out", B, i32, p),
+        ws.ptr, ws.nbytes, handle))
+    return out
+
+
+def cache_keep(cache: PagedCache, pages, lengths, path, accept_len, ws: Workspace, stream=None) -> None:
+    """Moves the accepted tokens' keys and values together in every layer: token path[b, j] of
+    request b to slot lengths[b] + 1 + j, for j < accept_len[b] (``path`` [B, N], ``accept_len`` [B] as
+    ``tree_verify`` returns them).  After it lengths[b] + 1 + accept_len[b] slots are used; the
+    caller updates ``lengths``."""
+    torch, _ = _types()
+    if path.dim() != 2:
+        raise ValueError(f"path: [B, N] is needed, not {tuple(path.shape)}")
+    _device(cache.k, ws)
+    handle, _ = _on(stream, cache.k)
+    B, N = path.shape
+    table, most, used = _slots(pages, lengths, B, cache.k)
+    _done("dspark_cache_keep", lib().dspark_cache_keep(
+        cache._ptr, B, N, table, most, used, _vector(path, "path", B, torch.int32, cache.k, N),
+        _vector(accept_len, "accept_len", B, torch.int32, cache.k), ws.ptr, ws.nbytes, handle))
