@@ -12,7 +12,7 @@
 namespace dspark {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 
 struct VerifyParams {
@@ -26,30 +26,70 @@ struct VerifyParams {
   int* err;
 };
 
-// A sum of non-negative fp32 numbers kept as hi + lo: Knuth's two-sum gives each addition's
-// rounding exactly, so that sums over a row are good to 2^-45 of themselves.  (Sums in 64 bits
-// would run at a sixty-fourth of the rate.)
+// Numbers kept as hi + lo, hi the nearest fp32 to both: Knuth's two-sum gives an addition's
+// rounding exactly and a fused multiply-add a product's, so that sums over a row are good to
+// 2^-45 of themselves.  (64-bit arithmetic runs at a sixty-fourth of the rate here, and an
+// addition takes some hundred cycles: walk, scans and draw in it took 12 of 20 us.)
 struct Sum2 {
   float hi, lo;
-  __device__ __forceinline__ void add(float x) {
+  __device__ __forceinline__ void add(float x) {       // hi + lo not renormalised
     const float s = hi + x, t = s - hi;
     lo += (hi - (s - t)) + (x - t);
     hi = s;
   }
-  __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
+  __device__ __forceinline__ Sum2 normal() const {     // |hi| >= |lo|
+    const float s = hi + lo;
+    return {s, lo - (s - hi)};
+  }
+  __device__ __forceinline__ bool beyond(const Sum2& o) const { return hi > o.hi || (hi == o.hi && lo > o.lo); }
 };
+__device__ __forceinline__ Sum2 operator+(const Sum2& a, const Sum2& b) {
+  Sum2 r = a;
+  r.add(b.hi);
+  r.lo += b.lo;
+  return r.normal();
+}
+__device__ __forceinline__ Sum2 operator*(const Sum2& a, const Sum2& b) {
+  const float p = a.hi * b.hi;
+  const Sum2 r = {p, fmaf(a.hi, b.hi, -p) + (a.hi * b.lo + a.lo * b.hi)};
+  return r.normal();
+}
+__device__ __forceinline__ Sum2 shfl_up(const Sum2& a, int m) {
+  return {__shfl_up_sync(0xffffffffu, a.hi, m), __shfl_up_sync(0xffffffffu, a.lo, m)};
+}
+__device__ __forceinline__ Sum2 warp_sum(Sum2 x) {
+#pragma unroll
+  for (int m = 16; m >= 1; m >>= 1)
+    x = x + Sum2{__shfl_xor_sync(0xffffffffu, x.hi, m), __shfl_xor_sync(0xffffffffu, x.lo, m)};
+  return x;
+}
+// inclusive sums over the lanes
+__device__ __forceinline__ Sum2 warp_scan(Sum2 x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int m = 1; m < 32; m *= 2) {
+    const Sum2 y = shfl_up(x, m);
+    if (lane >= m) x = y + x;
+  }
+  return x;
+}
 
 // What is left of the row p after `rejected` children: r = p, then r = max(r - s q, 0) for
 // each child drawn from q (s the sum before it, 1 at first), or r = 0 at their tokens.
 struct Left {
   int rounds;                // of q
-  const float* s;
+  const float* s;            // before round j > 0
   int points;                // rejected point masses
   const int* token;
-  __device__ __forceinline__ float of(float p, float q) const {
-    float r = p;
-    for (int j = 0; j < rounds; ++j) r = fmaxf(__fmaf_rn(-s[j], q, r), 0.f);
-    return r;
+  template <int N>
+  __device__ __forceinline__ void of(float (&r)[N], const float (&q)[N]) const {
+#pragma unroll
+    for (int e = 0; e < N; ++e) r[e] = fmaxf(r[e] - q[e], 0.f);       // s is 1 before the first
+    for (int j = 1; j < rounds; ++j) {
+      const float minus = -s[j];
+#pragma unroll
+      for (int e = 0; e < N; ++e) r[e] = fmaxf(__fmaf_rn(minus, q[e], r[e]), 0.f);
+    }
   }
   __device__ __forceinline__ bool struck(int v) const {
     bool hit = false;
@@ -58,324 +98,435 @@ struct Left {
   }
 };
 
-// The part of a row that one warp of the request's cluster sums: 16-byte chunks c0 .. c1 - 1 of
-// the row p, and the elements before the first chunk (the first warp) or behind the last.
+// A node's rows: whole 16-byte chunks of p, and the elements before the first and behind the
+// last.  q's chunks are loaded whole where they start where p's do.
 template <typename T>
-struct Part {
-  const T *p, *q;            // q null: none
+struct NodeRow {
+  static constexpr int N = Chunk<T>::N;
+  const T *p, *q;            // q null: not needed
   RowChunks rc;
-  bool q_fits;               // q's chunks start where p's do
-  int c0, c1;
+  bool q_fits;
   int V;
-  // the elements of chunk c (rc.head + c N ..): p into x, q into y
-  __device__ __forceinline__ void load(int c, uint4& x, uint4& y, float (&yf)[Chunk<T>::N]) const {
-    constexpr int N = Chunk<T>::N;
-    x = *(reinterpret_cast<const uint4*>(p + rc.head) + c);
-    if (!q) return;
-    if (q_fits) {
-      y = *(reinterpret_cast<const uint4*>(q + rc.head) + c);
-    } else {
+  __device__ __forceinline__ NodeRow(const T* p_, const T* q_, int V_) : p(p_), q(q_), V(V_) {
+    rc = row_chunks(p, V);
+    q_fits = q && ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15u) == 0;
+  }
+  // chunk c as loaded; mode 0: p alone, 1: and q's chunk, 2: and q's elements
+  struct Raw {
+    uint4 x, y;
+  };
+  template <int M>
+  __device__ __forceinline__ Raw load(int c) const {
+    Raw w;
+    w.x = __ldcs(reinterpret_cast<const uint4*>(p + rc.head) + c);
+    if constexpr (M == 1) w.y = __ldcs(reinterpret_cast<const uint4*>(q + rc.head) + c);
+    if constexpr (M == 2) {
+      T one[N];
 #pragma unroll
-      for (int e = 0; e < N; ++e) yf[e] = elem_to_float(q[rc.head + (long long)c * N + e]);
+      for (int e = 0; e < N; ++e) one[e] = q[rc.head + (long long)c * N + e];
+      w.y = *reinterpret_cast<const uint4*>(one);
     }
+    return w;
+  }
+  // what is left of a loaded chunk; `near`: a struck token may lie in it
+  template <int M>
+  __device__ __forceinline__ void left_of(const Raw& w, const Left& left, bool near, int c, float (&r)[N]) const {
+    unpack_chunk<T>(w.x, r);
+    if constexpr (M > 0) {
+      float g[N];
+      unpack_chunk<T>(w.y, g);
+      left.of(r, g);
+    }
+    if (M == 0 && near) {
+      const int v0 = rc.head + c * N;
+      for (int j = 0; j < left.points; ++j) {
+        const int at = left.token[j] - v0;
+#pragma unroll
+        for (int e = 0; e < N; ++e) r[e] = at == e ? 0.f : r[e];
+      }
+    }
+  }
+  __device__ __forceinline__ Raw load_any(int c) const { return !q ? load<0>(c) : q_fits ? load<1>(c) : load<2>(c); }
+  __device__ __forceinline__ void left_of_any(const Raw& w, const Left& left, int c, float (&r)[N]) const {
+    if (q) left_of<1>(w, left, false, c, r);
+    else left_of<0>(w, left, true, c, r);
+  }
+  __device__ __forceinline__ float element(const Left& left, int v) const {
+    if (left.struck(v)) return 0.f;
+    float r[1] = {elem_to_float(p[v])};
+    if (left.rounds) {
+      const float g[1] = {elem_to_float(q[v])};
+      left.of(r, g);
+    }
+    return r[0];
   }
 };
 
+template <int M>
+struct Int {
+  static constexpr int value = M;
+};
+
+struct Node {                // a token of the walk, and the target's probability of it
+  int up, tok;
+  float u, p;
+};
+struct Walk {                // where the walk stands: its node, the next one to look at
+  int at, next, accepted, rounds, points, row0;
+};
+
+// One cluster of C CTAs a request.  The first warp of every CTA walks the tree on the few
+// elements that decide (the rows of p and q are read only at the tokens), a lane two nodes; sums
+// over a whole row, which a second child drawn from q and the last draw need, are shared out
+// over the cluster's warps in order of the vocabulary.  So a request reads its last node's rows
+// of p and q once, which bounds a large batch; one request's time is its chain of dependent
+// loads: the tokens, the elements at them, the row, and the part of it that holds the draw.
 template <typename T>
-__device__ __forceinline__ void left_of_chunk(const Part<T>& part, const Left& left, bool struck, int c,
-                                              const uint4& x, const uint4& y, const float (&yf)[Chunk<T>::N],
-                                              float (&r)[Chunk<T>::N]) {
+__global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_constant__ VerifyParams p) {
   constexpr int N = Chunk<T>::N;
-  unpack_chunk<T>(x, r);
-  if (left.rounds) {
-    float g[N];
-    if (part.q_fits) unpack_chunk<T>(y, g);
-#pragma unroll
-    for (int e = 0; e < N; ++e) r[e] = left.of(r[e], part.q_fits ? g[e] : yf[e]);
-  }
-  if (struck) {
-#pragma unroll
-    for (int e = 0; e < N; ++e)
-      if (left.struck(part.rc.head + c * N + e)) r[e] = 0.f;
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ float left_of_element(const Part<T>& part, const Left& left, int v) {
-  if (left.struck(v)) return 0.f;
-  const float p = elem_to_float(part.p[v]);
-  return left.rounds ? left.of(p, elem_to_float(part.q[v])) : p;
-}
-
-__device__ __forceinline__ double warp_sum_f64(double x) {
-#pragma unroll
-  for (int m = 16; m >= 1; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
-  return x;
-}
-// inclusive sums over the lanes
-__device__ __forceinline__ double warp_scan_f64(double x) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int m = 1; m < 32; m *= 2) {
-    const double y = __shfl_up_sync(0xffffffffu, x, m);
-    if (lane >= m) x += y;
-  }
-  return x;
-}
-
-// One cluster of C CTAs a request.  Every CTA walks the tree by itself on the few elements that
-// decide (the rows of p and q are read only at the tokens); sums over a whole row, which a
-// second child drawn from q and the last draw need, are shared out over the cluster's warps in
-// order of the vocabulary.  So a request reads its last node's rows of p and q once, which
-// bounds a large batch; one request's time is its chain of dependent loads.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant__ VerifyParams p) {
-  constexpr int N = Chunk<T>::N;
-  __shared__ int par_s[kMaxTree], tok_s[kMaxTree];
-  __shared__ float u_s[kMaxTree], p_s[kMaxTree], q_s[kMaxTree];
+  constexpr int kParts = kMaxCluster * kWarps, kLaneParts = kParts / 32;
+  constexpr float kUp = 0x1p64f;             // keeps the tests' products of tiny numbers exact
+  using Row = NodeRow<T>;
   __shared__ float round_s[kMaxTree];        // s before round j of q
   __shared__ int point_s[kMaxTree];          // rejected point masses of the current node
-  __shared__ int path_s[kMaxTree];
-  __shared__ double warp_sum_s[2][kWarps];   // by pass, read by the cluster
-  __shared__ double all_s[kMaxCluster * kWarps + 1];
-  __shared__ double scan_s[kWarps];
-  __shared__ int state_s[6];
-  __shared__ double left_s;
-  __shared__ int pick_s;
+  __shared__ int path_s[kMaxTree], taken_s[kMaxTree];
+  __shared__ float2 sums_s[2][kParts];       // the cluster's warps' sums, by pass
+  __shared__ __align__(8) uint64_t sums_bar[2];
+  __shared__ Sum2 before_s[kParts + 1];      // the sums before each part, and of all
+  __shared__ Sum2 scan_s[kWarps];
+  __shared__ int state_s[5];                 // row, accepted, rounds, points, why the walk stopped
+  __shared__ Node node_s[kMaxTree];
+  __shared__ float q_s[kMaxTree];
+  __shared__ Walk walk_s;
+  __shared__ float draw_s;
+  __shared__ int pick_s, key_s, part_s[2];
+  const int C = 1 << p.log_C, W = C * kWarps, rank = blockIdx.x & (C - 1), b = blockIdx.x >> p.log_C;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    sm100::mbar_init(&sums_bar[0], 1);
+    sm100::mbar_init(&sums_bar[1], 1);
+    sm100::fence_mbar_init();
+    sm100::mbar_arrive_expect_tx(&sums_bar[0], (uint32_t)(W * sizeof(float2)));
+    sm100::mbar_arrive_expect_tx(&sums_bar[1], (uint32_t)(W * sizeof(float2)));
+  }
+  cluster_sync();                            // the others' barriers can be sent to
   pdl_wait();
   pdl_launch_dependents();
-  const int C = 1 << p.log_C, rank = blockIdx.x & (C - 1), b = blockIdx.x >> p.log_C;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const RequestRows rr = request_rows(p.rows, b, p.err);
-  const int n = rr.n;
   const T* P = static_cast<const T*>(p.p);
   const T* Q = static_cast<const T*>(p.q);
-  for (int i = tid; i < n; i += kThreads) {
-    const int row = rr.row0 + i;
-    const int up = i ? parent_of(p.rows.parents, row, i, p.err) : -1;
-    int x = i ? p.tokens[row] : 0;
-    if (x < 0 || x >= p.V) {
-      set_device_error(p.err, DSPARK_ERR_DEVICE_CHECK);
-      x = -1;
-    }
-    par_s[i] = up;
-    tok_s[i] = x;
-    u_s[i] = p.uniforms[row];
-    if (up >= 0 && x >= 0) {
-      p_s[i] = elem_to_float(P[(rr.row0 + up) * p.ld_p + x]);
-      q_s[i] = Q ? elem_to_float(Q[(rr.row0 + up) * p.ld_q + x]) : 1.f;
-    }
-  }
-  if (tid == 0) {
-    state_s[0] = 0;        // the current node
-    state_s[1] = 1;        // the next node to look at
-    state_s[2] = 0;        // accepted
-    state_s[3] = 0;        // rounds of q (with the sum of the last still unknown)
-    state_s[4] = 0;        // rejected point masses
-    left_s = 1.0;          // s
-  }
-  __syncthreads();
 
-  int pass = 0;
-  for (;;) {
-    // ---- the walk, until a sum over the row is needed (state_s[5]: 1) or it ends (2)
-    if (tid == 0) {
-      int at = state_s[0], i = state_s[1], accepted = state_s[2], rounds = state_s[3], points = state_s[4];
-      double s = left_s;
-      int why = n > 0 ? 2 : 3;
-      for (; i < n; ++i) {
-        if (par_s[i] != at) continue;
-        const int x = tok_s[i];
-        if (x < 0) continue;                       // (reported above; never accepted)
-        if (rounds > 0 && s < 0.0) {               // not known yet
+  // ---- the walk's nodes: two a lane of the first warp, which alone reads them again
+  if (warp == 0) {
+    const RequestRows rr = request_rows(p.rows, b, p.err);
+    float u[2] = {0.f, 0.f}, pv[2] = {0.f, 0.f}, qv[2] = {1.f, 1.f};
+    int up[2] = {-1, -1}, tok[2] = {-1, -1};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = lane + 32 * h;
+      if (i >= rr.n) continue;
+      u[h] = p.uniforms[rr.row0 + i];
+      if (i == 0) continue;
+      up[h] = parent_of(p.rows.parents, rr.row0 + i, i, p.err);
+      tok[h] = p.tokens[rr.row0 + i];
+      if (tok[h] < 0 || tok[h] >= p.V) {
+        set_device_error(p.err, DSPARK_ERR_DEVICE_CHECK);
+        up[h] = -1;                          // never accepted
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (up[h] >= 0) {
+        pv[h] = elem_to_float(P[(rr.row0 + up[h]) * p.ld_p + tok[h]]);
+        if (Q) qv[h] = elem_to_float(Q[(rr.row0 + up[h]) * p.ld_q + tok[h]]);
+      }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      node_s[lane + 32 * h] = {up[h], tok[h], u[h], pv[h]};
+      q_s[lane + 32 * h] = qv[h];
+    }
+    if (lane == 0) {
+      draw_s = u[0];
+      walk_s = {0, 1, 0, 0, 0, rr.row0};
+      state_s[4] = rr.n > 0 ? 0 : 3;
+    }
+    __syncwarp();
+  }
+
+  for (int pass = 0;; ) {
+    // ---- the walk, until a sum over the row is needed (why 1) or it ends (why 2)
+    if (warp == 0 && state_s[4] != 3) {
+      int why = 2;
+      const Node na = node_s[lane], nb = node_s[lane + 32];
+      const float qa = q_s[lane], qb = q_s[lane + 32];
+      auto [at, next, accepted, rounds, points, row0] = walk_s;
+      Sum2 s = {pass > 0 ? before_s[W].hi : 1.f, 0.f};     // a row's sum is held in 32 bits
+      bool have = true;                      // s is known
+      for (;;) {
+        const unsigned lo = __ballot_sync(0xffffffffu, na.up == at && lane >= next);
+        const unsigned hi = __ballot_sync(0xffffffffu, nb.up == at && lane + 32 >= next);
+        if (!(lo | hi)) break;
+        if (!have) {
           why = 1;
           break;
         }
-        float r = p_s[i];
-        bool yes;
+        const int i = lo ? __ffs(lo) - 1 : __ffs(hi) + 31, from = i & 31;
+        const bool high = i >= 32;
+        const int x = __shfl_sync(0xffffffffu, high ? nb.tok : na.tok, from);
+        const float ui = __shfl_sync(0xffffffffu, high ? nb.u : na.u, from);
+        const float qi = __shfl_sync(0xffffffffu, high ? qb : qa, from);
+        float r[1] = {__shfl_sync(0xffffffffu, high ? nb.p : na.p, from)};
+        next = i + 1;
         if (Q) {
-          for (int j = 0; j < rounds; ++j) r = fmaxf(__fmaf_rn(-round_s[j], q_s[i], r), 0.f);
-          yes = (double)u_s[i] * (double)q_s[i] * s < (double)r;
+          if (rounds) {
+            const float g[1] = {qi};
+            const Left left = {rounds, round_s, 0, nullptr};
+            left.of(r, g);
+          }
         } else {
-          for (int j = 0; j < points; ++j)
-            if (point_s[j] == x) r = 0.f;
-          yes = (double)u_s[i] * s < (double)r;
+          const bool gone = (lane < points && point_s[lane] == x) || (lane + 32 < points && point_s[lane + 32] == x);
+          if (__any_sync(0xffffffffu, gone)) r[0] = 0.f;
         }
-        if (yes) {
-          path_s[accepted++] = i;
+        const float qu = qi * kUp;
+        const Sum2 uq = {ui * qu, fmaf(ui, qu, -(ui * qu))}, test = uq * s;
+        if ((test.hi - r[0] * kUp) + test.lo < 0.f) {        // u q s < r
+          if (lane == 0) {
+            path_s[accepted] = i;
+            taken_s[accepted] = x;
+          }
+          ++accepted;
           at = i;
           rounds = points = 0;
-          s = 1.0;
+          s = {1.f, 0.f};
         } else if (Q) {
-          round_s[rounds++] = (float)s;
-          s = -1.0;
+          if (lane == 0) round_s[rounds] = s.hi;
+          ++rounds;
+          have = false;
         } else {
-          s -= (double)r;
-          point_s[points++] = x;
+          s.add(-r[0]);
+          s = s.normal();
+          if (lane == 0) point_s[points] = x;
+          ++points;
         }
+        __syncwarp();
       }
-      state_s[0] = at;
-      state_s[1] = i;
-      state_s[2] = accepted;
-      state_s[3] = rounds;
-      state_s[4] = points;
-      state_s[5] = why;
-      left_s = s;
+      if (lane == 0) {
+        walk_s = {at, next, accepted, rounds, points, row0};
+        state_s[0] = row0 + at;
+        state_s[1] = accepted;
+        state_s[2] = rounds;
+        state_s[3] = points;
+        state_s[4] = why;
+      }
     }
     __syncthreads();
-    const int why = state_s[5];
+    const int why = state_s[4];
     if (why == 3) break;
-    Left left = {state_s[3], round_s, state_s[4], point_s};
-    const int row = rr.row0 + state_s[0];
+    const long long row = state_s[0];
+    Left left = {state_s[2], round_s, state_s[3], point_s};
 
-    double total = 0.0;
-    Part<T> part;
-    bool struck = false;
+    Sum2 total = {0.f, 0.f};
+    bool late = false;
     for (int attempt = 0; attempt < 2; ++attempt) {
-      // ---- the warp's part of the row
-      const int W = C * kWarps, w = rank * kWarps + warp;
-      part.p = P + row * p.ld_p;
-      part.q = left.rounds ? Q + row * p.ld_q : nullptr;
-      part.V = p.V;
-      part.rc = row_chunks(part.p, p.V);
-      part.q_fits = part.q && ((reinterpret_cast<uintptr_t>(part.p) ^ reinterpret_cast<uintptr_t>(part.q)) & 15u) == 0;
-      part.c0 = (int)((long long)part.rc.chunks * w / W);
-      part.c1 = (int)((long long)part.rc.chunks * (w + 1) / W);
-      struck = false;
-      for (int j = 0; j < left.points; ++j) {
-        const int c = (left.token[j] - part.rc.head) / N;
-        struck = struck || (left.token[j] >= part.rc.head && c >= part.c0 && c < part.c1);
-      }
+      // ---- the warp's part of the row: chunks c0 .. c1 - 1
+      const Row nr(P + row * p.ld_p, left.rounds ? Q + row * p.ld_q : nullptr, p.V);
+      const int w = rank * kWarps + warp;
+      const int c0 = (int)((long long)nr.rc.chunks * w / W), c1 = (int)((long long)nr.rc.chunks * (w + 1) / W);
       Sum2 sum = {0.f, 0.f};
       constexpr int kBatch = 4;
-      for (int c = part.c0 + lane; c < part.c1; c += 32 * kBatch) {
-        uint4 x[kBatch], y[kBatch];
-        float yf[kBatch][N];
+      auto part = [&](auto mode) {           // 0: p alone, 1: q's chunks too, 2: q's elements
+        constexpr int M = decltype(mode)::value;
+        for (int c = c0 + lane; c < c1; c += 32 * kBatch) {
+          typename Row::Raw raw[kBatch];
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u)
-          if (c + 32 * u < part.c1) part.load(c + 32 * u, x[u], y[u], yf[u]);
+          for (int k = 0; k < kBatch; ++k) raw[k] = nr.template load<M>(min(c + 32 * k, c1 - 1));
+          // whether a struck token lies in these chunks (a batch spans 32 kBatch of them)
+          bool near = false;
+          if (M == 0)
+            for (int j = 0; j < left.points; ++j) {
+              const int d = left.token[j] - nr.rc.head - (c - lane) * N;
+              near = near || (d >= 0 && d < 32 * kBatch * N);
+            }
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          if (c + 32 * u >= part.c1) break;
-          float r[N];
-          left_of_chunk(part, left, struck, c + 32 * u, x[u], y[u], yf[u], r);
+          for (int k = 0; k < kBatch; ++k) {
+            if (c + 32 * k >= c1) break;
+            float r[N];
+            nr.template left_of<M>(raw[k], left, near, c + 32 * k, r);
 #pragma unroll
-          for (int e = 0; e < N; ++e) sum.add(r[e]);
+            for (int e = 0; e < N; ++e) sum.add(r[e]);
+          }
+        }
+      };
+      if (!nr.q) part(Int<0>{});
+      else if (nr.q_fits) part(Int<1>{});
+      else part(Int<2>{});
+      if (w == 0 && lane < nr.rc.head) sum.add(nr.element(left, lane));
+      if (w == W - 1 && lane < nr.rc.tail) sum.add(nr.element(left, p.V - nr.rc.tail + lane));
+      const Sum2 mine = warp_sum(sum.normal());
+      // ---- to the whole cluster.  Two buffers, whose barriers count the sums' bytes: one is
+      // sent to again only in the next pass but one, after its reader has sent in the next.
+      const int buf = pass & 1;
+      if (lane < C) send_f2(&sums_s[buf][w], &sums_bar[buf], lane, mine.hi, mine.lo);
+      if (warp == 0) {
+        late = !wait_cluster(&sums_bar[buf], (pass >> 1) & 1);
+        if (lane == 0) sm100::mbar_arrive_expect_tx(&sums_bar[buf], (uint32_t)(W * sizeof(float2)));
+        // the sums before each part, in the vocabulary's order: some parts in a row a lane
+        Sum2 x[kLaneParts], in = {0.f, 0.f};
+        const int each = (W + 31) / 32;
+#pragma unroll
+        for (int k = 0; k < kLaneParts; ++k) {
+          const int i = lane * each + k;
+          x[k] = in;
+          if (k < each && i < W) in = in + Sum2{sums_s[buf][i].x, sums_s[buf][i].y};
+        }
+        const Sum2 up_to = warp_scan(in);
+        Sum2 before = shfl_up(up_to, 1);
+        if (lane == 0) before = {0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < kLaneParts; ++k)
+          if (k < each && lane * each + k < W) before_s[lane * each + k] = before + x[k];
+        if (lane == 31) before_s[W] = up_to;
+        if (__any_sync(0xffffffffu, late) && lane == 0) {
+          set_device_error(p.err, DSPARK_ERR_TIMEOUT);
+          state_s[4] = 4;
         }
       }
-      if (w == 0 && lane < part.rc.head) sum.add(left_of_element(part, left, lane));
-      if (w == W - 1 && lane < part.rc.tail) sum.add(left_of_element(part, left, p.V - part.rc.tail + lane));
-      const double mine = warp_sum_f64(sum.value());
-      // ---- the cluster's sums.  Two buffers: a CTA writes one again only after the others
-      // have read it, since the barrier of the pass between lies behind those reads.
-      if (lane == 0) warp_sum_s[pass & 1][warp] = mine;
-      if (C > 1) cluster_sync();
-      else __syncthreads();
-      if (tid < W)
-        all_s[tid] = C > 1 ? __longlong_as_double((long long)cluster_ld_u64(
-                                 cluster_map(&warp_sum_s[pass & 1][tid & (kWarps - 1)], (uint32_t)(tid / kWarps))))
-                           : warp_sum_s[pass & 1][tid];
       ++pass;
       __syncthreads();
-      if (warp == 0) {
-        // exclusive sums, in the vocabulary's order
-        double carry = 0.0;
-        for (int t0 = 0; t0 < W; t0 += 32) {
-          const double x = t0 + lane < W ? all_s[t0 + lane] : 0.0;
-          const double in = warp_scan_f64(x), before = __shfl_up_sync(0xffffffffu, in, 1);
-          if (t0 + lane < W) all_s[t0 + lane] = carry + (lane ? before : 0.0);
-          carry += __shfl_sync(0xffffffffu, in, 31);
-        }
-        if (lane == 0) all_s[W] = carry;
-      }
-      __syncthreads();
-      total = all_s[W];
-      if (why == 1 || total > 0.0 || (!left.rounds && !left.points)) break;
+      if (state_s[4] == 4) break;
+      total = before_s[W];
+      if (why == 1 || total.hi > 0.f || (!left.rounds && !left.points)) break;
       left.rounds = left.points = 0;         // nothing is left: from the target's own row
     }
-    if (why == 1) {
-      if (tid == 0) left_s = (double)(float)total;     // s is held in 32 bits
-      __syncthreads();
-      continue;
-    }
+    if (state_s[4] == 4) break;
+    if (why == 1) continue;
 
     // ---- the last draw: the first v whose sum up to it exceeds u total
-    const int W = C * kWarps;
-    const bool valid = total > 0.0 && total < INFINITY;
-    const double t = (double)u_s[0] * total;
-    int target = W - 1;                      // the warp part that holds it
-    if (tid == 0) pick_s = -1;
-    if (valid) {
-      // (the last part that is not empty and starts at or before t)
-      int best = 0;
-      for (int w0 = lane; w0 < W; w0 += 32)
-        if (all_s[w0] <= t && all_s[w0 + 1] > all_s[w0]) best = max(best, w0);
-      target = __reduce_max_sync(0xffffffffu, best);
-    }
-    __syncthreads();
-    if (valid && target / kWarps == rank) {
-      // this CTA's threads share the part's chunks out again, in order
-      const int w = target;
-      const int c0 = (int)((long long)part.rc.chunks * w / W), c1 = (int)((long long)part.rc.chunks * (w + 1) / W);
-      const int head = w == 0 ? part.rc.head : 0, tail = w == W - 1 ? part.rc.tail : 0;
-      const int each = (c1 - c0 + kThreads - 1) / kThreads;
-      // thread's elements v0 .. v1 - 1
-      const int a0 = min(c0 + tid * each, c1), a1 = min(c0 + (tid + 1) * each, c1);
-      const int v0 = tid == 0 ? part.rc.head + c0 * N - head : part.rc.head + a0 * N;
-      const int v1 = part.rc.head + a1 * N + (tid == kThreads - 1 ? tail : 0);
-      Sum2 sum = {0.f, 0.f};
-      for (int v = v0; v < v1; ++v) sum.add(left_of_element(part, left, v));
-      const double mine = sum.value(), in = warp_scan_f64(mine);
-      if (lane == 31) scan_s[warp] = in;
-      __syncthreads();
-      double before = all_s[w];
-      for (int k = 0; k < warp; ++k) before += scan_s[k];
-      const double up_to = before + in;
-      // the first thread that goes beyond t; by rounding there may be none, then the last
-      // thread that has anything
-      const unsigned beyond = __ballot_sync(0xffffffffu, mine > 0.0 && up_to > t);
-      const unsigned any = __ballot_sync(0xffffffffu, mine > 0.0);
-      int key = INT_MAX;
-      if (beyond) key = warp * 32 + __ffs(beyond) - 1;
-      else if (any) key = (1 << 20) - (warp * 32 + 31 - __clz(any));   // (the last is the least of these)
-      __shared__ int key_s;
-      if (tid == 0) key_s = INT_MAX;
-      __syncthreads();
-      if (lane == 0) atomicMin(&key_s, key);
-      __syncthreads();
-      const int k = key_s, who = k > (1 << 19) && k != INT_MAX ? (1 << 20) - k : k;
-      if (tid == who) {
-        double acc = before + (in - mine);
-        int pick = -1;
-        for (int v = v0; v < v1; ++v) {
-          const float r = left_of_element(part, left, v);
-          if (!(r > 0.f)) continue;
-          pick = v;
-          acc += (double)r;
-          if (acc > t) break;
-        }
-        pick_s = pick;
-      }
-      __syncthreads();
-    }
-    // ---- results: the CTA that drew, or the first where nothing can be drawn
+    const bool valid = total.hi > 0.f && total.hi < INFINITY;
+    const Sum2 t = Sum2{draw_s, 0.f} * total;
+    // the last part that is not empty and starts at or before t
+    int target = 0;
+    for (int w0 = lane; w0 < W; w0 += 32)
+      if (!before_s[w0].beyond(t) && before_s[w0 + 1].beyond(before_s[w0])) target = w0;
+    target = __reduce_max_sync(0xffffffffu, target);
     const bool writer = valid ? target / kWarps == rank : rank == 0;
     if (writer) {
-      const int accepted = state_s[2];
+      if (tid == 0) pick_s = -1;
+      if (valid) {
+        const Row nr(P + row * p.ld_p, left.rounds ? Q + row * p.ld_q : nullptr, p.V);
+        int c0 = (int)((long long)nr.rc.chunks * target / W), c1 = (int)((long long)nr.rc.chunks * (target + 1) / W);
+        bool with_head = target == 0, with_tail = target == W - 1;
+        Sum2 base = before_s[target];
+        constexpr int kHold = 2;             // chunks that a thread holds
+        for (;;) {
+          // the threads share the chunks out again, in order; more than they hold are narrowed
+          // down to one thread's first
+          const int each = (c1 - c0 + kThreads - 1) / kThreads;
+          const bool last = each <= kHold;
+          const int a0 = min(c0 + tid * each, c1), a1 = min(a0 + each, c1);
+          const bool mine_head = with_head && tid == 0, mine_tail = with_tail && tid == kThreads - 1;
+          float held[kHold][N];
+          Sum2 sum = {0.f, 0.f};
+          if (mine_head)
+            for (int v = 0; v < nr.rc.head; ++v) sum.add(nr.element(left, v));
+          if (last) {
+            typename Row::Raw raw[kHold];
+#pragma unroll
+            for (int k = 0; k < kHold; ++k)
+              if (a0 + k < a1) raw[k] = nr.load_any(a0 + k);
+#pragma unroll
+            for (int k = 0; k < kHold; ++k)
+              if (a0 + k < a1) {
+                nr.left_of_any(raw[k], left, a0 + k, held[k]);
+#pragma unroll
+                for (int e = 0; e < N; ++e) sum.add(held[k][e]);
+              }
+          } else {
+            for (int c = a0; c < a1; ++c) {
+              float r[N];
+              nr.left_of_any(nr.load_any(c), left, c, r);
+#pragma unroll
+              for (int e = 0; e < N; ++e) sum.add(r[e]);
+            }
+          }
+          if (mine_tail)
+            for (int v = p.V - nr.rc.tail; v < p.V; ++v) sum.add(nr.element(left, v));
+          const Sum2 mine = sum.normal(), in = warp_scan(mine);
+          if (lane == 31) scan_s[warp] = in;
+          if (tid == 0) key_s = INT_MAX;
+          __syncthreads();
+          // the warps' sums again by every warp: the sums before its own
+          const Sum2 warps = warp_scan(lane < kWarps ? scan_s[lane] : Sum2{0.f, 0.f});
+          const int wb = max(warp - 1, 0);
+          Sum2 before = {__shfl_sync(0xffffffffu, warps.hi, wb), __shfl_sync(0xffffffffu, warps.lo, wb)};
+          before = warp ? base + before : base;
+          Sum2 mine_before = shfl_up(in, 1);
+          mine_before = lane ? before + mine_before : before;
+          // the first thread that goes beyond t; by rounding there may be none, then the last
+          // thread that has anything
+          const unsigned beyond = __ballot_sync(0xffffffffu, mine.hi > 0.f && (before + in).beyond(t));
+          const unsigned any = __ballot_sync(0xffffffffu, mine.hi > 0.f);
+          if (lane == 0 && any)
+            atomicMin(&key_s, beyond ? warp * 32 + __ffs(beyond) - 1
+                                     : (1 << 20) - (warp * 32 + 31 - __clz(any)));   // (the last is the least of these)
+          __syncthreads();
+          const int k = key_s, who = k > (1 << 19) && k != INT_MAX ? (1 << 20) - k : k;
+          if (who >= kThreads) break;        // (nothing: pick_s stays -1)
+          if (last) {
+            if (tid == who) {
+              Sum2 acc = mine_before;
+              int pick = -1;
+              bool done = false;
+              auto take = [&](int v, float r) {
+                if (done || !(r > 0.f)) return;
+                pick = v;
+                acc = acc + Sum2{r, 0.f};
+                done = acc.beyond(t);
+              };
+              if (mine_head)
+                for (int v = 0; v < nr.rc.head; ++v) take(v, nr.element(left, v));
+#pragma unroll
+              for (int h = 0; h < kHold; ++h)
+                if (a0 + h < a1) {
+#pragma unroll
+                  for (int e = 0; e < N; ++e) take(nr.rc.head + (a0 + h) * N + e, held[h][e]);
+                }
+              if (mine_tail)
+                for (int v = p.V - nr.rc.tail; v < p.V; ++v) take(v, nr.element(left, v));
+              pick_s = pick;
+            }
+            break;
+          }
+          if (tid == who) {
+            scan_s[0] = mine_before;
+            part_s[0] = a0;
+            part_s[1] = a1;
+          }
+          __syncthreads();
+          base = scan_s[0];
+          c0 = part_s[0];
+          c1 = part_s[1];
+          with_head = with_head && who == 0;
+          with_tail = with_tail && who == kThreads - 1;
+          __syncthreads();
+        }
+      }
+      __syncthreads();
+      // ---- results
+      const int k = state_s[1];
       if (tid == 0 && pick_s < 0) set_device_error(p.err, DSPARK_ERR_DEVICE_CHECK);
       for (int j = tid; j < p.rows.N; j += kThreads) {
-        const long long at = (long long)b * p.rows.N + j;
-        p.path[at] = j < accepted ? path_s[j] : -1;
-        p.out_tokens[at] = j < accepted ? tok_s[path_s[j]] : j == accepted ? pick_s : -1;
+        const long long o = (long long)b * p.rows.N + j;
+        p.path[o] = j < k ? path_s[j] : -1;
+        p.out_tokens[o] = j < k ? taken_s[j] : j == k ? pick_s : -1;
       }
       if (tid == 0) {
-        p.accept_len[b] = accepted;
-        p.n_out[b] = accepted + 1;
+        p.accept_len[b] = k;
+        p.n_out[b] = k + 1;
       }
     }
     break;
   }
-  if (n == 0 && rank == 0) {                 // no tokens: no answer
+  if (state_s[4] >= 3 && rank == 0) {        // no tokens, or a wait ran out: no answer
     for (int j = tid; j < p.rows.N; j += kThreads) {
       p.path[(long long)b * p.rows.N + j] = -1;
       p.out_tokens[(long long)b * p.rows.N + j] = -1;
@@ -385,7 +536,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
       p.n_out[b] = 0;
     }
   }
-  if (C > 1) cluster_sync();                 // nobody leaves while its sums may still be read
+  if (state_s[4] >= 3) cluster_sync();       // (else it has all that is sent to it)
 }
 
 template <typename T>
@@ -393,7 +544,7 @@ cudaError_t verify_for(VerifyParams p, cudaStream_t stream) {
   // CTAs a request: as many as keep the device busy, while every warp has a few chunks
   const int chunks = cdiv(p.V, Chunk<T>::N);
   p.log_C = 0;
-  while (p.log_C < 3 && (p.rows.B << p.log_C) < 608 && chunks >= (kThreads << (p.log_C + 1))) ++p.log_C;
+  while (p.log_C < 3 && (p.rows.B << p.log_C) < 304 && chunks >= (kThreads << (p.log_C + 1))) ++p.log_C;
   return launch_rows_cluster(verify_kernel<T>, (long long)p.rows.B << p.log_C, 1 << p.log_C, kThreads, 0, stream, p);
 }
 
