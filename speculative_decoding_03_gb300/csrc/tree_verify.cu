@@ -41,13 +41,14 @@ struct Sum2 {
     const float s = hi + lo;
     return {s, lo - (s - hi)};
   }
+  // (both renormalised)
   __device__ __forceinline__ bool beyond(const Sum2& o) const { return hi > o.hi || (hi == o.hi && lo > o.lo); }
 };
-__device__ __forceinline__ Sum2 operator+(const Sum2& a, const Sum2& b) {
+__device__ __forceinline__ Sum2 operator+(const Sum2& a, const Sum2& b) {      // not renormalised
   Sum2 r = a;
   r.add(b.hi);
   r.lo += b.lo;
-  return r.normal();
+  return r;
 }
 __device__ __forceinline__ Sum2 operator*(const Sum2& a, const Sum2& b) {
   const float p = a.hi * b.hi;
@@ -171,6 +172,15 @@ struct Node {                // a token of the walk, and the target's probabilit
   int up, tok;
   float u, p;
 };
+
+// u q s < r in effect exactly: q and r times 2^64, so that products of tiny numbers keep their
+// low parts
+__device__ __forceinline__ bool accepts(float u, float q, const Sum2& s, float r) {
+  constexpr float kUp = 0x1p64f;
+  const float a = q * kUp, b = u * a;
+  const Sum2 x = Sum2{b, fmaf(u, a, -b)} * s;
+  return (x.hi - r * kUp) + x.lo < 0.f;
+}
 struct Walk {                // where the walk stands: its node, the next one to look at
   int at, next, accepted, rounds, points, row0;
 };
@@ -185,7 +195,6 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_constant__ VerifyParams p) {
   constexpr int N = Chunk<T>::N;
   constexpr int kParts = kMaxCluster * kWarps, kLaneParts = kParts / 32;
-  constexpr float kUp = 0x1p64f;             // keeps the tests' products of tiny numbers exact
   using Row = NodeRow<T>;
   __shared__ float round_s[kMaxTree];        // s before round j of q
   __shared__ int point_s[kMaxTree];          // rejected point masses of the current node
@@ -198,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
   __shared__ Node node_s[kMaxTree];
   __shared__ float q_s[kMaxTree];
   __shared__ Walk walk_s;
-  __shared__ float draw_s;
+  __shared__ float draw_s, ends_s[32];
   __shared__ int pick_s, key_s, part_s[2];
   const int C = 1 << p.log_C, W = C * kWarps, rank = blockIdx.x & (C - 1), b = blockIdx.x >> p.log_C;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -209,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
     sm100::mbar_arrive_expect_tx(&sums_bar[0], (uint32_t)(W * sizeof(float2)));
     sm100::mbar_arrive_expect_tx(&sums_bar[1], (uint32_t)(W * sizeof(float2)));
   }
-  cluster_sync();                            // the others' barriers can be sent to
+  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
   pdl_wait();
   pdl_launch_dependents();
   const T* P = static_cast<const T*>(p.p);
@@ -261,6 +270,10 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
       auto [at, next, accepted, rounds, points, row0] = walk_s;
       Sum2 s = {pass > 0 ? before_s[W].hi : 1.f, 0.f};     // a row's sum is held in 32 bits
       bool have = true;                      // s is known
+      // a node's first child is tried against s = 1 and p itself: all nodes' at once
+      const Sum2 one = {1.f, 0.f};
+      const unsigned yes_lo = __ballot_sync(0xffffffffu, accepts(na.u, qa, one, na.p));
+      const unsigned yes_hi = __ballot_sync(0xffffffffu, accepts(nb.u, qb, one, nb.p));
       for (;;) {
         const unsigned lo = __ballot_sync(0xffffffffu, na.up == at && lane >= next);
         const unsigned hi = __ballot_sync(0xffffffffu, nb.up == at && lane + 32 >= next);
@@ -272,23 +285,23 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
         const int i = lo ? __ffs(lo) - 1 : __ffs(hi) + 31, from = i & 31;
         const bool high = i >= 32;
         const int x = __shfl_sync(0xffffffffu, high ? nb.tok : na.tok, from);
-        const float ui = __shfl_sync(0xffffffffu, high ? nb.u : na.u, from);
-        const float qi = __shfl_sync(0xffffffffu, high ? qb : qa, from);
         float r[1] = {__shfl_sync(0xffffffffu, high ? nb.p : na.p, from)};
         next = i + 1;
-        if (Q) {
-          if (rounds) {
+        bool yes = ((high ? yes_hi : yes_lo) >> from) & 1;
+        if (rounds | points) {
+          const float ui = __shfl_sync(0xffffffffu, high ? nb.u : na.u, from);
+          const float qi = __shfl_sync(0xffffffffu, high ? qb : qa, from);
+          if (Q) {
             const float g[1] = {qi};
             const Left left = {rounds, round_s, 0, nullptr};
             left.of(r, g);
+          } else {
+            const bool gone = (lane < points && point_s[lane] == x) || (lane + 32 < points && point_s[lane + 32] == x);
+            if (__any_sync(0xffffffffu, gone)) r[0] = 0.f;
           }
-        } else {
-          const bool gone = (lane < points && point_s[lane] == x) || (lane + 32 < points && point_s[lane + 32] == x);
-          if (__any_sync(0xffffffffu, gone)) r[0] = 0.f;
+          yes = accepts(ui, qi, s, r[0]);
         }
-        const float qu = qi * kUp;
-        const Sum2 uq = {ui * qu, fmaf(ui, qu, -(ui * qu))}, test = uq * s;
-        if ((test.hi - r[0] * kUp) + test.lo < 0.f) {        // u q s < r
+        if (yes) {
           if (lane == 0) {
             path_s[accepted] = i;
             taken_s[accepted] = x;
@@ -320,7 +333,10 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
     }
     __syncthreads();
     const int why = state_s[4];
-    if (why == 3) break;
+    if (why == 3) {
+      asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+      break;
+    }
     const long long row = state_s[0];
     Left left = {state_s[2], round_s, state_s[3], point_s};
 
@@ -332,9 +348,9 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
       const int w = rank * kWarps + warp;
       const int c0 = (int)((long long)nr.rc.chunks * w / W), c1 = (int)((long long)nr.rc.chunks * (w + 1) / W);
       Sum2 sum = {0.f, 0.f};
-      constexpr int kBatch = 4;
       auto part = [&](auto mode) {           // 0: p alone, 1: q's chunks too, 2: q's elements
         constexpr int M = decltype(mode)::value;
+        constexpr int kBatch = M == 0 ? 8 : M == 1 ? 5 : 2;     // chunks that a lane waits for at once
         for (int c = c0 + lane; c < c1; c += 32 * kBatch) {
           typename Row::Raw raw[kBatch];
 #pragma unroll
@@ -361,7 +377,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
       else part(Int<2>{});
       if (w == 0 && lane < nr.rc.head) sum.add(nr.element(left, lane));
       if (w == W - 1 && lane < nr.rc.tail) sum.add(nr.element(left, p.V - nr.rc.tail + lane));
-      const Sum2 mine = warp_sum(sum.normal());
+      const Sum2 mine = warp_sum(sum);
+      if (pass == 0) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // its barriers can be sent to
       // ---- to the whole cluster.  Two buffers, whose barriers count the sums' bytes: one is
       // sent to again only in the next pass but one, after its reader has sent in the next.
       const int buf = pass & 1;
@@ -383,8 +400,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
         if (lane == 0) before = {0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < kLaneParts; ++k)
-          if (k < each && lane * each + k < W) before_s[lane * each + k] = before + x[k];
-        if (lane == 31) before_s[W] = up_to;
+          if (k < each && lane * each + k < W) before_s[lane * each + k] = (before + x[k]).normal();
+        if (lane == 31) before_s[W] = up_to.normal();
         if (__any_sync(0xffffffffu, late) && lane == 0) {
           set_device_error(p.err, DSPARK_ERR_TIMEOUT);
           state_s[4] = 4;
@@ -450,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
           }
           if (mine_tail)
             for (int v = p.V - nr.rc.tail; v < p.V; ++v) sum.add(nr.element(left, v));
-          const Sum2 mine = sum.normal(), in = warp_scan(mine);
+          const Sum2 mine = sum, in = warp_scan(mine);
           if (lane == 31) scan_s[warp] = in;
           if (tid == 0) key_s = INT_MAX;
           __syncthreads();
@@ -463,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
           mine_before = lane ? before + mine_before : before;
           // the first thread that goes beyond t; by rounding there may be none, then the last
           // thread that has anything
-          const unsigned beyond = __ballot_sync(0xffffffffu, mine.hi > 0.f && (before + in).beyond(t));
+          const unsigned beyond = __ballot_sync(0xffffffffu, mine.hi > 0.f && (before + in).normal().beyond(t));
           const unsigned any = __ballot_sync(0xffffffffu, mine.hi > 0.f);
           if (lane == 0 && any)
             atomicMin(&key_s, beyond ? warp * 32 + __ffs(beyond) - 1
@@ -472,27 +489,31 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
           const int k = key_s, who = k > (1 << 19) && k != INT_MAX ? (1 << 20) - k : k;
           if (who >= kThreads) break;        // (nothing: pick_s stays -1)
           if (last) {
+            // the elements of that thread, at most 32 of them with a row's ends, a lane each
+            const int first = nr.rc.head + min(c0 + who * each, c1) * N - (with_head && who == 0 ? nr.rc.head : 0);
             if (tid == who) {
-              Sum2 acc = mine_before;
-              int pick = -1;
-              bool done = false;
-              auto take = [&](int v, float r) {
-                if (done || !(r > 0.f)) return;
-                pick = v;
-                acc = acc + Sum2{r, 0.f};
-                done = acc.beyond(t);
-              };
+              int m = 0;
               if (mine_head)
-                for (int v = 0; v < nr.rc.head; ++v) take(v, nr.element(left, v));
+                for (int v = 0; v < nr.rc.head; ++v) ends_s[m++] = nr.element(left, v);
 #pragma unroll
               for (int h = 0; h < kHold; ++h)
                 if (a0 + h < a1) {
 #pragma unroll
-                  for (int e = 0; e < N; ++e) take(nr.rc.head + (a0 + h) * N + e, held[h][e]);
+                  for (int e = 0; e < N; ++e) ends_s[m + e] = held[h][e];
+                  m += N;
                 }
               if (mine_tail)
-                for (int v = p.V - nr.rc.tail; v < p.V; ++v) take(v, nr.element(left, v));
-              pick_s = pick;
+                for (int v = p.V - nr.rc.tail; v < p.V; ++v) ends_s[m++] = nr.element(left, v);
+              for (; m < 32; ++m) ends_s[m] = 0.f;
+              scan_s[0] = mine_before;
+            }
+            __syncthreads();
+            if (warp == 0) {
+              const float r = ends_s[lane];
+              const Sum2 up_to = (scan_s[0] + warp_scan({r, 0.f})).normal();
+              const unsigned past = __ballot_sync(0xffffffffu, r > 0.f && up_to.beyond(t));
+              const unsigned some = __ballot_sync(0xffffffffu, r > 0.f);
+              if (lane == 0) pick_s = first + (past ? __ffs(past) - 1 : 31 - __clz(some));
             }
             break;
           }
@@ -541,10 +562,13 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
 
 template <typename T>
 cudaError_t verify_for(VerifyParams p, cudaStream_t stream) {
-  // CTAs a request: as many as keep the device busy, while every warp has a few chunks
+  // CTAs a request: as many as the device holds at once, two an SM, while every warp has a few
+  // chunks.  (256 chains of 129280 in fp32: 39 us with two CTAs each, 46 and 66 with four and
+  // eight, whose walks and draws come in more waves; 64 trees of 151936 in bf16: 15 us with
+  // four, 21 with eight.)
   const int chunks = cdiv(p.V, Chunk<T>::N);
   p.log_C = 0;
-  while (p.log_C < 3 && (p.rows.B << p.log_C) < 304 && chunks >= (kThreads << (p.log_C + 1))) ++p.log_C;
+  while (p.log_C < 3 && (p.rows.B << (p.log_C + 1)) <= 304 && chunks >= (kThreads << (p.log_C + 1))) ++p.log_C;
   return launch_rows_cluster(verify_kernel<T>, (long long)p.rows.B << p.log_C, 1 << p.log_C, kThreads, 0, stream, p);
 }
 
