@@ -80,6 +80,15 @@ __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+      "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,
                                             int w) {
   asm volatile(
@@ -107,7 +116,7 @@ __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
 struct Request {
   int row0, n, len, end, tiles, blocks, units;
 };
-__device__ __forceinline__ Request request_of(const AttendParams& p, int b) {
+__device__ __forceinline__ Request request_of(const AttendParams& p, int b, int block_rows) {
   Request r;
   const RequestRows rows = request_rows(p.rows, b, p.err);
   r.row0 = rows.row0;
@@ -116,7 +125,7 @@ __device__ __forceinline__ Request request_of(const AttendParams& p, int b) {
   if (r.len < 0) r.n = 0;
   r.end = r.len + r.n;
   r.tiles = r.n ? (r.end + kTile - 1) / kTile : 0;
-  r.blocks = r.n ? (r.n * p.group + kTile - 1) / kTile : 0;
+  r.blocks = r.n ? (r.n * p.group + block_rows - 1) / block_rows : 0;
   r.units = r.tiles * r.blocks * p.cs.heads;
   return r;
 }
@@ -124,21 +133,22 @@ __device__ __forceinline__ Request request_of(const AttendParams& p, int b) {
 // The pieces of a CTA's share [lo, hi) of the units, in order.
 struct Pieces {
   long long left;            // units still to come
-  int b, off;                // the next unit: `off` of request b's
+  int b, off, block_rows;    // the next unit: `off` of request b's
   Request r;
   // the current piece
   int block, head, tile0, n_tiles;
   bool whole;
-  __device__ __forceinline__ void start(const AttendParams& p, int b0, int off0, long long units) {
+  __device__ __forceinline__ void start(const AttendParams& p, int rows, int b0, int off0, long long units) {
+    block_rows = rows;
     b = b0;
     off = off0;
     left = units;
-    if (left > 0) r = request_of(p, b);
+    if (left > 0) r = request_of(p, b, block_rows);
   }
   __device__ __forceinline__ bool next(const AttendParams& p) {
     if (left <= 0) return false;
     while (off >= r.units) {
-      r = request_of(p, ++b);
+      r = request_of(p, ++b, block_rows);
       off = 0;
     }
     const int at = off / r.tiles;
@@ -152,6 +162,77 @@ struct Pieces {
     left -= n_tiles;
     return true;
   }
+  __device__ __forceinline__ int rows(const AttendParams& p) const {
+    return min(block_rows, r.n * p.group - block * block_rows);
+  }
+};
+
+// This CTA's share [lo, hi) of all units among the first G CTAs: a scan over the requests, each
+// thread some in a row.  start_s gets the first unit's request and its place among the request's.
+struct Share {
+  long long lo, hi, total, G;
+};
+__device__ __forceinline__ Share share_units(const AttendParams& p, int block_rows, long long* sums_s, int* start_s) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int each = (p.rows.B + kThreads - 1) / kThreads, b0 = tid * each, b1 = min(b0 + each, p.rows.B);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += request_of(p, b, block_rows).units;
+  long long in = mine;
+#pragma unroll
+  for (int m = 1; m < 32; m *= 2) {
+    const long long y = __shfl_up_sync(0xffffffffu, in, m);
+    if (lane >= m) in += y;
+  }
+  if (lane == 31) sums_s[warp] = in;
+  __syncthreads();
+  Share s = {0, 0, 0, 0};
+  long long before = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += sums_s[w];
+    s.total += sums_s[w];
+  }
+  s.G = min((long long)gridDim.x, s.total);
+  if (blockIdx.x < s.G) {
+    s.lo = s.total * blockIdx.x / s.G;
+    s.hi = s.total * (blockIdx.x + 1) / s.G;
+    if (before + in - mine <= s.lo && s.lo < before + in) {
+      long long at = before + in - mine;
+      for (int b = b0; b < b1; ++b) {
+        const int u = request_of(p, b, block_rows).units;
+        if (s.lo < at + u) {
+          start_s[0] = b;
+          start_s[1] = (int)(s.lo - at);
+          break;
+        }
+        at += u;
+      }
+    }
+  }
+  return s;
+}
+
+// CTAs that share the `tiles` units from g0 on, the first of which is this one's.
+__device__ __forceinline__ int parts_of(const Share& s, long long g0, int tiles) {
+  return (int)(((g0 + tiles) * s.G - 1) / s.total - blockIdx.x) + 1;
+}
+
+// Bounded waits: one that runs out reports it and makes the CTA's others return too.
+struct Waits {
+  volatile int* abort_s;
+  int* err;
+  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = sm_cycles();
+    for (;;) {
+      if (mbar_try_wait_sleep(bar, parity)) return true;
+      if (*abort_s) return false;
+      if (sm_cycles() - t0 > kWaitCycles) {
+        set_device_error(err, DSPARK_ERR_TIMEOUT);
+        *abort_s = 1;
+        return false;
+      }
+    }
+  }
 };
 
 // Position in the ring of the K or V tile j of a piece of n tiles: K_0, K_1, V_0, K_2, V_1, ..,
@@ -159,8 +240,75 @@ struct Pieces {
 __device__ __forceinline__ int k_item(int j) { return j ? 2 * j - 1 : 0; }
 __device__ __forceinline__ int v_item(int j, int n) { return j < n - 1 ? 2 * j + 2 : 2 * n - 1; }
 
+// The copying warp's side of the ring of S::kBufs buffers: tiles page by page, a lane a copy.
+template <typename S>
+struct TileCopies {
+  uint8_t* ring;
+  uint64_t *full, *empty;
+  const Waits& wait;
+  const AttendParams& p;
+  uint32_t item = 0;
+  // the page of each of the tile's copies (lane: copy)
+  __device__ __forceinline__ int pages_of(int b, int slot0, int end) const {
+    const int lane = threadIdx.x & 31, box = min(1 << p.slots.page_shift, kTile);
+    const int slot = slot0 + lane * box;
+    return lane < kTile / box && slot < end ? slot_page(p.slots, b, slot, p.err) : 0;
+  }
+  __device__ __forceinline__ bool copy(const CUtensorMap* map, int id, int slot0, int head, int end) {
+    const int lane = threadIdx.x & 31, page = 1 << p.slots.page_shift, box = min(page, kTile);
+    const int my_page = lane / S::kHalves, my_half = lane % S::kHalves;
+    const uint32_t st = item % S::kBufs;
+    if (!__all_sync(0xffffffffu, wait(&empty[st], ((item / S::kBufs) & 1) ^ 1))) return false;
+    const int n_pages = min(kTile / box, (end - slot0 + box - 1) / box);
+    if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(n_pages * box * 128 * S::kHalves));
+    __syncwarp();
+    const int pid = __shfl_sync(0xffffffffu, id, my_page);
+    if (my_page < n_pages)
+      tma_load_4d(ring + st * S::kBuf + my_half * S::kHalf + my_page * box * 128, map, &full[st], my_half * 64,
+                  slot0 & (page - 1), head, pid < 0 ? p.slots.n_pages : pid);
+    ++item;
+    return true;
+  }
+  // every issued copy lands before the CTA may exit
+  __device__ __forceinline__ void drain() const {
+    for (uint32_t i = item > (uint32_t)S::kBufs ? item - S::kBufs : 0; i < item; ++i)
+      mbar_wait(&full[i % S::kBufs], (i / S::kBufs) & 1);
+  }
+};
+
+// Slots behind the last hold anything, and a drafted token that some rows do not see may hold
+// values that are not finite: 0 x NaN must not reach them.  Clears line r of a value tile, or
+// (in_use) its values that are not finite, which are added again at the end; true if it had any.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_constant__ CUtensorMap k_map,
+__device__ __forceinline__ bool clear_line(uint8_t* line, int half_bytes, int r, bool in_use) {
+  bool bad = false;
+#pragma unroll 4
+  for (int c = 0; c < D / 8; ++c) {
+    uint4* at = reinterpret_cast<uint4*>(line + c / 8 * half_bytes + ((c ^ r) & 7) * 16);
+    if (!in_use) {
+      *at = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    float f[8];
+    unpack_chunk<T>(*at, f);
+    bool any = false;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const bool finite = f[e] - f[e] == 0.f;
+      any = any || !finite;
+      f[e] = finite ? f[e] : 0.f;
+    }
+    if (any) {
+      *at = pack_chunk<T>(f);
+      bad = true;
+    }
+  }
+  fence_proxy_async_smem();
+  return bad;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_constant__ CUtensorMap k_map,
                                                              const __grid_constant__ CUtensorMap v_map,
                                                              const __grid_constant__ AttendParams p) {
   using S = AttendSmem<D>;
@@ -210,103 +358,36 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   pdl_wait();
   pdl_launch_dependents();
 
-  // ---- this CTA's share of the units: a scan over the requests, each thread some in a row
-  const int each = (p.rows.B + kThreads - 1) / kThreads, b0 = tid * each, b1 = min(b0 + each, p.rows.B);
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += request_of(p, b).units;
-  long long in = mine;
-#pragma unroll
-  for (int m = 1; m < 32; m *= 2) {
-    const long long y = __shfl_up_sync(0xffffffffu, in, m);
-    if (lane >= m) in += y;
-  }
-  if (lane == 31) sums_s[warp] = in;
-  __syncthreads();
-  long long before = 0, total = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += sums_s[w];
-    total += sums_s[w];
-  }
-  const long long G = min((long long)gridDim.x, total);
-  const bool working = blockIdx.x < G;
-  const long long lo = working ? total * blockIdx.x / G : 0, hi = working ? total * (blockIdx.x + 1) / G : 0;
-  if (working && before + in - mine <= lo && lo < before + in) {
-    long long at = before + in - mine;
-    for (int b = b0; b < b1; ++b) {
-      const int u = request_of(p, b).units;
-      if (lo < at + u) {
-        start_s[0] = b;
-        start_s[1] = (int)(lo - at);
-        break;
-      }
-      at += u;
-    }
-  }
+  const Share share = share_units(p, kTile, sums_s, start_s);
   if (tid == 0) p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_s;
 
-  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    if (mbar_try_wait(bar, parity)) return true;
-    const long long t0 = sm_cycles();
-    for (;;) {
-      if (mbar_try_wait_sleep(bar, parity)) return true;
-      if (*abort_s) return false;
-      if (sm_cycles() - t0 > kWaitCycles) {
-        set_device_error(p.err, DSPARK_ERR_TIMEOUT);
-        *abort_s = 1;
-        return false;
-      }
-    }
-  };
+  const Waits wait{abort_s, p.err};
 
   Pieces pc;
-  if (working) pc.start(p, start_s[0], start_s[1], hi - lo);
-  else pc.left = 0;
+  pc.left = 0;
+  if (share.hi > share.lo) pc.start(p, kTile, start_s[0], start_s[1], share.hi - share.lo);
 
   if (warp == kProducerWarp) {
-    // ------------------------------------------------------------------- copies
-    const int shift = p.slots.page_shift, page = 1 << shift;
-    const int box = min(page, kTile), per_tile = kTile / box;     // lines of a copy, copies of a tile
-    const int my_page = lane / S::kHalves, my_half = lane % S::kHalves;
-    uint32_t item = 0;
+    TileCopies<S> copies{smem + S::kOffKV, kv_full, kv_empty, wait, p};
     bool ok = true;
-    auto copy = [&](const CUtensorMap* map, int id, int slot0, int head, int end) {
-      const uint32_t st = item % S::kBufs;
-      ok = wait(&kv_empty[st], ((item / S::kBufs) & 1) ^ 1);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return;
-      const int n_pages = min(per_tile, (end - slot0 + box - 1) / box);
-      if (lane == 0) mbar_arrive_expect_tx(&kv_full[st], (uint32_t)(n_pages * box * 128 * S::kHalves));
-      __syncwarp();
-      const int pid = __shfl_sync(0xffffffffu, id, my_page);
-      if (my_page < n_pages)
-        tma_load_4d(smem + S::kOffKV + st * S::kBuf + my_half * S::kHalf + my_page * box * 128, map, &kv_full[st],
-                    my_half * 64, slot0 & (page - 1), head, pid < 0 ? p.slots.n_pages : pid);
-      ++item;
-    };
-    auto pages_of = [&](int b, int slot0, int end) {
-      const int slot = slot0 + lane * box;
-      return lane < per_tile && slot < end ? slot_page(p.slots, b, slot, p.err) : 0;
-    };
     while (ok && pc.next(p)) {
       const int first = pc.tile0 * kTile, end = pc.r.end;
-      int id = pages_of(pc.b, first, end), id_v = 0;
+      int id = copies.pages_of(pc.b, first, end), id_v = 0;
       for (int j = 0; j < pc.n_tiles && ok; ++j) {
         const int slot0 = first + j * kTile;
-        const int id_next = j + 1 < pc.n_tiles ? pages_of(pc.b, slot0 + kTile, end) : 0;
-        copy(&k_map, id, slot0, pc.head, end);
-        if (ok && j > 0) copy(&v_map, id_v, slot0 - kTile, pc.head, end);
+        const int id_next = j + 1 < pc.n_tiles ? copies.pages_of(pc.b, slot0 + kTile, end) : 0;
+        ok = copies.copy(&k_map, id, slot0, pc.head, end);
+        if (ok && j > 0) ok = copies.copy(&v_map, id_v, slot0 - kTile, pc.head, end);
         id_v = id;
         id = id_next;
       }
-      if (ok) copy(&v_map, id_v, first + (pc.n_tiles - 1) * kTile, pc.head, end);
+      if (ok) ok = copies.copy(&v_map, id_v, first + (pc.n_tiles - 1) * kTile, pc.head, end);
     }
-    // every issued copy lands before the CTA may exit
-    for (uint32_t i = item > (uint32_t)S::kBufs ? item - S::kBufs : 0; i < item; ++i)
-      mbar_wait(&kv_full[i % S::kBufs], (i / S::kBufs) & 1);
+    copies.drain();
   } else if (warp == kIssueWarp) {
     // ----------------------------------------------------------------- products
     if (lane == 0) {
@@ -408,40 +489,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         const bool masked = slot0 + kTile > rq.len;
         ok = wait(&s_full[buf], (t >> 1) & 1);
         if (masked && ok) {
-          // slots behind the last hold anything, and a drafted token that some rows do not see
-          // may hold values that are not finite: 0 x NaN must not reach them.  Thread r clears
-          // line r of the value tile, or its values that are not finite (added again at the end).
+          // thread r looks after line r of the value tile
           const uint32_t it = base + v_item(j, n), st = it % S::kBufs;
           ok = wait(&kv_full[st], (it / S::kBufs) & 1);
           const int slot = slot0 + r;
-          if (ok && slot >= rq.len) {
-            uint8_t* line = smem + S::kOffKV + st * S::kBuf + r * 128;
-            bool bad = false;
-#pragma unroll 4
-            for (int c = 0; c < D / 8; ++c) {
-              uint4* at = reinterpret_cast<uint4*>(line + c / 8 * S::kHalf + ((c ^ r) & 7) * 16);
-              if (slot >= rq.end) {
-                *at = make_uint4(0, 0, 0, 0);
-              } else {
-                uint4 x = *at;
-                float f[8];
-                unpack_chunk<T>(x, f);
-                bool any = false;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const bool finite = f[e] - f[e] == 0.f;
-                  any = any || !finite;
-                  f[e] = finite ? f[e] : 0.f;
-                }
-                if (any) {
-                  *at = pack_chunk<T>(f);
-                  bad = true;
-                }
-              }
-            }
-            if (bad) bad_s[piece & 1] = (int)piece + 1;
-            fence_proxy_async_smem();
-          }
+          if (ok && slot >= rq.len &&
+              clear_line<T, D>(smem + S::kOffKV + st * S::kBuf + r * 128, S::kHalf, r, slot < rq.end))
+            bad_s[piece & 1] = (int)piece + 1;
         }
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -577,10 +631,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         }
       }
       if (!whole && tile0 == 0 && r == 0) {
-        // the first part of several: the CTA of the last tile says how many
-        const long long g0 = lo + (hi - lo) - n;              // (this is the CTA's last piece)
-        const long long last = ((g0 + rq.tiles) * G - 1) / total;
-        p.joins[blockIdx.x] = make_int4(b, block, head, (int)(last - blockIdx.x) + 1);
+        // the first part of several, and so the last piece of this CTA
+        p.joins[blockIdx.x] = make_int4(b, block, head, parts_of(share, share.hi - n, rq.tiles));
       }
       tc_fence_before_sync();
       base += 2 * n;
@@ -595,17 +647,492 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   }
 }
 
+// ------------------------------------------------------------------- up to 64 rows a head
+// The same with slots and rows exchanged: S^T = K Q^T has the 128 slots on the lanes and the rows
+// as columns, so that all four softmax warps are busy however few rows there are (one token of
+// a group of four has 4 rows: 16 columns a thread instead of 128) and the products cost by the
+// row.  P^T goes to shared memory, and O^T += V^T P^T.  A column's maximum lies across the warps: at
+// each tile they agree that no score exceeds its reference by more than 2^8; where one does, and
+// at a piece's first tile, they exchange maxima and rescale.  Each thread sums its own slots'
+// probabilities; the sums meet at the piece's end.
+//
+// Two more warps bring each piece's queries and what its rows see, a piece ahead, so that products
+// run on from piece to piece: S^T of the next piece's first tile forms before the last O^T.
+template <int D>
+struct NarrowSmem {
+  static constexpr int kRows = 64;
+  static constexpr int kBuf = kTile * D * 2;                 // bytes of a K or V tile
+  static constexpr int kHalves = D / 64;
+  static constexpr int kHalf = kTile * 128;
+  static constexpr int kQ = kRows * D * 2, kQHalf = kRows * 128, kP = kTile * 128;
+  static constexpr int kOffQ = 0, kOffP = 2 * kQ, kOffSmall = kOffP + 2 * kP;
+  static constexpr int kOffKV = kOffSmall + 7168;
+  static constexpr int kBufs = (232448 - kOffKV) / kBuf;
+  static constexpr int kBytes = kOffKV + kBufs * kBuf;
+  static_assert(kOffKV % 1024 == 0 && kBufs >= 4, "layout");
+};
+
+struct PieceInfo {           // what the loading warps say of a piece
+  int b, head, block, tile0, n_tiles, tiles, row0, n, len, end, rows;
+};
+
+// Position in the ring of the K or V tile t of a CTA's T: K_0, K_1, V_0, K_2, V_1, ..
+__device__ __forceinline__ uint32_t k_place(uint32_t t) { return t ? 2 * t - 1 : 0; }
+__device__ __forceinline__ uint32_t v_place(uint32_t t, uint32_t T) { return t + 1 < T ? 2 * t + 2 : 2 * T - 1; }
+
+// Sums (or maxima) over a warp's lanes of 16 columns: each exchange halves the columns that a
+// lane looks after; lanes 2 c and 2 c + 1 are left with column c's.
+template <bool Max>
+__device__ __forceinline__ float over_lanes(float (&v)[16], int lane) {
+  auto join = [](float a, float b) { return Max ? fmaxf(a, b) : a + b; };
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float got = __shfl_xor_sync(0xffffffffu, lane & 16 ? v[e] : v[e + 8], 16);
+    v[e] = join(lane & 16 ? v[e + 8] : v[e], got);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float got = __shfl_xor_sync(0xffffffffu, lane & 8 ? v[e] : v[e + 4], 8);
+    v[e] = join(lane & 8 ? v[e + 4] : v[e], got);
+  }
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const float got = __shfl_xor_sync(0xffffffffu, lane & 4 ? v[e] : v[e + 2], 4);
+    v[e] = join(lane & 4 ? v[e + 2] : v[e], got);
+  }
+  const float got = __shfl_xor_sync(0xffffffffu, lane & 2 ? v[0] : v[1], 2);
+  const float one = join(lane & 2 ? v[1] : v[0], got);
+  return join(one, __shfl_xor_sync(0xffffffffu, one, 1));
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid_constant__ CUtensorMap k_map,
+                                                                    const __grid_constant__ CUtensorMap v_map,
+                                                                    const __grid_constant__ AttendParams p) {
+  using S = NarrowSmem<D>;
+  constexpr bool kBf16 = __is_same(T, __nv_bfloat16);
+  constexpr int kRows = S::kRows, kChunks = kRows / 16, kLoadWarp = 2;
+  constexpr uint32_t kColO = 2 * kRows;                       // S 0 and 1 at columns 0 and 64
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* small = smem + S::kOffSmall;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(small);
+  uint64_t *kv_full = bars, *kv_empty = bars + S::kBufs, *s_full = bars + 2 * S::kBufs, *p_full = s_full + 2,
+           *o_full = s_full + 4, *q_full = s_full + 6, *q_free = s_full + 8, *drain = s_full + 10;
+  int* words = reinterpret_cast<int*>(small + 512);
+  volatile int* abort_s = words;
+  uint32_t* tmem_s = reinterpret_cast<uint32_t*>(words + 1);
+  volatile int* bad_s = words + 2;                           // by piece parity: piece + 1 with values not finite
+  int* start_s = words + 4;
+  volatile int* open_s = words + 6;                          // tile + 1 that left a column without a reference
+  volatile int* high_s = words + 8;                          // by tile mod 4: a score is far above its reference
+  long long* sums_s = reinterpret_cast<long long*>(small + 576);
+  PieceInfo* info_s = reinterpret_cast<PieceInfo*>(small + 640);                      // [2] by piece parity
+  int* parents_s = reinterpret_cast<int*>(small + 768);                               // [2 warps][64]
+  unsigned long long* sees_s = reinterpret_cast<unsigned long long*>(small + 1280);   // [2][64] by piece parity
+  long long* to_s = reinterpret_cast<long long*>(small + 2304);                       // [2][64]: a row's place in out
+  float* best_s = reinterpret_cast<float*>(small + 3328);    // [64]: a column's reference (log2), -inf: none yet
+  float* ref_s = best_s + 64;                                // [64]: the same, 0: none yet
+  float* scale_s = best_s + 128;                             // [64]: what O and l are multiplied by
+  float* inv_s = best_s + 192;                               // [64]: 1 / l
+  float* max_s = best_s + 256;                               // [4 warps][64]
+  float* sum_s = best_s + 512;                               // [4 warps][64], to byte 3328 + 3072
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (smem_u32(smem) & 1023u) {            // the swizzle needs it; the same for every thread
+    set_device_error(p.err, DSPARK_ERR_DEVICE_CHECK);
+    return;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < S::kBufs; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], kTile);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&q_full[i], kRows);
+      mbar_init(&q_free[i], kTile);
+      bad_s[i] = 0;
+    }
+    mbar_init(drain, 1);
+    *abort_s = 0;
+    *open_s = 0;
+    for (int i = 0; i < 4; ++i) high_s[i] = 0;
+    fence_mbar_init();
+  }
+  if (warp == kIssueWarp) {
+    tmem_alloc(tmem_s, 256);
+    tmem_relinquish();
+  }
+  if (warp == kProducerWarp && lane == 0) {
+    prefetch_tensormap(&k_map);
+    prefetch_tensormap(&v_map);
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  const Share share = share_units(p, kRows, sums_s, start_s);
+  if (tid == 0) p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_s;
+  const Waits wait{abort_s, p.err};
+  const uint32_t T_all = (uint32_t)(share.hi - share.lo);     // this CTA's tiles
+
+  if (warp == kProducerWarp) {
+    // ------------------------------------------------------------------- copies
+    Pieces pc;
+    pc.left = 0;
+    if (T_all) pc.start(p, kRows, start_s[0], start_s[1], T_all);
+    TileCopies<S> copies{smem + S::kOffKV, kv_full, kv_empty, wait, p};
+    bool ok = true, first = true;
+    int v_id = 0, v_slot0 = 0, v_head = 0, v_end = 0;         // the V tile that is still to come
+    while (ok && pc.next(p)) {
+      const int end = pc.r.end;
+      int slot0 = pc.tile0 * kTile, id = copies.pages_of(pc.b, slot0, end);
+      for (int j = 0; j < pc.n_tiles && ok; ++j, slot0 += kTile) {
+        const int id_next = j + 1 < pc.n_tiles ? copies.pages_of(pc.b, slot0 + kTile, end) : 0;
+        ok = copies.copy(&k_map, id, slot0, pc.head, end);
+        if (ok && !first) ok = copies.copy(&v_map, v_id, v_slot0, v_head, v_end);
+        first = false;
+        v_id = id;
+        v_slot0 = slot0;
+        v_head = pc.head;
+        v_end = end;
+        id = id_next;
+      }
+    }
+    if (ok && !first) copies.copy(&v_map, v_id, v_slot0, v_head, v_end);
+    copies.drain();
+  } else if (warp == kIssueWarp) {
+    // ----------------------------------------------------------------- products
+    if (lane == 0) {
+      const uint64_t q_desc = smem_desc(smem_u32(smem + S::kOffQ), 16u, 1024u, kSwizzle128B);
+      const uint64_t k_desc = smem_desc(smem_u32(smem + S::kOffKV), 16u, 1024u, kSwizzle128B);
+      // (head_dim 64: rows 64 to 127 of V^T are rows 0 to 63 again)
+      const uint64_t v_desc =
+          smem_desc(smem_u32(smem + S::kOffKV), D == 128 ? (uint32_t)S::kHalf : 0u, 1024u, kSwizzle128B);
+      const uint64_t p_desc = smem_desc(smem_u32(smem + S::kOffP), (uint32_t)S::kP, 1024u, kSwizzle128B);
+      bool ok = true;
+      auto values = [&](uint32_t t, int columns, bool fresh) {   // O^T += V^T P^T of tile t
+        const uint32_t buf = t & 1, it = v_place(t, T_all), st = it % S::kBufs;
+        const uint32_t id_p = idesc_16(kBf16, columns, 1) | (1u << 15);     // both operands along their rows
+        if (!(ok = wait(&p_full[buf], (t >> 1) & 1))) return;
+        if (!(ok = wait(&kv_full[st], (it / S::kBufs) & 1))) return;
+        tc_fence_after_sync();
+        const uint64_t d = v_desc + (uint64_t)(st * (S::kBuf >> 4)), b = p_desc + (uint64_t)(buf * (S::kP >> 4));
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          umma_bf16_f32(tmem + kColO, d + (uint64_t)(k * (2048 >> 4)), b + (uint64_t)(k * (2048 >> 4)), id_p,
+                        !fresh || k > 0 ? 1u : 0u);
+        umma_commit(&kv_empty[st]);
+        umma_commit(&o_full[buf]);
+      };
+      int columns_before = 0;
+      bool fresh = false;                      // whether the tile before was its piece's first
+      uint32_t t = 0;
+      for (uint32_t piece = 0; ok && t < T_all; ++piece) {
+        const uint32_t q = piece & 1;
+        if (!(ok = wait(&q_full[q], (piece >> 1) & 1))) break;
+        const int n = info_s[q].n_tiles, columns = (info_s[q].rows + 15) & ~15;
+        const uint32_t id_s = idesc_16(kBf16, columns, 0);
+        for (int j = 0; j < n && ok; ++j, ++t) {
+          const uint32_t it = k_place(t), st = it % S::kBufs;
+          if (!(ok = wait(&kv_full[st], (it / S::kBufs) & 1))) break;
+          tc_fence_after_sync();
+          const uint64_t d = k_desc + (uint64_t)(st * (S::kBuf >> 4)), b = q_desc + (uint64_t)(q * (S::kQ >> 4));
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            umma_bf16_f32(tmem + kRows * (t & 1), d + (uint64_t)((k / 4 * S::kHalf + k % 4 * 32) >> 4),
+                          b + (uint64_t)((k / 4 * S::kQHalf + k % 4 * 32) >> 4), id_s, k > 0 ? 1u : 0u);
+          umma_commit(&kv_empty[st]);
+          umma_commit(&s_full[t & 1]);
+          if (t > 0) values(t - 1, columns_before, fresh);
+          columns_before = columns;
+          fresh = j == 0;
+        }
+      }
+      if (ok && t > 0) values(t - 1, columns_before, fresh);
+      umma_commit(drain);
+      mbar_wait(drain, 0);
+    }
+    __syncwarp();
+  } else if (warp < kSoftmaxWarp) {
+    // ------------------------------------------------------------------ queries, a thread a row
+    const int col = tid - 32 * kLoadWarp;
+    int* par = parents_s + 64 * (warp - kLoadWarp);
+    Pieces pc;
+    pc.left = 0;
+    if (T_all) pc.start(p, kRows, start_s[0], start_s[1], T_all);
+    for (uint32_t piece = 0; pc.next(p); ++piece) {
+      const uint32_t q = piece & 1;
+      const int rows = pc.rows(p);
+      const int i_r = pc.block * kRows + col, i = i_r / p.group, head = pc.head * p.group + (i_r - i * p.group);
+      const bool live = col < rows;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q.p) +
+                                                        (long long)(pc.r.row0 + i) * p.q.row + head * p.q.head);
+      uint4 x[D / 8];
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) x[c] = live ? src[c] : make_uint4(0, 0, 0, 0);
+      unsigned long long sees = 0;
+      if (p.rows.parents) {
+        __syncwarp();
+        for (int a = lane; a < pc.r.n; a += 32) par[a] = parent_of(p.rows.parents, pc.r.row0 + a, a, p.err);
+        __syncwarp();
+        if (live)
+          for (int a = i; a >= 0; a = par[a]) sees |= 1ull << a;
+      } else if (live) {
+        sees = (2ull << i) - 1;                // (i = 63: all)
+      }
+      // the piece before the last has ended
+      if (!__all_sync(0xffffffffu, wait(&q_free[q], ((piece >> 1) & 1) ^ 1))) break;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c)
+        *reinterpret_cast<uint4*>(smem + S::kOffQ + q * S::kQ + c / 8 * S::kQHalf + col * 128 + ((c ^ col) & 7) * 16) = x[c];
+      sees_s[64 * q + col] = sees;
+      to_s[64 * q + col] = (long long)(pc.r.row0 + i) * p.out_row + head * p.out_head;
+      if (col == 0)
+        info_s[q] = {pc.b, pc.head, pc.block, pc.tile0, pc.n_tiles, pc.r.tiles, pc.r.row0, pc.r.n, pc.r.len, pc.r.end, rows};
+      fence_proxy_async_smem();
+      mbar_arrive(&q_full[q]);
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax
+    // These warps meet at a hardware barrier, so all of them run through all tiles: a wait that
+    // ran out ends the others' waits, and what they then compute is not written.
+    const int w4 = warp - kSoftmaxWarp, r = w4 * 32 + lane;     // slot of a tile; at the end, element of a head
+    const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
+    const float sl = p.scale_log2;
+    bool ok = true;
+    auto meet = []() { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+    uint32_t t = 0;
+    for (uint32_t piece = 0; t < T_all; ++piece) {
+      const uint32_t q = piece & 1;
+      ok = wait(&q_full[q], (piece >> 1) & 1) && ok;
+      const PieceInfo rq = info_s[q];
+      // (after a wait that ran out: whatever is there, but the same number of tiles for all)
+      const int rows = rq.rows, chunks = (rows + 15) / 16;
+      const int n = min(max(rq.n_tiles, 1), (int)(T_all - t)), tile0 = rq.tile0;
+      bool open = true;                        // a column has no reference yet
+      float l[kRows];                          // this thread's slots' part of the columns' sums
+#pragma unroll
+      for (int e = 0; e < kRows; ++e) l[e] = 0.f;
+      for (int j = 0; j < n; ++j, ++t) {
+        const uint32_t buf = t & 1;
+        const int slot0 = (tile0 + j) * kTile, slot = slot0 + r;
+        const bool masked = slot0 + kTile > rq.len;
+        ok = wait(&s_full[buf], (t >> 1) & 1) && ok;
+        if (masked) {
+          const uint32_t it = v_place(t, T_all), st = it % S::kBufs;
+          ok = wait(&kv_full[st], (it / S::kBufs) & 1) && ok;
+          if (ok && slot >= rq.len &&
+              clear_line<T, D>(smem + S::kOffKV + st * S::kBuf + r * 128, S::kHalf, r, slot < rq.end))
+            bad_s[q] = (int)piece + 1;
+        }
+        __syncwarp();
+        tc_fence_after_sync();
+        float x[kRows];
+        // the slot's scores (times scale and log2 e), less the references or as they are
+        auto scores = [&](bool less) {
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            if (c >= chunks) break;
+            uint32_t v[16];
+            tmem_ld_32x32b_sync<16>(tmem + lanes + kRows * buf + 16 * c, v);
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              float4 ref = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (less) ref = *reinterpret_cast<const float4*>(ref_s + 16 * c + e);
+              x[16 * c + e] = fmaf(__uint_as_float(v[e]), sl, -ref.x);
+              x[16 * c + e + 1] = fmaf(__uint_as_float(v[e + 1]), sl, -ref.y);
+              x[16 * c + e + 2] = fmaf(__uint_as_float(v[e + 2]), sl, -ref.z);
+              x[16 * c + e + 3] = fmaf(__uint_as_float(v[e + 3]), sl, -ref.w);
+            }
+            if (masked && slot >= rq.len) {
+              const int a = slot - rq.len;
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                x[16 * c + e] = a < 64 && (sees_s[64 * q + 16 * c + e] >> a) & 1 ? x[16 * c + e] : -INFINITY;
+            }
+          }
+        };
+        bool raise = open;
+        if (!open) {
+          scores(true);
+          float mx = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            if (c >= chunks) break;
+            float part[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) part[e] = x[16 * c + e];
+            mx = fmaxf(mx, max_of(part));
+          }
+          if (mx > kRaise) high_s[t & 3] = 1;
+        }
+        // (a tile's word is cleared two tiles later, two before it is used again; each tile has a
+        // meeting between)
+        if (r == 0) high_s[(t + 2) & 3] = 0;
+        meet();
+        raise = raise || high_s[t & 3] != 0;
+        if (raise) {
+          // ---- new references from the columns' maxima over the warps
+          scores(false);
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            if (c >= chunks) break;
+            float part[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) part[e] = x[16 * c + e];
+            const float m = over_lanes<true>(part, lane);
+            if (!(lane & 1)) max_s[64 * w4 + 16 * c + (lane >> 1)] = m;
+          }
+          meet();
+          if (r < kRows) {
+            const float mx = fmaxf(fmaxf(max_s[r], max_s[64 + r]), fmaxf(max_s[128 + r], max_s[192 + r]));
+            const float old = j > 0 ? best_s[r] : -INFINITY;
+            const bool up = mx - old > kRaise || old == -INFINITY;
+            const float now = up ? mx : old;
+            scale_s[r] = old == -INFINITY ? 0.f : up ? ex2_approx(old - now) : 1.f;
+            best_s[r] = now;
+            ref_s[r] = now == -INFINITY ? 0.f : now;
+            if (now == -INFINITY && r < rows) *open_s = (int)t + 1;
+          }
+          meet();
+          open = *open_s == (int)t + 1;
+          if (j > 0) {
+            // O and l of the tiles before, complete, on the new scale
+            ok = wait(&o_full[buf ^ 1], ((t - 1) >> 1) & 1) && ok;
+            __syncwarp();
+            tc_fence_after_sync();
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+              if (c >= chunks) break;
+              uint32_t v[16];
+              tmem_ld_32x32b_sync<16>(tmem + lanes + kColO + 16 * c, v);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                v[e] = __float_as_uint(__uint_as_float(v[e]) * scale_s[16 * c + e]);
+                l[16 * c + e] *= scale_s[16 * c + e];
+              }
+              tmem_st_32x32b_x16(tmem + lanes + kColO + 16 * c, v);
+            }
+            tmem_st_wait();
+          }
+          scores(true);
+        }
+        uint8_t* line = smem + S::kOffP + buf * S::kP + r * 128;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          if (c >= chunks) break;
+          uint32_t y[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float a = ex2_approx(x[16 * c + 2 * e]), d = ex2_approx(x[16 * c + 2 * e + 1]);
+            l[16 * c + 2 * e] += a;
+            l[16 * c + 2 * e + 1] += d;
+            y[e] = pack2<T>(a, d);
+          }
+          *reinterpret_cast<uint4*>(line + ((2 * c ^ r) & 7) * 16) = make_uint4(y[0], y[1], y[2], y[3]);
+          *reinterpret_cast<uint4*>(line + (((2 * c + 1) ^ r) & 7) * 16) = make_uint4(y[4], y[5], y[6], y[7]);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before_sync();
+        mbar_arrive(&p_full[buf]);
+      }
+      // ---- the piece's rows: sums over the warps, then O
+      const bool whole = n == rq.tiles;
+      float* part = p.partial + (long long)(2 * blockIdx.x + (tile0 == 0 ? 1 : 0)) * kTile * (D + 2);
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        if (c >= chunks) break;
+        float v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = l[16 * c + e];
+        const float s = over_lanes<false>(v, lane);
+        if (!(lane & 1)) sum_s[64 * w4 + 16 * c + (lane >> 1)] = s;
+      }
+      meet();
+      ok = ok && !*abort_s;
+      if (r < rows && r < kRows) {
+        const float s = (sum_s[r] + sum_s[64 + r]) + (sum_s[128 + r] + sum_s[192 + r]);
+        inv_s[r] = !whole ? 1.f : s > 0.f ? 1.f / s : s == 0.f ? 0.f : s;        // (NaN stays)
+        if (!whole && ok) {
+          part[r * (D + 2) + D] = best_s[r];
+          part[r * (D + 2) + D + 1] = s;
+        } else if (p.lse && ok) {
+          const int i_r = rq.block * kRows + r, i = i_r / p.group;
+          p.lse[(long long)(rq.row0 + i) * p.group * p.cs.heads + rq.head * p.group + (i_r - i * p.group)] =
+              s == 0.f ? -INFINITY : (best_s[r] + log2f(s)) * 0.6931471805599453f;
+        }
+      }
+      meet();
+      ok = wait(&o_full[(t - 1) & 1], ((t - 1) >> 1) & 1) && ok;
+      __syncwarp();
+      tc_fence_after_sync();
+      const bool bad = bad_s[q] == (int)piece + 1;
+#pragma unroll 1
+      for (int c = 0; c < chunks; ++c) {
+        uint32_t vo[16];
+        tmem_ld_32x32b_sync<16>(tmem + lanes + kColO + 16 * c, vo);
+        float o[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(vo[e]);
+        if (r >= D || !ok) continue;
+        if (bad) {
+          // the values that were left out, where a row sees their token
+          for (int a = 0; a < rq.n; ++a) {
+            const int at = rq.len + a;
+            if (at < tile0 * kTile || at >= (tile0 + n) * kTile) continue;
+            const int page = slot_page(p.slots, rq.b, at, p.err);
+            if (page < 0) continue;
+            const float f = elem_to_float(static_cast<const T*>(p.v)[page * p.cs.page + (at & ((1 << p.slots.page_shift) - 1)) * p.cs.slot +
+                                                                    rq.head * p.cs.head + r]);
+            if (f - f == 0.f) continue;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if ((sees_s[64 * q + 16 * c + e] >> a) & 1) o[e] += f;
+          }
+        }
+        const int left = rows - 16 * c;
+        if (whole) {
+          T* out = reinterpret_cast<T*>(p.out) + r;
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (e < left) out[to_s[64 * q + 16 * c + e]] = elem_from_float<T>(o[e] * inv_s[16 * c + e]);
+        } else {
+          float* to = part + 16 * c * (D + 2) + r;
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (e < left) to[e * (D + 2)] = o[e];
+        }
+      }
+      if (!whole && tile0 == 0 && r == 0 && ok)
+        // the first part of several, and so the last piece of this CTA
+        p.joins[blockIdx.x] = make_int4(rq.b, rq.block, rq.head, parts_of(share, share.hi - n, rq.tiles));
+      tc_fence_before_sync();
+      mbar_arrive(&q_free[q]);
+    }
+  }
+  __syncthreads();
+  if (warp == kIssueWarp) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 256);
+  }
+}
+
 // Joins the parts of a (request, row block, head) that several CTAs share: CTA (c, y) those of
 // the piece that CTA c began and left unfinished, 8 rows from 8 y on, a warp a row.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttendParams p) {
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttendParams p, int block_rows) {
   pdl_wait();
   pdl_launch_dependents();
   const int c = blockIdx.x, lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
   const int4 join = p.joins[c];
   if (join.w < 2) return;
   const RequestRows rows = request_rows(p.rows, join.x, nullptr);
-  const int i_r = join.y * kTile + r, i = i_r / p.group;
+  const int i_r = join.y * block_rows + r, i = i_r / p.group;
   if (i >= rows.n) return;
   auto part = [&](int k) {
     return p.partial + ((long long)(2 * (c + k) + (k == 0 ? 1 : 0)) * kTile + r) * (D + 2);
@@ -674,19 +1201,27 @@ template <typename T, int D>
 cudaError_t attend_for(AttendParams p, const TargetSlots& slots, bool bf16, cudaStream_t stream) {
   static std::atomic<int> cache[kMaxCachedDevices];
   int grid = per_device_grid(cache, []() {
-    return cudaFuncSetAttribute(attend_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                AttendSmem<D>::kBytes) == cudaSuccess ? 1 : -1;
+    return cudaFuncSetAttribute(attend_wide_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                AttendSmem<D>::kBytes) == cudaSuccess &&
+                   cudaFuncSetAttribute(attend_narrow_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        NarrowSmem<D>::kBytes) == cudaSuccess
+               ? 1 : -1;
   });
   if (grid <= 0) return cudaErrorInvalidConfiguration;
   if (grid > kMaxGrid) grid = kMaxGrid;
   CUtensorMap k_map, v_map;
   if (!encode_cache_map(&k_map, p.k, bf16, p.cs, slots) || !encode_cache_map(&v_map, p.v, bf16, p.cs, slots))
     return cudaErrorInvalidValue;
-  cudaError_t e = launch_pdl(attend_kernel<T, D>, dim3(grid), dim3(kThreads), AttendSmem<D>::kBytes, stream, k_map,
-                             v_map, p);
+  const int rows = p.rows.N * p.group;
+  const bool narrow = rows <= NarrowSmem<D>::kRows;
+  const cudaError_t e =
+      narrow ? launch_pdl(attend_narrow_kernel<T, D>, dim3(grid), dim3(kThreads), NarrowSmem<D>::kBytes, stream, k_map,
+                          v_map, p)
+             : launch_pdl(attend_wide_kernel<T, D>, dim3(grid), dim3(kThreads), AttendSmem<D>::kBytes, stream, k_map,
+                          v_map, p);
   if (e != cudaSuccess) return e;
-  const int rows = p.rows.N * p.group < kTile ? p.rows.N * p.group : kTile;
-  return launch_pdl(join_kernel<T, D>, dim3(grid, cdiv(rows, 8)), dim3(256), 0, stream, p);
+  return launch_pdl(join_kernel<T, D>, dim3(grid, cdiv(rows < kTile ? rows : kTile, 8)), dim3(256), 0, stream, p,
+                    narrow ? NarrowSmem<D>::kRows : kTile);
 }
 
 }  // namespace
