@@ -98,6 +98,12 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float a, float b);
 template <>
@@ -807,56 +813,66 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
     copies.drain();
   } else if (warp == kIssueWarp) {
     // ----------------------------------------------------------------- products
-    if (lane == 0) {
-      const uint64_t q_desc = smem_desc(smem_u32(smem + S::kOffQ), 16u, 1024u, kSwizzle128B);
-      const uint64_t k_desc = smem_desc(smem_u32(smem + S::kOffKV), 16u, 1024u, kSwizzle128B);
-      // (head_dim 64: rows 64 to 127 of V^T are rows 0 to 63 again)
-      const uint64_t v_desc =
-          smem_desc(smem_u32(smem + S::kOffKV), D == 128 ? (uint32_t)S::kHalf : 0u, 1024u, kSwizzle128B);
-      const uint64_t p_desc = smem_desc(smem_u32(smem + S::kOffP), (uint32_t)S::kP, 1024u, kSwizzle128B);
-      bool ok = true;
-      auto values = [&](uint32_t t, int columns, bool fresh) {   // O^T += V^T P^T of tile t
-        const uint32_t buf = t & 1, it = v_place(t, T_all), st = it % S::kBufs;
-        const uint32_t id_p = idesc_16(kBf16, columns, 1) | (1u << 15);     // both operands along their rows
-        if (!(ok = wait(&p_full[buf], (t >> 1) & 1))) return;
-        if (!(ok = wait(&kv_full[st], (it / S::kBufs) & 1))) return;
-        tc_fence_after_sync();
-        const uint64_t d = v_desc + (uint64_t)(st * (S::kBuf >> 4)), b = p_desc + (uint64_t)(buf * (S::kP >> 4));
+    // The whole warp runs along and one lane issues, on values that are the same in all lanes by
+    // construction: a lane on its own took 72 cycles an instruction.
+    const uint32_t T = __reduce_max_sync(0xffffffffu, T_all), tm = __reduce_max_sync(0xffffffffu, tmem);
+    const bool one = elect_one();
+    const uint64_t q_desc = smem_desc(smem_u32(smem + S::kOffQ), 16u, 1024u, kSwizzle128B);
+    const uint64_t k_desc = smem_desc(smem_u32(smem + S::kOffKV), 16u, 1024u, kSwizzle128B);
+    // (head_dim 64: rows 64 to 127 of V^T are rows 0 to 63 again)
+    const uint64_t v_desc =
+        smem_desc(smem_u32(smem + S::kOffKV), D == 128 ? (uint32_t)S::kHalf : 0u, 1024u, kSwizzle128B);
+    const uint64_t p_desc = smem_desc(smem_u32(smem + S::kOffP), (uint32_t)S::kP, 1024u, kSwizzle128B);
+    bool ok = true;
+    auto all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+    auto values = [&](uint32_t t, int columns, bool fresh) {   // O^T += V^T P^T of tile t
+      const uint32_t buf = t & 1, it = v_place(t, T), st = it % S::kBufs;
+      const uint32_t id_p = idesc_16(kBf16, columns, 1) | (1u << 15);     // both operands along their rows
+      if (!(ok = all(&p_full[buf], (t >> 1) & 1))) return;
+      if (!(ok = all(&kv_full[st], (it / S::kBufs) & 1))) return;
+      tc_fence_after_sync();
+      const uint64_t d = v_desc + (uint64_t)(st * (S::kBuf >> 4)), b = p_desc + (uint64_t)(buf * (S::kP >> 4));
+      if (one) {
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)
-          umma_bf16_f32(tmem + kColO, d + (uint64_t)(k * (2048 >> 4)), b + (uint64_t)(k * (2048 >> 4)), id_p,
+          umma_bf16_f32(tm + kColO, d + (uint64_t)(k * (2048 >> 4)), b + (uint64_t)(k * (2048 >> 4)), id_p,
                         !fresh || k > 0 ? 1u : 0u);
         umma_commit(&kv_empty[st]);
         umma_commit(&o_full[buf]);
-      };
-      int columns_before = 0;
-      bool fresh = false;                      // whether the tile before was its piece's first
-      uint32_t t = 0;
-      for (uint32_t piece = 0; ok && t < T_all; ++piece) {
-        const uint32_t q = piece & 1;
-        if (!(ok = wait(&q_full[q], (piece >> 1) & 1))) break;
-        const int n = info_s[q].n_tiles, columns = (info_s[q].rows + 15) & ~15;
-        const uint32_t id_s = idesc_16(kBf16, columns, 0);
-        for (int j = 0; j < n && ok; ++j, ++t) {
-          const uint32_t it = k_place(t), st = it % S::kBufs;
-          if (!(ok = wait(&kv_full[st], (it / S::kBufs) & 1))) break;
-          tc_fence_after_sync();
-          const uint64_t d = k_desc + (uint64_t)(st * (S::kBuf >> 4)), b = q_desc + (uint64_t)(q * (S::kQ >> 4));
+      }
+      __syncwarp();
+    };
+    int columns_before = 0;
+    bool fresh = false;                      // whether the tile before was its piece's first
+    uint32_t t = 0;
+    for (uint32_t piece = 0; ok && t < T; ++piece) {
+      const uint32_t q = piece & 1;
+      if (!(ok = all(&q_full[q], (piece >> 1) & 1))) break;
+      const int n = __reduce_max_sync(0xffffffffu, info_s[q].n_tiles);
+      const int columns = (__reduce_max_sync(0xffffffffu, info_s[q].rows) + 15) & ~15;
+      const uint32_t id_s = idesc_16(kBf16, columns, 0);
+      for (int j = 0; j < n && ok; ++j, ++t) {
+        const uint32_t it = k_place(t), st = it % S::kBufs;
+        if (!(ok = all(&kv_full[st], (it / S::kBufs) & 1))) break;
+        tc_fence_after_sync();
+        const uint64_t d = k_desc + (uint64_t)(st * (S::kBuf >> 4)), b = q_desc + (uint64_t)(q * (S::kQ >> 4));
+        if (one) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            umma_bf16_f32(tmem + kRows * (t & 1), d + (uint64_t)((k / 4 * S::kHalf + k % 4 * 32) >> 4),
+            umma_bf16_f32(tm + kRows * (t & 1), d + (uint64_t)((k / 4 * S::kHalf + k % 4 * 32) >> 4),
                           b + (uint64_t)((k / 4 * S::kQHalf + k % 4 * 32) >> 4), id_s, k > 0 ? 1u : 0u);
           umma_commit(&kv_empty[st]);
           umma_commit(&s_full[t & 1]);
-          if (t > 0) values(t - 1, columns_before, fresh);
-          columns_before = columns;
-          fresh = j == 0;
         }
+        __syncwarp();
+        if (t > 0) values(t - 1, columns_before, fresh);
+        columns_before = columns;
+        fresh = j == 0;
       }
-      if (ok && t > 0) values(t - 1, columns_before, fresh);
-      umma_commit(drain);
-      mbar_wait(drain, 0);
     }
+    if (ok && t > 0) values(t - 1, columns_before, fresh);
+    if (one) umma_commit(drain);
+    mbar_wait(drain, 0);
     __syncwarp();
   } else if (warp < kSoftmaxWarp) {
     // ------------------------------------------------------------------ queries, a thread a row
