@@ -703,7 +703,7 @@ dspark_status dspark_tree_attention(const dspark_paged_cache* cache, int layer, 
   if (cs.head_dim != 64 && cs.head_dim != 128) return DSPARK_ERR_UNSUPPORTED;
   // a request's (row block, head, tile) units are counted in 32 bits
   const long long blocks = cdiv((long long)N * (q_heads / cs.heads), 128);
-  if (q_heads > 65536 || (((long long)max_pages << slots.page_shift) / 128 + 1) * blocks * cs.heads >= (1LL << 31))
+  if (q_heads > 65536 || (((long long)max_pages << slots.page_shift) / 128 + 8) * blocks * cs.heads >= (1LL << 31))
     return DSPARK_ERR_UNSUPPORTED;
   if (!aligned(workspace, 256) || workspace_bytes < tree_attention_bytes(B, N, q_heads, cs.heads, cs.head_dim))
     return DSPARK_ERR_INVALID_ARG;

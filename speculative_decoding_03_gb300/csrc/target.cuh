@@ -35,15 +35,17 @@ __device__ __forceinline__ RequestRows request_rows(const TargetRows& t, int b, 
   return r;
 }
 
-// A request's tokens in the cache before the step; -1 (reported) where it and `more` others
+// A request's tokens in the cache before the step; -1 (reported) where they and `more` others
 // do not fit its pages.
-__device__ __forceinline__ int request_length(const TargetSlots& s, int b, int more, int* err) {
-  const int len = s.lengths[b];
+__device__ __forceinline__ int checked_length(const TargetSlots& s, int len, int more, int* err) {
   if (len < 0 || (long long)len + more > (long long)s.max_pages << s.page_shift) {
     set_device_error(err, DSPARK_ERR_DEVICE_CHECK);
     return -1;
   }
   return len;
+}
+__device__ __forceinline__ int request_length(const TargetSlots& s, int b, int more, int* err) {
+  return checked_length(s, s.lengths[b], more, err);
 }
 
 // The page of a slot; -1 (reported) where the table names none of the cache's.

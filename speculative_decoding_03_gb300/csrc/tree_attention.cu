@@ -38,6 +38,7 @@ constexpr int kTile = 128;                 // slots of a tile, and rows of a blo
 constexpr int kThreads = 256;
 constexpr int kProducerWarp = 0, kIssueWarp = 1, kSoftmaxWarp = 4;
 constexpr float kRaise = 8.f;              // log2 of what the maximum may lag behind
+constexpr int kPieceUnits = 3;             // what beginning and ending a piece costs, in tiles
 
 struct AttendParams {
   HeadRows q;
@@ -118,21 +119,22 @@ __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
 }
 
 // A request as the kernel sees it: rows, tokens before them, slots in all and 128-slot tiles
-// (0: nothing to do).
+// (0: nothing to do).  Its units are, for each (row block, head), kPieceUnits and its tiles.
 struct Request {
   int row0, n, len, end, tiles, blocks, units;
 };
 __device__ __forceinline__ Request request_of(const AttendParams& p, int b, int block_rows) {
   Request r;
+  const int length = p.slots.lengths[b];
   const RequestRows rows = request_rows(p.rows, b, p.err);
   r.row0 = rows.row0;
   r.n = rows.n;
-  r.len = r.n ? request_length(p.slots, b, r.n, p.err) : 0;
+  r.len = r.n ? checked_length(p.slots, length, r.n, p.err) : 0;
   if (r.len < 0) r.n = 0;
   r.end = r.len + r.n;
   r.tiles = r.n ? (r.end + kTile - 1) / kTile : 0;
   r.blocks = r.n ? (r.n * p.group + block_rows - 1) / block_rows : 0;
-  r.units = r.tiles * r.blocks * p.cs.heads;
+  r.units = (r.tiles + kPieceUnits) * r.blocks * p.cs.heads;
   return r;
 }
 
@@ -152,21 +154,23 @@ struct Pieces {
     if (left > 0) r = request_of(p, b, block_rows);
   }
   __device__ __forceinline__ bool next(const AttendParams& p) {
-    if (left <= 0) return false;
-    while (off >= r.units) {
-      r = request_of(p, ++b, block_rows);
-      off = 0;
+    while (left > 0) {
+      while (off >= r.units) {
+        r = request_of(p, ++b, block_rows);
+        off = 0;
+      }
+      const int span = r.tiles + kPieceUnits, at = off / span, from = off - at * span;
+      const int take = left < span - from ? (int)left : span - from;
+      block = at / p.cs.heads;
+      head = at - block * p.cs.heads;
+      tile0 = max(from - kPieceUnits, 0);
+      n_tiles = from + take - kPieceUnits - tile0;
+      whole = n_tiles == r.tiles;
+      off += take;
+      left -= take;
+      if (n_tiles > 0) return true;
     }
-    const int at = off / r.tiles;
-    block = at / p.cs.heads;
-    head = at - block * p.cs.heads;
-    tile0 = off - at * r.tiles;
-    n_tiles = r.tiles - tile0;
-    if (n_tiles > left) n_tiles = (int)left;
-    whole = n_tiles == r.tiles;
-    off += n_tiles;
-    left -= n_tiles;
-    return true;
+    return false;
   }
   __device__ __forceinline__ int rows(const AttendParams& p) const {
     return min(block_rows, r.n * p.group - block * block_rows);
@@ -204,7 +208,7 @@ __device__ __forceinline__ Share share_units(const AttendParams& p, int block_ro
     if (before + in - mine <= s.lo && s.lo < before + in) {
       long long at = before + in - mine;
       for (int b = b0; b < b1; ++b) {
-        const int u = request_of(p, b, block_rows).units;
+        const int u = each == 1 ? (int)mine : request_of(p, b, block_rows).units;
         if (s.lo < at + u) {
           start_s[0] = b;
           start_s[1] = (int)(s.lo - at);
@@ -217,7 +221,7 @@ __device__ __forceinline__ Share share_units(const AttendParams& p, int block_ro
   return s;
 }
 
-// CTAs that share the `tiles` units from g0 on, the first of which is this one's.
+// CTAs that share the `tiles` tiles whose units start at g0, the first of which is this one's.
 __device__ __forceinline__ int parts_of(const Share& s, long long g0, int tiles) {
   return (int)(((g0 + tiles) * s.G - 1) / s.total - blockIdx.x) + 1;
 }
@@ -241,52 +245,82 @@ struct Waits {
   }
 };
 
-// Position in the ring of the K or V tile j of a piece of n tiles: K_0, K_1, V_0, K_2, V_1, ..,
-// V_{n-1}, the order in which the products take them.
-__device__ __forceinline__ int k_item(int j) { return j ? 2 * j - 1 : 0; }
-__device__ __forceinline__ int v_item(int j, int n) { return j < n - 1 ? 2 * j + 2 : 2 * n - 1; }
-
-// The copying warp's side of the ring of S::kBufs buffers: tiles page by page, a lane a copy.
+// The copying warp's side of the ring of S::kBufs buffers: tiles page by page, a lane a copy.  A
+// tile's pages are looked up two tiles ahead, across pieces.
+struct TileAt {
+  int id, slot0, head, end;  // the page of each of its copies (lane: copy); end 0: no tile
+};
 template <typename S>
 struct TileCopies {
   uint8_t* ring;
   uint64_t *full, *empty;
   const Waits& wait;
   const AttendParams& p;
-  uint32_t item = 0;
-  // the page of each of the tile's copies (lane: copy)
-  __device__ __forceinline__ int pages_of(int b, int slot0, int end) const {
+  Pieces pc;
+  int left = 0, slot0 = 0;   // tiles of the piece still to come, and the next one's first slot
+  uint32_t item = 0, skipped = ~0u;
+  __device__ __forceinline__ TileAt fetch() {
+    if (left == 0) {
+      if (!pc.next(p)) return {0, 0, 0, 0};
+      left = pc.n_tiles;
+      slot0 = pc.tile0 * kTile;
+    }
     const int lane = threadIdx.x & 31, box = min(1 << p.slots.page_shift, kTile);
     const int slot = slot0 + lane * box;
-    return lane < kTile / box && slot < end ? slot_page(p.slots, b, slot, p.err) : 0;
+    const TileAt x = {lane < kTile / box && slot < pc.r.end ? slot_page(p.slots, pc.b, slot, p.err) : 0, slot0,
+                      pc.head, pc.r.end};
+    slot0 += kTile;
+    --left;
+    return x;
   }
-  __device__ __forceinline__ bool copy(const CUtensorMap* map, int id, int slot0, int head, int end) {
+  __device__ __forceinline__ bool copy(const CUtensorMap* map, const TileAt& x) {
     const int lane = threadIdx.x & 31, page = 1 << p.slots.page_shift, box = min(page, kTile);
     const int my_page = lane / S::kHalves, my_half = lane % S::kHalves;
     const uint32_t st = item % S::kBufs;
     if (!__all_sync(0xffffffffu, wait(&empty[st], ((item / S::kBufs) & 1) ^ 1))) return false;
-    const int n_pages = min(kTile / box, (end - slot0 + box - 1) / box);
+    const int n_pages = min(kTile / box, (x.end - x.slot0 + box - 1) / box);
     if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(n_pages * box * 128 * S::kHalves));
     __syncwarp();
-    const int pid = __shfl_sync(0xffffffffu, id, my_page);
+    const int pid = __shfl_sync(0xffffffffu, x.id, my_page);
     if (my_page < n_pages)
       tma_load_4d(ring + st * S::kBuf + my_half * S::kHalf + my_page * box * 128, map, &full[st], my_half * 64,
-                  slot0 & (page - 1), head, pid < 0 ? p.slots.n_pages : pid);
+                  x.slot0 & (page - 1), x.head, pid < 0 ? p.slots.n_pages : pid);
     ++item;
     return true;
   }
-  // every issued copy lands before the CTA may exit
-  __device__ __forceinline__ void drain() const {
+  // K_0, K_1, V_0, K_2, V_1, .., a place left out, V_last
+  __device__ __forceinline__ void run(const CUtensorMap* k_map, const CUtensorMap* v_map) {
+    TileAt a = fetch(), b = fetch(), v = {0, 0, 0, 0};
+    bool ok = true;
+    while (ok && a.end) {
+      ok = copy(k_map, a);
+      const TileAt c = fetch();
+      if (ok && v.end) ok = copy(v_map, v);
+      v = a;
+      a = b;
+      b = c;
+    }
+    if (ok && v.end) {
+      skipped = item++;
+      copy(v_map, v);
+    }
+    // every issued copy lands before the CTA may exit
     for (uint32_t i = item > (uint32_t)S::kBufs ? item - S::kBufs : 0; i < item; ++i)
-      mbar_wait(&full[i % S::kBufs], (i / S::kBufs) & 1);
+      if (i != skipped) mbar_wait(&full[i % S::kBufs], (i / S::kBufs) & 1);
   }
 };
+// Places in the ring of a CTA's K or V tile t.
+__device__ __forceinline__ uint32_t k_place(uint32_t t) { return t ? 2 * t - 1 : 0; }
+__device__ __forceinline__ uint32_t v_place(uint32_t t) { return 2 * t + 2; }
 
 // Slots behind the last hold anything, and a drafted token that some rows do not see may hold
 // values that are not finite: 0 x NaN must not reach them.  Clears line r of a value tile, or
 // (in_use) its values that are not finite, which are added again at the end; true if it had any.
 template <typename T, int D>
 __device__ __forceinline__ bool clear_line(uint8_t* line, int half_bytes, int r, bool in_use) {
+  // an exponent of ones, and what carries it (and no other) into the sign's place
+  constexpr uint32_t kOnes = __is_same(T, __nv_bfloat16) ? 0x7f807f80u : 0x7c007c00u;
+  constexpr uint32_t kLow = __is_same(T, __nv_bfloat16) ? 0x00800080u : 0x04000400u;
   bool bad = false;
 #pragma unroll 4
   for (int c = 0; c < D / 8; ++c) {
@@ -295,17 +329,14 @@ __device__ __forceinline__ bool clear_line(uint8_t* line, int half_bytes, int r,
       *at = make_uint4(0, 0, 0, 0);
       continue;
     }
-    float f[8];
-    unpack_chunk<T>(*at, f);
-    bool any = false;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const bool finite = f[e] - f[e] == 0.f;
-      any = any || !finite;
-      f[e] = finite ? f[e] : 0.f;
-    }
-    if (any) {
-      *at = pack_chunk<T>(f);
+    const uint4 v = *at;
+    auto carry = [](uint32_t w) { return ((w & kOnes) + kLow) & 0x80008000u; };
+    if (carry(v.x) | carry(v.y) | carry(v.z) | carry(v.w)) {
+      auto clear = [carry](uint32_t w) {
+        const uint32_t s = carry(w);
+        return w & ~((s & 0x8000u ? 0xffffu : 0u) | (s & 0x80000000u ? 0xffff0000u : 0u));
+      };
+      *at = make_uint4(clear(v.x), clear(v.y), clear(v.z), clear(v.w));
       bad = true;
     }
   }
@@ -378,75 +409,68 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
   if (share.hi > share.lo) pc.start(p, kTile, start_s[0], start_s[1], share.hi - share.lo);
 
   if (warp == kProducerWarp) {
-    TileCopies<S> copies{smem + S::kOffKV, kv_full, kv_empty, wait, p};
-    bool ok = true;
-    while (ok && pc.next(p)) {
-      const int first = pc.tile0 * kTile, end = pc.r.end;
-      int id = copies.pages_of(pc.b, first, end), id_v = 0;
-      for (int j = 0; j < pc.n_tiles && ok; ++j) {
-        const int slot0 = first + j * kTile;
-        const int id_next = j + 1 < pc.n_tiles ? copies.pages_of(pc.b, slot0 + kTile, end) : 0;
-        ok = copies.copy(&k_map, id, slot0, pc.head, end);
-        if (ok && j > 0) ok = copies.copy(&v_map, id_v, slot0 - kTile, pc.head, end);
-        id_v = id;
-        id = id_next;
-      }
-      if (ok) ok = copies.copy(&v_map, id_v, first + (pc.n_tiles - 1) * kTile, pc.head, end);
-    }
-    copies.drain();
+    TileCopies<S> copies{smem + S::kOffKV, kv_full, kv_empty, wait, p, pc};
+    copies.run(&k_map, &v_map);
   } else if (warp == kIssueWarp) {
     // ----------------------------------------------------------------- products
-    if (lane == 0) {
-      constexpr uint32_t id_s = idesc_16(kBf16, kTile, 0), id_o = idesc_16(kBf16, D, 1);
-      const uint64_t q_desc = smem_desc(smem_u32(smem + S::kOffQ), 16u, 1024u, kSwizzle128B);
-      const uint64_t k_desc = smem_desc(smem_u32(smem + S::kOffKV), 16u, 1024u, kSwizzle128B);
-      const uint64_t v_desc = smem_desc(smem_u32(smem + S::kOffKV), (uint32_t)S::kHalf, 1024u, kSwizzle128B);
-      uint32_t base = 0, tc = 0, piece = 0;
-      bool ok = true;
-      // (o_full by tile parity, like S: a waiter tells a phase from its neighbours only, and the
-      // softmax skips most of them; the tile's own S says that the product two before has ended)
-      auto values = [&](int j, int n) {              // O += P V of tile j of the piece's n
-        const uint32_t t = tc + j, buf = t & 1, it = base + v_item(j, n), st = it % S::kBufs;
-        if (!(ok = wait(&p_full[buf], (t >> 1) & 1))) return;
-        if (!(ok = wait(&kv_full[st], (it / S::kBufs) & 1))) return;
-        tc_fence_after_sync();
-        const uint64_t d = v_desc + (uint64_t)(st * (S::kBuf >> 4));
+    // The whole warp runs along and one lane issues, on values that are the same in all lanes by
+    // construction: a lane on its own took 72 cycles an instruction, this 26.
+    constexpr uint32_t id_s = idesc_16(kBf16, kTile, 0), id_o = idesc_16(kBf16, D, 1);
+    const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
+    const bool one = elect_one();
+    const uint64_t q_desc = smem_desc(smem_u32(smem + S::kOffQ), 16u, 1024u, kSwizzle128B);
+    const uint64_t k_desc = smem_desc(smem_u32(smem + S::kOffKV), 16u, 1024u, kSwizzle128B);
+    const uint64_t v_desc = smem_desc(smem_u32(smem + S::kOffKV), (uint32_t)S::kHalf, 1024u, kSwizzle128B);
+    uint32_t t = 0;
+    bool ok = true;
+    auto all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+    // (o_full by tile parity, like S: a waiter tells a phase from its neighbours only, and the
+    // softmax skips most of them; the tile's own S says that the product two before has ended)
+    auto values = [&](uint32_t t, bool fresh) {      // O += P V of tile t
+      const uint32_t buf = t & 1, it = v_place(t), st = it % S::kBufs;
+      if (!(ok = all(&p_full[buf], (t >> 1) & 1))) return;
+      if (!(ok = all(&kv_full[st], (it / S::kBufs) & 1))) return;
+      tc_fence_after_sync();
+      const uint64_t d = v_desc + (uint64_t)(st * (S::kBuf >> 4));
+      if (one) {
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)
-          umma_ts_bf16_f32(tmem + kColO, tmem + kColP + 64 * buf + 8 * k, d + (uint64_t)(k * (2048 >> 4)), id_o,
-                           j > 0 || k > 0 ? 1u : 0u);
+          umma_ts_bf16_f32(tm + kColO, tm + kColP + 64 * buf + 8 * k, d + (uint64_t)(k * (2048 >> 4)), id_o,
+                           !fresh || k > 0 ? 1u : 0u);
         umma_commit(&kv_empty[st]);
         umma_commit(&o_full[buf]);
-      };
-      for (; ok && pc.next(p); ++piece) {
-        if (!(ok = wait(q_full, piece & 1))) break;
-        const int n = pc.n_tiles;
-        for (int j = 0; j < n && ok; ++j) {
-          const uint32_t t = tc + j, it = base + k_item(j), st = it % S::kBufs;
-          if (!(ok = wait(&kv_full[st], (it / S::kBufs) & 1))) break;
-          tc_fence_after_sync();
-          const uint64_t d = k_desc + (uint64_t)(st * (S::kBuf >> 4));
+      }
+      __syncwarp();
+    };
+    for (uint32_t piece = 0; ok && pc.next(p); ++piece) {
+      if (!(ok = all(q_full, piece & 1))) break;
+      const int n = __reduce_max_sync(0xffffffffu, pc.n_tiles);
+      for (int j = 0; j < n && ok; ++j, ++t) {
+        const uint32_t it = k_place(t), st = it % S::kBufs;
+        if (!(ok = all(&kv_full[st], (it / S::kBufs) & 1))) break;
+        tc_fence_after_sync();
+        const uint64_t d = k_desc + (uint64_t)(st * (S::kBuf >> 4));
+        if (one) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            umma_bf16_f32(tmem + 128 * (t & 1), q_desc + (uint64_t)((k / 4 * S::kHalf + k % 4 * 32) >> 4),
+            umma_bf16_f32(tm + 128 * (t & 1), q_desc + (uint64_t)((k / 4 * S::kHalf + k % 4 * 32) >> 4),
                           d + (uint64_t)((k / 4 * S::kHalf + k % 4 * 32) >> 4), id_s, k > 0 ? 1u : 0u);
           umma_commit(&kv_empty[st]);
           umma_commit(&s_full[t & 1]);
-          if (j > 0) values(j - 1, n);
         }
-        if (ok) values(n - 1, n);
-        base += 2 * n;
-        tc += n;
+        __syncwarp();
+        if (j > 0) values(t - 1, j == 1);
       }
-      umma_commit(drain);
-      mbar_wait(drain, 0);
+      if (ok) values(t - 1, n == 1);
     }
+    if (one) umma_commit(drain);
+    mbar_wait(drain, 0);
     __syncwarp();
   } else if (warp >= kSoftmaxWarp) {
     // ------------------------------------------------------------------ softmax
     const int w4 = warp - kSoftmaxWarp, r = w4 * 32 + lane;     // row of the block
     const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
-    uint32_t base = 0, tc = 0, piece = 0;
+    uint32_t tc = 0, piece = 0;
     int* par = parents_s + 64 * w4;
     const float sl = p.scale_log2;
     bool ok = true;
@@ -496,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
         ok = wait(&s_full[buf], (t >> 1) & 1);
         if (masked && ok) {
           // thread r looks after line r of the value tile
-          const uint32_t it = base + v_item(j, n), st = it % S::kBufs;
+          const uint32_t it = v_place(t), st = it % S::kBufs;
           ok = wait(&kv_full[st], (it / S::kBufs) & 1);
           const int slot = slot0 + r;
           if (ok && slot >= rq.len &&
@@ -641,7 +665,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
         p.joins[blockIdx.x] = make_int4(b, block, head, parts_of(share, share.hi - n, rq.tiles));
       }
       tc_fence_before_sync();
-      base += 2 * n;
       tc += n;
       ++piece;
     }
@@ -678,37 +701,46 @@ struct NarrowSmem {
   static_assert(kOffKV % 1024 == 0 && kBufs >= 4, "layout");
 };
 
-struct PieceInfo {           // what the loading warps say of a piece
+struct PieceInfo {           // what the loading warps say of a piece; no tiles: it was the last
   int b, head, block, tile0, n_tiles, tiles, row0, n, len, end, rows;
 };
 
-// Position in the ring of the K or V tile t of a CTA's T: K_0, K_1, V_0, K_2, V_1, ..
-__device__ __forceinline__ uint32_t k_place(uint32_t t) { return t ? 2 * t - 1 : 0; }
-__device__ __forceinline__ uint32_t v_place(uint32_t t, uint32_t T) { return t + 1 < T ? 2 * t + 2 : 2 * T - 1; }
+// A barrier of the four softmax warps; true in all of them if `any` is in one.
+__device__ __forceinline__ bool meet_or(bool any) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 128, p;\n\t"
+      "selp.b32 %0, 1, 0, q;\n\t}" : "=r"(r) : "r"((int)any) : "memory");
+  return r != 0;
+}
 
-// Sums (or maxima) over a warp's lanes of 16 columns: each exchange halves the columns that a
-// lane looks after; lanes 2 c and 2 c + 1 are left with column c's.
-template <bool Max>
-__device__ __forceinline__ float over_lanes(float (&v)[16], int lane) {
-  auto join = [](float a, float b) { return Max ? fmaxf(a, b) : a + b; };
+__device__ __forceinline__ float warp_max(float x) {      // (NaN only if every lane's is)
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Sums over a warp's lanes of 16 columns: each exchange halves the columns that a lane looks
+// after; lanes 2 c and 2 c + 1 are left with column c's.
+__device__ __forceinline__ float sum_over_lanes(float (&v)[16], int lane) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const float got = __shfl_xor_sync(0xffffffffu, lane & 16 ? v[e] : v[e + 8], 16);
-    v[e] = join(lane & 16 ? v[e + 8] : v[e], got);
+    v[e] = (lane & 16 ? v[e + 8] : v[e]) + got;
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const float got = __shfl_xor_sync(0xffffffffu, lane & 8 ? v[e] : v[e + 4], 8);
-    v[e] = join(lane & 8 ? v[e + 4] : v[e], got);
+    v[e] = (lane & 8 ? v[e + 4] : v[e]) + got;
   }
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const float got = __shfl_xor_sync(0xffffffffu, lane & 4 ? v[e] : v[e + 2], 4);
-    v[e] = join(lane & 4 ? v[e + 2] : v[e], got);
+    v[e] = (lane & 4 ? v[e + 2] : v[e]) + got;
   }
   const float got = __shfl_xor_sync(0xffffffffu, lane & 2 ? v[0] : v[1], 2);
-  const float one = join(lane & 2 ? v[1] : v[0], got);
-  return join(one, __shfl_xor_sync(0xffffffffu, one, 1));
+  const float one = (lane & 2 ? v[1] : v[0]) + got;
+  return one + __shfl_xor_sync(0xffffffffu, one, 1);
 }
 
 template <typename T, int D>
@@ -729,17 +761,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
   uint32_t* tmem_s = reinterpret_cast<uint32_t*>(words + 1);
   volatile int* bad_s = words + 2;                           // by piece parity: piece + 1 with values not finite
   int* start_s = words + 4;
-  volatile int* open_s = words + 6;                          // tile + 1 that left a column without a reference
-  volatile int* high_s = words + 8;                          // by tile mod 4: a score is far above its reference
   long long* sums_s = reinterpret_cast<long long*>(small + 576);
   PieceInfo* info_s = reinterpret_cast<PieceInfo*>(small + 640);                      // [2] by piece parity
   int* parents_s = reinterpret_cast<int*>(small + 768);                               // [2 warps][64]
-  unsigned long long* sees_s = reinterpret_cast<unsigned long long*>(small + 1280);   // [2][64] by piece parity
-  long long* to_s = reinterpret_cast<long long*>(small + 2304);                       // [2][64]: a row's place in out
+  // [2] by piece parity [64 tokens][2]: the columns that see a token, and [64]: a column's place in out
+  uint32_t* seen_s = reinterpret_cast<uint32_t*>(small + 1280);
+  long long* to_s = reinterpret_cast<long long*>(small + 2304);
   float* best_s = reinterpret_cast<float*>(small + 3328);    // [64]: a column's reference (log2), -inf: none yet
   float* ref_s = best_s + 64;                                // [64]: the same, 0: none yet
   float* scale_s = best_s + 128;                             // [64]: what O and l are multiplied by
-  float* inv_s = best_s + 192;                               // [64]: 1 / l
+  float* down_s = best_s + 192;                              // [64]: by what the reference rose; at the end, 1 / l
   float* max_s = best_s + 256;                               // [4 warps][64]
   float* sum_s = best_s + 512;                               // [4 warps][64], to byte 3328 + 3072
 
@@ -763,8 +794,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
     }
     mbar_init(drain, 1);
     *abort_s = 0;
-    *open_s = 0;
-    for (int i = 0; i < 4; ++i) high_s[i] = 0;
     fence_mbar_init();
   }
   if (warp == kIssueWarp) {
@@ -784,38 +813,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_s;
   const Waits wait{abort_s, p.err};
-  const uint32_t T_all = (uint32_t)(share.hi - share.lo);     // this CTA's tiles
+  Pieces pc;
+  pc.left = 0;
 
   if (warp == kProducerWarp) {
-    // ------------------------------------------------------------------- copies
-    Pieces pc;
-    pc.left = 0;
-    if (T_all) pc.start(p, kRows, start_s[0], start_s[1], T_all);
-    TileCopies<S> copies{smem + S::kOffKV, kv_full, kv_empty, wait, p};
-    bool ok = true, first = true;
-    int v_id = 0, v_slot0 = 0, v_head = 0, v_end = 0;         // the V tile that is still to come
-    while (ok && pc.next(p)) {
-      const int end = pc.r.end;
-      int slot0 = pc.tile0 * kTile, id = copies.pages_of(pc.b, slot0, end);
-      for (int j = 0; j < pc.n_tiles && ok; ++j, slot0 += kTile) {
-        const int id_next = j + 1 < pc.n_tiles ? copies.pages_of(pc.b, slot0 + kTile, end) : 0;
-        ok = copies.copy(&k_map, id, slot0, pc.head, end);
-        if (ok && !first) ok = copies.copy(&v_map, v_id, v_slot0, v_head, v_end);
-        first = false;
-        v_id = id;
-        v_slot0 = slot0;
-        v_head = pc.head;
-        v_end = end;
-        id = id_next;
-      }
-    }
-    if (ok && !first) copies.copy(&v_map, v_id, v_slot0, v_head, v_end);
-    copies.drain();
+    if (share.hi > share.lo) pc.start(p, kRows, start_s[0], start_s[1], share.hi - share.lo);
+    TileCopies<S> copies{smem + S::kOffKV, kv_full, kv_empty, wait, p, pc};
+    copies.run(&k_map, &v_map);
   } else if (warp == kIssueWarp) {
     // ----------------------------------------------------------------- products
-    // The whole warp runs along and one lane issues, on values that are the same in all lanes by
-    // construction: a lane on its own took 72 cycles an instruction.
-    const uint32_t T = __reduce_max_sync(0xffffffffu, T_all), tm = __reduce_max_sync(0xffffffffu, tmem);
+    const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
     const bool one = elect_one();
     const uint64_t q_desc = smem_desc(smem_u32(smem + S::kOffQ), 16u, 1024u, kSwizzle128B);
     const uint64_t k_desc = smem_desc(smem_u32(smem + S::kOffKV), 16u, 1024u, kSwizzle128B);
@@ -826,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
     bool ok = true;
     auto all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
     auto values = [&](uint32_t t, int columns, bool fresh) {   // O^T += V^T P^T of tile t
-      const uint32_t buf = t & 1, it = v_place(t, T), st = it % S::kBufs;
+      const uint32_t buf = t & 1, it = v_place(t), st = it % S::kBufs;
       const uint32_t id_p = idesc_16(kBf16, columns, 1) | (1u << 15);     // both operands along their rows
       if (!(ok = all(&p_full[buf], (t >> 1) & 1))) return;
       if (!(ok = all(&kv_full[st], (it / S::kBufs) & 1))) return;
@@ -845,11 +852,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
     int columns_before = 0;
     bool fresh = false;                      // whether the tile before was its piece's first
     uint32_t t = 0;
-    for (uint32_t piece = 0; ok && t < T; ++piece) {
+    for (uint32_t piece = 0; ok; ++piece) {
       const uint32_t q = piece & 1;
       if (!(ok = all(&q_full[q], (piece >> 1) & 1))) break;
       const int n = __reduce_max_sync(0xffffffffu, info_s[q].n_tiles);
       const int columns = (__reduce_max_sync(0xffffffffu, info_s[q].rows) + 15) & ~15;
+      if (n == 0) break;
       const uint32_t id_s = idesc_16(kBf16, columns, 0);
       for (int j = 0; j < n && ok; ++j, ++t) {
         const uint32_t it = k_place(t), st = it % S::kBufs;
@@ -878,11 +886,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
     // ------------------------------------------------------------------ queries, a thread a row
     const int col = tid - 32 * kLoadWarp;
     int* par = parents_s + 64 * (warp - kLoadWarp);
-    Pieces pc;
-    pc.left = 0;
-    if (T_all) pc.start(p, kRows, start_s[0], start_s[1], T_all);
-    for (uint32_t piece = 0; pc.next(p); ++piece) {
+    if (share.hi > share.lo) pc.start(p, kRows, start_s[0], start_s[1], share.hi - share.lo);
+    for (uint32_t piece = 0;; ++piece) {
       const uint32_t q = piece & 1;
+      const bool more = pc.next(p);
+      if (!more) {
+        if (__all_sync(0xffffffffu, wait(&q_free[q], ((piece >> 1) & 1) ^ 1))) {
+          if (col == 0) info_s[q].n_tiles = 0;
+          mbar_arrive(&q_full[q]);
+        }
+        break;
+      }
       const int rows = pc.rows(p);
       const int i_r = pc.block * kRows + col, i = i_r / p.group, head = pc.head * p.group + (i_r - i * p.group);
       const bool live = col < rows;
@@ -906,7 +920,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
 #pragma unroll
       for (int c = 0; c < D / 8; ++c)
         *reinterpret_cast<uint4*>(smem + S::kOffQ + q * S::kQ + c / 8 * S::kQHalf + col * 128 + ((c ^ col) & 7) * 16) = x[c];
-      sees_s[64 * q + col] = sees;
+      for (int a = 0; a < pc.r.n; ++a) {
+        const uint32_t who = __ballot_sync(0xffffffffu, (sees >> a) & 1);
+        if (lane == (a & 31)) seen_s[128 * q + 2 * a + (warp - kLoadWarp)] = who;
+      }
       to_s[64 * q + col] = (long long)(pc.r.row0 + i) * p.out_row + head * p.out_head;
       if (col == 0)
         info_s[q] = {pc.b, pc.head, pc.block, pc.tile0, pc.n_tiles, pc.r.tiles, pc.r.row0, pc.r.n, pc.r.len, pc.r.end, rows};
@@ -915,21 +932,24 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
     }
   } else {
     // ------------------------------------------------------------------ softmax
-    // These warps meet at a hardware barrier, so all of them run through all tiles: a wait that
-    // ran out ends the others' waits, and what they then compute is not written.
+    // These warps meet at barriers, so they leave together: a wait that ran out ends the others'
+    // waits, and the next barrier tells all.
     const int w4 = warp - kSoftmaxWarp, r = w4 * 32 + lane;     // slot of a tile; at the end, element of a head
     const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
     const float sl = p.scale_log2;
-    bool ok = true;
-    auto meet = []() { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+    bool ok = true, lost = false;
     uint32_t t = 0;
-    for (uint32_t piece = 0; t < T_all; ++piece) {
+    for (uint32_t piece = 0;; ++piece) {
       const uint32_t q = piece & 1;
+      if (r < kRows) {
+        best_s[r] = -INFINITY;
+        ref_s[r] = 0.f;
+      }
       ok = wait(&q_full[q], (piece >> 1) & 1) && ok;
+      if (meet_or(!ok)) break;
       const PieceInfo rq = info_s[q];
-      // (after a wait that ran out: whatever is there, but the same number of tiles for all)
-      const int rows = rq.rows, chunks = (rows + 15) / 16;
-      const int n = min(max(rq.n_tiles, 1), (int)(T_all - t)), tile0 = rq.tile0;
+      const int rows = rq.rows, chunks = (rows + 15) / 16, n = rq.n_tiles, tile0 = rq.tile0;
+      if (n == 0) break;
       bool open = true;                        // a column has no reference yet
       float l[kRows];                          // this thread's slots' part of the columns' sums
 #pragma unroll
@@ -938,85 +958,79 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
         const uint32_t buf = t & 1;
         const int slot0 = (tile0 + j) * kTile, slot = slot0 + r;
         const bool masked = slot0 + kTile > rq.len;
+        uint2 seen = make_uint2(~0u, ~0u);     // the columns that see this slot
+        if (masked && slot >= rq.len)
+          seen = slot < rq.end ? *reinterpret_cast<const uint2*>(seen_s + 128 * q + 2 * (slot - rq.len)) : make_uint2(0, 0);
         ok = wait(&s_full[buf], (t >> 1) & 1) && ok;
-        if (masked) {
-          const uint32_t it = v_place(t, T_all), st = it % S::kBufs;
-          ok = wait(&kv_full[st], (it / S::kBufs) & 1) && ok;
-          if (ok && slot >= rq.len &&
-              clear_line<T, D>(smem + S::kOffKV + st * S::kBuf + r * 128, S::kHalf, r, slot < rq.end))
-            bad_s[q] = (int)piece + 1;
-        }
         __syncwarp();
         tc_fence_after_sync();
-        float x[kRows];
-        // the slot's scores (times scale and log2 e), less the references or as they are
-        auto scores = [&](bool less) {
+        // the slot's scores (times scale and log2 e), less the columns' references
+        float x[kRows], mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          if (c >= chunks) break;
+          uint32_t v[16];
+          tmem_ld_32x32b_sync<16>(tmem + lanes + kRows * buf + 16 * c, v);
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const float4 ref = *reinterpret_cast<const float4*>(ref_s + 16 * c + e);
+            x[16 * c + e] = fmaf(__uint_as_float(v[e]), sl, -ref.x);
+            x[16 * c + e + 1] = fmaf(__uint_as_float(v[e + 1]), sl, -ref.y);
+            x[16 * c + e + 2] = fmaf(__uint_as_float(v[e + 2]), sl, -ref.z);
+            x[16 * c + e + 3] = fmaf(__uint_as_float(v[e + 3]), sl, -ref.w);
+          }
+          if (masked) {
+            const uint32_t bits = c < 2 ? seen.x : seen.y;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[16 * c + e] = bits & (1u << (16 * (c & 1) + e)) ? x[16 * c + e] : -INFINITY;
+          }
+          float part[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) part[e] = x[16 * c + e];
+          mx = fmaxf(mx, max_of(part));
+        }
+        if (open || meet_or(mx > kRaise || !ok)) {
+          // ---- new references from the columns' maxima over the warps
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) {
             if (c >= chunks) break;
-            uint32_t v[16];
-            tmem_ld_32x32b_sync<16>(tmem + lanes + kRows * buf + 16 * c, v);
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
-              float4 ref = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (less) ref = *reinterpret_cast<const float4*>(ref_s + 16 * c + e);
-              x[16 * c + e] = fmaf(__uint_as_float(v[e]), sl, -ref.x);
-              x[16 * c + e + 1] = fmaf(__uint_as_float(v[e + 1]), sl, -ref.y);
-              x[16 * c + e + 2] = fmaf(__uint_as_float(v[e + 2]), sl, -ref.z);
-              x[16 * c + e + 3] = fmaf(__uint_as_float(v[e + 3]), sl, -ref.w);
-            }
-            if (masked && slot >= rq.len) {
-              const int a = slot - rq.len;
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                x[16 * c + e] = a < 64 && (sees_s[64 * q + 16 * c + e] >> a) & 1 ? x[16 * c + e] : -INFINITY;
+              float4 m;
+              m.x = warp_max(x[16 * c + e]);
+              m.y = warp_max(x[16 * c + e + 1]);
+              m.z = warp_max(x[16 * c + e + 2]);
+              m.w = warp_max(x[16 * c + e + 3]);
+              if (lane == 0) *reinterpret_cast<float4*>(max_s + 64 * w4 + 16 * c + e) = m;
             }
           }
-        };
-        bool raise = open;
-        if (!open) {
-          scores(true);
-          float mx = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c) {
-            if (c >= chunks) break;
-            float part[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) part[e] = x[16 * c + e];
-            mx = fmaxf(mx, max_of(part));
-          }
-          if (mx > kRaise) high_s[t & 3] = 1;
-        }
-        // (a tile's word is cleared two tiles later, two before it is used again; each tile has a
-        // meeting between)
-        if (r == 0) high_s[(t + 2) & 3] = 0;
-        meet();
-        raise = raise || high_s[t & 3] != 0;
-        if (raise) {
-          // ---- new references from the columns' maxima over the warps
-          scores(false);
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c) {
-            if (c >= chunks) break;
-            float part[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) part[e] = x[16 * c + e];
-            const float m = over_lanes<true>(part, lane);
-            if (!(lane & 1)) max_s[64 * w4 + 16 * c + (lane >> 1)] = m;
-          }
-          meet();
-          if (r < kRows) {
-            const float mx = fmaxf(fmaxf(max_s[r], max_s[64 + r]), fmaxf(max_s[128 + r], max_s[192 + r]));
-            const float old = j > 0 ? best_s[r] : -INFINITY;
-            const bool up = mx - old > kRaise || old == -INFINITY;
-            const float now = up ? mx : old;
-            scale_s[r] = old == -INFINITY ? 0.f : up ? ex2_approx(old - now) : 1.f;
+          if ((lost = meet_or(!ok))) break;
+          bool none = false;
+          if (r < kRows && r < 16 * chunks) {
+            const float m = fmaxf(fmaxf(max_s[r], max_s[64 + r]), fmaxf(max_s[128 + r], max_s[192 + r]));
+            const float old = best_s[r], ref = ref_s[r];
+            const bool first = old == -INFINITY, up = first || m > kRaise;
+            const float now = first ? m : up ? ref + m : old;
+            const float down = first ? (m == -INFINITY ? 0.f : m) : up ? now - ref : 0.f;
             best_s[r] = now;
             ref_s[r] = now == -INFINITY ? 0.f : now;
-            if (now == -INFINITY && r < rows) *open_s = (int)t + 1;
+            down_s[r] = down;
+            scale_s[r] = first ? 0.f : up ? ex2_approx(-down) : 1.f;
+            none = now == -INFINITY && r < rows;
           }
-          meet();
-          open = *open_s == (int)t + 1;
+          open = meet_or(none);
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            if (c >= chunks) break;
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              const float4 down = *reinterpret_cast<const float4*>(down_s + 16 * c + e);
+              x[16 * c + e] -= down.x;
+              x[16 * c + e + 1] -= down.y;
+              x[16 * c + e + 2] -= down.z;
+              x[16 * c + e + 3] -= down.w;
+            }
+          }
           if (j > 0) {
             // O and l of the tiles before, complete, on the new scale
             ok = wait(&o_full[buf ^ 1], ((t - 1) >> 1) & 1) && ok;
@@ -1036,7 +1050,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
             }
             tmem_st_wait();
           }
-          scores(true);
         }
         uint8_t* line = smem + S::kOffP + buf * S::kP + r * 128;
 #pragma unroll
@@ -1053,10 +1066,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
           *reinterpret_cast<uint4*>(line + ((2 * c ^ r) & 7) * 16) = make_uint4(y[0], y[1], y[2], y[3]);
           *reinterpret_cast<uint4*>(line + (((2 * c + 1) ^ r) & 7) * 16) = make_uint4(y[4], y[5], y[6], y[7]);
         }
+        if (masked) {
+          const uint32_t it = v_place(t), st = it % S::kBufs;
+          ok = wait(&kv_full[st], (it / S::kBufs) & 1) && ok;
+          if (ok && slot >= rq.len &&
+              clear_line<T, D>(smem + S::kOffKV + st * S::kBuf + r * 128, S::kHalf, r, slot < rq.end))
+            bad_s[q] = (int)piece + 1;
+          __syncwarp();
+        }
         fence_proxy_async_smem();
         tc_fence_before_sync();
         mbar_arrive(&p_full[buf]);
       }
+      if (lost) break;
       // ---- the piece's rows: sums over the warps, then O
       const bool whole = n == rq.tiles;
       float* part = p.partial + (long long)(2 * blockIdx.x + (tile0 == 0 ? 1 : 0)) * kTile * (D + 2);
@@ -1066,25 +1088,24 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
         float v[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] = l[16 * c + e];
-        const float s = over_lanes<false>(v, lane);
+        const float s = sum_over_lanes(v, lane);
         if (!(lane & 1)) sum_s[64 * w4 + 16 * c + (lane >> 1)] = s;
       }
-      meet();
-      ok = ok && !*abort_s;
+      if (meet_or(!ok)) break;
       if (r < rows && r < kRows) {
         const float s = (sum_s[r] + sum_s[64 + r]) + (sum_s[128 + r] + sum_s[192 + r]);
-        inv_s[r] = !whole ? 1.f : s > 0.f ? 1.f / s : s == 0.f ? 0.f : s;        // (NaN stays)
-        if (!whole && ok) {
+        down_s[r] = !whole ? 1.f : s > 0.f ? 1.f / s : s == 0.f ? 0.f : s;       // (NaN stays)
+        if (!whole) {
           part[r * (D + 2) + D] = best_s[r];
           part[r * (D + 2) + D + 1] = s;
-        } else if (p.lse && ok) {
+        } else if (p.lse) {
           const int i_r = rq.block * kRows + r, i = i_r / p.group;
           p.lse[(long long)(rq.row0 + i) * p.group * p.cs.heads + rq.head * p.group + (i_r - i * p.group)] =
               s == 0.f ? -INFINITY : (best_s[r] + log2f(s)) * 0.6931471805599453f;
         }
       }
-      meet();
-      ok = wait(&o_full[(t - 1) & 1], ((t - 1) >> 1) & 1) && ok;
+      meet_or(false);
+      ok = wait(&o_full[(t - 1) & 1], ((t - 1) >> 1) & 1);
       __syncwarp();
       tc_fence_after_sync();
       const bool bad = bad_s[q] == (int)piece + 1;
@@ -1106,9 +1127,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
             const float f = elem_to_float(static_cast<const T*>(p.v)[page * p.cs.page + (at & ((1 << p.slots.page_shift) - 1)) * p.cs.slot +
                                                                     rq.head * p.cs.head + r]);
             if (f - f == 0.f) continue;
+            const uint32_t bits = seen_s[128 * q + 2 * a + c / 2] >> (16 * (c & 1));
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              if ((sees_s[64 * q + 16 * c + e] >> a) & 1) o[e] += f;
+              if ((bits >> e) & 1) o[e] += f;
           }
         }
         const int left = rows - 16 * c;
@@ -1116,7 +1138,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
           T* out = reinterpret_cast<T*>(p.out) + r;
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            if (e < left) out[to_s[64 * q + 16 * c + e]] = elem_from_float<T>(o[e] * inv_s[16 * c + e]);
+            if (e < left) out[to_s[64 * q + 16 * c + e]] = elem_from_float<T>(o[e] * down_s[16 * c + e]);
         } else {
           float* to = part + 16 * c * (D + 2) + r;
 #pragma unroll
