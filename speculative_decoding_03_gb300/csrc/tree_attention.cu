@@ -38,9 +38,18 @@ constexpr int kTile = 128;                 // slots of a tile, and rows of a blo
 constexpr int kThreads = 256;
 constexpr int kProducerWarp = 0, kIssueWarp = 1, kSoftmaxWarp = 4;
 constexpr float kRaise = 8.f;              // log2 of what the maximum may lag behind
-constexpr int kPieceUnits = 3;             // what beginning and ending a piece costs, in tiles
+constexpr int kPieceUnits = 4;             // what beginning and ending a piece costs, in tiles
+
+// How a tile's lines lie in memory and in shared memory, in groups of 8 lines of 128 bytes.
+//   kHalvesApart: a copy takes 64 elements of a page's lines; the groups of a half follow each
+//                 other (the only form for heads of 64)
+//   kHeadsInLine: heads of 128 side by side in a line: a copy takes both halves of a page's lines,
+//                 group by group, half by half, and there are half as many copies
+//   kHeadsApart:  the same where a page's heads are one after the other
+enum TileForm { kHalvesApart, kHeadsInLine, kHeadsApart };
 
 struct AttendParams {
+  TileForm form;
   HeadRows q;
   char* out;
   long long out_row, out_head;
@@ -90,13 +99,19 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
       : "memory");
 }
 
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,
-                                            int w) {
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,
+                                            int w, int v, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "l"(policy)
       : "memory");
+}
+// L2 policy: these lines go first (keys and values that no other CTA reads)
+__device__ __forceinline__ uint64_t policy_evict_first() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -257,6 +272,7 @@ struct TileCopies {
   const Waits& wait;
   const AttendParams& p;
   Pieces pc;
+  uint64_t policy;
   int left = 0, slot0 = 0;   // tiles of the piece still to come, and the next one's first slot
   uint32_t item = 0, skipped = ~0u;
   __device__ __forceinline__ TileAt fetch() {
@@ -275,16 +291,25 @@ struct TileCopies {
   }
   __device__ __forceinline__ bool copy(const CUtensorMap* map, const TileAt& x) {
     const int lane = threadIdx.x & 31, page = 1 << p.slots.page_shift, box = min(page, kTile);
-    const int my_page = lane / S::kHalves, my_half = lane % S::kHalves;
+    const int halves = p.form == kHalvesApart ? S::kHalves : 1;
+    const int my_page = lane / halves, my_half = lane % halves;
     const uint32_t st = item % S::kBufs;
     if (!__all_sync(0xffffffffu, wait(&empty[st], ((item / S::kBufs) & 1) ^ 1))) return false;
     const int n_pages = min(kTile / box, (x.end - x.slot0 + box - 1) / box);
     if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(n_pages * box * 128 * S::kHalves));
     __syncwarp();
-    const int pid = __shfl_sync(0xffffffffu, x.id, my_page);
-    if (my_page < n_pages)
-      tma_load_4d(ring + st * S::kBuf + my_half * S::kHalf + my_page * box * 128, map, &full[st], my_half * 64,
-                  x.slot0 & (page - 1), x.head, pid < 0 ? p.slots.n_pages : pid);
+    int pid = __shfl_sync(0xffffffffu, x.id, my_page);
+    if (pid < 0) pid = p.slots.n_pages;        // (behind the last: zeros)
+    if (my_page < n_pages) {
+      uint8_t* to = ring + st * S::kBuf;
+      const int line = x.slot0 & (page - 1);
+      if (p.form == kHalvesApart)
+        tma_load_5d(to + my_half * S::kHalf + my_page * box * 128, map, &full[st], my_half * 64, line, x.head, pid, 0, policy);
+      else if (p.form == kHeadsInLine)
+        tma_load_5d(to + my_page * box * 256, map, &full[st], 0, 0, 2 * x.head, line >> 3, pid, policy);
+      else
+        tma_load_5d(to + my_page * box * 256, map, &full[st], 0, 0, 0, line >> 3, pid * p.cs.heads + x.head, policy);
+    }
     ++item;
     return true;
   }
@@ -317,14 +342,16 @@ __device__ __forceinline__ uint32_t v_place(uint32_t t) { return 2 * t + 2; }
 // values that are not finite: 0 x NaN must not reach them.  Clears line r of a value tile, or
 // (in_use) its values that are not finite, which are added again at the end; true if it had any.
 template <typename T, int D>
-__device__ __forceinline__ bool clear_line(uint8_t* line, int half_bytes, int r, bool in_use) {
+__device__ __forceinline__ bool clear_line(uint8_t* tile, TileForm form, int r, bool in_use) {
+  const int group = form == kHalvesApart ? 1024 : 2048, half = form == kHalvesApart ? kTile * 128 : 1024;
+  uint8_t* line = tile + (r >> 3) * group + (r & 7) * 128;
   // an exponent of ones, and what carries it (and no other) into the sign's place
   constexpr uint32_t kOnes = __is_same(T, __nv_bfloat16) ? 0x7f807f80u : 0x7c007c00u;
   constexpr uint32_t kLow = __is_same(T, __nv_bfloat16) ? 0x00800080u : 0x04000400u;
   bool bad = false;
 #pragma unroll 4
   for (int c = 0; c < D / 8; ++c) {
-    uint4* at = reinterpret_cast<uint4*>(line + c / 8 * half_bytes + ((c ^ r) & 7) * 16);
+    uint4* at = reinterpret_cast<uint4*>(line + c / 8 * half + ((c ^ r) & 7) * 16);
     if (!in_use) {
       *at = make_uint4(0, 0, 0, 0);
       continue;
@@ -409,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
   if (share.hi > share.lo) pc.start(p, kTile, start_s[0], start_s[1], share.hi - share.lo);
 
   if (warp == kProducerWarp) {
-    TileCopies<S> copies{smem + S::kOffKV, kv_full, kv_empty, wait, p, pc};
+    TileCopies<S> copies{smem + S::kOffKV, kv_full, kv_empty, wait, p, pc, policy_evict_first()};
     copies.run(&k_map, &v_map);
   } else if (warp == kIssueWarp) {
     // ----------------------------------------------------------------- products
@@ -419,8 +446,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
     const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
     const bool one = elect_one();
     const uint64_t q_desc = smem_desc(smem_u32(smem + S::kOffQ), 16u, 1024u, kSwizzle128B);
-    const uint64_t k_desc = smem_desc(smem_u32(smem + S::kOffKV), 16u, 1024u, kSwizzle128B);
-    const uint64_t v_desc = smem_desc(smem_u32(smem + S::kOffKV), (uint32_t)S::kHalf, 1024u, kSwizzle128B);
+    const uint32_t group = p.form == kHalvesApart ? 1024u : 2048u, half = p.form == kHalvesApart ? S::kHalf : 1024u;
+    const uint64_t k_desc = smem_desc(smem_u32(smem + S::kOffKV), 16u, group, kSwizzle128B);
+    const uint64_t v_desc = smem_desc(smem_u32(smem + S::kOffKV), half, group, kSwizzle128B);
     uint32_t t = 0;
     bool ok = true;
     auto all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
@@ -435,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
       if (one) {
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)
-          umma_ts_bf16_f32(tm + kColO, tm + kColP + 64 * buf + 8 * k, d + (uint64_t)(k * (2048 >> 4)), id_o,
+          umma_ts_bf16_f32(tm + kColO, tm + kColP + 64 * buf + 8 * k, d + (uint64_t)(k * (group >> 3)), id_o,
                            !fresh || k > 0 ? 1u : 0u);
         umma_commit(&kv_empty[st]);
         umma_commit(&o_full[buf]);
@@ -454,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
             umma_bf16_f32(tm + 128 * (t & 1), q_desc + (uint64_t)((k / 4 * S::kHalf + k % 4 * 32) >> 4),
-                          d + (uint64_t)((k / 4 * S::kHalf + k % 4 * 32) >> 4), id_s, k > 0 ? 1u : 0u);
+                          d + (uint64_t)((k / 4 * half + k % 4 * 32) >> 4), id_s, k > 0 ? 1u : 0u);
           umma_commit(&kv_empty[st]);
           umma_commit(&s_full[t & 1]);
         }
@@ -524,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
           ok = wait(&kv_full[st], (it / S::kBufs) & 1);
           const int slot = slot0 + r;
           if (ok && slot >= rq.len &&
-              clear_line<T, D>(smem + S::kOffKV + st * S::kBuf + r * 128, S::kHalf, r, slot < rq.end))
+              clear_line<T, D>(smem + S::kOffKV + st * S::kBuf, p.form, r, slot < rq.end))
             bad_s[piece & 1] = (int)piece + 1;
         }
         ok = __all_sync(0xffffffffu, ok);
@@ -818,17 +846,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
 
   if (warp == kProducerWarp) {
     if (share.hi > share.lo) pc.start(p, kRows, start_s[0], start_s[1], share.hi - share.lo);
-    TileCopies<S> copies{smem + S::kOffKV, kv_full, kv_empty, wait, p, pc};
+    TileCopies<S> copies{smem + S::kOffKV, kv_full, kv_empty, wait, p, pc, policy_evict_first()};
     copies.run(&k_map, &v_map);
   } else if (warp == kIssueWarp) {
     // ----------------------------------------------------------------- products
     const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
     const bool one = elect_one();
     const uint64_t q_desc = smem_desc(smem_u32(smem + S::kOffQ), 16u, 1024u, kSwizzle128B);
-    const uint64_t k_desc = smem_desc(smem_u32(smem + S::kOffKV), 16u, 1024u, kSwizzle128B);
+    const uint32_t group = p.form == kHalvesApart ? 1024u : 2048u, half = p.form == kHalvesApart ? S::kHalf : 1024u;
+    const uint64_t k_desc = smem_desc(smem_u32(smem + S::kOffKV), 16u, group, kSwizzle128B);
     // (head_dim 64: rows 64 to 127 of V^T are rows 0 to 63 again)
-    const uint64_t v_desc =
-        smem_desc(smem_u32(smem + S::kOffKV), D == 128 ? (uint32_t)S::kHalf : 0u, 1024u, kSwizzle128B);
+    const uint64_t v_desc = smem_desc(smem_u32(smem + S::kOffKV), D == 128 ? half : 0u, group, kSwizzle128B);
     const uint64_t p_desc = smem_desc(smem_u32(smem + S::kOffP), (uint32_t)S::kP, 1024u, kSwizzle128B);
     bool ok = true;
     auto all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
@@ -842,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
       if (one) {
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)
-          umma_bf16_f32(tm + kColO, d + (uint64_t)(k * (2048 >> 4)), b + (uint64_t)(k * (2048 >> 4)), id_p,
+          umma_bf16_f32(tm + kColO, d + (uint64_t)(k * (group >> 3)), b + (uint64_t)(k * (2048 >> 4)), id_p,
                         !fresh || k > 0 ? 1u : 0u);
         umma_commit(&kv_empty[st]);
         umma_commit(&o_full[buf]);
@@ -867,7 +895,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
         if (one) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            umma_bf16_f32(tm + kRows * (t & 1), d + (uint64_t)((k / 4 * S::kHalf + k % 4 * 32) >> 4),
+            umma_bf16_f32(tm + kRows * (t & 1), d + (uint64_t)((k / 4 * half + k % 4 * 32) >> 4),
                           b + (uint64_t)((k / 4 * S::kQHalf + k % 4 * 32) >> 4), id_s, k > 0 ? 1u : 0u);
           umma_commit(&kv_empty[st]);
           umma_commit(&s_full[t & 1]);
@@ -1070,7 +1098,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
           const uint32_t it = v_place(t), st = it % S::kBufs;
           ok = wait(&kv_full[st], (it / S::kBufs) & 1) && ok;
           if (ok && slot >= rq.len &&
-              clear_line<T, D>(smem + S::kOffKV + st * S::kBuf + r * 128, S::kHalf, r, slot < rq.end))
+              clear_line<T, D>(smem + S::kOffKV + st * S::kBuf, p.form, r, slot < rq.end))
             bad_s[q] = (int)piece + 1;
           __syncwarp();
         }
@@ -1217,19 +1245,33 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Atten
     p.lse[(long long)row * p.group * p.cs.heads + head] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
 }
 
+TileForm tile_form(const CacheStrides& cs, const TargetSlots& slots) {
+  if (cs.head_dim != 128) return kHalvesApart;
+  if (cs.heads == 1 || cs.head == 128) return kHeadsInLine;
+  return slots.n_pages == 1 || (cs.page == cs.heads * cs.head && (long long)slots.n_pages * cs.heads < (1LL << 31))
+             ? kHeadsApart : kHalvesApart;
+}
+
 bool encode_cache_map(CUtensorMap* map, const void* base, bool bf16, const CacheStrides& cs,
-                      const TargetSlots& slots) {
+                      const TargetSlots& slots, TileForm form) {
   EncodeTiledFn fn = tensor_map_encoder();
   if (!fn) return false;
-  const int page = 1 << slots.page_shift;
-  cuuint64_t dims[4] = {(cuuint64_t)cs.head_dim, (cuuint64_t)page, (cuuint64_t)cs.heads, (cuuint64_t)slots.n_pages};
-  cuuint64_t strides[3] = {(cuuint64_t)cs.slot * 2, (cuuint64_t)cs.head * 2, (cuuint64_t)cs.page * 2};
-  cuuint32_t box[4] = {64, (cuuint32_t)(page < kTile ? page : kTile), 1, 1};
-  cuuint32_t ones[4] = {1, 1, 1, 1};
-  return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
-            const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const cuuint64_t page = (cuuint64_t)1 << slots.page_shift, heads = (cuuint64_t)cs.heads,
+                   pages = (cuuint64_t)slots.n_pages;
+  const cuuint64_t slot_b = (cuuint64_t)cs.slot * 2, head_b = (cuuint64_t)cs.head * 2, page_b = (cuuint64_t)cs.page * 2;
+  const cuuint32_t lines = (cuuint32_t)(page < kTile ? page : kTile);
+  cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+  auto encode = [&](const cuuint64_t (&dims)[5], const cuuint64_t (&strides)[4], const cuuint32_t (&box)[5]) {
+    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
+              const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  if (form == kHalvesApart)
+    return encode({(cuuint64_t)cs.head_dim, page, heads, pages, 1}, {slot_b, head_b, page_b, 16}, {64, lines, 1, 1, 1});
+  if (form == kHeadsInLine)
+    return encode({64, 8, 2 * heads, page / 8, pages}, {slot_b, 128, 8 * slot_b, page_b}, {64, 8, 2, lines / 8, 1});
+  return encode({64, 8, 2, page / 8, pages * heads}, {slot_b, 128, 8 * slot_b, head_b}, {64, 8, 2, lines / 8, 1});
 }
 
 constexpr int kMaxGrid = 160;              // CTAs of the persistent grid at most
@@ -1248,7 +1290,9 @@ cudaError_t attend_for(AttendParams p, const TargetSlots& slots, bool bf16, cuda
   if (grid <= 0) return cudaErrorInvalidConfiguration;
   if (grid > kMaxGrid) grid = kMaxGrid;
   CUtensorMap k_map, v_map;
-  if (!encode_cache_map(&k_map, p.k, bf16, p.cs, slots) || !encode_cache_map(&v_map, p.v, bf16, p.cs, slots))
+  p.form = tile_form(p.cs, slots);
+  if (!encode_cache_map(&k_map, p.k, bf16, p.cs, slots, p.form) ||
+      !encode_cache_map(&v_map, p.v, bf16, p.cs, slots, p.form))
     return cudaErrorInvalidValue;
   const int rows = p.rows.N * p.group;
   const bool narrow = rows <= NarrowSmem<D>::kRows;
