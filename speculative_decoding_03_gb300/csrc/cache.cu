@@ -21,167 +21,188 @@ struct AppendParams {
   TargetSlots slots;
   Rotation rot;
   HeadNorm norm;
-  int q_heads;
+  int q_heads, parts;
   int* err;
 };
 
 constexpr int kMaxHalf = 128;            // pairs of a head (head_dim <= 256)
 
-// Cosine and sine of position x frequency.  The product is formed and reduced by multiples of
-// 2 pi (its double and the next 53 bits: Cody and Waite's two-term reduction) in 64 bits: at
-// position 2^20 an fp32 product is off by up to 0.03, at 2^31 this one by 3e-7.
+// Cosine and sine of position x frequency, which is reduced to a turn in whole numbers: the
+// frequency's 24 bits times 2^64 / (2 pi) are at most 2^-65 of a turn off for each unit of
+// frequency, and the position's multiple wraps at whole turns by itself.  So at position 2^31 and
+// frequency 1 the angle is off by 2^-34 of a turn before it is rounded to fp32 (an fp32 product
+// would be off by tens of turns), without an instruction in 64-bit floating point: those take
+// 100 cycles and more here, and five of them stood between a row's length and its stores.
 __device__ __forceinline__ float2 turn_of(int position, float freq) {
-  const double angle = (double)position * (double)freq;
-  const double turns = rint(angle * 0.15915494309189535);
-  double r = fma(turns, -6.283185307179586, angle);
-  r = fma(turns, -2.4492935982947064e-16, r);
+  constexpr unsigned long long kTurns = 2935890503282001226ull;      // 2^64 / (2 pi)
+  const uint32_t bits = __float_as_uint(freq);
+  const int exponent = (int)(bits >> 23 & 255);
+  const unsigned long long m = (unsigned long long)(exponent ? (bits & 0x7fffffu) | 0x800000u : (bits & 0x7fffffu) << 1) << 40;
+  const unsigned long long hi = __umul64hi(m, kTurns), lo = m * kTurns;   // |freq| = m 2^(exponent - 190)
+  const int up = exponent - 126;                                     // turns x 2^64 = (hi:lo >> 64) 2^up
+  unsigned long long turns = up <= -64 || up >= 128 ? 0 : up < 0 ? hi >> -up : up == 0 ? hi
+                           : up < 64 ? hi << up | lo >> (64 - up) : lo << (up - 64);
+  turns *= (unsigned long long)(long long)position;
+  if (bits >> 31) turns = 0 - turns;
   float2 cs;
-  sincosf((float)r, &cs.y, &cs.x);
+  sincospif((float)(long long)turns * 0x1p-63f, &cs.y, &cs.x);
+  if (exponent == 255) cs.x = cs.y = __int_as_float(0x7fc00000);     // of no angle
   return cs;
 }
 
-// One CTA a row, LG lanes a head vector (16 bytes a lane): x' = rot(x rsqrt(mean x^2 + eps) w),
-// sums and products in fp32 and one rounding where it is stored.  Each element is read and
-// written once, so memory bounds it; a row's loads are all issued before its angles are
-// computed, once for all its heads.
+// A row's LG lanes a head vector (16 bytes a lane): x' = rot(x rsqrt(mean x^2 + eps) w), sums and
+// products in fp32 and one rounding where it is stored.  Each element is read and written once, so
+// memory bounds it.  A warp takes a row, or one of `parts` parts of its heads, and waits for no
+// other: a lane has the same elements of each of its heads, so it holds their cosines and sines
+// in registers, 1 to 4 of which each lane computes for the warp.
+constexpr int kAppendWarps = 8, kAppendBatch = 4, kAppendCtas = 4;
+
 template <typename T, int LG>
-__global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ AppendParams p) {
-  constexpr int kBatch = 4;
-  __shared__ float cos_s[kMaxHalf], sin_s[kMaxHalf];
-  __shared__ int depth_s;
+__global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas) append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int G = 32 / LG;               // heads side by side
+  __shared__ float2 turn_s[kAppendWarps][kMaxHalf];
   pdl_wait();
   pdl_launch_dependents();
-  const int b = blockIdx.y, i = blockIdx.x, tid = threadIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, at = lane & (LG - 1), group = lane / LG;
+  const long long task = (long long)blockIdx.x * kAppendWarps + warp;
+  const long long place = task / p.parts;
+  const int part = (int)(task - place * p.parts);
+  const int b = (int)(place / p.rows.N), i = (int)(place - (long long)b * p.rows.N);
+  if (b >= p.rows.B) return;
+  const int length = p.slots.lengths[b];
   const RequestRows r = request_rows(p.rows, b, p.err);
   if (i >= r.n) return;
-  const int len = request_length(p.slots, b, r.n, p.err);
+  const int len = checked_length(p.slots, length, r.n, p.err);
   if (len < 0) return;
   const int row = r.row0 + i, slot = len + i;
-  const int D = p.cs.head_dim, lane = tid & (LG - 1), group = tid / LG, groups = blockDim.x / LG;
-  const bool on = lane * 8 < D;
-  const int n_vec = p.q_heads + 2 * p.cs.heads;
-  auto source = [&](int vec) {
-    const HeadRows& h = vec < p.q_heads ? p.q : vec < p.q_heads + p.cs.heads ? p.k : p.v;
-    const int head = vec < p.q_heads ? vec : vec < p.q_heads + p.cs.heads ? vec - p.q_heads : vec - p.q_heads - p.cs.heads;
-    return reinterpret_cast<const uint4*>(static_cast<const T*>(h.p) + row * h.row + head * h.head) + lane;
-  };
-  uint4 x[kBatch];
-  auto load = [&](int first) {
+  const int D = p.cs.head_dim, half = p.rot.inv_freq ? p.rot.rotated / 2 : 0;
+  const bool on = at * 8 < D;
+  const int n_q = p.q_heads, n_qk = n_q + p.cs.heads, step = p.parts * G;
+  const T* q = static_cast<const T*>(p.q.p) + row * p.q.row + at * 8;
+  const T* k = static_cast<const T*>(p.k.p) + row * p.k.row + at * 8;
+  auto load = [&](int first, uint4 (&x)[kAppendBatch]) {
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int vec = first + u * groups;
-      if (vec < n_vec && on) x[u] = *source(vec);
+    for (int u = 0; u < kAppendBatch; ++u) {
+      const int vec = first + u * step + group;
+      x[u] = make_uint4(0, 0, 0, 0);
+      if (vec < n_qk && on)
+        x[u] = *reinterpret_cast<const uint4*>(vec < n_q ? q + vec * p.q.head : k + (vec - n_q) * p.k.head);
     }
   };
-  load(group);
+  uint4 x[kAppendBatch];
+  load(part * G, x);
   const int page = slot_page(p.slots, b, slot, p.err);
-  const int half = p.rot.inv_freq ? p.rot.rotated / 2 : 0;
+
+  // ---- the angles of this lane's elements
+  float c[8], s[8];
+  const int h8 = half / 8;                 // (half a multiple of 8: pairs are whole chunks apart)
+  const bool low = at < h8, rotated = at < 2 * h8;
   if (half) {
     int depth = i;
     if (p.rows.parents) {
-      // a tree has at most 64 tokens: the first warp holds its parents, two a lane
-      if (tid < 32) {
-        const int a = tid < r.n ? parent_of(p.rows.parents, r.row0 + tid, tid, p.err) : -1;
-        const int c = tid + 32 < r.n ? parent_of(p.rows.parents, r.row0 + tid + 32, tid + 32, p.err) : -1;
-        depth = -1;
-        for (int at = i; at >= 0; ++depth) {
-          const int lo = __shfl_sync(0xffffffffu, a, at & 31), hi = __shfl_sync(0xffffffffu, c, at & 31);
-          at = at < 32 ? lo : hi;
-        }
-        if (tid == 0) depth_s = depth;
+      // a tree has at most 64 tokens: the warp holds their parents, two a lane
+      const int a = lane < r.n ? parent_of(p.rows.parents, r.row0 + lane, lane, p.err) : -1;
+      const int d = lane + 32 < r.n ? parent_of(p.rows.parents, r.row0 + lane + 32, lane + 32, p.err) : -1;
+      depth = -1;
+      for (int up = i; up >= 0; ++depth) {
+        const int lo = __shfl_sync(0xffffffffu, a, up & 31), hi = __shfl_sync(0xffffffffu, d, up & 31);
+        up = up < 32 ? lo : hi;
       }
-      __syncthreads();
-      depth = depth_s;
     }
-    for (int j = tid; j < half; j += blockDim.x) {
-      const float2 cs = turn_of(len + depth, p.rot.inv_freq[j]);
-      cos_s[j] = cs.x;
-      sin_s[j] = cs.y;
+    for (int j = lane; j < half; j += 32) turn_s[warp][j] = turn_of(len + depth, p.rot.inv_freq[j]);
+    __syncwarp();
+    if (rotated) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float2 t = turn_s[warp][p.rot.interleaved ? at * 4 + e / 2 : (low ? at : at - h8) * 8 + e];
+        c[e] = t.x;
+        s[e] = (p.rot.interleaved ? !(e & 1) : low) ? -t.y : t.y;
+      }
     }
-    __syncthreads();
   }
-  const long long line = page < 0 ? 0
-      : page * p.cs.page + (slot & ((1 << p.slots.page_shift) - 1)) * p.cs.slot;
-  for (int first = group; first - group < n_vec; first += kBatch * groups) {
-    if (first != group) load(first);
+  const int other = !rotated ? at : low ? at + h8 : at - h8;
+
+  T* q_out = reinterpret_cast<T*>(p.q_out) + row * p.q_out_row + at * 8;
+  const long long line = page < 0 ? 0 : page * p.cs.page + (slot & ((1 << p.slots.page_shift) - 1)) * p.cs.slot;
+  T* k_cache = reinterpret_cast<T*>(p.k_cache) + line + at * 8;
+  const bool norm = p.norm.q_weight || p.norm.k_weight;
+  for (int first = part * G; first < n_qk; first += kAppendBatch * step) {
+    if (first != part * G) load(first, x);
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int vec = first + u * groups;
-      if (first - group + u * groups >= n_vec) break;      // (the same for every lane)
-      const bool is_q = vec < p.q_heads, is_k = !is_q && vec < p.q_heads + p.cs.heads;
-      const bool live = vec < n_vec && on;
-      const float* w = is_q ? p.norm.q_weight : is_k ? p.norm.k_weight : nullptr;
+    for (int u = 0; u < kAppendBatch; ++u) {
+      const int vec = first + u * step + group;
+      if (vec - group >= n_qk) break;      // (the same for every lane)
+      const bool is_q = vec < n_q;
+      const float* weight = is_q ? p.norm.q_weight : p.norm.k_weight;
       uint4 y = x[u];
-      // (all lanes of a warp take part in the exchanges, whatever their vectors are)
-      if (p.norm.q_weight || p.norm.k_weight || half) {
+      if (norm || half) {                  // (what is neither normalised nor rotated passes as its bits)
         float f[8];
-        unpack_chunk<T>(live ? x[u] : make_uint4(0, 0, 0, 0), f);
-        if (p.norm.q_weight || p.norm.k_weight) {
-          float s = 0.f;
+        unpack_chunk<T>(x[u], f);
+        if (norm) {
+          float sum = 0.f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) s = fmaf(f[e], f[e], s);
+          for (int e = 0; e < 8; ++e) sum = fmaf(f[e], f[e], sum);
 #pragma unroll
-          for (int m = LG / 2; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-          if (w && live) {
-            const float scale = 1.f / sqrtf(s / (float)D + p.norm.eps);
-            const float4 w0 = reinterpret_cast<const float4*>(w)[2 * lane], w1 = reinterpret_cast<const float4*>(w)[2 * lane + 1];
+          for (int m = LG / 2; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+          if (weight && on) {
+            const float scale = 1.f / sqrtf(sum / (float)D + p.norm.eps);
+            const float4 w0 = reinterpret_cast<const float4*>(weight)[2 * at], w1 = reinterpret_cast<const float4*>(weight)[2 * at + 1];
             const float wv[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] = f[e] * scale * wv[e];
           }
         }
-        if (half && p.rot.interleaved) {
-          if ((is_q || is_k) && lane * 8 < 2 * half) {
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-              const float c = cos_s[lane * 4 + e / 2], s = sin_s[lane * 4 + e / 2];
-              const float a = f[e], d = f[e + 1];
-              f[e] = a * c - d * s;
-              f[e + 1] = d * c + a * s;
-            }
-          }
-        } else if (half) {
-          // pair j of element j and j + half, half a multiple of 8: whole chunks apart
-          const int h8 = half / 8;
-          const bool low = lane < h8, rotated = lane < 2 * h8;
-          const int other = rotated ? (low ? lane + h8 : lane - h8) : lane;
+        if (half) {
           float g[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) g[e] = __shfl_sync(0xffffffffu, f[e], other, LG);
-          if ((is_q || is_k) && rotated) {
-            const int j0 = (low ? lane : lane - h8) * 8;
+          for (int e = 0; e < 8; ++e)
+            g[e] = p.rot.interleaved ? f[e ^ 1] : __shfl_sync(0xffffffffu, f[e], other, LG);
+          if (rotated) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float c = cos_s[j0 + e], s = sin_s[j0 + e];
-              f[e] = low ? f[e] * c - g[e] * s : f[e] * c + g[e] * s;
-            }
+            for (int e = 0; e < 8; ++e) f[e] = fmaf(f[e], c[e], g[e] * s[e]);
           }
         }
-        // values, and what is neither normalised nor rotated, pass as their bits
-        if ((is_q || is_k) && (w || half)) y = pack_chunk<T>(f);
+        if (weight || half) y = pack_chunk<T>(f);
       }
-      if (!live) continue;
-      if (is_q) {
-        *(reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.q_out) + row * p.q_out_row + vec * p.q_out_head) + lane) = y;
-      } else if (page >= 0) {
-        const int head = vec - p.q_heads - (is_k ? 0 : p.cs.heads);
-        T* cache = reinterpret_cast<T*>(is_k ? p.k_cache : p.v_cache);
-        *(reinterpret_cast<uint4*>(cache + line + head * p.cs.head) + lane) = y;
-      }
+      if (!on || vec >= n_qk) continue;
+      if (is_q) *reinterpret_cast<uint4*>(q_out + vec * p.q_out_head) = y;
+      else if (page >= 0) *reinterpret_cast<uint4*>(k_cache + (vec - n_q) * p.cs.head) = y;
     }
+  }
+  // ---- values
+  const T* v = static_cast<const T*>(p.v.p) + row * p.v.row + at * 8;
+  T* v_cache = reinterpret_cast<T*>(p.v_cache) + line + at * 8;
+  if (page < 0 || !on) return;
+  for (int first = (p.parts - 1 - part) * G + group; first < p.cs.heads; first += kAppendBatch * step) {
+#pragma unroll
+    for (int u = 0; u < kAppendBatch; ++u)
+      if (first + u * step < p.cs.heads) x[u] = *reinterpret_cast<const uint4*>(v + (first + u * step) * p.v.head);
+#pragma unroll
+    for (int u = 0; u < kAppendBatch; ++u)
+      if (first + u * step < p.cs.heads) *reinterpret_cast<uint4*>(v_cache + (first + u * step) * p.cs.head) = x[u];
   }
 }
 
 template <typename T>
-cudaError_t append_for(const AppendParams& p, cudaStream_t stream) {
+cudaError_t append_for(AppendParams p, cudaStream_t stream) {
   const int chunks = p.cs.head_dim / 8;
   int lg = 2;
   while (lg < chunks) lg *= 2;
-  const int n_vec = p.q_heads + 2 * p.cs.heads;
-  int threads = cdiv((long long)n_vec * lg, 32) * 32;
-  if (threads > 256) threads = 256;
-  const dim3 grid((unsigned)p.rows.N, (unsigned)p.rows.B);
-  auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(threads), 0, stream, p); };
+  static std::atomic<int> cache[kMaxCachedDevices];
+  const int sms = per_device_grid(cache, []() { return 1; });
+  if (sms <= 0) return cudaErrorInvalidConfiguration;
+  // as many warps as the device holds, and none without a head: a row alone takes 3.3 us in 20
+  // parts and 5.3 in 3, 12,004 rows of 9 KB 47 us in one part each (69% of the copy bandwidth) and
+  // 62 with a fifth CTA an SM, whose registers do not suffice
+  const long long places = (long long)p.rows.N * p.rows.B;
+  const int most = cdiv(p.q_heads + p.cs.heads, 32 / lg);
+  const long long wanted = (long long)sms * kAppendCtas * kAppendWarps / places;
+  p.parts = wanted < 1 ? 1 : wanted < most ? (int)wanted : most;
+  const long long ctas = cdiv(places * p.parts, (long long)kAppendWarps);
+  if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  auto go = [&](auto kernel) {
+    return launch_pdl(kernel, dim3((unsigned)ctas), dim3(32 * kAppendWarps), 0, stream, p);
+  };
   switch (lg) {
     case 2: return go(append_kernel<T, 2>);
     case 4: return go(append_kernel<T, 4>);
@@ -272,7 +293,7 @@ cudaError_t launch_cache_append(const HeadRows& q, const HeadRows& k, const Head
                                 const CacheStrides& cs, int dtype, const TargetRows& rows, const TargetSlots& slots,
                                 const Rotation& rot, const HeadNorm& norm, int* err, cudaStream_t stream) {
   AppendParams p = {q, k, v, static_cast<char*>(q_out), static_cast<char*>(k_cache), static_cast<char*>(v_cache),
-                    q_out_row, q_out_head, cs, rows, slots, rot, norm, q_heads, err};
+                    q_out_row, q_out_head, cs, rows, slots, rot, norm, q_heads, 1, err};
   return dtype == DSPARK_BF16 ? append_for<__nv_bfloat16>(p, stream) : append_for<__half>(p, stream);
 }
 

@@ -24,7 +24,7 @@ import ctypes
 from typing import Dict, Optional
 
 from . import DSparkError, Workspace, lib
-from .rows import _device, _done, _on, _rows, _types, _vector
+from .rows import _NOTHING, _device, _done, _on, _rows, _types, _vector
 
 
 class _CacheStruct(ctypes.Structure):
@@ -57,57 +57,74 @@ class PagedCache:
         stride = [0 if size == 1 else step for size, step in zip(shape, stride)]
         self.k, self.v = k, v
         self.layers, self.n_pages, self.page_size, self.heads, self.head_dim = shape
-        self.dtype, self.device = k.dtype, k.device
+        self.dtype, self.device, self.index = k.dtype, k.device, k.get_device()
         self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), codes[k.dtype], *shape, *stride[:4])
         self._ptr = ctypes.addressof(self._struct)
 
 
-def _tokens(lead, starts, counts, nodes, like):
-    """(B or None, N, rows, starts, counts) of rows with the leading dimensions ``lead``."""
+# The checks of a call take longer than its kernel for a single token, so they ask a tensor as
+# little as they can (0.1 us a question), and the checks that tell what is wrong run only then.
+
+def _begin(like, ws, stream):
+    """(device index, stream handle, context in which outputs are allocated for it)."""
     torch, _ = _types()
+    dev = like.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice() or ws.buf.get_device() != dev:
+        _device(like, ws)
+    if stream is None:
+        return dev, torch._C._cuda_getCurrentRawStream(dev), _NOTHING
+    return (dev, *_on(stream, like))
+
+
+def _flat(t, name, n, dtype, like, dev, k=1):
+    """Pointer of a contiguous input or output of n x k entries; None stays None."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.numel() == n * k and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    return _vector(t, name, n, dtype, like, None if k == 1 else k)
+
+
+def _tokens(lead, starts, counts, nodes, like, dev, i32):
+    """(B, N, rows, starts, counts) of rows with the leading dimensions ``lead``."""
     if starts is None:
         if len(lead) != 2:
             raise ValueError(f"rows [B, N, ...] are needed where starts is not given, not {tuple(lead)}")
         B, N = lead
-        return B, N, B * N, None, _vector(counts, "counts", B, torch.int32, like)
+        return B, N, B * N, None, _flat(counts, "counts", B, i32, like, dev)
     if len(lead) != 1 or counts is not None or nodes is None:
         raise ValueError("packed rows have one leading dimension, starts and nodes, and no counts")
-    if starts.numel() < 1:
-        raise ValueError("starts: [B + 1] entries are needed")
     B = starts.numel() - 1
-    return B, nodes, lead[0], _vector(starts, "starts", B + 1, torch.int32, like), None
+    if B < 0:
+        raise ValueError("starts: [B + 1] entries are needed")
+    return B, nodes, lead[0], _flat(starts, "starts", B + 1, i32, like, dev), None
 
 
-def _slots(pages, lengths, B, like):
-    torch, _ = _types()
+def _slots(pages, lengths, B, like, dev, i32):
     if pages.dim() != 2:
         raise ValueError(f"pages: a table [B, max_pages] is needed, not {tuple(pages.shape)}")
     most = pages.shape[1]
-    return (_vector(pages, "pages", B, torch.int32, like, most), most,
-            _vector(lengths, "lengths", B, torch.int32, like))
+    return _flat(pages, "pages", B, i32, like, dev, most), most, _flat(lengths, "lengths", B, i32, like, dev)
 
 
 def _heads(t, name, lead, dim, cache):
     """(pointer, row stride, head stride, heads) of rows of heads."""
-    if t.dtype is not cache.dtype or t.device != cache.device:
+    if t.dtype is not cache.dtype or t.get_device() != cache.index:
         raise ValueError(f"{name}: {cache.dtype} on {cache.device} is needed, not {t.dtype} on {t.device}")
     shape, stride = t.shape, t.stride()
     if len(shape) != len(lead) + 2 or shape[:-2] != lead or shape[-1] != dim:
         raise ValueError(f"{name}: {tuple(lead)} rows of heads of {dim} are needed, not {tuple(shape)}")
     if stride[-1] != 1:
         raise ValueError(f"{name}: its last dimension is not contiguous (strides {tuple(stride)})")
-    if len(lead) == 1:
-        row = stride[0]
-    else:
-        row = stride[1]
-        if lead[0] > 1:
-            if lead[1] == 1:
-                row = stride[0]
-            elif stride[0] != lead[1] * row:
+    heads, n, row = shape[-2], lead[0], stride[0]
+    if len(lead) == 2:
+        N = lead[1]
+        if N != 1:
+            row = stride[1]
+            if n > 1 and stride[0] != N * row:
                 raise ValueError(f"{name}: its leading dimensions do not flatten into rows of one stride "
                                  f"(shape {tuple(shape)}, strides {tuple(stride)})")
-    heads = shape[-2]
-    n = lead[0] if len(lead) == 1 else lead[0] * lead[1]
+        n *= N
     return t.data_ptr(), row if n > 1 else 0, stride[-2] if heads > 1 else 0, heads
 
 
@@ -124,12 +141,11 @@ def cache_append(cache: PagedCache, k, v, pages, lengths, ws: Workspace, q=None,
     times frequency, in pairs (j, j + R / 2), or (2 j, 2 j + 1) with ``interleaved``; the position is
     lengths[b] plus the token's depth in its tree.  A chain may be of any length (a prompt)."""
     torch, _ = _types()
-    f32 = torch.float32
-    _device(k, ws)
-    handle, allocate = _on(stream, k)
+    i32, f32 = torch.int32, torch.float32
+    dev, handle, allocate = _begin(k, ws, stream)
     D = cache.head_dim
     lead = k.shape[:-2]
-    B, N, rows, s, c = _tokens(lead, starts, counts, nodes, k)
+    B, N, rows, s, c = _tokens(lead, starts, counts, nodes, k, dev, i32)
     k_p, k_row, k_head, heads = _heads(k, "k", lead, D, cache)
     v_p, v_row, v_head, v_heads = _heads(v, "v", lead, D, cache)
     if heads != cache.heads or v_heads != heads:
@@ -146,12 +162,12 @@ def cache_append(cache: PagedCache, k, v, pages, lengths, ws: Workspace, q=None,
     elif q_out is not None:
         raise ValueError("q_out is given without q")
     rotated = 0 if inv_freq is None else 2 * inv_freq.numel()
-    table, most, used = _slots(pages, lengths, B, k)
+    table, most, used = _slots(pages, lengths, B, k, dev, i32)
     _done("dspark_cache_append", lib().dspark_cache_append(
-        cache._ptr, layer, s, c, _vector(parents, "parents", rows, torch.int32, k), B, N, rows, table, most, used,
+        cache._ptr, layer, s, c, _flat(parents, "parents", rows, i32, k, dev), B, N, rows, table, most, used,
         k_p, k_row, k_head, v_p, v_row, v_head, q_p or None, q_row, q_head, q_heads, o_p or None, o_row, o_head,
-        _vector(inv_freq, "inv_freq", rotated // 2, f32, k), rotated, interleaved,
-        _vector(q_weight, "q_weight", D, f32, k), _vector(k_weight, "k_weight", D, f32, k), eps,
+        _flat(inv_freq, "inv_freq", rotated // 2, f32, k, dev), rotated, interleaved,
+        _flat(q_weight, "q_weight", D, f32, k, dev), _flat(k_weight, "k_weight", D, f32, k, dev), eps,
         ws.ptr, ws.nbytes, handle))
     return q_out
 
@@ -173,10 +189,10 @@ def tree_attention(q, cache: PagedCache, pages, lengths, ws: Workspace, starts=N
     ``q``; ``lse`` [..., q_heads] fp32, if given, gets the logarithms of the softmax's sums.
     head_dim is 64 or 128, and a request has at most 64 tokens."""
     torch, _ = _types()
-    _device(q, ws)
-    handle, allocate = _on(stream, q)
+    i32 = torch.int32
+    dev, handle, allocate = _begin(q, ws, stream)
     lead, D = q.shape[:-2], cache.head_dim
-    B, N, rows, s, c = _tokens(lead, starts, counts, nodes, q)
+    B, N, rows, s, c = _tokens(lead, starts, counts, nodes, q, dev, i32)
     q_p, q_row, q_head, q_heads = _heads(q, "q", lead, D, cache)
     if out is None:
         with allocate:
@@ -184,11 +200,11 @@ def tree_attention(q, cache: PagedCache, pages, lengths, ws: Workspace, starts=N
     o_p, o_row, o_head, o_heads = _heads(out, "out", lead, D, cache)
     if o_heads != q_heads:
         raise ValueError(f"out: {q_heads} heads are needed, not {o_heads}")
-    table, most, used = _slots(pages, lengths, B, q)
+    table, most, used = _slots(pages, lengths, B, q, dev, i32)
     _done("dspark_tree_attention", lib().dspark_tree_attention(
-        cache._ptr, layer, s, c, _vector(parents, "parents", rows, torch.int32, q), B, N, rows, table, most, used,
+        cache._ptr, layer, s, c, _flat(parents, "parents", rows, i32, q, dev), B, N, rows, table, most, used,
         q_p, q_row, q_head, q_heads, D ** -0.5 if scale is None else scale, o_p, o_row, o_head,
-        _vector(lse, "lse", rows, torch.float32, q, q_heads), ws.ptr, ws.nbytes, handle))
+        _flat(lse, "lse", rows, torch.float32, q, dev, q_heads), ws.ptr, ws.nbytes, handle))
     return out
 
 
@@ -206,13 +222,12 @@ def tree_verify(p, tokens, uniforms, ws: Workspace, q=None, starts=None, counts=
     torch, _ = _types()
     i32 = torch.int32
     code, n, V, ld = _rows(p, "p")
-    _device(p, ws)
-    handle, allocate = _on(stream, p)
-    B, N, rows, s, c = _tokens(p.shape[:-1], starts, counts, nodes, p)
+    dev, handle, allocate = _begin(p, ws, stream)
+    B, N, rows, s, c = _tokens(p.shape[:-1], starts, counts, nodes, p, dev, i32)
     ld_q, q_p = ld, None
     if q is not None:
         code_q, n_q, V_q, ld_q = _rows(q, "q")
-        if (code_q, n_q, V_q) != (code, n, V) or q.device != p.device:
+        if (code_q, n_q, V_q) != (code, n, V) or q.get_device() != dev:
             raise ValueError(f"q: {n} x {V} {p.dtype} on {p.device} are needed, not {tuple(q.shape)} {q.dtype}")
         q_p = q.data_ptr()
     if out is None:
@@ -222,10 +237,10 @@ def tree_verify(p, tokens, uniforms, ws: Workspace, q=None, starts=None, counts=
                    "out_tokens": torch.empty((B, N), dtype=i32, device=p.device),
                    "n_out": torch.empty(B, dtype=i32, device=p.device)}
     _done("dspark_tree_verify", lib().dspark_tree_verify(
-        p.data_ptr(), ld, q_p, ld_q, code, V, _vector(tokens, "tokens", rows, i32, p),
-        _vector(uniforms, "uniforms", rows, torch.float32, p), s, c, _vector(parents, "parents", rows, i32, p), B, N,
-        rows, _vector(out["accept_len"], "accept_len", B, i32, p), _vector(out["path"], "path", B, i32, p, N),
-        _vector(out["out_tokens"], "out_tokens", B, i32, p, N), _vector(out["n_out"], "n_out", B, i32, p),
+        p.data_ptr(), ld, q_p, ld_q, code, V, _flat(tokens, "tokens", rows, i32, p, dev),
+        _flat(uniforms, "uniforms", rows, torch.float32, p, dev), s, c, _flat(parents, "parents", rows, i32, p, dev),
+        B, N, rows, _flat(out["accept_len"], "accept_len", B, i32, p, dev), _flat(out["path"], "path", B, i32, p, dev, N),
+        _flat(out["out_tokens"], "out_tokens", B, i32, p, dev, N), _flat(out["n_out"], "n_out", B, i32, p, dev),
         ws.ptr, ws.nbytes, handle))
     return out
 
@@ -238,10 +253,10 @@ def cache_keep(cache: PagedCache, pages, lengths, path, accept_len, ws: Workspac
     torch, _ = _types()
     if path.dim() != 2:
         raise ValueError(f"path: [B, N] is needed, not {tuple(path.shape)}")
-    _device(cache.k, ws)
-    handle, _ = _on(stream, cache.k)
+    i32, k = torch.int32, cache.k
+    dev, handle, _ = _begin(k, ws, stream)
     B, N = path.shape
-    table, most, used = _slots(pages, lengths, B, cache.k)
+    table, most, used = _slots(pages, lengths, B, k, dev, i32)
     _done("dspark_cache_keep", lib().dspark_cache_keep(
-        cache._ptr, B, N, table, most, used, _vector(path, "path", B, torch.int32, cache.k, N),
-        _vector(accept_len, "accept_len", B, torch.int32, cache.k), ws.ptr, ws.nbytes, handle))
+        cache._ptr, B, N, table, most, used, _flat(path, "path", B, i32, k, dev, N),
+        _flat(accept_len, "accept_len", B, i32, k, dev), ws.ptr, ws.nbytes, handle))
