@@ -485,7 +485,8 @@ dspark_status dspark_last_device_status(void* workspace, cudaStream_t stream) {
   if (cudaMemcpy(&code, workspace, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
     return DSPARK_ERR_CUDA;
   if (code != 0) {
-    if (cudaMemset(workspace, 0, sizeof(int)) != cudaSuccess) return DSPARK_ERR_CUDA;
+    // (with the counts of CTAs that a call which failed may have left there)
+    if (cudaMemset(workspace, 0, 256) != cudaSuccess) return DSPARK_ERR_CUDA;
     return (dspark_status)code;
   }
   return DSPARK_OK;

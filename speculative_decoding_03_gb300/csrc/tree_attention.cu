@@ -16,8 +16,8 @@
 // while this one's softmax runs.  The running maximum is raised only when a tile exceeds it by
 // more than 2^8 (then O, in tensor memory, is rescaled; P <= 256 keeps its 16-bit rounding
 // relative).  Pieces that hold only some of their tiles leave O, maximum and sum in the
-// workspace in fp32, and a second kernel joins them in tile order, so results do not depend on
-// the order in which CTAs run.
+// workspace in fp32, and the CTA that comes last joins them in tile order, so results do not
+// depend on the order in which CTAs run.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -38,6 +38,8 @@ constexpr int kTile = 128;                 // slots of a tile, and rows of a blo
 constexpr int kThreads = 256;
 constexpr int kProducerWarp = 0, kIssueWarp = 1, kSoftmaxWarp = 4;
 constexpr float kRaise = 8.f;              // log2 of what the maximum may lag behind
+constexpr int kMaxGrid = 160;              // CTAs of the persistent grid at most
+constexpr int kJoinRows = 16, kJoinParts = 24;   // what one CTA joins at most
 constexpr int kPieceUnits = 4;             // what beginning and ending a piece costs, in tiles
 
 // How a tile's lines lie in memory and in shared memory, in groups of 8 lines of 128 bytes.
@@ -60,8 +62,11 @@ struct AttendParams {
   TargetSlots slots;
   int group;                               // query heads a key head
   float scale_log2;
-  float* partial;                          // [2 CTAs][128][head_dim + 2]
-  int4* joins;                             // [CTAs]: request, row block, head, parts
+  float* partial;                          // [2 CTAs][128][head_dim]
+  float2* sums;                            // [2 CTAs][128] maxima (log2) and sums
+  bool join_apart;                         // parts are joined by a kernel of their own
+  uint32_t* arrived;                       // a byte a CTA: parts that have come of the piece it began
+  int4* joins;                             // [CTAs]: request, row block, head, parts of the piece it began
   int* err;
 };
 
@@ -155,18 +160,22 @@ __device__ __forceinline__ Request request_of(const AttendParams& p, int b, int 
 
 // The pieces of a CTA's share [lo, hi) of the units, in order.
 struct Pieces {
-  long long left;            // units still to come
+  long long left, unit;      // units still to come, the next one's place among all
   int b, off, block_rows;    // the next unit: `off` of request b's
   Request r;
   // the current piece
   int block, head, tile0, n_tiles;
+  long long unit0;           // tile 0's place among all units
   bool whole;
-  __device__ __forceinline__ void start(const AttendParams& p, int rows, int b0, int off0, long long units) {
+  __device__ __forceinline__ void start(const AttendParams& p, int rows, const int* start_s, long long lo,
+                                        long long hi) {
     block_rows = rows;
-    b = b0;
-    off = off0;
-    left = units;
-    if (left > 0) r = request_of(p, b, block_rows);
+    left = hi - lo;
+    if (left <= 0) return;
+    b = start_s[0];
+    off = start_s[1];
+    unit = lo;
+    r = request_of(p, b, block_rows);
   }
   __device__ __forceinline__ bool next(const AttendParams& p) {
     while (left > 0) {
@@ -181,6 +190,8 @@ struct Pieces {
       tile0 = max(from - kPieceUnits, 0);
       n_tiles = from + take - kPieceUnits - tile0;
       whole = n_tiles == r.tiles;
+      unit0 = unit - from + kPieceUnits;
+      unit += take;
       off += take;
       left -= take;
       if (n_tiles > 0) return true;
@@ -236,10 +247,17 @@ __device__ __forceinline__ Share share_units(const AttendParams& p, int block_ro
   return s;
 }
 
-// CTAs that share the `tiles` tiles whose units start at g0, the first of which is this one's.
-__device__ __forceinline__ int parts_of(const Share& s, long long g0, int tiles) {
-  return (int)(((g0 + tiles) * s.G - 1) / s.total - blockIdx.x) + 1;
+// The CTAs that share the `tiles` tiles whose units start at unit0: the first, and how many.
+struct Parts {
+  int first, n;
+};
+__device__ __forceinline__ Parts parts_of(const Share& s, long long unit0, int tiles) {
+  auto cta = [&](long long unit) { return (int)(((unit + 1) * s.G - 1) / s.total); };
+  const int first = cta(unit0);
+  return {first, cta(unit0 + tiles - 1) - first + 1};
 }
+// Where CTA `cta` leaves a part: a piece's first (its CTA's last piece) or another (its CTA's first).
+__device__ __forceinline__ int part_place(int cta, bool first) { return 2 * cta + (first ? 1 : 0); }
 
 // Bounded waits: one that runs out reports it and makes the CTA's others return too.
 struct Waits {
@@ -371,6 +389,121 @@ __device__ __forceinline__ bool clear_line(uint8_t* tile, TileForm form, int r, 
   return bad;
 }
 
+// A barrier of the four softmax warps; true in all of them if `any` is in one.
+__device__ __forceinline__ bool meet_or(bool any) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 128, p;\n\t"
+      "selp.b32 %0, 1, 0, q;\n\t}" : "=r"(r) : "r"((int)any) : "memory");
+  return r != 0;
+}
+
+// The four softmax warps' part of a piece is written: true in all of them if it was the last to
+// come, whose CTA joins all.  The count is left at zero for the next call.  (A part that could not
+// be computed is not counted: then nobody joins, and the status says why.)
+__device__ __forceinline__ bool last_part(const AttendParams& p, const Parts& parts, bool ok, int* word_s) {
+  if (meet_or(!ok)) return false;
+  if ((threadIdx.x & 127) == 0) {
+    // (bytes 64 to 127 and 132 to 255 of the workspace: another call counts at 128)
+    uint32_t* word = p.arrived + (parts.first >> 2) + (parts.first >= 64 ? 1 : 0);
+    const int shift = 8 * (parts.first & 3);
+    __threadfence();
+    const bool last = (int)(atomicAdd(word, 1u << shift) >> shift & 255) == parts.n - 1;
+    __threadfence();
+    if (last) atomicSub(word, (uint32_t)parts.n << shift);
+    *word_s = last;
+  }
+  meet_or(false);
+  return *word_s != 0;
+}
+
+// Joins the parts of `rows` rows of a piece, the first of which is row `first` of its request's head,
+// a warp 4 of them at once: o = sum_k 2^(m_k - M) o_k / sum_k 2^(m_k - M) l_k, in the parts' order.
+// The parts' outputs come while their maxima do.
+template <typename T, int D>
+__device__ __forceinline__ void join_parts(const AttendParams& p, const Parts& parts, int row0, int first, int rows,
+                                           int head0) {
+  const int lane = threadIdx.x & 31, w4 = (threadIdx.x >> 5) & 3;
+  constexpr int E = D / 32;
+  auto line = [&](int k, int row) { return (long long)part_place(parts.first + k, k == 0) * kTile + row; };
+  float x[4][4][E];
+  auto load = [&](int k0, int r0) {        // parts k0 .. k0 + 3 of the rows r0 + 4 u
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bool on = k0 + j < parts.n && r0 + 4 * u < rows;
+        const float* from = p.partial + line(k0 + j, r0 + 4 * u) * D + lane * E;
+        if constexpr (E == 4) {
+          const float4 v = on ? __ldcg(reinterpret_cast<const float4*>(from)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          x[j][u][0] = v.x;
+          x[j][u][1] = v.y;
+          x[j][u][2] = v.z;
+          x[j][u][3] = v.w;
+        } else {
+          const float2 v = on ? __ldcg(reinterpret_cast<const float2*>(from)) : make_float2(0.f, 0.f);
+          x[j][u][0] = v.x;
+          x[j][u][1] = v.y;
+        }
+      }
+  };
+#pragma unroll 1
+  for (int r0 = w4; r0 < rows; r0 += 16) {
+    load(0, r0);
+    // lane 8 u + k looks after row r0 + 4 u and the parts k, k + 8, ..
+    const int my_row = r0 + 4 * (lane >> 3), my_k = lane & 7;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (my_k < parts.n && my_row < rows) ml = __ldcg(p.sums + line(my_k, my_row));
+    float M = ml.x;
+    for (int k = my_k + 8; k < parts.n; k += 8)
+      if (my_row < rows) M = fmaxf(M, __ldcg(p.sums + line(k, my_row)).x);
+#pragma unroll
+    for (int m = 4; m >= 1; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
+    float o[4][E], l = 0.f, f = 0.f;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[u][e] = 0.f;
+#pragma unroll 1
+    for (int k0 = 0; k0 < parts.n; k0 += 4) {
+      if ((k0 & 7) == 0) {
+        if (k0 > 0) {
+          ml = make_float2(-INFINITY, 0.f);
+          if (k0 + my_k < parts.n && my_row < rows) ml = __ldcg(p.sums + line(k0 + my_k, my_row));
+        }
+        f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+        l = fmaf(ml.y, f, l);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float fj = __shfl_sync(0xffffffffu, f, 8 * u + (k0 & 4) + j);
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[u][e] = fmaf(x[j][u][e], fj, o[u][e]);
+        }
+      if (k0 + 4 < parts.n) load(k0 + 4, r0);
+    }
+#pragma unroll
+    for (int m = 4; m >= 1; m >>= 1) l += __shfl_xor_sync(0xffffffffu, l, m);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int r = r0 + 4 * u;
+      const float lu = __shfl_sync(0xffffffffu, l, 8 * u), Mu = __shfl_sync(0xffffffffu, M, 8 * u);
+      if (r >= rows) continue;
+      const float inv = lu > 0.f ? 1.f / lu : lu == 0.f ? 0.f : lu;       // (NaN stays)
+      const int i_r = first + r, i = i_r / p.group, row = row0 + i;
+      const int head = head0 * p.group + (i_r - i * p.group);
+      T* dst = reinterpret_cast<T*>(p.out) + row * p.out_row + head * p.out_head + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; e += 2)
+        *reinterpret_cast<uint32_t*>(dst + e) = pack2<T>(o[u][e] * inv, o[u][e + 1] * inv);
+      if (p.lse && lane == 0)
+        p.lse[(long long)row * p.group * p.cs.heads + head] = lu == 0.f ? -INFINITY : (Mu + log2f(lu)) * 0.6931471805599453f;
+    }
+  }
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_constant__ CUtensorMap k_map,
                                                              const __grid_constant__ CUtensorMap v_map,
@@ -423,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
   pdl_launch_dependents();
 
   const Share share = share_units(p, kTile, sums_s, start_s);
-  if (tid == 0) p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (tid == 0 && p.join_apart) p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -433,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
 
   Pieces pc;
   pc.left = 0;
-  if (share.hi > share.lo) pc.start(p, kTile, start_s[0], start_s[1], share.hi - share.lo);
+  pc.start(p, kTile, start_s, share.lo, share.hi);
 
   if (warp == kProducerWarp) {
     TileCopies<S> copies{smem + S::kOffKV, kv_full, kv_empty, wait, p, pc, policy_evict_first()};
@@ -534,14 +667,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
 
     bool more = pc.next(p);
     if (more) begin();
-    while (more && ok) {
+    while (more) {
       const int b = pc.b, head = pc.head, block = pc.block, tile0 = pc.tile0, n = pc.n_tiles;
       const bool whole = pc.whole, my_busy = busy;
       const Request rq = pc.r;
       const int my_row = row, my_head = q_head;
       const unsigned long long my_sees = sees;
       float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < n; ++j) {
+      for (int j = 0; j < n && ok; ++j) {
         const uint32_t t = tc + j, buf = t & 1;
         const int slot0 = (tile0 + j) * kTile;
         const bool masked = slot0 + kTile > rq.len;
@@ -623,19 +756,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
         }
         mbar_arrive(&p_full[buf]);
       }
-      if (!ok) break;
       // the next piece's queries go in while this one's last product runs
+      const Parts parts = whole ? Parts{0, 1} : parts_of(share, pc.unit0, rq.tiles);
       more = pc.next(p);
-      if (more) begin();
+      if (more && ok) begin();
       const uint32_t t_last = tc + n - 1;
-      ok = __all_sync(0xffffffffu, wait(&o_full[t_last & 1], (t_last >> 1) & 1));
-      if (!ok) break;
+      ok = ok && __all_sync(0xffffffffu, wait(&o_full[t_last & 1], (t_last >> 1) & 1));
       tc_fence_after_sync();
       const bool bad = bad_s[piece & 1] == (int)piece + 1;
-      if (my_busy) {
+      if (my_busy && ok) {
         const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;     // (NaN stays)
-        const int slot_part = 2 * blockIdx.x + (tile0 == 0 ? 1 : 0);
-        float* part = p.partial + ((long long)slot_part * kTile + r) * (D + 2);
+        const long long line = (long long)part_place(blockIdx.x, tile0 == 0) * kTile + r;
+        float* part = p.partial + line * D;
         T* dst = reinterpret_cast<T*>(p.out) + my_row * p.out_row + my_head * p.out_head;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
@@ -673,24 +805,27 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
               }
             } else {
 #pragma unroll
-              for (int e = 0; e < 32; e += 2)
-                *reinterpret_cast<float2*>(part + 32 * c + e) = make_float2(o[e], o[e + 1]);
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<float4*>(part + 32 * c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
           }
         }
         if (my_row >= 0) {
           if (!whole) {
-            part[D] = m == -INFINITY ? -INFINITY : m * sl;
-            part[D + 1] = l;
+            p.sums[line] = make_float2(m == -INFINITY ? -INFINITY : m * sl, l);
           } else if (p.lse) {
             p.lse[(long long)my_row * p.group * p.cs.heads + my_head] =
                 l == 0.f ? -INFINITY : (m * sl + log2f(l)) * 0.6931471805599453f;
           }
         }
       }
-      if (!whole && tile0 == 0 && r == 0) {
-        // the first part of several, and so the last piece of this CTA
-        p.joins[blockIdx.x] = make_int4(b, block, head, parts_of(share, share.hi - n, rq.tiles));
+      // (a warp whose wait ran out still meets the others)
+      if (!whole) {
+        if (p.join_apart) {
+          if (tile0 == 0 && r == 0 && ok) p.joins[blockIdx.x] = make_int4(b, block, head, parts.n);
+        } else if (last_part(p, parts, ok, words + 6)) {
+          join_parts<T, D>(p, parts, rq.row0, block * kTile, min(kTile, rq.n * p.group - block * kTile), head);
+        }
       }
       tc_fence_before_sync();
       tc += n;
@@ -731,16 +866,8 @@ struct NarrowSmem {
 
 struct PieceInfo {           // what the loading warps say of a piece; no tiles: it was the last
   int b, head, block, tile0, n_tiles, tiles, row0, n, len, end, rows;
+  Parts parts;
 };
-
-// A barrier of the four softmax warps; true in all of them if `any` is in one.
-__device__ __forceinline__ bool meet_or(bool any) {
-  int r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 128, p;\n\t"
-      "selp.b32 %0, 1, 0, q;\n\t}" : "=r"(r) : "r"((int)any) : "memory");
-  return r != 0;
-}
 
 __device__ __forceinline__ float warp_max(float x) {      // (NaN only if every lane's is)
   float y;
@@ -835,7 +962,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
   pdl_wait();
   pdl_launch_dependents();
   const Share share = share_units(p, kRows, sums_s, start_s);
-  if (tid == 0) p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (tid == 0 && p.join_apart) p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -845,7 +972,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
   pc.left = 0;
 
   if (warp == kProducerWarp) {
-    if (share.hi > share.lo) pc.start(p, kRows, start_s[0], start_s[1], share.hi - share.lo);
+    pc.start(p, kRows, start_s, share.lo, share.hi);
     TileCopies<S> copies{smem + S::kOffKV, kv_full, kv_empty, wait, p, pc, policy_evict_first()};
     copies.run(&k_map, &v_map);
   } else if (warp == kIssueWarp) {
@@ -914,7 +1041,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
     // ------------------------------------------------------------------ queries, a thread a row
     const int col = tid - 32 * kLoadWarp;
     int* par = parents_s + 64 * (warp - kLoadWarp);
-    if (share.hi > share.lo) pc.start(p, kRows, start_s[0], start_s[1], share.hi - share.lo);
+    pc.start(p, kRows, start_s, share.lo, share.hi);
     for (uint32_t piece = 0;; ++piece) {
       const uint32_t q = piece & 1;
       const bool more = pc.next(p);
@@ -954,7 +1081,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
       }
       to_s[64 * q + col] = (long long)(pc.r.row0 + i) * p.out_row + head * p.out_head;
       if (col == 0)
-        info_s[q] = {pc.b, pc.head, pc.block, pc.tile0, pc.n_tiles, pc.r.tiles, pc.r.row0, pc.r.n, pc.r.len, pc.r.end, rows};
+        info_s[q] = {pc.b, pc.head, pc.block, pc.tile0, pc.n_tiles, pc.r.tiles, pc.r.row0, pc.r.n, pc.r.len, pc.r.end, rows,
+                     pc.whole ? Parts{0, 1} : parts_of(share, pc.unit0, pc.r.tiles)};
       fence_proxy_async_smem();
       mbar_arrive(&q_full[q]);
     }
@@ -1109,7 +1237,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
       if (lost) break;
       // ---- the piece's rows: sums over the warps, then O
       const bool whole = n == rq.tiles;
-      float* part = p.partial + (long long)(2 * blockIdx.x + (tile0 == 0 ? 1 : 0)) * kTile * (D + 2);
+      const long long line = (long long)part_place(blockIdx.x, tile0 == 0) * kTile;
+      float* part = p.partial + line * D;
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
         if (c >= chunks) break;
@@ -1124,8 +1253,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
         const float s = (sum_s[r] + sum_s[64 + r]) + (sum_s[128 + r] + sum_s[192 + r]);
         down_s[r] = !whole ? 1.f : s > 0.f ? 1.f / s : s == 0.f ? 0.f : s;       // (NaN stays)
         if (!whole) {
-          part[r * (D + 2) + D] = best_s[r];
-          part[r * (D + 2) + D + 1] = s;
+          p.sums[line + r] = make_float2(best_s[r], s);
         } else if (p.lse) {
           const int i_r = rq.block * kRows + r, i = i_r / p.group;
           p.lse[(long long)(rq.row0 + i) * p.group * p.cs.heads + rq.head * p.group + (i_r - i * p.group)] =
@@ -1168,17 +1296,21 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
           for (int e = 0; e < 16; ++e)
             if (e < left) out[to_s[64 * q + 16 * c + e]] = elem_from_float<T>(o[e] * down_s[16 * c + e]);
         } else {
-          float* to = part + 16 * c * (D + 2) + r;
+          float* to = part + 16 * c * D + r;
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            if (e < left) to[e * (D + 2)] = o[e];
+            if (e < left) to[e * D] = o[e];
         }
       }
-      if (!whole && tile0 == 0 && r == 0 && ok)
-        // the first part of several, and so the last piece of this CTA
-        p.joins[blockIdx.x] = make_int4(rq.b, rq.block, rq.head, parts_of(share, share.hi - n, rq.tiles));
       tc_fence_before_sync();
       mbar_arrive(&q_free[q]);
+      if (!whole) {
+        if (p.join_apart) {
+          if (tile0 == 0 && r == 0 && ok) p.joins[blockIdx.x] = make_int4(rq.b, rq.block, rq.head, rq.parts.n);
+        } else if (last_part(p, rq.parts, ok, words + 6)) {
+          join_parts<T, D>(p, rq.parts, rq.row0, rq.block * kRows, rows, rq.head);
+        }
+      }
     }
   }
   __syncthreads();
@@ -1188,61 +1320,22 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
   }
 }
 
-// Joins the parts of a (request, row block, head) that several CTAs share: CTA (c, y) those of
-// the piece that CTA c began and left unfinished, 8 rows from 8 y on, a warp a row.
+// The same in a kernel of its own: CTA (c, y) the parts of the piece that CTA c began and left
+// unfinished, the rows from 16 y on.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttendParams p, int block_rows) {
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttendParams p, int block_rows) {
   pdl_wait();
   pdl_launch_dependents();
-  const int c = blockIdx.x, lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
-  const int4 join = p.joins[c];
+  const int4 join = p.joins[blockIdx.x];
   if (join.w < 2) return;
   const RequestRows rows = request_rows(p.rows, join.x, nullptr);
-  const int i_r = join.y * block_rows + r, i = i_r / p.group;
-  if (i >= rows.n) return;
-  auto part = [&](int k) {
-    return p.partial + ((long long)(2 * (c + k) + (k == 0 ? 1 : 0)) * kTile + r) * (D + 2);
-  };
-  float M = -INFINITY;
-  for (int k = lane; k < join.w; k += 32) M = fmaxf(M, part(k)[D]);
-#pragma unroll
-  for (int m = 16; m >= 1; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
-  constexpr int E = D / 32;
-  float o[E], l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-  for (int k0 = 0; k0 < join.w; k0 += 4) {
-    float x[4][E], ml[4][2];
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (k0 + u < join.w) {
-        const float* a = part(k0 + u);
-        ml[u][0] = a[D];
-        ml[u][1] = a[D + 1];
-#pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const float2 v = *reinterpret_cast<const float2*>(a + lane * E + e);
-          x[u][e] = v.x;
-          x[u][e + 1] = v.y;
-        }
-      }
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (k0 + u < join.w) {
-        const float f = ml[u][0] == -INFINITY ? 0.f : ex2_approx(ml[u][0] - M);
-        l = fmaf(ml[u][1], f, l);
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(x[u][e], f, o[e]);
-      }
-  }
-  const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
-  const int row = rows.row0 + i, head = join.z * p.group + (i_r - i * p.group);
-  T* dst = reinterpret_cast<T*>(p.out) + row * p.out_row + head * p.out_head + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; e += 2)
-    *reinterpret_cast<uint32_t*>(dst + e) = pack2<T>(o[e] * inv, o[e + 1] * inv);
-  if (p.lse && lane == 0)
-    p.lse[(long long)row * p.group * p.cs.heads + head] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+  const int first = join.y * block_rows + 16 * blockIdx.y;
+  const int n = min(min(block_rows - 16 * (int)blockIdx.y, 16), rows.n * p.group - first);
+  if (n <= 0) return;
+  AttendParams q = p;
+  q.partial += 16 * blockIdx.y * D;
+  q.sums += 16 * blockIdx.y;
+  join_parts<T, D>(q, {(int)blockIdx.x, join.w}, rows.row0, first, n, join.z);
 }
 
 TileForm tile_form(const CacheStrides& cs, const TargetSlots& slots) {
@@ -1274,8 +1367,7 @@ bool encode_cache_map(CUtensorMap* map, const void* base, bool bf16, const Cache
   return encode({64, 8, 2, page / 8, pages * heads}, {slot_b, 128, 8 * slot_b, head_b}, {64, 8, 2, lines / 8, 1});
 }
 
-constexpr int kMaxGrid = 160;              // CTAs of the persistent grid at most
-size_t joins_bytes() { return align_up((size_t)kMaxGrid * sizeof(int4), 256); }
+static_assert(kMaxGrid <= 188, "the counts' place");
 
 template <typename T, int D>
 cudaError_t attend_for(AttendParams p, const TargetSlots& slots, bool bf16, cudaStream_t stream) {
@@ -1296,13 +1388,21 @@ cudaError_t attend_for(AttendParams p, const TargetSlots& slots, bool bf16, cuda
     return cudaErrorInvalidValue;
   const int rows = p.rows.N * p.group;
   const bool narrow = rows <= NarrowSmem<D>::kRows;
+  // A piece has one of its request's heads, so at most a head's share of the grid in parts and the
+  // two at its ends, and a tile each.  Up to 16 rows of few parts are joined by the CTA that comes
+  // last (a token of 4 rows and 8 parts: 11.3 us either way; 35 short requests without parts: 9.8
+  // us, and 11.7 with a second kernel that finds nothing to do); more of them would keep that CTA
+  // from its other pieces (128 rows of 6 parts: 28 us, and 14 by a kernel of their own).
+  const int most_tiles = (int)((((long long)slots.max_pages << slots.page_shift) + kTile - 1) / kTile);
+  const int most_parts = min(grid / p.cs.heads + 2, most_tiles);
+  p.join_apart = most_parts > 1 && (rows > kJoinRows || most_parts > kJoinParts);
   const cudaError_t e =
       narrow ? launch_pdl(attend_narrow_kernel<T, D>, dim3(grid), dim3(kThreads), NarrowSmem<D>::kBytes, stream, k_map,
                           v_map, p)
              : launch_pdl(attend_wide_kernel<T, D>, dim3(grid), dim3(kThreads), AttendSmem<D>::kBytes, stream, k_map,
                           v_map, p);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(join_kernel<T, D>, dim3(grid, cdiv(rows < kTile ? rows : kTile, 8)), dim3(256), 0, stream, p,
+  if (e != cudaSuccess || !p.join_apart) return e;
+  return launch_pdl(join_kernel<T, D>, dim3(grid, cdiv(rows < kTile ? rows : kTile, 16)), dim3(128), 0, stream, p,
                     narrow ? NarrowSmem<D>::kRows : kTile);
 }
 
@@ -1313,7 +1413,7 @@ size_t tree_attention_bytes(int B, int N, int q_heads, int heads, int head_dim) 
   (void)N;
   (void)q_heads;
   (void)heads;
-  return 256 + joins_bytes() + (size_t)2 * kMaxGrid * kTile * (head_dim + 2) * sizeof(float);
+  return 256 + align_up(kMaxGrid * sizeof(int4), 256) + (size_t)2 * kMaxGrid * kTile * (head_dim + 2) * sizeof(float);
 }
 
 cudaError_t launch_tree_attention(const HeadRows& q, int q_heads, const void* k_cache, const void* v_cache,
@@ -1333,8 +1433,10 @@ cudaError_t launch_tree_attention(const HeadRows& q, int q_heads, const void* k_
   p.slots = slots;
   p.group = q_heads / cs.heads;
   p.scale_log2 = scale * kLog2e;
+  p.arrived = ws_at<uint32_t>(ws, 64);
   p.joins = ws_at<int4>(ws, 256);
-  p.partial = ws_at<float>(ws, 256 + joins_bytes());
+  p.partial = ws_at<float>(ws, 256 + align_up(kMaxGrid * sizeof(int4), 256));
+  p.sums = reinterpret_cast<float2*>(p.partial + (size_t)2 * kMaxGrid * kTile * cs.head_dim);
   p.err = err;
   const bool bf16 = dtype == DSPARK_BF16;
   if (cs.head_dim == 128)
