@@ -1067,17 +1067,24 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
         __syncwarp();
         if (live)
           for (int a = i; a >= 0; a = par[a]) sees |= 1ull << a;
-      } else if (live) {
-        sees = (2ull << i) - 1;                // (i = 63: all)
       }
       // the piece before the last has ended
       if (!__all_sync(0xffffffffu, wait(&q_free[q], ((piece >> 1) & 1) ^ 1))) break;
 #pragma unroll
       for (int c = 0; c < D / 8; ++c)
         *reinterpret_cast<uint4*>(smem + S::kOffQ + q * S::kQ + c / 8 * S::kQHalf + col * 128 + ((c ^ col) & 7) * 16) = x[c];
-      for (int a = 0; a < pc.r.n; ++a) {
-        const uint32_t who = __ballot_sync(0xffffffffu, (sees >> a) & 1);
-        if (lane == (a & 31)) seen_s[128 * q + 2 * a + (warp - kLoadWarp)] = who;
+      if (p.rows.parents) {
+#pragma unroll 4
+        for (int a = 0; a < pc.r.n; ++a) {
+          const uint32_t who = __ballot_sync(0xffffffffu, (sees >> a) & 1);
+          if (lane == (a & 31)) seen_s[128 * q + 2 * a + (warp - kLoadWarp)] = who;
+        }
+      } else {
+        // token a of a chain: the columns from a group - first on
+        for (int a = lane; a < pc.r.n; a += 32) {
+          const int from = a * p.group - pc.block * kRows - 32 * (warp - kLoadWarp);
+          seen_s[128 * q + 2 * a + (warp - kLoadWarp)] = from >= 32 ? 0u : ~0u << max(from, 0);
+        }
       }
       to_s[64 * q + col] = (long long)(pc.r.row0 + i) * p.out_row + head * p.out_head;
       if (col == 0)
@@ -1266,12 +1273,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
       tc_fence_after_sync();
       const bool bad = bad_s[q] == (int)piece + 1;
 #pragma unroll 1
-      for (int c = 0; c < chunks; ++c) {
-        uint32_t vo[16];
-        tmem_ld_32x32b_sync<16>(tmem + lanes + kColO + 16 * c, vo);
-        float o[16];
+      for (int w = 0; w < 2; ++w) {            // 32 rows at a time
+        const int left = rows - 32 * w;
+        if (left <= 0) break;
+        uint32_t v[32];
+        tmem_ld_32x32b_sync<32>(tmem + lanes + kColO + 32 * w, v);
+        float o[32];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(vo[e]);
+        for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(v[e]);
         if (r >= D || !ok) continue;
         if (bad) {
           // the values that were left out, where a row sees their token
@@ -1283,22 +1292,25 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
             const float f = elem_to_float(static_cast<const T*>(p.v)[page * p.cs.page + (at & ((1 << p.slots.page_shift) - 1)) * p.cs.slot +
                                                                     rq.head * p.cs.head + r]);
             if (f - f == 0.f) continue;
-            const uint32_t bits = seen_s[128 * q + 2 * a + c / 2] >> (16 * (c & 1));
+            const uint32_t bits = seen_s[128 * q + 2 * a + w];
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
+            for (int e = 0; e < 32; ++e)
               if ((bits >> e) & 1) o[e] += f;
           }
         }
-        const int left = rows - 16 * c;
         if (whole) {
           T* out = reinterpret_cast<T*>(p.out) + r;
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (e < left) out[to_s[64 * q + 16 * c + e]] = elem_from_float<T>(o[e] * down_s[16 * c + e]);
+          for (int e = 0; e < 32; e += 2) {
+            const longlong2 to = *reinterpret_cast<const longlong2*>(to_s + 64 * q + 32 * w + e);
+            const float2 inv = *reinterpret_cast<const float2*>(down_s + 32 * w + e);
+            if (e < left) out[to.x] = elem_from_float<T>(o[e] * inv.x);
+            if (e + 1 < left) out[to.y] = elem_from_float<T>(o[e + 1] * inv.y);
+          }
         } else {
-          float* to = part + 16 * c * D + r;
+          float* to = part + 32 * w * D + r;
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
+          for (int e = 0; e < 32; ++e)
             if (e < left) to[e * D] = o[e];
         }
       }
