@@ -158,7 +158,13 @@ __device__ __forceinline__ Request request_of(const AttendParams& p, int b, int 
   return r;
 }
 
-// The pieces of a CTA's share [lo, hi) of the units, in order.
+// A CTA's share [lo, hi) of all `total` units, which the first G CTAs have.
+struct Share {
+  long long lo, hi, total, G;
+  int b, off;                // the first unit's request, and its place among the request's
+};
+
+// The pieces of a CTA's share of the units, in order.
 struct Pieces {
   long long left, unit;      // units still to come, the next one's place among all
   int b, off, block_rows;    // the next unit: `off` of request b's
@@ -167,14 +173,13 @@ struct Pieces {
   int block, head, tile0, n_tiles;
   long long unit0;           // tile 0's place among all units
   bool whole;
-  __device__ __forceinline__ void start(const AttendParams& p, int rows, const int* start_s, long long lo,
-                                        long long hi) {
+  __device__ __forceinline__ void start(const AttendParams& p, int rows, const Share& s) {
     block_rows = rows;
-    left = hi - lo;
+    left = s.hi - s.lo;
     if (left <= 0) return;
-    b = start_s[0];
-    off = start_s[1];
-    unit = lo;
+    b = s.b;
+    off = s.off;
+    unit = s.lo;
     r = request_of(p, b, block_rows);
   }
   __device__ __forceinline__ bool next(const AttendParams& p) {
@@ -203,13 +208,35 @@ struct Pieces {
   }
 };
 
+// a / b of numbers >= 0 (a 64-bit division takes some 150 cycles)
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return (unsigned long long)(a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
+
 // This CTA's share [lo, hi) of all units among the first G CTAs: a scan over the requests, each
-// thread some in a row.  start_s gets the first unit's request and its place among the request's.
-struct Share {
-  long long lo, hi, total, G;
-};
+// thread some in a row.
 __device__ __forceinline__ Share share_units(const AttendParams& p, int block_rows, long long* sums_s, int* start_s) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (p.rows.B <= 32) {
+    // every warp looks at all requests, and none waits for another
+    const long long mine = lane < p.rows.B ? request_of(p, lane, block_rows).units : 0;
+    long long in = mine;
+#pragma unroll
+    for (int m = 1; m < 32; m *= 2) {
+      const long long y = __shfl_up_sync(0xffffffffu, in, m);
+      if (lane >= m) in += y;
+    }
+    Share s = {0, 0, __shfl_sync(0xffffffffu, in, 31), 0};
+    s.G = min((long long)gridDim.x, s.total);
+    if (blockIdx.x < s.G) {
+      s.lo = quotient(s.total * blockIdx.x, s.G);
+      s.hi = quotient(s.total * (blockIdx.x + 1), s.G);
+      const int at = __ffs(__ballot_sync(0xffffffffu, s.lo < in)) - 1;
+      s.b = at;
+      s.off = (int)(s.lo - __shfl_sync(0xffffffffu, in - mine, at));
+    }
+    return s;
+  }
   const int each = (p.rows.B + kThreads - 1) / kThreads, b0 = tid * each, b1 = min(b0 + each, p.rows.B);
   long long mine = 0;
   for (int b = b0; b < b1; ++b) mine += request_of(p, b, block_rows).units;
@@ -221,7 +248,7 @@ __device__ __forceinline__ Share share_units(const AttendParams& p, int block_ro
   }
   if (lane == 31) sums_s[warp] = in;
   __syncthreads();
-  Share s = {0, 0, 0, 0};
+  Share s = {0, 0, 0, 0, 0, 0};
   long long before = 0;
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += sums_s[w];
@@ -229,8 +256,8 @@ __device__ __forceinline__ Share share_units(const AttendParams& p, int block_ro
   }
   s.G = min((long long)gridDim.x, s.total);
   if (blockIdx.x < s.G) {
-    s.lo = s.total * blockIdx.x / s.G;
-    s.hi = s.total * (blockIdx.x + 1) / s.G;
+    s.lo = quotient(s.total * blockIdx.x, s.G);
+    s.hi = quotient(s.total * (blockIdx.x + 1), s.G);
     if (before + in - mine <= s.lo && s.lo < before + in) {
       long long at = before + in - mine;
       for (int b = b0; b < b1; ++b) {
@@ -244,6 +271,9 @@ __device__ __forceinline__ Share share_units(const AttendParams& p, int block_ro
       }
     }
   }
+  __syncthreads();
+  s.b = start_s[0];
+  s.off = start_s[1];
   return s;
 }
 
@@ -252,7 +282,7 @@ struct Parts {
   int first, n;
 };
 __device__ __forceinline__ Parts parts_of(const Share& s, long long unit0, int tiles) {
-  auto cta = [&](long long unit) { return (int)(((unit + 1) * s.G - 1) / s.total); };
+  auto cta = [&](long long unit) { return (int)quotient((unit + 1) * s.G - 1, s.total); };
   const int first = cta(unit0);
   return {first, cta(unit0 + tiles - 1) - first + 1};
 }
@@ -552,21 +582,20 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
     prefetch_tensormap(&k_map);
     prefetch_tensormap(&v_map);
   }
-  pdl_wait();
-  pdl_launch_dependents();
-
-  const Share share = share_units(p, kTile, sums_s, start_s);
-  if (tid == 0 && p.join_apart) p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_s;
+  pdl_wait();
+  pdl_launch_dependents();
+  const Share share = share_units(p, kTile, sums_s, start_s);
+  if (tid == 0 && p.join_apart) p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
 
   const Waits wait{abort_s, p.err};
 
   Pieces pc;
   pc.left = 0;
-  pc.start(p, kTile, start_s, share.lo, share.hi);
+  pc.start(p, kTile, share);
 
   if (warp == kProducerWarp) {
     TileCopies<S> copies{smem + S::kOffKV, kv_full, kv_empty, wait, p, pc, policy_evict_first()};
@@ -959,20 +988,20 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
     prefetch_tensormap(&k_map);
     prefetch_tensormap(&v_map);
   }
-  pdl_wait();
-  pdl_launch_dependents();
-  const Share share = share_units(p, kRows, sums_s, start_s);
-  if (tid == 0 && p.join_apart) p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_s;
+  pdl_wait();
+  pdl_launch_dependents();
+  const Share share = share_units(p, kRows, sums_s, start_s);
+  if (tid == 0 && p.join_apart) p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
   const Waits wait{abort_s, p.err};
   Pieces pc;
   pc.left = 0;
 
   if (warp == kProducerWarp) {
-    pc.start(p, kRows, start_s, share.lo, share.hi);
+    pc.start(p, kRows, share);
     TileCopies<S> copies{smem + S::kOffKV, kv_full, kv_empty, wait, p, pc, policy_evict_first()};
     copies.run(&k_map, &v_map);
   } else if (warp == kIssueWarp) {
@@ -1041,7 +1070,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
     // ------------------------------------------------------------------ queries, a thread a row
     const int col = tid - 32 * kLoadWarp;
     int* par = parents_s + 64 * (warp - kLoadWarp);
-    pc.start(p, kRows, start_s, share.lo, share.hi);
+    pc.start(p, kRows, share);
     for (uint32_t piece = 0;; ++piece) {
       const uint32_t q = piece & 1;
       const bool more = pc.next(p);
@@ -1060,6 +1089,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
       uint4 x[D / 8];
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) x[c] = live ? src[c] : make_uint4(0, 0, 0, 0);
+      // (while the queries come)
+      const Parts parts = pc.whole ? Parts{0, 1} : parts_of(share, pc.unit0, pc.r.tiles);
       unsigned long long sees = 0;
       if (p.rows.parents) {
         __syncwarp();
@@ -1088,8 +1119,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
       }
       to_s[64 * q + col] = (long long)(pc.r.row0 + i) * p.out_row + head * p.out_head;
       if (col == 0)
-        info_s[q] = {pc.b, pc.head, pc.block, pc.tile0, pc.n_tiles, pc.r.tiles, pc.r.row0, pc.r.n, pc.r.len, pc.r.end, rows,
-                     pc.whole ? Parts{0, 1} : parts_of(share, pc.unit0, pc.r.tiles)};
+        info_s[q] = {pc.b, pc.head, pc.block, pc.tile0, pc.n_tiles, pc.r.tiles, pc.r.row0, pc.r.n, pc.r.len, pc.r.end, rows, parts};
       fence_proxy_async_smem();
       mbar_arrive(&q_full[q]);
     }
