@@ -17,7 +17,8 @@
  *     contiguous, 16-byte aligned.  The library allocates no memory: scratch space comes
  *     from the caller's workspace (size from dspark_workspace_bytes; 256-byte aligned,
  *     zero-filled before its first use: its first 256 bytes hold the device status
- *     word).  One workspace may serve all calls of a step as long as they run in order
+ *     word and counts that are zero between calls; dspark_last_device_status clears
+ *     them when it reports an error).  One workspace may serve all calls of a step as long as they run in order
  *     on one stream; calls that overlap on the GPU must not share a workspace.
  *   - bf16 weights are passed as their uint16_t bit patterns.
  *   - Every call is asynchronous on `stream` and may be captured in a CUDA graph.
@@ -593,8 +594,8 @@ dspark_status dspark_embed_grad(const void* d_out, int dtype, int64_t ld, const 
  *
  * Counts outside [0, N], rows outside the batch, lengths that the table has no room for, pages
  * outside the cache and parents that are not before their token record
- * DSPARK_ERR_DEVICE_CHECK: the request, slot or parent counts as none.  B < 65536, B = 0 launches
- * nothing.  The workspace is any of this library's (256 bytes suffice) unless a call names its
+ * DSPARK_ERR_DEVICE_CHECK: the request, slot or parent counts as none (where starts descend, rows
+ * of other requests may count as none, too).  B < 65536, B = 0 launches nothing.  The workspace is any of this library's (256 bytes suffice) unless a call names its
  * own size.
  */
 typedef struct {
@@ -612,7 +613,8 @@ typedef struct {
  *   (x_a, x_b) = (x_a cos - x_b sin, x_b cos + x_a sin),  angle position * inv_freq[j]
  * of pairs j: elements j and j + rotated / 2, or 2 j and 2 j + 1 (interleaved); elements from
  * `rotated` on stay.  position = lengths[b] + the token's depth in its tree (a chain: its place).
- * Angles are formed in 64 bits, the rest in fp32, with one rounding where a value is stored.
+ * Angles are formed in whole numbers (2^-34 of a turn off at most at position 2^31 and frequency
+ * 1), the rest is in fp32, with one rounding where a value is stored.
  * q_out may be q itself (same strides); arrays overlap in no other way.
  *
  *   strides of rows and heads in elements, multiples of 8; pointers 16-byte aligned; inv_freq and

@@ -50,12 +50,28 @@ __device__ __forceinline__ float2 turn_of(int position, float freq) {
   return cs;
 }
 
+// The last of the B requests whose rows start at or before `row`, 32 looked at at once by the
+// warp; -1: none does.
+__device__ __forceinline__ int request_of_row(const int32_t* starts, int B, int row) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, end = B;
+  while (end - lo > 32) {
+    const int step = (end - lo + 31) / 32, at = lo + lane * step;
+    const int before = __popc(__ballot_sync(0xffffffffu, at < end && starts[at < end ? at : lo] <= row));
+    if (before == 0) return -1;
+    lo += (before - 1) * step;
+    end = min(lo + step, end);
+  }
+  const int at = lo + lane;
+  return lo - 1 + __popc(__ballot_sync(0xffffffffu, at < end && starts[at < end ? at : lo] <= row));
+}
+
 // A row's LG lanes a head vector (16 bytes a lane): x' = rot(x rsqrt(mean x^2 + eps) w), sums and
 // products in fp32 and one rounding where it is stored.  Each element is read and written once, so
 // memory bounds it.  A warp takes a row, or one of `parts` parts of its heads, and waits for no
 // other: a lane has the same elements of each of its heads, so it holds their cosines and sines
 // in registers, 1 to 4 of which each lane computes for the warp.
-constexpr int kAppendWarps = 8, kAppendBatch = 4, kAppendCtas = 4;
+constexpr int kAppendWarps = 8, kAppendBatch = 4, kAppendCtas = 4, kAppendMost = 16;
 
 template <typename T, int LG>
 __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas) append_kernel(const __grid_constant__ AppendParams p) {
@@ -67,7 +83,21 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas) append_kernel(
   const long long task = (long long)blockIdx.x * kAppendWarps + warp;
   const long long place = task / p.parts;
   const int part = (int)(task - place * p.parts);
-  const int b = (int)(place / p.rows.N), i = (int)(place - (long long)b * p.rows.N);
+  int b, i;
+  if (p.rows.starts) {
+    // a place is a row: it finds its request, and one for each request checks what is said of that
+    if (place < p.rows.B && part == 0 && lane == 0) {
+      const RequestRows r = request_rows(p.rows, (int)place, p.err);
+      if (r.n > 0) request_length(p.slots, (int)place, r.n, p.err);
+    }
+    if (place >= p.rows.rows) return;
+    b = request_of_row(p.rows.starts, p.rows.B, (int)place);
+    if (b < 0) return;
+    i = (int)place - p.rows.starts[b];
+  } else {
+    b = (int)(place / p.rows.N);
+    i = (int)(place - (long long)b * p.rows.N);
+  }
   if (b >= p.rows.B) return;
   const int length = p.slots.lengths[b];
   const RequestRows r = request_rows(p.rows, b, p.err);
@@ -194,10 +224,12 @@ cudaError_t append_for(AppendParams p, cudaStream_t stream) {
   // as many warps as the device holds, and none without a head: a row alone takes 3.3 us in 20
   // parts and 5.3 in 3, 12,004 rows of 9 KB 47 us in one part each (69% of the copy bandwidth) and
   // 62 with a fifth CTA an SM, whose registers do not suffice
-  const long long places = (long long)p.rows.N * p.rows.B;
+  const long long places = !p.rows.starts ? (long long)p.rows.N * p.rows.B
+                         : p.rows.rows > p.rows.B ? p.rows.rows : p.rows.B;
   const int most = cdiv(p.q_heads + p.cs.heads, 32 / lg);
   const long long wanted = (long long)sms * kAppendCtas * kAppendWarps / places;
-  p.parts = wanted < 1 ? 1 : wanted < most ? (int)wanted : most;
+  const int least = cdiv(most, kAppendMost);
+  p.parts = wanted < least ? least : wanted < most ? (int)wanted : most;
   const long long ctas = cdiv(places * p.parts, (long long)kAppendWarps);
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   auto go = [&](auto kernel) {
