@@ -1,4 +1,5 @@
-"""In-tree build of libdspark.so (the CUDA kernels behind the C ABI) for sm_103a.
+"""In-tree build of libdspark.so (the CUDA kernels behind the C ABI) for sm_103a, and of the
+Python module of calls.cpp beside it.
 
 Each .cu file is compiled to an object in parallel, then linked into one shared library
 with the CUDA runtime linked statically (the driver is reached through the runtime's
@@ -11,12 +12,14 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libdspark.so")
+CALLS = os.path.join(BUILD, "_dspark_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -36,18 +39,19 @@ def _sources():
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
-        [os.path.join(ROOT, "include", "dspark.h")]
+        [os.path.join(ROOT, "include", "dspark.h"), os.path.join(CSRC, "calls.cpp")]
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALLS):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
-    """Compile every kernel source for sm_103a and link libdspark.so; returns its path."""
+    """Compile every kernel source for sm_103a and link libdspark.so (returns its path), and the
+    Python module."""
     if not force and not _stale():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
@@ -64,8 +68,19 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
             print(res.stdout + res.stderr)
         return obj
 
+    def compile_calls():
+        tmp = CALLS + ".tmp"
+        cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I",
+               sysconfig.get_paths()["include"], os.path.join(CSRC, "calls.cpp"), "-o", tmp]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"g++ failed on calls.cpp:\n{res.stdout}\n{res.stderr}")
+        os.replace(tmp, CALLS)
+
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+        calls = ex.submit(compile_calls)
         objs = list(ex.map(compile_one, _sources()))
+        calls.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs
     res = subprocess.run(cmd, capture_output=True, text=True)

@@ -21,9 +21,12 @@ is reported by ``ws.status()``.
 from __future__ import annotations
 
 import ctypes
+import functools
+import importlib.machinery
+import importlib.util
 from typing import Dict, Optional
 
-from . import DSparkError, Workspace, lib
+from . import DSparkError, Workspace, _build, lib
 from .rows import _NOTHING, _device, _done, _on, _rows, _types, _vector
 
 
@@ -60,10 +63,26 @@ class PagedCache:
         self.dtype, self.device, self.index = k.dtype, k.device, k.get_device()
         self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), codes[k.dtype], *shape, *stride[:4])
         self._ptr = ctypes.addressof(self._struct)
+        self._key = (self._ptr, self.dtype, self.index, self.heads, self.head_dim)
 
 
-# The checks of a call take longer than its kernel for a single token, so they ask a tensor as
-# little as they can (0.1 us a question), and the checks that tell what is wrong run only then.
+@functools.lru_cache(maxsize=None)
+def _calls():
+    """The module that checks and makes a well-formed call in C (calls.cpp): for a single token the checks
+    below take longer than the kernel.  Its functions return a status, or None where a check failed
+    or an output is to be made: then the checks below are made, which say what is wrong."""
+    torch, _ = _types()
+    L = lib()
+    loader = importlib.machinery.ExtensionFileLoader("_dspark_calls", _build.CALLS)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_dspark_calls", loader))
+    loader.exec_module(module)
+    module.setup(*(ctypes.cast(getattr(L, "dspark_" + name), ctypes.c_void_p).value
+                   for name in ("cache_append", "tree_attention", "tree_verify", "cache_keep")),
+                 torch.float32, torch.bfloat16, torch.float16, torch.int32, torch._C._cuda_getDevice,
+                 torch._C._cuda_getCurrentRawStream)
+    return module
+
+
 
 def _begin(like, ws, stream):
     """(device index, stream handle, context in which outputs are allocated for it)."""
@@ -140,6 +159,12 @@ def cache_append(cache: PagedCache, k, v, pages, lengths, ws: Workspace, q=None,
     weight.  ``inv_freq`` [R / 2] fp32: the first R elements of each head are rotated by position
     times frequency, in pairs (j, j + R / 2), or (2 j, 2 j + 1) with ``interleaved``; the position is
     lengths[b] plus the token's depth in its tree.  A chain may be of any length (a prompt)."""
+    if stream is None:
+        code = _calls().append(cache, k, v, pages, lengths, ws, q, q_out, starts, counts, nodes, parents, inv_freq,
+                               interleaved, q_weight, k_weight, eps, layer)
+        if code is not None:
+            _done("dspark_cache_append", code)
+            return q_out
     torch, _ = _types()
     i32, f32 = torch.int32, torch.float32
     dev, handle, allocate = _begin(k, ws, stream)
@@ -188,6 +213,12 @@ def tree_attention(q, cache: PagedCache, pages, lengths, ws: Workspace, starts=N
     itself.  ``scale`` (default head_dim ** -0.5) multiplies the scores.  Returns ``out`` like
     ``q``; ``lse`` [..., q_heads] fp32, if given, gets the logarithms of the softmax's sums.
     head_dim is 64 or 128, and a request has at most 64 tokens."""
+    if stream is None:
+        code = _calls().attend(q, cache, pages, lengths, ws, starts, counts, nodes, parents,
+                               cache.head_dim ** -0.5 if scale is None else scale, out, lse, layer)
+        if code is not None:
+            _done("dspark_tree_attention", code)
+            return out
     torch, _ = _types()
     i32 = torch.int32
     dev, handle, allocate = _begin(q, ws, stream)
@@ -219,6 +250,12 @@ def tree_verify(p, tokens, uniforms, ws: Workspace, q=None, starts=None, counts=
     that the draft names without chance (greedy drafts, its most probable tokens).  Returns (or
     fills ``out``) a dict of int32 tensors: ``accept_len`` [B], ``path`` [B, N] the accepted tokens'
     places, ``out_tokens`` [B, N] their ids and the last token, ``n_out`` [B]; -1 behind them."""
+    if stream is None and out is not None:
+        code = _calls().verify(p, tokens, uniforms, ws, q, starts, counts, nodes, parents, out["accept_len"],
+                               out["path"], out["out_tokens"], out["n_out"])
+        if code is not None:
+            _done("dspark_tree_verify", code)
+            return out
     torch, _ = _types()
     i32 = torch.int32
     code, n, V, ld = _rows(p, "p")
@@ -250,6 +287,10 @@ def cache_keep(cache: PagedCache, pages, lengths, path, accept_len, ws: Workspac
     request b to slot lengths[b] + 1 + j, for j < accept_len[b] (``path`` [B, N], ``accept_len`` [B] as
     ``tree_verify`` returns them).  After it lengths[b] + 1 + accept_len[b] slots are used; the
     caller updates ``lengths``."""
+    if stream is None:
+        code = _calls().keep(cache, pages, lengths, path, accept_len, ws)
+        if code is not None:
+            return _done("dspark_cache_keep", code)
     torch, _ = _types()
     if path.dim() != 2:
         raise ValueError(f"path: [B, N] is needed, not {tuple(path.shape)}")

@@ -357,3 +357,79 @@ def test_nothing_to_do(packed):
     ds.tree_attention(e, cache, empty, i32([]), ws, **none)
     ds.cache_append(cache, e[..., :2, :], e[..., :2, :], empty, i32([]), ws, **none)
     assert ws.status() == 0
+
+
+# ------------------------------------------------------------------ refusals from Python
+
+def _refused():
+    t = lambda *shape, dtype=BF16: torch.zeros(*shape, dtype=dtype, device="cuda")  # noqa: E731
+    k = t(3, 16, 2, 64)
+    good = dict(cache=ds.PagedCache(k, t(3, 16, 2, 64)), k=t(2, 4, 2, 64), v=t(2, 4, 2, 64), pages=i32([[0, 1], [2, 1]]),
+                lengths=i32([0, 0]), ws=ds.Workspace.of_bytes(ds.tree_attention_workspace_bytes(2, 4, 4, 2, 64)),
+                q=t(2, 4, 4, 64), q_out=t(2, 4, 4, 64))
+    attend = {a: good[a] for a in ("cache", "pages", "lengths", "ws", "q")} | dict(out=t(2, 4, 4, 64))
+    verify = dict(p=torch.full((2, 4, 9), 1 / 9, device="cuda"), tokens=i32([[0] * 4] * 2), ws=good["ws"],
+                  uniforms=torch.zeros(2, 4, device="cuda"),
+                  out={a: i32([0, 0]) for a in ("accept_len", "n_out")} | {a: i32([[0] * 4] * 2) for a in ("path", "out_tokens")})
+    keep = dict(cache=good["cache"], pages=good["pages"], lengths=good["lengths"], path=i32([[-1] * 4] * 2),
+                accept_len=i32([0, 0]), ws=good["ws"])
+    wide, cpu = t(2, 4, 4, 128), torch.zeros(2, dtype=torch.int32)
+    return [
+        (ds.cache_append, good, [
+            dict(k=t(2, 4, 2, 64, dtype=F16)), dict(k=t(2, 4, 3, 64)), dict(v=t(2, 3, 2, 64)), dict(v=t(2, 4, 2, 32)),
+            dict(q=t(2, 4, 4, 64).transpose(0, 1)), dict(q=wide[..., ::2]), dict(q_out=t(2, 4, 5, 64)), dict(q=None),
+            dict(pages=i32([0, 1])), dict(pages=i32([[0, 1]])), dict(lengths=cpu), dict(lengths=i32([0, 0, 0])),
+            dict(lengths=torch.zeros(2, dtype=torch.int64, device="cuda")), dict(counts=i32([1])), dict(starts=i32([0, 1, 2])),
+            dict(parents=i32([[0] * 4])), dict(inv_freq=t(8)), dict(inv_freq=t(33, dtype=F32)), dict(inv_freq=t(4, dtype=F32)),
+            dict(q_weight=t(32, dtype=F32)), dict(eps=-1.0), dict(eps=math.nan), dict(layer=1), dict(layer=-1),
+            dict(nodes=3, starts=i32([0, 1, 2]), counts=i32([1, 1])), dict(k=good["k"].cpu())]),
+        (ds.tree_attention, attend, [
+            dict(q=t(2, 4, 3, 64)), dict(q=t(2, 4, 4, 64, dtype=F16)), dict(out=t(2, 4, 2, 64)), dict(out=wide[..., ::2]),
+            dict(scale=0.0), dict(scale=-1.0), dict(scale=math.inf), dict(lse=t(2, 4, dtype=F32)), dict(lse=t(2, 4, 4)),
+            dict(ws=ds.Workspace.of_bytes(256)), dict(parents=i32([[0] * 4])), dict(pages=good["pages"].t()), dict(layer=7),
+            dict(counts=torch.zeros(4, dtype=torch.int32, device="cuda")[::2])]),
+        (ds.tree_verify, verify, [
+            dict(p=t(2, 4, 9, dtype=torch.float64)), dict(p=t(8, 9, dtype=F32)), dict(q=t(2, 4, 9)), dict(q=t(2, 4, 8, dtype=F32)),
+            dict(tokens=i32([0] * 7)), dict(tokens=t(2, 4, dtype=F32)), dict(uniforms=t(2, 4)),
+            dict(out=verify["out"] | dict(path=i32([[0] * 3] * 2))), dict(out=verify["out"] | dict(n_out=cpu))]),
+        (ds.cache_keep, keep, [
+            dict(path=i32([0] * 8)), dict(path=i32([[0] * 4])), dict(accept_len=cpu), dict(accept_len=i32([0])),
+            dict(pages=i32([[0, 1]])), dict(path=i32([[0] * 65] * 2))]),
+    ]
+
+
+def test_calls_refuse_from_python():
+    """Every bad argument raises, on the current stream and on a given one, and nothing is written."""
+    for call, good, bads in _refused():
+        ws = good["ws"]
+        for bad in bads:
+            for stream in (None, torch.cuda.current_stream()):
+                tensors = [x for x in (good | bad).values() if torch.is_tensor(x)]
+                before = [x.clone() for x in tensors]
+                with pytest.raises((ValueError, ds.DSparkError)):
+                    call(**(good | bad), stream=stream)
+                assert all(torch.equal(x, y) for x, y in zip(tensors, before))
+        for stream in (None, torch.cuda.current_stream()):
+            call(**good, stream=stream)                    # and what is good is taken
+        assert ws.status() == 0, call
+
+
+def test_strided_rows_and_forms_of_arguments():
+    """Rows inside a wider projection (two and one leading dimensions), whole numbers for floats, and no
+    outputs: as with contiguous rows and outputs that are given."""
+    batch = Batch([3, 2], [20, 7], 16)
+    k, v = new_cache(batch, 2, 64, BF16, fill=0.0)
+    fill_cache(batch, k, v)
+    cache, ws = ds.PagedCache(k, v), workspace(batch, 4, 2, 64)
+    wide = torch.randn(2, 3, 10, 64, generator=gen(51), device="cuda").to(BF16)
+    q = wide[:, :, 3:7]
+    want = ds.tree_attention(q.contiguous(), cache, batch.pages, batch.lens, ws, out=torch.zeros_like(q.contiguous()), scale=1.0,
+                             **batch.kw)
+    for out in (None, torch.zeros(2, 3, 6, 64, dtype=BF16, device="cuda")[:, :, 1:5]):
+        got = ds.tree_attention(q, cache, batch.pages, batch.lens, ws, out=out, scale=1, **batch.kw)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1, :2], want[1, :2])
+    flat = wide.view(6, 10, 64)[:, 3:7]
+    got = ds.tree_attention(flat, cache, batch.pages, batch.lens, ws, starts=i32([0, 3, 5]), nodes=3, scale=1.0)
+    alone = ds.tree_attention(wide[:1, :, 3:7], cache, batch.pages[:1], batch.lens[:1], ws, scale=1.0)
+    assert torch.equal(got[:3], want[0]) and torch.equal(got[3:5], want[1, :2]) and torch.equal(alone[0], want[0])
+    assert ws.status() == 0
