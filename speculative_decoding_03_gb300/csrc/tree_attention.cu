@@ -927,13 +927,13 @@ __device__ __forceinline__ float sum_over_lanes(float (&v)[16], int lane) {
   return one + __shfl_xor_sync(0xffffffffu, one, 1);
 }
 
-template <typename T, int D>
+template <typename T, int D, int kChunks>
 __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid_constant__ CUtensorMap k_map,
                                                                     const __grid_constant__ CUtensorMap v_map,
                                                                     const __grid_constant__ AttendParams p) {
   using S = NarrowSmem<D>;
   constexpr bool kBf16 = __is_same(T, __nv_bfloat16);
-  constexpr int kRows = S::kRows, kChunks = kRows / 16, kLoadWarp = 2;
+  constexpr int kRows = S::kRows, kColumns = 16 * kChunks, kLoadWarp = 2;
   constexpr uint32_t kColO = 2 * kRows;                       // S 0 and 1 at columns 0 and 64
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* small = smem + S::kOffSmall;
@@ -1144,9 +1144,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
       const int rows = rq.rows, chunks = (rows + 15) / 16, n = rq.n_tiles, tile0 = rq.tile0;
       if (n == 0) break;
       bool open = true;                        // a column has no reference yet
-      float l[kRows];                          // this thread's slots' part of the columns' sums
+      float l[kColumns];                       // this thread's slots' part of the columns' sums
 #pragma unroll
-      for (int e = 0; e < kRows; ++e) l[e] = 0.f;
+      for (int e = 0; e < kColumns; ++e) l[e] = 0.f;
       for (int j = 0; j < n; ++j, ++t) {
         const uint32_t buf = t & 1;
         const int slot0 = (tile0 + j) * kTile, slot = slot0 + r;
@@ -1158,7 +1158,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
         __syncwarp();
         tc_fence_after_sync();
         // the slot's scores (times scale and log2 e), less the columns' references
-        float x[kRows], mx = -INFINITY;
+        float x[kColumns], mx = -INFINITY;
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
           if (c >= chunks) break;
@@ -1303,7 +1303,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
       tc_fence_after_sync();
       const bool bad = bad_s[q] == (int)piece + 1;
 #pragma unroll 1
-      for (int w = 0; w < 2; ++w) {            // 32 rows at a time
+      for (int w = 0; w < (kChunks + 1) / 2; ++w) {      // 32 rows at a time
         const int left = rows - 32 * w;
         if (left <= 0) break;
         uint32_t v[32];
@@ -1419,7 +1419,9 @@ cudaError_t attend_for(AttendParams p, const TargetSlots& slots, bool bf16, cuda
   int grid = per_device_grid(cache, []() {
     return cudaFuncSetAttribute(attend_wide_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 AttendSmem<D>::kBytes) == cudaSuccess &&
-                   cudaFuncSetAttribute(attend_narrow_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                   cudaFuncSetAttribute(attend_narrow_kernel<T, D, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        NarrowSmem<D>::kBytes) == cudaSuccess &&
+                   cudaFuncSetAttribute(attend_narrow_kernel<T, D, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         NarrowSmem<D>::kBytes) == cudaSuccess
                ? 1 : -1;
   });
@@ -1441,7 +1443,7 @@ cudaError_t attend_for(AttendParams p, const TargetSlots& slots, bool bf16, cuda
   const int most_parts = min(grid / p.cs.heads + 2, most_tiles);
   p.join_apart = most_parts > 1 && (rows > kJoinRows || most_parts > kJoinParts);
   const cudaError_t e =
-      narrow ? launch_pdl(attend_narrow_kernel<T, D>, dim3(grid), dim3(kThreads), NarrowSmem<D>::kBytes, stream, k_map,
+      narrow ? launch_pdl(rows <= 16 ? attend_narrow_kernel<T, D, 1> : attend_narrow_kernel<T, D, 4>, dim3(grid), dim3(kThreads), NarrowSmem<D>::kBytes, stream, k_map,
                           v_map, p)
              : launch_pdl(attend_wide_kernel<T, D>, dim3(grid), dim3(kThreads), AttendSmem<D>::kBytes, stream, k_map,
                           v_map, p);
