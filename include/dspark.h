@@ -613,8 +613,9 @@ typedef struct {
  *   (x_a, x_b) = (x_a cos - x_b sin, x_b cos + x_a sin),  angle position * inv_freq[j]
  * of pairs j: elements j and j + rotated / 2, or 2 j and 2 j + 1 (interleaved); elements from
  * `rotated` on stay.  position = lengths[b] + the token's depth in its tree (a chain: its place).
- * Angles are formed in whole numbers (2^-34 of a turn off at most at position 2^31 and frequency
- * 1), the rest is in fp32, with one rounding where a value is stored.
+ * Angles are formed in whole numbers (2^-35 of a turn off at most at position 2^30 and frequency
+ * 1; a frequency that is not finite turns its pairs into NaN), the rest is in fp32, with one
+ * rounding where a value is stored.
  * q_out may be q itself (same strides); arrays overlap in no other way.
  *
  *   strides of rows and heads in elements, multiples of 8; pointers 16-byte aligned; inv_freq and

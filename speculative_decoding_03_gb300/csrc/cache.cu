@@ -29,9 +29,9 @@ constexpr int kMaxHalf = 128;            // pairs of a head (head_dim <= 256)
 
 // Cosine and sine of position x frequency, which is reduced to a turn in whole numbers: the
 // frequency's 24 bits times 2^64 / (2 pi) are at most 2^-65 of a turn off for each unit of
-// frequency, and the position's multiple wraps at whole turns by itself.  So at position 2^31 and
-// frequency 1 the angle is off by 2^-34 of a turn before it is rounded to fp32 (an fp32 product
-// would be off by tens of turns), without an instruction in 64-bit floating point: those take
+// frequency, and the position's multiple wraps at whole turns by itself.  So at position 2^30 and
+// frequency 1 the angle is off by 2^-35 of a turn before it is rounded to fp32 (an fp32 product
+// would be off by some turns), without an instruction in 64-bit floating point: those take
 // 100 cycles and more here, and five of them stood between a row's length and its stores.
 __device__ __forceinline__ float2 turn_of(int position, float freq) {
   constexpr unsigned long long kTurns = 2935890503282001226ull;      // 2^64 / (2 pi)
@@ -221,16 +221,17 @@ cudaError_t append_for(AppendParams p, cudaStream_t stream) {
   static std::atomic<int> cache[kMaxCachedDevices];
   const int sms = per_device_grid(cache, []() { return 1; });
   if (sms <= 0) return cudaErrorInvalidConfiguration;
-  // as many warps as the device holds, and none without a head: a row alone takes 3.3 us in 20
-  // parts and 5.3 in 3, 12,004 rows of 9 KB 47 us in one part each (69% of the copy bandwidth) and
-  // 62 with a fifth CTA an SM, whose registers do not suffice
+  // as many warps as the device holds, none without a head and none with more than 16 head
+  // vectors: a row alone takes 3.4 us in 20 parts and 5.3 in 3; 12,004 rows of 9 KB take 47.5 us in one
+  // part each (69% of the copy bandwidth), 50 and 55 in two and four, 62 with a fifth CTA an SM, whose
+  // registers do not suffice; 2500 places of 40 heads of 256 45 us in one part each and 24 in three
   const long long places = !p.rows.starts ? (long long)p.rows.N * p.rows.B
                          : p.rows.rows > p.rows.B ? p.rows.rows : p.rows.B;
   const int most = cdiv(p.q_heads + p.cs.heads, 32 / lg);
   const long long wanted = (long long)sms * kAppendCtas * kAppendWarps / places;
   const int least = cdiv(most, kAppendMost);
   p.parts = wanted < least ? least : wanted < most ? (int)wanted : most;
-  const long long ctas = cdiv(places * p.parts, (long long)kAppendWarps);
+  const long long ctas = (places * p.parts + kAppendWarps - 1) / kAppendWarps;
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   auto go = [&](auto kernel) {
     return launch_pdl(kernel, dim3((unsigned)ctas), dim3(32 * kAppendWarps), 0, stream, p);

@@ -11,13 +11,19 @@
 // A persistent CTA per SM takes an equal, contiguous share of all (request, row block, head,
 // 128-slot tile) units, in that order: a piece is what it has of one (request, row block, head).
 // One warp copies key and value tiles by TMA (page by page, 128-byte swizzle) into a ring of
-// buffers, one thread issues the products S = Q K^T and O += P V, and four warps, a thread a
-// row, turn S into P.  S is double-buffered in tensor memory, so the next tile's S forms
-// while this one's softmax runs.  The running maximum is raised only when a tile exceeds it by
-// more than 2^8 (then O, in tensor memory, is rescaled; P <= 256 keeps its 16-bit rounding
-// relative).  Pieces that hold only some of their tiles leave O, maximum and sum in the
-// workspace in fp32, and the CTA that comes last joins them in tile order, so results do not
-// depend on the order in which CTAs run.
+// buffers, one issues the products S = Q K^T and O += P V, and four warps turn S into P: a thread
+// a row here, a thread a slot where a key head has up to 64 rows (below).  S is double-buffered in
+// tensor memory, so the next tile's S forms while this one's softmax runs.  The running maximum is
+// raised only when a tile exceeds it by more than 2^8 (then O, in tensor memory, is rescaled; P <=
+// 256 keeps its 16-bit rounding relative).  Pieces that hold only some of their tiles leave O,
+// maximum and sum in the workspace in fp32; they are joined in tile order by the CTA that comes
+// last or by a kernel of their own, so results do not depend on the order in which CTAs run.
+//
+// Measured on a GB300 (graphs of calls, other inputs in turn): two chains of 8 over 130,000 slots, 32
+// heads on 8 of 128, 162 to 167 us, 95% of the copy bandwidth; 32 trees of up to 16 over 4000 slots in
+// pages of 16 94.5 us, 82%; 128 chains of up to 8 over 1 to 2999 slots, 16 heads on 2 of 64, 38.5 us, 38%,
+// bound by the latency of a tile's steps (1500 cycles) and of a piece's beginning and end (6000);
+// one token over 1000 slots 10.2 us, launch and latency.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -40,7 +46,9 @@ constexpr int kProducerWarp = 0, kIssueWarp = 1, kSoftmaxWarp = 4;
 constexpr float kRaise = 8.f;              // log2 of what the maximum may lag behind
 constexpr int kMaxGrid = 160;              // CTAs of the persistent grid at most
 constexpr int kJoinRows = 16, kJoinParts = 24;   // what one CTA joins at most
-constexpr int kPieceUnits = 4;             // what beginning and ending a piece costs, in tiles
+// What beginning and ending a piece costs, in tiles: with it in the shares 128 unequal chains take 39
+// us, without 53, with 8 of them 41.
+constexpr int kPieceUnits = 4;
 
 // How a tile's lines lie in memory and in shared memory, in groups of 8 lines of 128 bytes.
 //   kHalvesApart: a copy takes 64 elements of a page's lines; the groups of a half follow each
@@ -879,6 +887,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
 //
 // Two more warps bring each piece's queries and what its rows see, a piece ahead, so that products
 // run on from piece to piece: S^T of the next piece's first tile forms before the last O^T.
+//
+// Up to 16 rows have a kernel with one chunk of 16 columns for itself: its code is read in less time
+// when a launch begins (one token 10.2 instead of 10.8 us).
 template <int D>
 struct NarrowSmem {
   static constexpr int kRows = 64;
@@ -956,7 +967,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
   float* scale_s = best_s + 128;                             // [64]: what O and l are multiplied by
   float* down_s = best_s + 192;                              // [64]: by what the reference rose; at the end, 1 / l
   float* max_s = best_s + 256;                               // [4 warps][64]
-  float* sum_s = best_s + 512;                               // [4 warps][64], to byte 3328 + 3072
+  float* sum_s = best_s + 512;                               // [4 warps][64]
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (smem_u32(smem) & 1023u) {            // the swizzle needs it; the same for every thread
