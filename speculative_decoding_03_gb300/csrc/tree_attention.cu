@@ -170,6 +170,7 @@ __device__ __forceinline__ Request request_of(const AttendParams& p, int b, int 
 struct Share {
   long long lo, hi, total, G;
   int b, off;                // the first unit's request, and its place among the request's
+  Request r;
 };
 
 // The pieces of a CTA's share of the units, in order.
@@ -188,7 +189,7 @@ struct Pieces {
     b = s.b;
     off = s.off;
     unit = s.lo;
-    r = request_of(p, b, block_rows);
+    r = s.r;
   }
   __device__ __forceinline__ bool next(const AttendParams& p) {
     while (left > 0) {
@@ -227,14 +228,17 @@ __device__ __forceinline__ Share share_units(const AttendParams& p, int block_ro
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (p.rows.B <= 32) {
     // every warp looks at all requests, and none waits for another
-    const long long mine = lane < p.rows.B ? request_of(p, lane, block_rows).units : 0;
+    Request r = {};
+    if (lane < p.rows.B) r = request_of(p, lane, block_rows);
+    const long long mine = r.units;
     long long in = mine;
 #pragma unroll
     for (int m = 1; m < 32; m *= 2) {
       const long long y = __shfl_up_sync(0xffffffffu, in, m);
       if (lane >= m) in += y;
     }
-    Share s = {0, 0, __shfl_sync(0xffffffffu, in, 31), 0};
+    Share s = {};
+    s.total = __shfl_sync(0xffffffffu, in, 31);
     s.G = min((long long)gridDim.x, s.total);
     if (blockIdx.x < s.G) {
       s.lo = quotient(s.total * blockIdx.x, s.G);
@@ -242,6 +246,13 @@ __device__ __forceinline__ Share share_units(const AttendParams& p, int block_ro
       const int at = __ffs(__ballot_sync(0xffffffffu, s.lo < in)) - 1;
       s.b = at;
       s.off = (int)(s.lo - __shfl_sync(0xffffffffu, in - mine, at));
+      s.r.row0 = __shfl_sync(0xffffffffu, r.row0, at);
+      s.r.n = __shfl_sync(0xffffffffu, r.n, at);
+      s.r.len = __shfl_sync(0xffffffffu, r.len, at);
+      s.r.end = s.r.len + s.r.n;
+      s.r.tiles = __shfl_sync(0xffffffffu, r.tiles, at);
+      s.r.blocks = __shfl_sync(0xffffffffu, r.blocks, at);
+      s.r.units = __shfl_sync(0xffffffffu, r.units, at);
     }
     return s;
   }
@@ -256,7 +267,7 @@ __device__ __forceinline__ Share share_units(const AttendParams& p, int block_ro
   }
   if (lane == 31) sums_s[warp] = in;
   __syncthreads();
-  Share s = {0, 0, 0, 0, 0, 0};
+  Share s = {};
   long long before = 0;
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += sums_s[w];
@@ -280,8 +291,11 @@ __device__ __forceinline__ Share share_units(const AttendParams& p, int block_ro
     }
   }
   __syncthreads();
-  s.b = start_s[0];
-  s.off = start_s[1];
+  if (s.hi > s.lo) {
+    s.b = start_s[0];
+    s.off = start_s[1];
+    s.r = request_of(p, s.b, block_rows);
+  }
   return s;
 }
 
