@@ -74,7 +74,8 @@ struct AttendParams {
   float2* sums;                            // [2 CTAs][128] maxima (log2) and sums
   bool join_apart;                         // parts are joined by a kernel of their own
   uint32_t* arrived;                       // a byte a CTA: parts that have come of the piece it began
-  int4* joins;                             // [CTAs]: request, row block, head, parts of the piece it began
+  int4* joins;                             // [CTAs]: of the piece it began its request's first row, its first
+                                           // row of the head, rows 2^16 + head, and parts
   int* err;
 };
 
@@ -873,7 +874,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
       // (a warp whose wait ran out still meets the others)
       if (!whole) {
         if (p.join_apart) {
-          if (tile0 == 0 && r == 0 && ok) p.joins[blockIdx.x] = make_int4(b, block, head, parts.n);
+          if (tile0 == 0 && r == 0 && ok)
+            p.joins[blockIdx.x] = make_int4(rq.row0, block * kTile, min(kTile, rq.n * p.group - block * kTile) << 16 | head, parts.n);
         } else if (last_part(p, parts, ok, words + 6)) {
           join_parts<T, D>(p, parts, rq.row0, block * kTile, min(kTile, rq.n * p.group - block * kTile), head);
         }
@@ -1373,7 +1375,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
       mbar_arrive(&q_free[q]);
       if (!whole) {
         if (p.join_apart) {
-          if (tile0 == 0 && r == 0 && ok) p.joins[blockIdx.x] = make_int4(rq.b, rq.block, rq.head, rq.parts.n);
+          if (tile0 == 0 && r == 0 && ok)
+            p.joins[blockIdx.x] = make_int4(rq.row0, rq.block * kRows, rows << 16 | rq.head, rq.parts.n);
         } else if (last_part(p, rq.parts, ok, words + 6)) {
           join_parts<T, D>(p, rq.parts, rq.row0, rq.block * kRows, rows, rq.head);
         }
@@ -1390,19 +1393,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
 // The same in a kernel of its own: CTA (c, y) the parts of the piece that CTA c began and left
 // unfinished, the rows from 16 y on.
 template <typename T, int D>
-__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttendParams p, int block_rows) {
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttendParams p) {
   pdl_wait();
   pdl_launch_dependents();
   const int4 join = p.joins[blockIdx.x];
   if (join.w < 2) return;
-  const RequestRows rows = request_rows(p.rows, join.x, nullptr);
-  const int first = join.y * block_rows + 16 * blockIdx.y;
-  const int n = min(min(block_rows - 16 * (int)blockIdx.y, 16), rows.n * p.group - first);
+  const int n = min((join.z >> 16) - 16 * (int)blockIdx.y, 16);
   if (n <= 0) return;
   AttendParams q = p;
   q.partial += 16 * blockIdx.y * D;
   q.sums += 16 * blockIdx.y;
-  join_parts<T, D>(q, {(int)blockIdx.x, join.w}, rows.row0, first, n, join.z);
+  join_parts<T, D>(q, {(int)blockIdx.x, join.w}, join.x, join.y + 16 * blockIdx.y, n, join.z & 0xffff);
 }
 
 TileForm tile_form(const CacheStrides& cs, const TargetSlots& slots) {
@@ -1473,8 +1474,7 @@ cudaError_t attend_for(AttendParams p, const TargetSlots& slots, bool bf16, cuda
              : launch_pdl(attend_wide_kernel<T, D>, dim3(grid), dim3(kThreads), AttendSmem<D>::kBytes, stream, k_map,
                           v_map, p);
   if (e != cudaSuccess || !p.join_apart) return e;
-  return launch_pdl(join_kernel<T, D>, dim3(grid, cdiv(rows < kTile ? rows : kTile, 16)), dim3(128), 0, stream, p,
-                    narrow ? NarrowSmem<D>::kRows : kTile);
+  return launch_pdl(join_kernel<T, D>, dim3(grid, cdiv(rows < kTile ? rows : kTile, 16)), dim3(128), 0, stream, p);
 }
 
 }  // namespace
