@@ -612,7 +612,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
   pdl_wait();
   pdl_launch_dependents();
   const Share share = share_units(p, kTile, sums_s, start_s);
-  if (tid == 0 && p.join_apart) p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+  // (by the thread that may write it again)
+  if (tid == 32 * kSoftmaxWarp && p.join_apart) p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
 
   const Waits wait{abort_s, p.err};
 
@@ -1022,7 +1023,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
   pdl_wait();
   pdl_launch_dependents();
   const Share share = share_units(p, kRows, sums_s, start_s);
-  if (tid == 0 && p.join_apart) p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+  // (by the thread that may write it again)
+  if (tid == 32 * kSoftmaxWarp && p.join_apart) p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
   const Waits wait{abort_s, p.err};
   Pieces pc;
   pc.left = 0;
