@@ -980,7 +980,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
   uint32_t* seen_s = reinterpret_cast<uint32_t*>(small + 1280);
   long long* to_s = reinterpret_cast<long long*>(small + 2304);
   float* best_s = reinterpret_cast<float*>(small + 3328);    // [64]: a column's reference (log2), -inf: none yet
-  float* ref_s = best_s + 64;                                // [64]: the same, 0: none yet
+  float* less_s = best_s + 64;                               // [64]: its negative, 0: none yet
   float* scale_s = best_s + 128;                             // [64]: what O and l are multiplied by
   float* down_s = best_s + 192;                              // [64]: by what the reference rose; at the end, 1 / l
   float* max_s = best_s + 256;                               // [4 warps][64]
@@ -1165,7 +1165,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
       const uint32_t q = piece & 1;
       if (r < kRows) {
         best_s[r] = -INFINITY;
-        ref_s[r] = 0.f;
+        less_s[r] = 0.f;
       }
       ok = wait(&q_full[q], (piece >> 1) & 1) && ok;
       if (meet_or(!ok)) break;
@@ -1173,9 +1173,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
       const int rows = rq.rows, chunks = (rows + 15) / 16, n = rq.n_tiles, tile0 = rq.tile0;
       if (n == 0) break;
       bool open = true;                        // a column has no reference yet
-      float l[kColumns];                       // this thread's slots' part of the columns' sums
+      F2 l[kColumns / 2];                      // this thread's slots' part of the columns' sums
 #pragma unroll
-      for (int e = 0; e < kColumns; ++e) l[e] = 0.f;
+      for (int e = 0; e < kColumns / 2; ++e) l[e] = f2(0.f, 0.f);
+      const F2 sl2 = f2(sl, sl);
       for (int j = 0; j < n; ++j, ++t) {
         const uint32_t buf = t & 1;
         const int slot0 = (tile0 + j) * kTile, slot = slot0 + r;
@@ -1195,11 +1196,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
           tmem_ld_32x32b_sync<16>(tmem + lanes + kRows * buf + 16 * c, v);
 #pragma unroll
           for (int e = 0; e < 16; e += 4) {
-            const float4 ref = *reinterpret_cast<const float4*>(ref_s + 16 * c + e);
-            x[16 * c + e] = fmaf(__uint_as_float(v[e]), sl, -ref.x);
-            x[16 * c + e + 1] = fmaf(__uint_as_float(v[e + 1]), sl, -ref.y);
-            x[16 * c + e + 2] = fmaf(__uint_as_float(v[e + 2]), sl, -ref.z);
-            x[16 * c + e + 3] = fmaf(__uint_as_float(v[e + 3]), sl, -ref.w);
+            const float4 less = *reinterpret_cast<const float4*>(less_s + 16 * c + e);
+            const F2 lo = f2_fma(f2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sl2, f2(less.x, less.y));
+            const F2 hi = f2_fma(f2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), sl2, f2(less.z, less.w));
+            f2_get(lo, x[16 * c + e], x[16 * c + e + 1]);
+            f2_get(hi, x[16 * c + e + 2], x[16 * c + e + 3]);
           }
           if (masked) {
             const uint32_t bits = c < 2 ? seen.x : seen.y;
@@ -1230,12 +1231,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
           bool none = false;
           if (r < kRows && r < 16 * chunks) {
             const float m = fmaxf(fmaxf(max_s[r], max_s[64 + r]), fmaxf(max_s[128 + r], max_s[192 + r]));
-            const float old = best_s[r], ref = ref_s[r];
+            const float old = best_s[r], ref = -less_s[r];
             const bool first = old == -INFINITY, up = first || m > kRaise;
             const float now = first ? m : up ? ref + m : old;
             const float down = first ? (m == -INFINITY ? 0.f : m) : up ? now - ref : 0.f;
             best_s[r] = now;
-            ref_s[r] = now == -INFINITY ? 0.f : now;
+            less_s[r] = now == -INFINITY ? 0.f : -now;
             down_s[r] = down;
             scale_s[r] = first ? 0.f : up ? ex2_approx(-down) : 1.f;
             none = now == -INFINITY && r < rows;
@@ -1264,10 +1265,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
               uint32_t v[16];
               tmem_ld_32x32b_sync<16>(tmem + lanes + kColO + 16 * c, v);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                v[e] = __float_as_uint(__uint_as_float(v[e]) * scale_s[16 * c + e]);
-                l[16 * c + e] *= scale_s[16 * c + e];
-              }
+              for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * scale_s[16 * c + e]);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                l[8 * c + e] = f2_mul(l[8 * c + e], f2(scale_s[16 * c + 2 * e], scale_s[16 * c + 2 * e + 1]));
               tmem_st_32x32b_x16(tmem + lanes + kColO + 16 * c, v);
             }
             tmem_st_wait();
@@ -1281,8 +1282,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float a = ex2_approx(x[16 * c + 2 * e]), d = ex2_approx(x[16 * c + 2 * e + 1]);
-            l[16 * c + 2 * e] += a;
-            l[16 * c + 2 * e + 1] += d;
+            l[8 * c + e] = f2_add(l[8 * c + e], f2(a, d));
             y[e] = pack2<T>(a, d);
           }
           *reinterpret_cast<uint4*>(line + ((2 * c ^ r) & 7) * 16) = make_uint4(y[0], y[1], y[2], y[3]);
@@ -1310,7 +1310,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
         if (c >= chunks) break;
         float v[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = l[16 * c + e];
+        for (int e = 0; e < 8; ++e) f2_get(l[8 * c + e], v[2 * e], v[2 * e + 1]);
         const float s = sum_over_lanes(v, lane);
         if (!(lane & 1)) sum_s[64 * w4 + 16 * c + (lane >> 1)] = s;
       }
