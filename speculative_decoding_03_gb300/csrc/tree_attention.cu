@@ -790,20 +790,25 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
           }
           // (a row with no slot yet: every s is -inf and every p 0)
           const float off = m == -INFINITY ? 0.f : -m * sl;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const F2 sl2 = f2(sl, sl), off2 = f2(off, off);
+          F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             uint32_t x[32];
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-              const float a = ex2_approx(fmaf(s[64 * c + 2 * e], sl, off));
-              const float d = ex2_approx(fmaf(s[64 * c + 2 * e + 1], sl, off));
-              sum[e & 3] += a + d;
+              float a, d;
+              f2_get(f2_fma(f2(s[64 * c + 2 * e], s[64 * c + 2 * e + 1]), sl2, off2), a, d);
+              a = ex2_approx(a);
+              d = ex2_approx(d);
+              sum[e & 1] = f2_add(sum[e & 1], f2(a, d));
               x[e] = pack2<T>(a, d);
             }
             tmem_st_32x32b_x32(tmem + lanes + kColP + 64 * buf + 32 * c, x);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          float even, odd;
+          f2_get(f2_add(sum[0], sum[1]), even, odd);
+          l += even + odd;
           tmem_st_wait();
           tc_fence_before_sync();
         }
