@@ -20,10 +20,10 @@
 // last or by a kernel of their own, so results do not depend on the order in which CTAs run.
 //
 // Measured on a GB300 (graphs of calls, other inputs in turn): two chains of 8 over 130,000 slots, 32
-// heads on 8 of 128, 162 to 167 us, 95% of the copy bandwidth; 32 trees of up to 16 over 4000 slots in
-// pages of 16 94.5 us, 82%; 128 chains of up to 8 over 1 to 2999 slots, 16 heads on 2 of 64, 38.5 us, 38%,
-// bound by the latency of a tile's steps (1500 cycles) and of a piece's beginning and end (6000);
-// one token over 1000 slots 10.2 us, launch and latency.
+// heads on 8 of 128, 163 to 166 us, 96% of the copy bandwidth; 32 trees of up to 16 over 4000 slots in
+// pages of 16 93.7 us, 83%; 128 chains of up to 8 over 1 to 2999 slots, 16 heads on 2 of 64, 38.1 us, 39%,
+// bound by the latency of a tile's steps (1450 cycles) and of a piece's beginning and end (6000);
+// one token over 1000 slots 10 us, launch and latency.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -1413,6 +1413,89 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Atten
   join_parts<T, D>(q, {(int)blockIdx.x, join.w}, join.x, join.y + 16 * blockIdx.y, n, join.z & 0xffff);
 }
 
+// The same for pieces of many parts: the rows from 4 y on, the parts shared out over the four warps in
+// order, whose sums the first warps add up in that order, a warp a row.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) join_many_kernel(const __grid_constant__ AttendParams p) {
+  constexpr int E = D / 32, kAhead = 4;
+  __shared__ float o_s[4][4][D], l_s[4][4];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int4 join = p.joins[blockIdx.x];
+  if (join.w < 2) return;
+  const int r0 = 4 * blockIdx.y, rows = min((join.z >> 16) - r0, 4);
+  if (rows <= 0) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto line = [&](int k, int r) { return (long long)part_place(blockIdx.x + k, k == 0) * kTile + r0 + r; };
+  // every warp: the rows' maxima over all parts, lane 8 u + k those of row u and the parts k, k + 8, ..
+  float M = -INFINITY;
+  if ((lane >> 3) < rows)
+    for (int k = lane & 7; k < join.w; k += 8) M = fmaxf(M, __ldcg(p.sums + line(k, lane >> 3)).x);
+#pragma unroll
+  for (int m = 4; m >= 1; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
+  const int k_begin = join.w * warp / 4, k_end = join.w * (warp + 1) / 4;
+  float o[4][E], l[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    l[u] = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[u][e] = 0.f;
+  }
+  for (int k0 = k_begin; k0 < k_end; k0 += kAhead) {
+    float x[kAhead][4][E];
+    float2 ml[kAhead][4];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bool on = k0 + j < k_end && u < rows;
+        ml[j][u] = on ? __ldcg(p.sums + line(k0 + j, u)) : make_float2(-INFINITY, 0.f);
+        const float* from = p.partial + line(k0 + j, u) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float2 v = on ? __ldcg(reinterpret_cast<const float2*>(from + e)) : make_float2(0.f, 0.f);
+          x[j][u][e] = v.x;
+          x[j][u][e + 1] = v.y;
+        }
+      }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float f = ml[j][u].x == -INFINITY ? 0.f : ex2_approx(ml[j][u].x - __shfl_sync(0xffffffffu, M, 8 * u));
+        l[u] = fmaf(ml[j][u].y, f, l[u]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[u][e] = fmaf(x[j][u][e], f, o[u][e]);
+      }
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) o_s[warp][u][lane * E + e] = o[u][e];
+    if (lane == 0) l_s[warp][u] = l[u];
+  }
+  __syncthreads();
+  const float Mr = __shfl_sync(0xffffffffu, M, 8 * warp);
+  if (warp >= rows) return;
+  const float lr = (l_s[0][warp] + l_s[1][warp]) + (l_s[2][warp] + l_s[3][warp]);
+  const float inv = lr > 0.f ? 1.f / lr : lr == 0.f ? 0.f : lr;         // (NaN stays)
+  const int i_r = join.y + r0 + warp, i = i_r / p.group, row = join.x + i;
+  const int head = (join.z & 0xffff) * p.group + (i_r - i * p.group);
+  T* dst = reinterpret_cast<T*>(p.out) + row * p.out_row + head * p.out_head + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; e += 2) {
+    float y[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int at = lane * E + e + h;
+      y[h] = ((o_s[0][warp][at] + o_s[1][warp][at]) + (o_s[2][warp][at] + o_s[3][warp][at])) * inv;
+    }
+    *reinterpret_cast<uint32_t*>(dst + e) = pack2<T>(y[0], y[1]);
+  }
+  if (p.lse && lane == 0)
+    p.lse[(long long)row * p.group * p.cs.heads + head] = lr == 0.f ? -INFINITY : (Mr + log2f(lr)) * 0.6931471805599453f;
+}
+
 TileForm tile_form(const CacheStrides& cs, const TargetSlots& slots) {
   if (cs.head_dim != 128) return kHalvesApart;
   if (cs.heads == 1 || cs.head == 128) return kHeadsInLine;
@@ -1481,7 +1564,13 @@ cudaError_t attend_for(AttendParams p, const TargetSlots& slots, bool bf16, cuda
              : launch_pdl(attend_wide_kernel<T, D>, dim3(grid), dim3(kThreads), AttendSmem<D>::kBytes, stream, k_map,
                           v_map, p);
   if (e != cudaSuccess || !p.join_apart) return e;
-  return launch_pdl(join_kernel<T, D>, dim3(grid, cdiv(rows < kTile ? rows : kTile, 16)), dim3(128), 0, stream, p);
+  // Many parts of a piece, taking all requests to be alike, are shared out over a CTA's warps (16 parts
+  // of 48 rows 14.7 to 13.9 us in all, 19 of 128 rows 38.9 to 36.9), unless the four times as many
+  // CTAs that then find no rows cost more (9 parts of 128 rows 19.1 to 22.6).
+  const int alike = (int)(grid / ((long long)p.rows.B * p.cs.heads * cdiv(rows, kTile))) + 2;
+  const int per_cta = min(alike, most_parts) * 8 > min(rows, kTile) ? 4 : 16;
+  return launch_pdl(per_cta == 4 ? join_many_kernel<T, D> : join_kernel<T, D>,
+                    dim3(grid, cdiv(rows < kTile ? rows : kTile, per_cta)), dim3(128), 0, stream, p);
 }
 
 }  // namespace

@@ -38,6 +38,8 @@ PARTS = [
     ([17], [2500], 128, 1, 1, 128),           # 17 rows
     ([33, 64], [700, 2100], 16, 2, 2, 128),
     ([64, 3], [4000, 10], 256, 16, 2, 64),    # 512 rows in blocks of 128
+    ([40], [9000], 32, 4, 2, 64),             # many parts of 80 rows
+    ([8, 3], [7000, 2000], 16, 8, 2, 128),    # and of 32
     ([5] * 33, [40 * i for i in range(33)], 16, 6, 3, 64),       # more requests than a warp looks at
 ]
 
