@@ -83,7 +83,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas) append_kernel(
   const long long task = (long long)blockIdx.x * kAppendWarps + warp;
   const long long place = task / p.parts;
   const int part = (int)(task - place * p.parts);
-  int b, i;
+  int b;
+  long long first_row;                     // of the request's token 0, as the starts have it
   if (p.rows.starts) {
     // a place is a row: it finds its request, and one for each request checks what is said of that
     if (place < p.rows.B && part == 0 && lane == 0) {
@@ -93,15 +94,17 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas) append_kernel(
     if (place >= p.rows.rows) return;
     b = request_of_row(p.rows.starts, p.rows.B, (int)place);
     if (b < 0) return;
-    i = (int)place - p.rows.starts[b];
+    first_row = p.rows.starts[b];
   } else {
     b = (int)(place / p.rows.N);
-    i = (int)(place - (long long)b * p.rows.N);
+    first_row = (long long)b * p.rows.N;
   }
   if (b >= p.rows.B) return;
   const int length = p.slots.lengths[b];
   const RequestRows r = request_rows(p.rows, b, p.err);
-  if (i >= r.n) return;
+  // (starts that descend may find a request that begins behind the row)
+  if (place < first_row || place - first_row >= r.n) return;
+  const int i = (int)(place - first_row);
   const int len = checked_length(p.slots, length, r.n, p.err);
   if (len < 0) return;
   const int row = r.row0 + i, slot = len + i;
