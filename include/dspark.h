@@ -688,7 +688,8 @@ dspark_status dspark_tree_verify(const void* p, int64_t ld_p, const void* q, int
  * accept_len [B] as dspark_tree_verify wrote them; path[b, j] > j).  Token 0's slot stays, so
  * lengths[b] + 1 + accept_len[b] slots are then used.  Other slots keep what they hold.  Pages
  * belong to one request each.  An accept_len outside [0, N - 1] moves nothing of its request
- * and a path entry outside (j, N) not its token; both record DSPARK_ERR_DEVICE_CHECK.
+ * and a path entry outside (j, N) not its token; both record DSPARK_ERR_DEVICE_CHECK.  A request
+ * with an accept_len of 0 is not looked at further, so its pages may be full.
  */
 dspark_status dspark_cache_keep(const dspark_paged_cache* cache, int B, int N, const int32_t* pages,
                                 int max_pages, const int32_t* lengths, const int32_t* path,

@@ -271,11 +271,13 @@ __global__ void __launch_bounds__(256) keep_kernel(const __grid_constant__ KeepP
   pdl_launch_dependents();
   const int b = blockIdx.y, layer = blockIdx.x >> 1, tid = threadIdx.x;
   if (tid < 32) {
-    const int a = p.accept_len[b], len = request_length(p.slots, b, 1, p.err);
+    const int a = p.accept_len[b], length = p.slots.lengths[b];
     int moves = 0;
     if (a < 0 || a > p.N - 1) {
       set_device_error(p.err, DSPARK_ERR_DEVICE_CHECK);
-    } else if (len >= 0) {
+    } else if (a > 0 && checked_length(p.slots, length, 1 + a, p.err) >= 0) {
+      // (a request of which nothing is kept may have its pages full)
+      const int len = length;
       for (int j0 = 0; j0 < a; j0 += 32) {
         const int j = j0 + tid;
         long long from = -1, to = -1;

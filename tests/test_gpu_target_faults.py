@@ -62,3 +62,67 @@ def test_append_of_starts_that_descend(starts, own):
         page, line = batch.place(b, [batch.lengths[b] + i])
         assert torch.equal(k[page, line][0], new_k[row]) and torch.equal(v[page, line][0], new_v[row])
         assert torch.equal(q_out[row], q[row])
+
+
+# --------------------------------------------------------------------------- keeping
+
+def kept(batch, k, v, paths):
+    """What ``cache_keep`` leaves of [layers, ...] caches, for paths {request: [(j, place), ..]}."""
+    want = [k.clone(), v.clone()]
+    for b, moves in paths.items():
+        for j, node in moves:
+            src, dst = batch.place(b, [batch.lengths[b] + node]), batch.place(b, [batch.lengths[b] + 1 + j])
+            for new, old in zip(want, (k, v)):
+                new[:, dst[0], dst[1]] = old[:, src[0], src[1]]
+    return want
+
+
+def test_keep_of_requests_whose_pages_are_full():
+    """A request without tokens whose pages are full is not looked at; one that accepts all it has
+    room for is kept, and one that accepts more is not."""
+    batch = Batch([0, 4, 0, 4], [32, 28, 32, 29], 16, N=6, spare=4)
+    assert batch.max_pages == 3
+    pages = batch.pages[:, :2].contiguous()                   # room for 32 slots of each
+    k, v = (noise(t, 63 + j) for j, t in enumerate(new_cache(batch, 2, 64, BF16, layers=2)))
+    ws, cache = workspace(), ds.PagedCache(k, v)
+    path = i32([[-1] * 6, [1, 3, -1, -1, -1, -1], [-1] * 6, [-1] * 6])
+    want = kept(batch, k, v, {1: [(1, 3)]})
+    ds.cache_keep(cache, pages, batch.lens, path, i32([0, 2, 0, 0]), ws)
+    assert ws.status() == 0
+    assert torch.equal(k, want[0]) and torch.equal(v, want[1])
+    want = kept(batch, k, v, {1: [(0, 2)]})
+    path = i32([[1] + [-1] * 5, [2] + [-1] * 5, [-1] * 6, [1, 2, 3, -1, -1, -1]])
+    ds.cache_keep(cache, pages, batch.lens, path, i32([1, 1, 0, 3]), ws)
+    assert ws.status() == DEVICE_CHECK and ws.status() == 0
+    assert torch.equal(k, want[0]) and torch.equal(v, want[1])
+
+
+BAD_KEEPS = [
+    # what the second of three requests has, and its moves that are still made
+    (dict(accept=-1), []), (dict(accept=8), []), (dict(accept=1 << 30), []), (dict(length=-1), []),
+    (dict(length=(1 << 31) - 1), []), (dict(length=1 << 20), []),
+    (dict(path=[3, 1, 6]), [(0, 3), (2, 6)]), (dict(path=[3, -1, 6]), [(0, 3), (2, 6)]),
+    (dict(path=[3, 8, 6]), [(0, 3), (2, 6)]), (dict(path=[0, 5, 6]), [(1, 5), (2, 6)]),
+    (dict(path=[3, 1 << 30, 6]), [(0, 3), (2, 6)]),
+    (dict(path=[3, 7, 5]), [(0, 3), (2, 5)]),                  # a slot behind the table's last page
+    (dict(page=-1), []), (dict(page=1 << 20), []),
+]
+
+
+@pytest.mark.parametrize("bad,moves", BAD_KEEPS, ids=[str(b[0]) for b in BAD_KEEPS])
+def test_keep_of_what_is_out_of_range(bad, moves):
+    """What is refused of one request is reported and moves nothing; the rest moves as ever."""
+    batch = Batch([8, 7, 8], [20, 25, 5], 16, N=8)
+    k, v = (noise(t, 65 + j) for j, t in enumerate(new_cache(batch, 2, 64, BF16, layers=2)))
+    path = np.full((3, 8), -1, np.int32)
+    path[0, :2], path[2, :3] = [2, 5], [3, 4, 7]
+    mine = bad.get("path", [3, 5, 6])
+    path[1, :len(mine)] = mine
+    accept, lengths, pages = [2, bad.get("accept", 3), 3], [20, bad.get("length", 25), 5], batch.pages.clone()
+    if "page" in bad:
+        pages[1, 1] = bad["page"]                              # slots 16 to 31: all of its tokens'
+    want = kept(batch, k, v, {0: [(0, 2), (1, 5)], 1: moves, 2: [(0, 3), (1, 4), (2, 7)]})
+    ws = workspace()
+    ds.cache_keep(ds.PagedCache(k, v), pages, i32(lengths), i32(path.tolist()), i32(accept), ws)
+    assert ws.status() == DEVICE_CHECK and ws.status() == 0
+    assert torch.equal(k, want[0]) and torch.equal(v, want[1])
