@@ -673,7 +673,8 @@ dspark_status dspark_tree_attention(const dspark_paged_cache* cache, int layer, 
  *   the last token; n_out [B] = accept_len + 1; -1 behind them.  A request without tokens has
  *   n_out 0.  tokens [rows] int32 (token 0's is not looked at); one outside [0, V) is never
  *   accepted, and a row with nothing to draw from gives -1: both record
- *   DSPARK_ERR_DEVICE_CHECK.  p's and q's leading dimensions are in elements (any alignment).
+ *   DSPARK_ERR_DEVICE_CHECK.  So does a row that is drawn from and whose p, or q where a child of
+ *   it was rejected, holds a NaN, or whose sum is infinite.  p's and q's leading dimensions are in elements (any alignment).
  */
 dspark_status dspark_tree_verify(const void* p, int64_t ld_p, const void* q, int64_t ld_q, int dtype,
                                  int V, const int32_t* tokens, const float* uniforms,

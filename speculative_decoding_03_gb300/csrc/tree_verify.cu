@@ -75,6 +75,13 @@ __device__ __forceinline__ Sum2 warp_scan(Sum2 x) {
   return x;
 }
 
+// max(x, 0), NaN where x is (fmaxf would make it 0, and the row's sum would not show it)
+__device__ __forceinline__ float above_zero(float x) {
+  float y;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // What is left of the row p after `rejected` children: r = p, then r = max(r - s q, 0) for
 // each child drawn from q (s the sum before it, 1 at first), or r = 0 at their tokens.
 struct Left {
@@ -85,11 +92,11 @@ struct Left {
   template <int N>
   __device__ __forceinline__ void of(float (&r)[N], const float (&q)[N]) const {
 #pragma unroll
-    for (int e = 0; e < N; ++e) r[e] = fmaxf(r[e] - q[e], 0.f);       // s is 1 before the first
+    for (int e = 0; e < N; ++e) r[e] = above_zero(r[e] - q[e]);       // s is 1 before the first
     for (int j = 1; j < rounds; ++j) {
       const float minus = -s[j];
 #pragma unroll
-      for (int e = 0; e < N; ++e) r[e] = fmaxf(__fmaf_rn(minus, q[e], r[e]), 0.f);
+      for (int e = 0; e < N; ++e) r[e] = above_zero(__fmaf_rn(minus, q[e], r[e]));
     }
   }
   __device__ __forceinline__ bool struck(int v) const {
@@ -317,8 +324,10 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
         } else {
           s.add(-r[0]);
           s = s.normal();
-          if (lane == 0) point_s[points] = x;
-          ++points;
+          if (r[0] == r[0]) {                // (NaN stays, for the row's sum to show)
+            if (lane == 0) point_s[points] = x;
+            ++points;
+          }
         }
         __syncwarp();
       }
@@ -411,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
       __syncthreads();
       if (state_s[4] == 4) break;
       total = before_s[W];
-      if (why == 1 || total.hi > 0.f || (!left.rounds && !left.points)) break;
+      if (why == 1 || total.hi != 0.f || (!left.rounds && !left.points)) break;
       left.rounds = left.points = 0;         // nothing is left: from the target's own row
     }
     if (state_s[4] == 4) break;

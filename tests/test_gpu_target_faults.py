@@ -126,3 +126,59 @@ def test_keep_of_what_is_out_of_range(bad, moves):
     ds.cache_keep(ds.PagedCache(k, v), pages, i32(lengths), i32(path.tolist()), i32(accept), ws)
     assert ws.status() == DEVICE_CHECK and ws.status() == 0
     assert torch.equal(k, want[0]) and torch.equal(v, want[1])
+
+
+# ---------------------------------------------------------------------- verification
+
+def rejected(dtype, V=3001, B=4, N=4, seed=70):
+    """Requests whose children, siblings of one root, are all rejected; p, q, tokens, u, parents."""
+    g = gen(seed)
+    p = torch.softmax(torch.randn(B, N, V, generator=g, device="cuda"), -1)
+    q = torch.softmax(torch.randn(B, N, V, generator=g, device="cuda"), -1)
+    tokens = i32([[0, 7, 8, 9]] * B)
+    p[:, 0, 7:10] = 0.0
+    parents = i32([[-1, 0, 0, 0]] * B)
+    u = torch.full((B, N), 0.5, device="cuda")
+    return p.to(dtype), q.to(dtype), tokens, u, parents
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("where", ["p", "q", "p at a child", "q at a child", "p is infinite", "both infinite"])
+@pytest.mark.parametrize("children", [1, 3])
+def test_verify_reports_what_is_not_finite(dtype, where, children):
+    """A NaN, or an infinite probability, in the row that a request draws from is reported and gives no
+    token, whatever was rejected before; the other requests are answered as ever."""
+    p, q, tokens, u, parents = rejected(dtype, V=40000 if children == 1 else 3001)     # by clusters, by a CTA
+    counts = i32([1 + children] * 4)
+    ws = workspace()
+    want = {}
+    for drawn in (True, False):
+        want[drawn] = ds.tree_verify(p, tokens, u, ws, q=q if drawn else None, counts=counts, parents=parents)
+        assert ws.status() == 0 and (want[drawn]["n_out"] == 1).all() and (want[drawn]["out_tokens"][:, 0] >= 0).all()
+    at = 7 if "child" in where else 2500
+    if where.startswith(("p", "both")):
+        p[2, 0, at] = math.inf if "infinite" in where else math.nan
+    if where.startswith(("q", "both")):
+        q[2, 0, at] = math.inf if "infinite" in where else math.nan
+    for drawn in (True, False):
+        if not drawn and where.startswith("q"):
+            continue
+        got = ds.tree_verify(p, tokens, u, ws, q=q if drawn else None, counts=counts, parents=parents)
+        assert ws.status() == DEVICE_CHECK and ws.status() == 0
+        assert got["out_tokens"][2].tolist() == [-1] * 4 and got["accept_len"][2] == 0
+        for key, value in want[drawn].items():
+            others = torch.tensor([0, 1, 3], device="cuda")
+            assert torch.equal(got[key][others], value[others]), key
+
+
+@pytest.mark.parametrize("drawn", [True, False])
+def test_verify_reads_no_more_than_it_answers_from(drawn):
+    """NaN in rows of tokens that are not reached, and in a row all of whose probability is left."""
+    p, q, tokens, u, parents = rejected(F32)
+    p[:, 0, 7] = 0.9                                           # the first child is accepted
+    p[:, 2:], q[:, 2:] = math.nan, math.nan
+    p[:, 0, 2500], q[:, 0, 2500] = math.nan, math.nan
+    ws = workspace()
+    got = ds.tree_verify(p, tokens, u, ws, q=q if drawn else None, parents=parents)
+    assert ws.status() == 0 and (got["accept_len"] == 1).all() and (got["path"][:, 0] == 1).all()
+    assert (got["out_tokens"][:, :2] >= 0).all()
