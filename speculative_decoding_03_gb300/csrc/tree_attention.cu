@@ -218,6 +218,22 @@ struct Pieces {
   }
 };
 
+// A slot on a page that the cache does not have counts as none: the copies bring zeroes for it (and
+// report it), and its scores are masked.  Whether a piece has such slots, `lanes` threads look at its
+// pages for, beside the loads of its queries.
+__device__ __forceinline__ bool on_a_page(const TargetSlots& s, int b, int slot) {
+  return (unsigned)s.pages[(long long)b * s.max_pages + (slot >> s.page_shift)] < (unsigned)s.n_pages;
+}
+__device__ __forceinline__ bool lacks_pages(const TargetSlots& s, const Pieces& pc, int lane, int lanes) {
+  const int32_t* table = s.pages + (long long)pc.b * s.max_pages;
+  const int last = (min(pc.r.end, (pc.tile0 + pc.n_tiles) * kTile) - 1) >> s.page_shift;
+  bool lacks = false;
+#pragma unroll 4
+  for (int i = (pc.tile0 * kTile >> s.page_shift) + lane; i <= last; i += lanes)
+    lacks |= (unsigned)table[i] >= (unsigned)s.n_pages;
+  return lacks;
+}
+
 // a / b of numbers >= 0 (a 64-bit division takes some 150 cycles)
 __device__ __forceinline__ long long quotient(long long a, long long b) {
   return (unsigned long long)(a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
@@ -692,6 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
     int row = -1, q_head = 0;                  // this thread's row of q, -1: none
     unsigned long long sees = 0;               // the tokens that it attends to
     bool busy = false;                         // the warp has a row
+    bool lacks = false;                        // the piece has slots on no page
     auto begin = [&]() {                       // the piece's queries into shared memory
       const int i_r = pc.block * kTile + r, i = i_r / p.group;
       busy = pc.block * kTile + w4 * 32 < pc.r.n * p.group;
@@ -701,6 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
       uint4 x[D / 8];
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) x[c] = row >= 0 ? src[c] : make_uint4(0, 0, 0, 0);
+      lacks = __any_sync(0xffffffffu, lacks_pages(p.slots, pc, lane, 32));
       sees = 0;
       if (p.rows.parents) {
         __syncwarp();
@@ -722,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
     if (more) begin();
     while (more) {
       const int b = pc.b, head = pc.head, block = pc.block, tile0 = pc.tile0, n = pc.n_tiles;
-      const bool whole = pc.whole, my_busy = busy;
+      const bool whole = pc.whole, my_busy = busy, my_lacks = lacks;
       const Request rq = pc.r;
       const int my_row = row, my_head = q_head;
       const unsigned long long my_sees = sees;
@@ -730,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
       for (int j = 0; j < n && ok; ++j) {
         const uint32_t t = tc + j, buf = t & 1;
         const int slot0 = (tile0 + j) * kTile;
-        const bool masked = slot0 + kTile > rq.len;
+        const bool masked = slot0 + kTile > rq.len || my_lacks;
         ok = wait(&s_full[buf], (t >> 1) & 1);
         if (masked && ok) {
           // thread r looks after line r of the value tile
@@ -762,6 +780,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
               uint32_t bits = a >= 32 ? 0xffffffffu : a > 0 ? (1u << a) - 1 : 0u;
               if (a >= 0) bits |= a < 32 ? (uint32_t)(my_sees << a) : 0u;
               else if (a > -64) bits |= (uint32_t)(my_sees >> -a);
+              if (my_lacks) {
+                const int slot = slot0 + 32 * c + lane;
+                bits &= __ballot_sync(0xffffffffu, slot < rq.end && on_a_page(p.slots, b, slot));
+              }
 #pragma unroll
               for (int e = 0; e < 32; ++e) s[32 * c + e] = (bits >> e) & 1 ? s[32 * c + e] : -INFINITY;
             }
@@ -978,6 +1000,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
   uint32_t* tmem_s = reinterpret_cast<uint32_t*>(words + 1);
   volatile int* bad_s = words + 2;                           // by piece parity: piece + 1 with values not finite
   int* start_s = words + 4;
+  int* lacks_s = words + 8;                                  // [2 warps] by piece parity: it has slots on no page
   long long* sums_s = reinterpret_cast<long long*>(small + 576);
   PieceInfo* info_s = reinterpret_cast<PieceInfo*>(small + 640);                      // [2] by piece parity
   int* parents_s = reinterpret_cast<int*>(small + 768);                               // [2 warps][64]
@@ -1123,6 +1146,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
       uint4 x[D / 8];
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) x[c] = live ? src[c] : make_uint4(0, 0, 0, 0);
+      const bool lacks = lacks_pages(p.slots, pc, col, 64);
       // (while the queries come)
       const Parts parts = pc.whole ? Parts{0, 1} : parts_of(share, pc.unit0, pc.r.tiles);
       unsigned long long sees = 0;
@@ -1152,6 +1176,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
         }
       }
       to_s[64 * q + col] = (long long)(pc.r.row0 + i) * p.out_row + head * p.out_head;
+      const bool any_lacks = __any_sync(0xffffffffu, lacks);
+      if (lane == 0) lacks_s[2 * q + (warp - kLoadWarp)] = any_lacks;
       if (col == 0)
         info_s[q] = {pc.b, pc.head, pc.block, pc.tile0, pc.n_tiles, pc.r.tiles, pc.r.row0, pc.r.n, pc.r.len, pc.r.end, rows, parts};
       fence_proxy_async_smem();
@@ -1177,6 +1203,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
       const PieceInfo rq = info_s[q];
       const int rows = rq.rows, chunks = (rows + 15) / 16, n = rq.n_tiles, tile0 = rq.tile0;
       if (n == 0) break;
+      const bool lacks = lacks_s[2 * q] | lacks_s[2 * q + 1];
       bool open = true;                        // a column has no reference yet
       F2 l[kColumns / 2];                      // this thread's slots' part of the columns' sums
 #pragma unroll
@@ -1185,10 +1212,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
       for (int j = 0; j < n; ++j, ++t) {
         const uint32_t buf = t & 1;
         const int slot0 = (tile0 + j) * kTile, slot = slot0 + r;
-        const bool masked = slot0 + kTile > rq.len;
+        const bool masked = slot0 + kTile > rq.len || lacks;
         uint2 seen = make_uint2(~0u, ~0u);     // the columns that see this slot
         if (masked && slot >= rq.len)
           seen = slot < rq.end ? *reinterpret_cast<const uint2*>(seen_s + 128 * q + 2 * (slot - rq.len)) : make_uint2(0, 0);
+        if (lacks && slot < rq.end && !on_a_page(p.slots, rq.b, slot)) seen = make_uint2(0, 0);
         ok = wait(&s_full[buf], (t >> 1) & 1) && ok;
         __syncwarp();
         tc_fence_after_sync();

@@ -10,7 +10,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 ds = pytest.importorskip("speculative_decoding_03_gb300")
 if torch.cuda.is_available():
-    from _target import Batch, gen, i32, new_cache, workspace
+    from _target import Batch, attention_tolerance, fill_cache, gen, i32, new_cache, sees, workspace
 
 BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
 DEVICE_CHECK = 5
@@ -182,3 +182,75 @@ def test_verify_reads_no_more_than_it_answers_from(drawn):
     got = ds.tree_verify(p, tokens, u, ws, q=q if drawn else None, parents=parents)
     assert ws.status() == 0 and (got["accept_len"] == 1).all() and (got["path"][:, 0] == 1).all()
     assert (got["out_tokens"][:, :2] >= 0).all()
+
+
+# -------------------------------------------------------------------------- attention
+
+def attention_without(batch, q, k, v, scale, gone):
+    """(out, lse, spread, size) of the live rows in 64 bits, where the slots gone[b] count as none."""
+    Hkv, D = k.shape[-2:]
+    flat = q.reshape(batch.rows, q.shape[-2], D)
+    parts = []
+    for b in range(batch.B):
+        n, l = batch.counts[b], batch.lengths[b]
+        if not n:
+            continue
+        page, line = batch.place(b, np.arange(l + n))
+        kk, vv = k[page, line].double(), v[page, line].double()
+        mask = torch.zeros(n, l + n, dtype=torch.bool)
+        mask[:, :l] = True
+        for i in range(n):
+            mask[i, [l + a for a in sees(batch.trees[b], i)]] = True
+        mask[:, [s for s in gone.get(b, []) if s < l + n]] = False
+        mask = mask.cuda()[:, None, None]
+        x = flat[batch.first[b]:batch.first[b] + n].double().view(n, Hkv, -1, D)
+        s = torch.where(mask, torch.einsum("nhgd,lhd->nhgl", x, kk) * scale, -math.inf)
+        p = torch.nan_to_num(torch.softmax(s, -1))            # (a row of no slots: zeroes)
+        o, a = torch.einsum("nhgl,lhd->nhgd", p, vv), torch.einsum("nhgl,lhd->nhgd", p, vv.abs())
+        big = (torch.einsum("nhgd,lhd->nhgl", x.abs(), kk.abs()) * scale).amax(-1)
+        parts.append((o.reshape(n, -1, D), torch.logsumexp(s, -1).reshape(n, -1), a.reshape(n, -1, D), big.reshape(n, -1)))
+    return [torch.cat(t) for t in zip(*parts)]
+
+
+GONE = [
+    # counts, lengths, page, q_heads, heads, D, and the pages of each request that are none
+    ([3, 4], [100, 20], 16, 4, 2, 128, {0: [0, 3]}),          # up to 16 rows a key head: a lone tile
+    ([3, 4], [700, 20], 16, 4, 2, 64, {0: [1, 40], 1: [1]}),  # parts, and the tokens' own page
+    ([1], [3000], 16, 4, 1, 128, {0: [0, 50, 100, 187]}),     # parts joined by the last
+    ([1], [3100], 256, 4, 1, 128, {0: [0, 5]}),               # and by a kernel; tiles that hold nothing
+    ([12, 9], [300, 0], 32, 8, 2, 128, {0: [2, 9], 1: [0]}),  # up to 64 rows
+    ([12], [2000], 128, 3, 1, 64, {0: [0, 1, 15]}),
+    ([40, 17], [260, 129], 64, 8, 2, 128, {0: [0, 4], 1: [1]}),       # more, in two row blocks
+    ([33], [3000], 16, 4, 1, 64, {0: [0, 1, 2, 3, 4, 5, 6, 7, 9, 100]}),
+    ([5, 2], [40, 0], 16, 2, 1, 64, {0: [0, 1, 2], 1: [0]}),  # no page at all
+    ([20, 2], [40, 0], 16, 16, 2, 128, {0: [0, 1, 2, 3], 1: [0]}),
+]
+
+
+@pytest.mark.parametrize("case", GONE, ids=[f"{i}" for i in range(len(GONE))])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_attention_of_pages_that_are_none(case, dtype):
+    """Slots on a page outside the cache take no part: the others are attended to as without them, in
+    outputs and sums, and rows with nothing left get zeroes and -inf."""
+    counts, lengths, page, Hq, Hkv, D, pages_gone = case
+    batch = Batch(counts, lengths, page, seed=80, tree=True)
+    k, v = new_cache(batch, Hkv, D, dtype)
+    fill_cache(batch, k, v)
+    pages = batch.pages.clone()
+    gone = {b: [s for i in at for s in range(page * i, page * (i + 1))] for b, at in pages_gone.items()}
+    for b, at in pages_gone.items():
+        for j, i in enumerate(at):
+            pages[b, i] = (-1, batch.n_pages, -(1 << 31), (1 << 31) - 1)[j % 4]
+    q = torch.randn(batch.lead + (Hq, D), generator=gen(81), device="cuda").to(dtype)
+    out, lse = torch.full_like(q, 5.0), torch.full(batch.lead + (Hq,), 5.0, device="cuda")
+    ws = workspace(batch, Hq, Hkv, D)
+    ds.tree_attention(q, ds.PagedCache(k, v), pages, batch.lens, ws, out=out, lse=lse, **batch.kw)
+    assert ws.status() == DEVICE_CHECK and ws.status() == 0
+    ref, ref_lse, spread, size = attention_without(batch, q, k, v, D ** -0.5, gone)
+    rows = batch.live_rows()
+    tol = attention_tolerance(batch, ref, spread, size, v, dtype)
+    assert ((out.view(batch.rows, Hq, D)[rows].double() - ref).abs() <= tol).all()
+    got, none = lse.view(batch.rows, Hq)[rows].double(), torch.isinf(ref_lse)
+    assert torch.equal(got == -math.inf, none)
+    bound = size * (D + 4) * 2.0 ** -23 + (max(lengths) / 32 + 128) * 2.0 ** -23 + torch.nan_to_num(ref_lse).abs() * 2.0 ** -22
+    assert ((got - ref_lse).abs() <= bound)[~none].all()
