@@ -286,6 +286,8 @@ PyObject* verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int32_t *tokens, *parents;
   const float* uniforms;
   int32_t *accept_len, *path, *out_tokens, *n_out;
+  for (int i = 9; i < n; ++i)
+    if (a[i] == Py_None) return unchecked();             // an output that is to be made
   if (n != 13 || !w.take(a[0], a[3]) || !p.take(a[0], w.dev) ||
       !t.take(p.shape.v, p.shape.n - 1, a[5], a[6], a[7], w.dev))
     return unchecked();

@@ -247,12 +247,13 @@ def tree_verify(p, tokens, uniforms, ws: Workspace, q=None, starts=None, counts=
     ``tokens`` [...] int32 (a request's first is its last committed token), ``uniforms`` [...] fp32 in
     [0, 1): the first token's is the last draw's, the others' decide their token.  ``q`` [..., V]: the
     distribution from which a token's children were drawn, each independently; None: children
-    that the draft names without chance (greedy drafts, its most probable tokens).  Returns (or
-    fills ``out``) a dict of int32 tensors: ``accept_len`` [B], ``path`` [B, N] the accepted tokens'
-    places, ``out_tokens`` [B, N] their ids and the last token, ``n_out`` [B]; -1 behind them."""
+    that the draft names without chance (greedy drafts, its most probable tokens).  Returns a dict
+    of int32 tensors: ``accept_len`` [B], ``path`` [B, N] the accepted tokens' places, ``out_tokens``
+    [B, N] their ids and the last token, ``n_out`` [B]; -1 behind them.  It is ``out`` if that is
+    given: entries that it holds are written, those that it lacks are made."""
     if stream is None and out is not None:
-        code = _calls().verify(p, tokens, uniforms, ws, q, starts, counts, nodes, parents, out["accept_len"],
-                               out["path"], out["out_tokens"], out["n_out"])
+        code = _calls().verify(p, tokens, uniforms, ws, q, starts, counts, nodes, parents, out.get("accept_len"),
+                               out.get("path"), out.get("out_tokens"), out.get("n_out"))
         if code is not None:
             _done("dspark_tree_verify", code)
             return out
@@ -268,11 +269,11 @@ def tree_verify(p, tokens, uniforms, ws: Workspace, q=None, starts=None, counts=
             raise ValueError(f"q: {n} x {V} {p.dtype} on {p.device} are needed, not {tuple(q.shape)} {q.dtype}")
         q_p = q.data_ptr()
     if out is None:
-        with allocate:
-            out = {"accept_len": torch.empty(B, dtype=i32, device=p.device),
-                   "path": torch.empty((B, N), dtype=i32, device=p.device),
-                   "out_tokens": torch.empty((B, N), dtype=i32, device=p.device),
-                   "n_out": torch.empty(B, dtype=i32, device=p.device)}
+        out = {}
+    for key, shape in (("accept_len", (B,)), ("path", (B, N)), ("out_tokens", (B, N)), ("n_out", (B,))):
+        if out.get(key) is None:
+            with allocate:
+                out[key] = torch.empty(shape, dtype=i32, device=p.device)
     _done("dspark_tree_verify", lib().dspark_tree_verify(
         p.data_ptr(), ld, q_p, ld_q, code, V, _flat(tokens, "tokens", rows, i32, p, dev),
         _flat(uniforms, "uniforms", rows, torch.float32, p, dev), s, c, _flat(parents, "parents", rows, i32, p, dev),

@@ -184,6 +184,24 @@ def test_verify_reads_no_more_than_it_answers_from(drawn):
     assert (got["out_tokens"][:, :2] >= 0).all()
 
 
+@pytest.mark.parametrize("given", [[], ["path"], ["accept_len", "out_tokens"], ["n_out", "path", "accept_len", "out_tokens"]])
+@pytest.mark.parametrize("on_stream", [False, True])
+def test_verify_makes_the_outputs_that_it_lacks(given, on_stream):
+    """A dict of some of the outputs is filled: what it holds is written, what it lacks is made."""
+    p, q, tokens, u, parents = rejected(F32)
+    stream = torch.cuda.current_stream() if on_stream else None
+    want = ds.tree_verify(p, tokens, u, workspace(), q=q, parents=parents)
+    mine = {key: torch.full_like(want[key], -9) for key in given}
+    out = dict(mine)
+    if given == ["path"]:
+        out["n_out"] = None
+    got = ds.tree_verify(p, tokens, u, workspace(), q=q, parents=parents, out=out, stream=stream)
+    assert got is out and set(got) == set(want)
+    assert all(got[key] is t for key, t in mine.items())
+    for key, value in want.items():
+        assert torch.equal(got[key], value), key
+
+
 # -------------------------------------------------------------------------- attention
 
 def attention_without(batch, q, k, v, scale, gone):
