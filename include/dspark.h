@@ -644,7 +644,7 @@ dspark_status dspark_cache_append(const dspark_paged_cache* cache, int layer, co
  * of -inf.
  *
  *   q, out [rows, q_heads, head_dim] of the cache's type (strides as above), q_heads a multiple of
- *   heads; head_dim 64 or 128; scale > 0; workspace of
+ *   heads; head_dim 64 or 128; scale > 0, scale log2(e) finite in fp32; workspace of
  *   dspark_tree_attention_workspace_bytes (0 on bad shapes).
  */
 size_t dspark_tree_attention_workspace_bytes(int B, int N, int q_heads, int heads, int head_dim);

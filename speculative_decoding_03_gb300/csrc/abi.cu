@@ -697,7 +697,9 @@ dspark_status dspark_tree_attention(const dspark_paged_cache* cache, int layer, 
   if (st == DSPARK_OK) st = check_heads(q, q_row, q_head, rows);
   if (st == DSPARK_OK) st = check_heads(out, out_row, out_head, rows);
   if (st != DSPARK_OK) return st;
-  if (layer < 0 || layer >= cache->layers || q_heads < 1 || q_heads % cs.heads != 0 || !(scale > 0.f) || !finite(scale))
+  // (scores are formed times scale log2(e))
+  if (layer < 0 || layer >= cache->layers || q_heads < 1 || q_heads % cs.heads != 0 || !(scale > 0.f) ||
+      !finite(scale * kLog2e))
     return DSPARK_ERR_INVALID_ARG;
   if ((q_heads > 1 && out_head < cs.head_dim) || (rows > 1 && out_row < cs.head_dim)) return DSPARK_ERR_INVALID_ARG;
   if (!aligned_or_null(lse, 4)) return DSPARK_ERR_INVALID_ARG;
