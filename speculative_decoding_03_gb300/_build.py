@@ -13,13 +13,15 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libdspark.so")
-CALLS = os.path.join(BUILD, "_dspark_calls.so")
+# (named after the interpreter whose C API it is compiled against: another's is another file)
+CALLS = os.path.join(BUILD, "_dspark_calls" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -39,20 +41,42 @@ def _sources():
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
-        [os.path.join(ROOT, "include", "dspark.h"), os.path.join(CSRC, "calls.cpp")]
+        [os.path.join(ROOT, "include", "dspark.h")]
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CALLS):
+def _stale(target, deps) -> bool:
+    return not os.path.exists(target) or any(os.path.getmtime(p) > os.path.getmtime(target) for p in deps)
+
+
+def build_calls(force: bool = False) -> bool:
+    """Compile the Python module of calls.cpp.  Where that cannot be done (no headers of this interpreter)
+    it is left out with a warning, and the calls are checked in Python: target.py has every check."""
+    source = os.path.join(CSRC, "calls.cpp")
+    if not force and not _stale(CALLS, [source, os.path.join(ROOT, "include", "dspark.h")]):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
-    return any(os.path.getmtime(p) > t for p in _deps())
+    tmp = CALLS + ".tmp"
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I",
+           sysconfig.get_paths()["include"], source, "-o", tmp]
+    try:
+        os.makedirs(BUILD, exist_ok=True)
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode == 0:
+            os.replace(tmp, CALLS)
+            return True
+        why = f"{res.stdout}\n{res.stderr}"
+    except OSError as e:
+        why = str(e)
+    if os.path.exists(CALLS):
+        os.remove(CALLS)                     # (an older one may call the library otherwise)
+    warnings.warn(f"the module of calls.cpp was not built, calls are checked in Python: {why}", RuntimeWarning)
+    return False
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     """Compile every kernel source for sm_103a and link libdspark.so (returns its path), and the
     Python module."""
-    if not force and not _stale():
+    if not force and not _stale(LIB, _deps()):
+        build_calls()
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     flags = NVCC_FLAGS + list(extra_flags or [])
@@ -68,17 +92,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
             print(res.stdout + res.stderr)
         return obj
 
-    def compile_calls():
-        tmp = CALLS + ".tmp"
-        cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I",
-               sysconfig.get_paths()["include"], os.path.join(CSRC, "calls.cpp"), "-o", tmp]
-        res = subprocess.run(cmd, capture_output=True, text=True)
-        if res.returncode != 0:
-            raise RuntimeError(f"g++ failed on calls.cpp:\n{res.stdout}\n{res.stderr}")
-        os.replace(tmp, CALLS)
-
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
-        calls = ex.submit(compile_calls)
+        calls = ex.submit(build_calls, force)
         objs = list(ex.map(compile_one, _sources()))
         calls.result()
     tmp = LIB + ".tmp"

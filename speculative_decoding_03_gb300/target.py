@@ -24,6 +24,8 @@ import ctypes
 import functools
 import importlib.machinery
 import importlib.util
+import os
+import warnings
 from typing import Dict, Optional
 
 from . import DSparkError, Workspace, _build, lib
@@ -66,22 +68,40 @@ class PagedCache:
         self._key = (self._ptr, self.dtype, self.index, self.heads, self.head_dim)
 
 
+class _Unchecked:
+    """In the place of the module: every call is left to the checks below."""
+    append = attend = verify = keep = staticmethod(lambda *args: None)
+
+
+def _module():
+    """The module of calls.cpp; None where it was not built for this interpreter."""
+    if not os.path.exists(_build.CALLS):
+        return None
+    loader = importlib.machinery.ExtensionFileLoader("_dspark_calls", _build.CALLS)
+    try:
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_dspark_calls", loader))
+        loader.exec_module(module)
+    except ImportError as e:
+        warnings.warn(f"{_build.CALLS} cannot be loaded, calls are checked in Python: {e}", RuntimeWarning)
+        return None
+    return module
+
+
 @functools.lru_cache(maxsize=None)
 def _calls():
-    """The module that checks and makes a well-formed call in C (calls.cpp): for a single token the checks
+    """What checks and makes a well-formed call in C (calls.cpp): for a single token the checks
     below take longer than the kernel.  Its functions return a status, or None where a check failed
     or an output is to be made: then the checks below are made, which say what is wrong."""
     torch, _ = _types()
     L = lib()
-    loader = importlib.machinery.ExtensionFileLoader("_dspark_calls", _build.CALLS)
-    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_dspark_calls", loader))
-    loader.exec_module(module)
+    module = _module()
+    if module is None:
+        return _Unchecked
     module.setup(*(ctypes.cast(getattr(L, "dspark_" + name), ctypes.c_void_p).value
                    for name in ("cache_append", "tree_attention", "tree_verify", "cache_keep")),
                  torch.float32, torch.bfloat16, torch.float16, torch.int32, torch._C._cuda_getDevice,
                  torch._C._cuda_getCurrentRawStream)
     return module
-
 
 
 def _begin(like, ws, stream):

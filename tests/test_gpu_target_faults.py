@@ -9,6 +9,7 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 ds = pytest.importorskip("speculative_decoding_03_gb300")
+from speculative_decoding_03_gb300 import target  # noqa: E402
 if torch.cuda.is_available():
     from _target import Batch, attention_tolerance, fill_cache, gen, i32, new_cache, sees, workspace
 
@@ -272,3 +273,40 @@ def test_attention_of_pages_that_are_none(case, dtype):
     assert torch.equal(got == -math.inf, none)
     bound = size * (D + 4) * 2.0 ** -23 + (max(lengths) / 32 + 128) * 2.0 ** -23 + torch.nan_to_num(ref_lse).abs() * 2.0 ** -22
     assert ((got - ref_lse).abs() <= bound)[~none].all()
+
+
+# --------------------------------------------------------- calls that are checked in Python
+
+def test_calls_without_the_module(monkeypatch, tmp_path):
+    """Where the module of the checks in C is not there the calls give the same bits."""
+    batch = Batch([3, 7, 0], [20, 45, 5], 16, N=7, tree=True)
+    g = gen(90)
+    x = torch.randn(batch.lead + (8, 64), generator=g, device="cuda").to(BF16)
+    p = torch.softmax(2 * torch.randn(batch.lead + (301,), generator=g, device="cuda"), -1)
+    tokens, u = p.argmax(-1).to(torch.int32), torch.rand(batch.lead, generator=g, device="cuda")
+
+    def step():
+        k, v = new_cache(batch, 2, 64, BF16, fill=0.0)
+        fill_cache(batch, k, v, tokens=False)
+        cache, ws = ds.PagedCache(k, v), workspace(batch, 4, 2, 64)
+        q = torch.zeros_like(x[..., :4, :])
+        out, lse = torch.zeros_like(q), torch.zeros(batch.lead + (4,), device="cuda")
+        answer = {key: torch.zeros(shape, dtype=torch.int32, device="cuda")
+                  for key, shape in (("accept_len", 3), ("path", (3, 7)), ("out_tokens", (3, 7)), ("n_out", 3))}
+        ds.cache_append(cache, x[..., 4:6, :], x[..., 6:, :], batch.pages, batch.lens, ws, q=x[..., :4, :], q_out=q, **batch.kw)
+        ds.tree_attention(q, cache, batch.pages, batch.lens, ws, out=out, lse=lse, **batch.kw)
+        ds.tree_verify(p, tokens, u, ws, out=answer, **batch.kw)
+        ds.cache_keep(cache, batch.pages, batch.lens, answer["path"], answer["accept_len"], ws)
+        assert ws.status() == 0
+        return [k, v, q, out, lse, *answer.values()]
+
+    want = step()
+    assert target._calls() is not target._Unchecked
+    monkeypatch.setattr(target._build, "CALLS", str(tmp_path / "none.so"))
+    target._calls.cache_clear()
+    try:
+        got = step()
+        assert target._calls() is target._Unchecked
+    finally:
+        target._calls.cache_clear()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
