@@ -219,19 +219,48 @@ struct Pieces {
 };
 
 // A slot on a page that the cache does not have counts as none: the copies bring zeroes for it (and
-// report it), and its scores are masked.  Whether a piece has such slots, `lanes` threads look at its
-// pages for, beside the loads of its queries.
-__device__ __forceinline__ bool on_a_page(const TargetSlots& s, int b, int slot) {
-  return (unsigned)s.pages[(long long)b * s.max_pages + (slot >> s.page_shift)] < (unsigned)s.n_pages;
-}
+// report it), and its scores are masked, slot by slot in what may hold such slots:
+//   up to 64 rows: the pieces whose pages the loading warps found not all there, a piece ahead (a word
+//     that the copying warp writes, read at each tile, cost 38.7 instead of 38.0 us for 128 chains)
+//   more rows: all tiles of a CTA once the copying warp has seen such a page.  It says before it copies
+//     tile t how many tiles it has looked at and whether all their pages are there, in one word; one that
+//     does not yet count tile t has the tile's slots looked up, too (looked up by the softmax warps
+//     with the queries: two long trees 38.6 instead of 36.9 us)
+__device__ __forceinline__ bool is_page(const TargetSlots& s, int page) { return (unsigned)page < (unsigned)s.n_pages; }
+__device__ __forceinline__ const int32_t* pages_of(const TargetSlots& s, int b) { return s.pages + (long long)b * s.max_pages; }
+
+// A thread's look at every `lanes`th page of a piece, from its place `lane` on.
 __device__ __forceinline__ bool lacks_pages(const TargetSlots& s, const Pieces& pc, int lane, int lanes) {
-  const int32_t* table = s.pages + (long long)pc.b * s.max_pages;
+  const int32_t* table = pages_of(s, pc.b);
   const int last = (min(pc.r.end, (pc.tile0 + pc.n_tiles) * kTile) - 1) >> s.page_shift;
-  bool lacks = false;
+  int i = (pc.tile0 * kTile >> s.page_shift) + lane;
+  bool lacks = i <= last && !is_page(s, table[i]);
+  if (i + lanes <= last) {
 #pragma unroll 4
-  for (int i = (pc.tile0 * kTile >> s.page_shift) + lane; i <= last; i += lanes)
-    lacks |= (unsigned)table[i] >= (unsigned)s.n_pages;
+    for (i += lanes; i <= last; i += lanes) lacks |= !is_page(s, table[i]);
+  }
   return lacks;
+}
+__device__ __forceinline__ bool may_lack_pages(volatile uint32_t* looked_s, uint32_t t) {
+  const uint32_t word = *looked_s;
+  return (word & 1u) || (word >> 1) <= t;
+}
+
+// A tile's scores (of 32 rows at `scores` in tensor memory) of slots on no page or behind the last: -inf.
+// A function of its own, because the softmax's registers are full and its code is read once a launch.
+__device__ __noinline__ void drop_scores(const int32_t* pages, int page_shift, int n_pages, int slot0, int end, uint32_t scores) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    const int slot = slot0 + 32 * c + lane;
+    const uint32_t bits = __ballot_sync(0xffffffffu, slot < end && (unsigned)pages[slot >> page_shift] < (unsigned)n_pages);
+    uint32_t x[32];
+    tmem_ld_32x32b_sync<32>(scores + 32 * c, x);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) x[e] = (bits >> e) & 1 ? x[e] : 0xff800000u;
+    tmem_st_32x32b_x32(scores + 32 * c, x);
+  }
+  tmem_st_wait();
 }
 
 // a / b of numbers >= 0 (a 64-bit division takes some 150 cycles)
@@ -360,8 +389,9 @@ struct TileCopies {
   const AttendParams& p;
   Pieces pc;
   uint64_t policy;
+  volatile uint32_t* looked_s;   // null: nobody asks
   int left = 0, slot0 = 0;   // tiles of the piece still to come, and the next one's first slot
-  uint32_t item = 0, skipped = ~0u;
+  uint32_t item = 0, skipped = ~0u, looked = 0;
   __device__ __forceinline__ TileAt fetch() {
     if (left == 0) {
       if (!pc.next(p)) return {0, 0, 0, 0};
@@ -405,6 +435,10 @@ struct TileCopies {
     TileAt a = fetch(), b = fetch(), v = {0, 0, 0, 0};
     bool ok = true;
     while (ok && a.end) {
+      if (looked_s) {
+        looked = (looked + 2) | (__any_sync(0xffffffffu, a.id < 0) ? 1u : 0u);
+        if ((threadIdx.x & 31) == 0) *looked_s = looked;
+      }
       ok = copy(k_map, a);
       const TileAt c = fetch();
       if (ok && v.end) ok = copy(v_map, v);
@@ -589,6 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
   uint32_t* tmem_s = reinterpret_cast<uint32_t*>(words + 1);
   int* bad_s = words + 2;                                    // by piece parity: piece + 1 with non-finite values
   int* start_s = words + 4;                                  // first request and unit of this CTA's share
+  volatile uint32_t* looked_s = reinterpret_cast<uint32_t*>(words + 8);        // tiles whose pages are known
   long long* sums_s = reinterpret_cast<long long*>(smem + S::kOffBar + 640);   // [8 warps] and the total
   int* parents_s = reinterpret_cast<int*>(smem + S::kOffBar + 1024);          // [4 warps][64]
 
@@ -611,6 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
     mbar_init(q_full, kTile);
     mbar_init(drain, 1);
     *abort_s = 0;
+    *looked_s = 0;
     fence_mbar_init();
   }
   if (warp == kIssueWarp) {
@@ -638,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
   pc.start(p, kTile, share);
 
   if (warp == kProducerWarp) {
-    TileCopies<S> copies{smem + S::kOffKV, kv_full, kv_empty, wait, p, pc, policy_evict_first()};
+    TileCopies<S> copies{smem + S::kOffKV, kv_full, kv_empty, wait, p, pc, policy_evict_first(), looked_s};
     copies.run(&k_map, &v_map);
   } else if (warp == kIssueWarp) {
     // ----------------------------------------------------------------- products
@@ -708,7 +744,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
     int row = -1, q_head = 0;                  // this thread's row of q, -1: none
     unsigned long long sees = 0;               // the tokens that it attends to
     bool busy = false;                         // the warp has a row
-    bool lacks = false;                        // the piece has slots on no page
     auto begin = [&]() {                       // the piece's queries into shared memory
       const int i_r = pc.block * kTile + r, i = i_r / p.group;
       busy = pc.block * kTile + w4 * 32 < pc.r.n * p.group;
@@ -718,7 +753,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
       uint4 x[D / 8];
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) x[c] = row >= 0 ? src[c] : make_uint4(0, 0, 0, 0);
-      lacks = __any_sync(0xffffffffu, lacks_pages(p.slots, pc, lane, 32));
       sees = 0;
       if (p.rows.parents) {
         __syncwarp();
@@ -740,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
     if (more) begin();
     while (more) {
       const int b = pc.b, head = pc.head, block = pc.block, tile0 = pc.tile0, n = pc.n_tiles;
-      const bool whole = pc.whole, my_busy = busy, my_lacks = lacks;
+      const bool whole = pc.whole, my_busy = busy;
       const Request rq = pc.r;
       const int my_row = row, my_head = q_head;
       const unsigned long long my_sees = sees;
@@ -748,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
       for (int j = 0; j < n && ok; ++j) {
         const uint32_t t = tc + j, buf = t & 1;
         const int slot0 = (tile0 + j) * kTile;
-        const bool masked = slot0 + kTile > rq.len || my_lacks;
+        const bool masked = slot0 + kTile > rq.len;
         ok = wait(&s_full[buf], (t >> 1) & 1);
         if (masked && ok) {
           // thread r looks after line r of the value tile
@@ -763,6 +797,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
         if (!ok) break;
         if (my_busy) {
           tc_fence_after_sync();
+          if (__any_sync(0xffffffffu, may_lack_pages(looked_s, t)))
+            drop_scores(pages_of(p.slots, b), p.slots.page_shift, p.slots.n_pages, slot0, rq.end,
+                        tmem + lanes + 128 * buf);
           float s[kTile];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -780,10 +817,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
               uint32_t bits = a >= 32 ? 0xffffffffu : a > 0 ? (1u << a) - 1 : 0u;
               if (a >= 0) bits |= a < 32 ? (uint32_t)(my_sees << a) : 0u;
               else if (a > -64) bits |= (uint32_t)(my_sees >> -a);
-              if (my_lacks) {
-                const int slot = slot0 + 32 * c + lane;
-                bits &= __ballot_sync(0xffffffffu, slot < rq.end && on_a_page(p.slots, b, slot));
-              }
 #pragma unroll
               for (int e = 0; e < 32; ++e) s[32 * c + e] = (bits >> e) & 1 ? s[32 * c + e] : -INFINITY;
             }
@@ -1059,7 +1092,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
 
   if (warp == kProducerWarp) {
     pc.start(p, kRows, share);
-    TileCopies<S> copies{smem + S::kOffKV, kv_full, kv_empty, wait, p, pc, policy_evict_first()};
+    TileCopies<S> copies{smem + S::kOffKV, kv_full, kv_empty, wait, p, pc, policy_evict_first(), nullptr};
     copies.run(&k_map, &v_map);
   } else if (warp == kIssueWarp) {
     // ----------------------------------------------------------------- products
@@ -1146,7 +1179,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
       uint4 x[D / 8];
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) x[c] = live ? src[c] : make_uint4(0, 0, 0, 0);
-      const bool lacks = lacks_pages(p.slots, pc, col, 64);
+      const bool lacks = lacks_pages(p.slots, pc, col, 2 * 32);
       // (while the queries come)
       const Parts parts = pc.whole ? Parts{0, 1} : parts_of(share, pc.unit0, pc.r.tiles);
       unsigned long long sees = 0;
@@ -1216,7 +1249,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
         uint2 seen = make_uint2(~0u, ~0u);     // the columns that see this slot
         if (masked && slot >= rq.len)
           seen = slot < rq.end ? *reinterpret_cast<const uint2*>(seen_s + 128 * q + 2 * (slot - rq.len)) : make_uint2(0, 0);
-        if (lacks && slot < rq.end && !on_a_page(p.slots, rq.b, slot)) seen = make_uint2(0, 0);
+        if (lacks && slot < rq.end && !is_page(p.slots, pages_of(p.slots, rq.b)[slot >> p.slots.page_shift]))
+          seen = make_uint2(0, 0);
         ok = wait(&s_full[buf], (t >> 1) & 1) && ok;
         __syncwarp();
         tc_fence_after_sync();
