@@ -275,6 +275,75 @@ def test_attention_of_pages_that_are_none(case, dtype):
     assert ((got - ref_lse).abs() <= bound)[~none].all()
 
 
+# rows a key head (12 tokens' query heads): up to 16 and 64 rows, and one and two blocks of 128
+GROUPS = [1, 2, 8, 16]
+
+
+@pytest.mark.parametrize("group", GROUPS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("length", [0, 120, 500, 2500])        # the last two shared out in parts
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_attention_of_values_and_keys_that_are_not_finite(group, D, length, bad):
+    """A token's value that is not finite reaches the rows that see the token and no others, by every
+    kernel and through the joining of parts; so does its key."""
+    batch = Batch([12], [length], 16, seed=11, tree=True)
+    k, v = new_cache(batch, 2, D, BF16)
+    fill_cache(batch, k, v)
+    clean = v.clone()
+    page, line = batch.place(0, [length + 3])
+    v[page, line, 1, 5] = bad                                 # token 3's value of head 1, two elements
+    v[page, line, 1, D - 1] = bad
+    q = torch.randn(1, 12, 2 * group, D, generator=gen(9), device="cuda").to(BF16)
+    ws = workspace(batch, 2 * group, 2, D)
+    cache = ds.PagedCache(k, v)
+    out = ds.tree_attention(q, cache, batch.pages, batch.lens, ws, **batch.kw)
+    hit = torch.tensor([3 in sees(batch.trees[0], i) for i in range(12)], device="cuda")
+    assert hit.any() and not hit.all()
+    seen = torch.zeros_like(out, dtype=torch.bool)
+    seen[0, :, group:, 5] = hit[:, None]
+    seen[0, :, group:, D - 1] = hit[:, None]
+    got = out[seen]
+    assert torch.isnan(got).all() if math.isnan(bad) else (got == bad).all()
+    v.copy_(clean)
+    want = ds.tree_attention(q, cache, batch.pages, batch.lens, ws, **batch.kw)
+    assert torch.isfinite(want).all() and torch.equal(out[~seen], want[~seen])
+    # two tokens' values that are opposite infinities, where both are seen
+    if math.isinf(bad):
+        v[page, line, 1, 5] = bad
+        root = batch.place(0, [length])
+        v[root[0], root[1], 1, 5] = -bad
+        out = ds.tree_attention(q, cache, batch.pages, batch.lens, ws, **batch.kw)
+        assert torch.isnan(out[0, hit][:, group:, 5]).all() and (out[0, ~hit][:, group:, 5] == -bad).all()
+        v.copy_(clean)
+    k[page, line, 1, 5] = bad
+    out = ds.tree_attention(q, cache, batch.pages, batch.lens, ws, **batch.kw)
+    reach = torch.zeros_like(seen)
+    reach[0, :, group:] = hit[:, None, None]
+    assert torch.equal(out[~reach], want[~reach])
+    if math.isnan(bad):
+        assert torch.isnan(out[reach]).all()
+    assert ws.status() == 0
+
+
+@pytest.mark.parametrize("group", GROUPS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("length", [300, 2500])
+def test_attention_of_queries_that_are_not_finite(group, D, length):
+    """A query head of NaN gives NaN of its own row alone."""
+    batch = Batch([12], [length], 16)
+    k, v = new_cache(batch, 2, D, F16)
+    fill_cache(batch, k, v)
+    q = torch.randn(1, 12, 2 * group, D, generator=gen(1), device="cuda").to(F16)
+    ws = workspace(batch, 2 * group, 2, D)
+    want = ds.tree_attention(q, ds.PagedCache(k, v), batch.pages, batch.lens, ws, **batch.kw)
+    q[0, 7, group, D - 2] = math.nan
+    out = ds.tree_attention(q, ds.PagedCache(k, v), batch.pages, batch.lens, ws, **batch.kw)
+    other = torch.ones_like(out, dtype=torch.bool)
+    other[0, 7, group] = False
+    assert torch.isnan(out[0, 7, group]).all() and torch.isfinite(want).all()
+    assert torch.equal(out[other], want[other]) and ws.status() == 0
+
+
 # --------------------------------------------------------- calls that are checked in Python
 
 def test_calls_without_the_module(monkeypatch, tmp_path):
