@@ -28,9 +28,10 @@ struct AppendParams {
 constexpr int kMaxHalf = 128;            // pairs of a head (head_dim <= 256)
 
 // Cosine and sine of position x frequency, which is reduced to a turn in whole numbers: the
-// frequency's 24 bits times 2^64 / (2 pi) are at most 2^-65 of a turn off for each unit of
-// frequency, and the position's multiple wraps at whole turns by itself.  So at position 2^30 and
-// frequency 1 the angle is off by 2^-35 of a turn before it is rounded to fp32 (an fp32 product
+// frequency's 24 bits times 2^64 / (2 pi), rounded to a whole number (half a unit for each unit of
+// frequency), are cut off to whole 2^-64 turns (a unit), and the position's multiple wraps at
+// whole turns by itself.  So a position is off by (frequency / 2 + 1) 2^-64 of a turn at most, and
+// position 2^30 at frequencies up to 1 by 1.5 x 2^-34 before it is rounded to fp32 (an fp32 product
 // would be off by some turns), without an instruction in 64-bit floating point: those take
 // 100 cycles and more here, and five of them stood between a row's length and its stores.
 __device__ __forceinline__ float2 turn_of(int position, float freq) {

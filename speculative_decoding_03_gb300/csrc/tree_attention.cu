@@ -20,10 +20,10 @@
 // last or by a kernel of their own, so results do not depend on the order in which CTAs run.
 //
 // Measured on a GB300 (graphs of calls, other inputs in turn): two chains of 8 over 130,000 slots, 32
-// heads on 8 of 128, 163 to 166 us, 96% of the copy bandwidth; 32 trees of up to 16 over 4000 slots in
-// pages of 16 93.7 us, 83%; 128 chains of up to 8 over 1 to 2999 slots, 16 heads on 2 of 64, 38.1 us, 39%,
+// heads on 8 of 128, 160 to 166 us, 95 to 98% of the copy bandwidth; 32 trees of up to 16 over 4000 slots in
+// pages of 16 92 to 94 us, 84%; 128 chains of up to 8 over 1 to 2999 slots, 16 heads on 2 of 64, 38.1 us, 39%,
 // bound by the latency of a tile's steps (1450 cycles) and of a piece's beginning and end (6000);
-// one token over 1000 slots 10 us, launch and latency.
+// one token over 1000 slots 10.1 us, launch and latency.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -986,12 +986,6 @@ struct PieceInfo {           // what the loading warps say of a piece; no tiles:
   Parts parts;
 };
 
-__device__ __forceinline__ float warp_max(float x) {      // (NaN only if every lane's is)
-  float y;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Sums over a warp's lanes of 16 columns: each exchange halves the columns that a lane looks
 // after; lanes 2 c and 2 c + 1 are left with column c's.
 __device__ __forceinline__ float sum_over_lanes(float (&v)[16], int lane) {
@@ -1287,7 +1281,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const __grid
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
               float4 m;
-              m.x = warp_max(x[16 * c + e]);
+              m.x = warp_max(x[16 * c + e]);     // (NaN only if every lane's is)
               m.y = warp_max(x[16 * c + e + 1]);
               m.z = warp_max(x[16 * c + e + 2]);
               m.w = warp_max(x[16 * c + e + 3]);
