@@ -613,8 +613,8 @@ typedef struct {
  *   (x_a, x_b) = (x_a cos - x_b sin, x_b cos + x_a sin),  angle position * inv_freq[j]
  * of pairs j: elements j and j + rotated / 2, or 2 j and 2 j + 1 (interleaved); elements from
  * `rotated` on stay.  position = lengths[b] + the token's depth in its tree (a chain: its place).
- * Angles are formed in whole numbers (2^-35 of a turn off at most at position 2^30 and frequency
- * 1; a frequency that is not finite turns its pairs into NaN), the rest is in fp32, with one
+ * Angles are formed in whole numbers (at most 1.5 x 2^-34 of a turn off at position 2^30 and
+ * frequencies up to 1; a frequency that is not finite turns its pairs into NaN), the rest is in fp32, with one
  * rounding where a value is stored.
  * q_out may be q itself (same strides); arrays overlap in no other way.
  *
